@@ -62,6 +62,14 @@ _SIGNATURES = {
                                       _I64, _P, _I32, _I32, _I32, _I32, _I32, _F32, _P, _P]),
     "lat_kv_append": (_I32, [_I32, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _I32,
                              _I32, _I32, _I32, _P, _P]),
+    "lat_kv_q4_row_bytes": (_I32, [_I32]),
+    "lat_kv_append_q4": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _I32, _I32,
+                                _I32, _I32, _P, _P]),
+    "lat_kv_expand_q4": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _P, _P, _I64, _P, _I32, _I32,
+                                _I32, _I32, _P, _P]),
+    "lat_attn_decode_q4_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "lat_attn_decode_q4": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I32, _P, _I64, _P,
+                                  _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P, _SZ, _P, _P]),
     "lat_test_prefill_timeout": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32,
                                         _I32, _I32, _I32, _U64, _P, _P]),
     "lat_test_decode_timeout": (_I32, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _I64,
@@ -219,6 +227,49 @@ def lat_kv_append(dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_s
         dt, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride, cache_seq_stride,
         capacity, _ptr(k_new), _ptr(v_new), new_rs, _ptr(pos), n_new, batch, n_kv_heads,
         head_dim, _ptr(status), _stream(stream)), "lat_kv_append")
+
+
+def lat_kv_q4_row_bytes(head_dim) -> int:
+    """Bytes of one 4-bit cache row (a token's K and V of one head); 0 if not built."""
+    return library().lat_kv_q4_row_bytes(head_dim)
+
+
+def lat_kv_append_q4(dt, cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, k_new,
+                     v_new, new_rs, pos, n_new, batch, n_kv_heads, head_dim, status=None,
+                     stream=None):
+    """Quantise new K/V rows into a 4-bit cache (cache strides in bytes)."""
+    _check(library().lat_kv_append_q4(
+        dt, _ptr(cache), cache_rs, cache_head_stride, cache_seq_stride, capacity, _ptr(k_new),
+        _ptr(v_new), new_rs, _ptr(pos), n_new, batch, n_kv_heads, head_dim, _ptr(status),
+        _stream(stream)), "lat_kv_append_q4")
+
+
+def lat_kv_expand_q4(dt, cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, k_out,
+                     v_out, out_rs, pos, n_rows, batch, n_kv_heads, head_dim, status=None,
+                     stream=None):
+    """Read rows of a 4-bit cache back as K and V rows."""
+    _check(library().lat_kv_expand_q4(
+        dt, _ptr(cache), cache_rs, cache_head_stride, cache_seq_stride, capacity, _ptr(k_out),
+        _ptr(v_out), out_rs, _ptr(pos), n_rows, batch, n_kv_heads, head_dim, _ptr(status),
+        _stream(stream)), "lat_kv_expand_q4")
+
+
+def lat_attn_decode_q4_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim,
+                                      max_kv_len) -> int:
+    return library().lat_attn_decode_q4_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim,
+                                                       max_kv_len)
+
+
+def lat_attn_decode_q4(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride,
+                       kv_lens, max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads,
+                       head_dim, window, scale, softcap, workspace, workspace_bytes,
+                       status=None, stream=None):
+    """Decode over a 4-bit cache (cache strides in bytes)."""
+    _check(library().lat_attn_decode_q4(
+        dt, _ptr(q), q_rs, _ptr(cache), cache_rs, cache_head_stride, cache_seq_stride,
+        _ptr(kv_lens), max_kv_len, _ptr(out), out_rs, _ptr(lse), batch, n_heads, n_kv_heads,
+        head_dim, window, scale, softcap, _ptr(workspace), workspace_bytes, _ptr(status),
+        _stream(stream)), "lat_attn_decode_q4")
 
 
 def lat_test_prefill_timeout(q, q_rs, k, k_rs, v, v_rs, out, out_rs, batch, seq_len, n_heads,

@@ -668,3 +668,160 @@ lat_status lat_kv_append_ring(lat_dtype dt, void *k_cache, void *v_cache, int64_
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- 4-bit KV cache
+
+namespace {
+
+// 4-D map of a 4-bit cache in 32-bit words: (word of the row, KV head, row < rows, sequence)
+// with a [row, 1, box_rows, 1] box; a warp's rows land one behind another.
+bool make_q4_map(CUtensorMap *m, const void *base, int row_bytes, int heads, int rows, int batch,
+                 int64_t row_stride, int64_t head_stride, int64_t seq_stride, int box_rows) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)row_bytes / 4, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)head_stride, (cuuint64_t)row_stride, (cuuint64_t)seq_stride};
+    const cuuint32_t box[4] = {(cuuint32_t)row_bytes / 4, 1, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool q4_strides_ok(int64_t row, int64_t head, int64_t seq) {
+    return row > 0 && head > 0 && seq > 0 && row % 16 == 0 && head % 16 == 0 && seq % 16 == 0;
+}
+
+lat_status q4_store_impl(lat_dtype dt, void *cache, int64_t cache_rs, int64_t cache_head_stride,
+                         int64_t cache_seq_stride, int capacity, const void *k, const void *v, void *k_out,
+                         void *v_out, int64_t rs, const int32_t *pos, int n, int batch, int n_kv_heads,
+                         int head_dim, bool expand, int32_t *status, void *stream) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || n < 0 || capacity < 0 || n_kv_heads <= 0) return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0 || n == 0) return LAT_OK;
+    if (!cache || !pos || (expand ? (!k_out || !v_out) : (!k || !v))) return LAT_ERR_INVALID_ARG;
+    if (!aligned16(cache) || !q4_strides_ok(cache_rs, cache_head_stride, cache_seq_stride) ||
+        rs < (int64_t)n_kv_heads * head_dim)
+        return LAT_ERR_INVALID_ARG;
+    if ((int64_t)batch * n > 0x7fffffffLL / n_kv_heads) return LAT_ERR_UNSUPPORTED;
+    lat::Q4StoreArgs a{};
+    a.cache = static_cast<unsigned char *>(cache);
+    a.cache_rs = cache_rs;
+    a.cache_head = cache_head_stride;
+    a.cache_seq = cache_seq_stride;
+    a.k = k;
+    a.v = v;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.rs = rs;
+    const int64_t es = dt == LAT_BF16 ? 2 : 4;
+    a.vec = rs * es % 16 == 0 && (expand ? aligned16(k_out) && aligned16(v_out) : aligned16(k) && aligned16(v));
+    a.pos = pos;
+    a.capacity = capacity;
+    a.n = n;
+    a.batch = batch;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.status = status;
+    return lat::launch_q4_store(a, dt == LAT_BF16, expand, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LAT_OK
+               : LAT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lat_kv_q4_row_bytes(int head_dim) { return lat::q4_row_bytes(head_dim); }
+
+lat_status lat_kv_append_q4(lat_dtype dt, void *cache, int64_t cache_rs, int64_t cache_head_stride,
+                            int64_t cache_seq_stride, int capacity, const void *k_new, const void *v_new,
+                            int64_t new_rs, const int32_t *pos, int n_new, int batch, int n_kv_heads,
+                            int head_dim, int32_t *status, void *stream) {
+    return q4_store_impl(dt, cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, k_new, v_new, nullptr,
+                         nullptr, new_rs, pos, n_new, batch, n_kv_heads, head_dim, false, status, stream);
+}
+
+lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs, int64_t cache_head_stride,
+                            int64_t cache_seq_stride, int capacity, void *k_out, void *v_out, int64_t out_rs,
+                            const int32_t *pos, int n_rows, int batch, int n_kv_heads, int head_dim,
+                            int32_t *status, void *stream) {
+    return q4_store_impl(dt, const_cast<void *>(cache), cache_rs, cache_head_stride, cache_seq_stride, capacity,
+                         nullptr, nullptr, k_out, v_out, out_rs, pos, n_rows, batch, n_kv_heads, head_dim, true,
+                         status, stream);
+}
+
+size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                         int max_kv_len) {
+    if ((dt != LAT_F32 && dt != LAT_BF16) || batch < 0 || batch > 65535 || n_heads <= 0 || n_kv_heads <= 0 ||
+        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || max_kv_len < 0)
+        return 0;
+    int sms = 0;
+    lat::Q4Plan plan;
+    if (!current_sm_count(&sms) ||
+        !lat::plan_decode_q4(batch, n_heads, n_kv_heads, head_dim, dt == LAT_BF16, max_kv_len, sms, &plan))
+        return 0;
+    return plan.total_bytes;
+}
+
+lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const void *cache, int64_t cache_rs,
+                              int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
+                              int max_kv_len, void *out, int64_t out_rs, float *lse, int batch, int n_heads,
+                              int n_kv_heads, int head_dim, int window, float scale, float softcap,
+                              void *workspace, size_t workspace_bytes, int32_t *status, void *stream) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (!(softcap >= 0.f) || !isfinite(softcap) || !isfinite(scale)) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || max_kv_len < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0)
+        return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0) return LAT_OK;
+    if (!q || !cache || !kv_lens || !out) return LAT_ERR_INVALID_ARG;
+    const int64_t per16 = dt == LAT_BF16 ? 8 : 4;  // elements in 16 bytes
+    if (q_rs < (int64_t)n_heads * head_dim || out_rs < (int64_t)n_heads * head_dim || q_rs % per16 ||
+        out_rs % per16 || !aligned16(q) || !aligned16(cache) || !aligned16(out) ||
+        !q4_strides_ok(cache_rs, cache_head_stride, cache_seq_stride))
+        return LAT_ERR_INVALID_ARG;
+    if (batch > 65535) return LAT_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
+    lat::Q4Plan plan;
+    if (!lat::plan_decode_q4(batch, n_heads, n_kv_heads, head_dim, dt == LAT_BF16, max_kv_len, sms, &plan))
+        return LAT_ERR_UNSUPPORTED;
+    if (workspace == nullptr || workspace_bytes < plan.total_bytes ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return LAT_ERR_WORKSPACE;
+    lat::Q4DecodeArgs a{};
+    if (max_kv_len > 0 &&
+        !make_q4_map(&a.tm, cache, lat::q4_row_bytes(head_dim), n_kv_heads, max_kv_len, batch, cache_rs,
+                     cache_head_stride, cache_seq_stride, plan.box_rows))
+        return LAT_ERR_CUDA;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    a.q = q;
+    a.q_rs = q_rs;
+    a.kv_lens = kv_lens;
+    a.max_kv_len = max_kv_len;
+    a.out = out;
+    a.out_rs = out_rs;
+    a.lse = lse;
+    a.batch = batch;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.window = window < 0 ? 0 : window;
+    a.scale_log2 = scale * kLog2e;
+    a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
+    a.raw_over_cap = softcap > 0.f ? scale / softcap : 0.f;
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_lse = reinterpret_cast<float *>(ws + plan.part_o_bytes);
+    a.piece_count = reinterpret_cast<int32_t *>(ws + plan.part_o_bytes + plan.part_lse_bytes);
+    a.max_splits = plan.max_splits;
+    a.min_tiles = plan.min_tiles;
+    a.timeout_ns = kDefaultTimeoutNs;
+    a.status = status;
+    return lat::launch_decode_q4(a, dt == LAT_BF16, plan.grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LAT_OK
+               : LAT_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -111,6 +111,49 @@ constexpr int64_t kDecodeMaxUnits = int64_t(1) << 23;
 int decode_bf16_tile_keys(int head_dim);     // cache rows per TMA box for this head_dim
 cudaError_t launch_decode_bf16(const DecodeArgs &a, int grid, cudaStream_t s);
 
+// ---------------------------------------------------------------- 4-bit KV cache
+// bytes of one cached row (a token's K and V of one head), 0 for head sizes not built
+int q4_row_bytes(int head_dim);
+struct Q4StoreArgs {
+    unsigned char *cache;                     // strides in bytes
+    int64_t cache_rs, cache_head, cache_seq;
+    const void *k, *v;                        // append: the new rows
+    void *k_out, *v_out;                      // expand: the rows read back
+    int64_t rs;                               // their row stride in elements
+    int vec;                                  // 16-byte vectors on that side
+    const int32_t *pos;
+    int capacity, n, batch, n_kv_heads, head_dim;
+    int32_t *status;
+};
+// batch * n * n_kv_heads < 2^31
+cudaError_t launch_q4_store(const Q4StoreArgs &a, bool bf16, bool expand, cudaStream_t s);
+
+struct Q4DecodeArgs {
+    CUtensorMap tm;  // 4-D map of 32-bit words (word, head, row < max_kv_len, sequence)
+    const void *q;
+    int64_t q_rs;
+    const int32_t *kv_lens;
+    int max_kv_len;
+    void *out;
+    int64_t out_rs;
+    float *lse;
+    int batch, n_heads, n_kv_heads, head_dim, window;
+    float scale_log2, cap_log2, raw_over_cap;  // as in DecodeArgs
+    float *part_o;         // [batch, n_heads, max_splits, head_dim]
+    float *part_lse;       // [batch, n_heads, max_splits], log2 domain
+    int32_t *piece_count;  // [batch, n_heads]
+    int max_splits, min_tiles;
+    uint64_t timeout_ns;
+    int32_t *status;
+};
+struct Q4Plan {
+    int grid, min_tiles, max_splits, box_rows;
+    size_t part_o_bytes, part_lse_bytes, total_bytes;
+};
+bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,
+                    Q4Plan *p);
+cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, int grid, cudaStream_t s);
+
 // ---------------------------------------------------------------- bf16 tensor-core prefill
 struct PrefillTcArgs {
     CUtensorMap tm_q, tm_k, tm_v;  // 4-D maps (d, head, row, batch), 128-byte swizzle

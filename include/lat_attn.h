@@ -314,6 +314,81 @@ lat_status lat_qkv_norm_rope_append(lat_dtype dt, const void *qkv, int64_t qkv_r
                                     int n_new, int batch, int n_heads, int n_kv_heads,
                                     int head_dim, int32_t *status, void *stream);
 
+/*
+ * The 4-bit KV cache: lat_kv_q4_row_bytes, lat_kv_append_q4, lat_kv_expand_q4 and
+ * lat_attn_decode_q4.  The pages keep their caches in 16 bits; this one holds a decode
+ * step's bytes at 1.25 per channel of K and V instead of 4.
+ *
+ * One cache row is one token's K and V of one KV head, lat_kv_q4_row_bytes(head_dim) bytes
+ * (80, 128, 160, 320, 640 at head_dim 64, 80, 128, 256, 512; 0 for sizes not built).  Row j
+ * of sequence b and KV head hk is at byte b*cache_seq_stride + j*cache_rs +
+ * hk*cache_head_stride of `cache`: these three strides are in BYTES, positive multiples of
+ * 16, and the cache is 16-byte aligned, else LAT_ERR_INVALID_ARG.
+ *
+ * Channels are quantised in groups of 32 along the head (head_dim 80: 32, 32, 16), K and V
+ * apart.  With mn = min(0, min x) and mx = max(0, max x) over a group:
+ *   s = bf16((mx - mn) / 15)  (difference and quotient in fp32),
+ *   z = nearest whole number to -mn / s,  c = nearest to x / s, plus z, each in 0 .. 15,
+ * and the group reads back as s * (c - z): 0 is exact, a value is off by at most half a step
+ * s (at the ends of the grid by up to one step more, where s or z was rounded).  A group
+ * that holds a NaN or an infinity, or spans more than the largest fp32, reads back as NaN.
+ * The order of the codes within a row belongs to the library.
+ */
+int lat_kv_q4_row_bytes(int head_dim);
+
+/*
+ * lat_kv_append_q4 — lat_kv_append into a 4-bit cache: row pos[b] + t of sequence b takes
+ * new row t, quantised, for t < n_new.  New rows as in lat_kv_append (element (b,t,hk,d) at
+ * k_new[(b*n_new + t)*new_rs + hk*head_dim + d]); dt is their type.  A sequence whose rows
+ * would fall outside [0, capacity) is skipped whole and sets *status = LAT_ERR_BOUNDS.
+ * batch * n_new * n_kv_heads must stay below 2^31, else LAT_ERR_UNSUPPORTED.
+ */
+lat_status lat_kv_append_q4(lat_dtype dt, void *cache, int64_t cache_rs,
+                            int64_t cache_head_stride, int64_t cache_seq_stride, int capacity,
+                            const void *k_new, const void *v_new, int64_t new_rs,
+                            const int32_t *pos, int n_new, int batch, int n_kv_heads,
+                            int head_dim, int32_t *status, void *stream);
+
+/*
+ * lat_kv_expand_q4 — the reverse: rows pos[b] .. pos[b] + n_rows - 1 of sequence b read back
+ * as K and V rows of type dt (element (b,t,hk,d) at k_out[(b*n_rows + t)*out_rs +
+ * hk*head_dim + d], v_out alike; one rounding to dt), the layout that lat_attn_prefill
+ * takes: a chunk of a prompt is appended, its sequence's rows are read back, and its queries
+ * attend to them.  Other rules as in lat_kv_append_q4; a sequence out of range leaves its
+ * output rows as they were.
+ */
+lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs,
+                            int64_t cache_head_stride, int64_t cache_seq_stride, int capacity,
+                            void *k_out, void *v_out, int64_t out_rs, const int32_t *pos,
+                            int n_rows, int batch, int n_kv_heads, int head_dim,
+                            int32_t *status, void *stream);
+
+/*
+ * lat_attn_decode_q4 — lat_attn_decode_softcap over a 4-bit cache: one query token per
+ * sequence, at position kv_lens[b] - 1, over the cached keys max(0, kv_lens[b] - window) ..
+ * kv_lens[b] - 1 (all of them when window <= 0), keys and values as they read back; softcap
+ * finite and >= 0, 0 = none.  dt is the type of q and out.
+ * q, out, lse, kv_lens, max_kv_len and the status are lat_attn_decode's; a sequence of length
+ * 0 gets out = 0, lse = -inf.  q and out must be 16-byte aligned and their row strides
+ * multiples of 16 bytes, else LAT_ERR_INVALID_ARG.  Every sequence's cache must hold at
+ * least max_kv_len rows; rows at or past kv_lens[b] may hold any bytes.
+ * workspace: at least lat_attn_decode_q4_workspace_size(...) bytes of device memory with the
+ * same sizes (for either dt), 256-byte aligned, else LAT_ERR_WORKSPACE.  It needs no
+ * clearing; calls sharing one must not overlap on the GPU.  Its size depends on the current
+ * device's SM count.
+ * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, batch * n_heads * ceil(head_dim / 128)
+ * < 2^31.
+ */
+size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads,
+                                         int head_dim, int max_kv_len);
+lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const void *cache,
+                              int64_t cache_rs, int64_t cache_head_stride,
+                              int64_t cache_seq_stride, const int32_t *kv_lens, int max_kv_len,
+                              void *out, int64_t out_rs, float *lse, int batch, int n_heads,
+                              int n_kv_heads, int head_dim, int window, float scale,
+                              float softcap, void *workspace, size_t workspace_bytes,
+                              int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
