@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(32 * kStoreWarps) append_q4_kernel(const Q4Sto
         // a NaN, an infinity or a range past the largest number has no grid: the scale is NaN
         // and so is what the group reads back as
         bad |= !(range <= 3.4028235e38f);
-        __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.f));
+        __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.f / 15.f));
         const float s = __bfloat162float(sb);
         const bool flat = bad || !(s > 0.f);
         // (a scale whose reciprocal could overflow is taken 2^100 times as large, exactly)

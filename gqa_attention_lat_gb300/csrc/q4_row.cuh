@@ -2,7 +2,7 @@
 //
 // Channels come in groups of 32 (head_dim 80 is taken as 96, zeros behind).  With
 // mn = min(0, x) and mx = max(0, x) over a group,
-//   s = bf16((mx - mn) / 15),  z = clamp(rint(-mn / s), 0, 15),
+//   s = bf16((mx - mn) * (1/15)) in fp32,  z = clamp(rint(-mn / s), 0, 15),
 //   c = clamp(rint(x / s) + z, 0, 15),  and the group reads back as s * (c - z).
 // The zero point lies on the grid, so c - z is an integer of at most 4 bits and a sign:
 // exact in bf16, with no additive term beside the products of an attention.

@@ -327,7 +327,7 @@ lat_status lat_qkv_norm_rope_append(lat_dtype dt, const void *qkv, int64_t qkv_r
  *
  * Channels are quantised in groups of 32 along the head (head_dim 80: 32, 32, 16), K and V
  * apart.  With mn = min(0, min x) and mx = max(0, max x) over a group:
- *   s = bf16((mx - mn) / 15)  (difference and quotient in fp32),
+ *   s = bf16((mx - mn) * (1/15))  (difference, constant and product in fp32),
  *   z = nearest whole number to -mn / s,  c = nearest to x / s, plus z, each in 0 .. 15,
  * and the group reads back as s * (c - z): 0 is exact, a value is off by at most half a step
  * s (at the ends of the grid by up to one step more, where s or z was rounded).  A group

@@ -1,8 +1,8 @@
 """fp64 oracle of the 4-bit KV cache: what a row of channels reads back as.
 
 By the definition, a group of 32 channels at a time (the last one of a head may be shorter):
-mn = min(0, min x), mx = max(0, max x); s = bf16((mx - mn) / 15) with the difference and the
-quotient in fp32; z = nearest(-mn / s); c = nearest(x / s) + z; z and c held in 0 .. 15; the
+mn = min(0, min x), mx = max(0, max x); s = bf16((mx - mn) * (1 / 15)) with the difference,
+the constant and the product in fp32; z = nearest(-mn / s); c = nearest(x / s) + z; z and c held in 0 .. 15; the
 group reads back as s * (c - z).  A group without a finite grid reads back as NaN.  The
 quotients are taken in fp64, where the quotient of a 24-bit by an 8-bit number cannot round
 onto a half that it is not.
@@ -12,6 +12,7 @@ from __future__ import annotations
 import numpy as np
 
 GROUP = 32
+FIFTEENTH = np.float32(1) / np.float32(15)
 
 
 def bf16(x):
@@ -32,7 +33,7 @@ def readback(x) -> np.ndarray:
             mx = np.maximum(g.max(-1), np.float32(0))
             span = (mx - mn).astype(np.float32)
             grid = np.isfinite(span) & np.isfinite(g).all(-1)
-            s = bf16(np.where(grid, span, 0).astype(np.float32) / np.float32(15)).astype(np.float64)
+            s = bf16(np.where(grid, span, 0).astype(np.float32) * FIFTEENTH).astype(np.float64)
             div = np.where(s > 0, s, 1.0)[..., None]
             flat = (s <= 0)[..., None]
             z = np.clip(np.rint(-np.where(grid, mn, 0).astype(np.float64)[..., None] / div), 0, 15)
