@@ -70,6 +70,16 @@ _SIGNATURES = {
     "lat_attn_decode_q4_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "lat_attn_decode_q4": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I32, _P, _I64, _P,
                                   _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P, _SZ, _P, _P]),
+    "lat_kv_block_bounds": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64, _I32,
+                                   _P, _I32, _I32, _I32, _I32, _P, _P]),
+    "lat_attn_select_blocks_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
+    "lat_attn_select_blocks": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _P,
+                                      _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _SZ, _P,
+                                      _P]),
+    "lat_attn_decode_blocks_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "lat_attn_decode_blocks": (_I32, [_I32, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I32,
+                                      _P, _I32, _P, _I64, _P, _I32, _I32, _I32, _I32, _F32,
+                                      _F32, _P, _SZ, _P, _P]),
     "lat_test_prefill_timeout": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32,
                                         _I32, _I32, _I32, _U64, _P, _P]),
     "lat_test_decode_timeout": (_I32, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _I64,
@@ -270,6 +280,52 @@ def lat_attn_decode_q4(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_se
         _ptr(kv_lens), max_kv_len, _ptr(out), out_rs, _ptr(lse), batch, n_heads, n_kv_heads,
         head_dim, window, scale, softcap, _ptr(workspace), workspace_bytes, _ptr(status),
         _stream(stream)), "lat_attn_decode_q4")
+
+
+def lat_kv_block_bounds(dt, k_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity,
+                        bounds, bounds_rs, bounds_head_stride, bounds_seq_stride, block_size,
+                        pos, n_new, batch, n_kv_heads, head_dim, status=None, stream=None):
+    """Bring the bounds of the blocks that hold the newly appended keys up to date."""
+    _check(library().lat_kv_block_bounds(
+        dt, _ptr(k_cache), cache_rs, cache_head_stride, cache_seq_stride, capacity, _ptr(bounds),
+        bounds_rs, bounds_head_stride, bounds_seq_stride, block_size, _ptr(pos), n_new, batch,
+        n_kv_heads, head_dim, _ptr(status), _stream(stream)), "lat_kv_block_bounds")
+
+
+def lat_attn_select_blocks_workspace_size(batch, n_kv_heads, block_size, max_kv_len) -> int:
+    return library().lat_attn_select_blocks_workspace_size(batch, n_kv_heads, block_size,
+                                                           max_kv_len)
+
+
+def lat_attn_select_blocks(dt, q, q_rs, bounds, bounds_rs, bounds_head_stride,
+                           bounds_seq_stride, block_size, kv_lens, max_kv_len, blocks, n_sel,
+                           n_first, n_last, batch, n_heads, n_kv_heads, head_dim, workspace,
+                           workspace_bytes, status=None, stream=None):
+    """Choose the blocks that each KV head keeps, into int32 blocks [batch, n_kv_heads, n_sel]."""
+    _check(library().lat_attn_select_blocks(
+        dt, _ptr(q), q_rs, _ptr(bounds), bounds_rs, bounds_head_stride, bounds_seq_stride,
+        block_size, _ptr(kv_lens), max_kv_len, _ptr(blocks), n_sel, n_first, n_last, batch,
+        n_heads, n_kv_heads, head_dim, _ptr(workspace), workspace_bytes, _ptr(status),
+        _stream(stream)), "lat_attn_select_blocks")
+
+
+def lat_attn_decode_blocks_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim, block_size,
+                                          n_sel) -> int:
+    return library().lat_attn_decode_blocks_workspace_size(dt, batch, n_heads, n_kv_heads,
+                                                           head_dim, block_size, n_sel)
+
+
+def lat_attn_decode_blocks(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+                           cache_seq_stride, kv_lens, max_kv_len, block_size, blocks, n_sel,
+                           out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim, scale,
+                           softcap, workspace, workspace_bytes, status=None, stream=None):
+    """Decode over the listed blocks of the cache alone."""
+    _check(library().lat_attn_decode_blocks(
+        dt, _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
+        cache_seq_stride, _ptr(kv_lens), max_kv_len, block_size, _ptr(blocks), n_sel, _ptr(out),
+        out_rs, _ptr(lse), batch, n_heads, n_kv_heads, head_dim, scale, softcap,
+        _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)),
+        "lat_attn_decode_blocks")
 
 
 def lat_test_prefill_timeout(q, q_rs, k, k_rs, v, v_rs, out, out_rs, batch, seq_len, n_heads,

@@ -22,7 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblat_attn.so")
 
 SOURCES = ["api.cu", "kv_append.cu", "row_attention_f32.cu", "decode_bf16.cu", "prefill_tc.cu",
-           "decode_static.cu", "qkv_producer.cu", "kv_q4.cu", "decode_q4.cu"]
+           "decode_static.cu", "qkv_producer.cu", "kv_q4.cu", "decode_q4.cu",
+           "block_select.cu", "decode_blocks_f32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                  "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -349,7 +349,8 @@ lat_status decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k_
                        void *out, int64_t out_rs, float *lse, int batch, int n_heads,
                        int n_kv_heads, int head_dim, int window, float scale, float softcap,
                        int ring, void *workspace, size_t workspace_bytes, int32_t *status,
-                       void *stream, uint64_t timeout_ns, int skip_load) {
+                       void *stream, uint64_t timeout_ns, int skip_load,
+                       const int32_t *blocks = nullptr, int n_sel = 0, int block_size = 0) {
     if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
     if (!(softcap >= 0.f) || !isfinite(softcap)) return LAT_ERR_INVALID_ARG;
     // a ring cache keeps only the last `ring` positions: the window must fit in it
@@ -407,8 +408,10 @@ lat_status decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k_
     // rows per sequence: the ring, or every position up to max_kv_len; the scratch layout
     // is sized by the same count (a ring's visible keys never exceed it)
     const int rows = ring > 0 ? ring : max_kv_len;
+    // over chosen blocks the stream is as long as the list at most
+    const int range = blocks != nullptr ? n_sel * block_size : rows;
     lat::DecodePlan plan;
-    if (!lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, rows, window, sms, &plan))
+    if (!lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, range, window, sms, &plan))
         return LAT_ERR_UNSUPPORTED;
     if (workspace == nullptr || workspace_bytes < plan.total_bytes ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -460,6 +463,9 @@ lat_status decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k_
     a.head_dim = head_dim;
     a.window = window;
     a.ring = ring;
+    a.blocks = blocks;
+    a.n_sel = n_sel;
+    a.block_size = block_size;
     a.scale_log2 = scale * kLog2e;
     a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
     a.raw_over_cap = softcap > 0.f ? scale / softcap : 0.f;
@@ -822,6 +828,210 @@ lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const v
     return lat::launch_decode_q4(a, dt == LAT_BF16, plan.grid, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? LAT_OK
                : LAT_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- choice of cached blocks
+
+namespace {
+
+bool block_size_ok(int block_size) { return block_size >= 16 && block_size <= 1024 && block_size % 16 == 0; }
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// blocks that max_kv_len keys fill
+int64_t max_blocks_of(int max_kv_len, int block_size) { return ((int64_t)max_kv_len + block_size - 1) / block_size; }
+
+}  // namespace
+
+extern "C" {
+
+lat_status lat_kv_block_bounds(lat_dtype dt, const void *k_cache, int64_t cache_rs, int64_t cache_head_stride,
+                               int64_t cache_seq_stride, int capacity, void *bounds, int64_t bounds_rs,
+                               int64_t bounds_head_stride, int64_t bounds_seq_stride, int block_size,
+                               const int32_t *pos, int n_new, int batch, int n_kv_heads, int head_dim,
+                               int32_t *status, void *stream) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || n_new < 0 || capacity < 0 || n_kv_heads <= 0 || !block_size_ok(block_size))
+        return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0 || n_new == 0) return LAT_OK;
+    if (!k_cache || !bounds || !pos) return LAT_ERR_INVALID_ARG;
+    const int64_t per16 = dt == LAT_BF16 ? 8 : 4;  // elements in 16 bytes
+    if (!aligned16(k_cache) || !aligned16(bounds) || cache_rs <= 0 || cache_head_stride <= 0 ||
+        cache_seq_stride <= 0 || bounds_rs <= 0 || bounds_head_stride <= 0 || bounds_seq_stride <= 0 ||
+        cache_rs % per16 || cache_head_stride % per16 || cache_seq_stride % per16 || bounds_rs % per16 ||
+        bounds_head_stride % per16 || bounds_seq_stride % per16)
+        return LAT_ERR_INVALID_ARG;
+    // n_new rows touch at most this many blocks, wherever they begin
+    const int64_t touched = ((int64_t)n_new + block_size - 2) / block_size + 1;
+    if ((int64_t)batch * touched > 0x7fffffffLL / n_kv_heads) return LAT_ERR_UNSUPPORTED;
+    lat::BoundsArgs a{};
+    a.k_cache = k_cache;
+    a.cache_rs = cache_rs;
+    a.cache_head = cache_head_stride;
+    a.cache_seq = cache_seq_stride;
+    a.bounds = bounds;
+    a.bounds_rs = bounds_rs;
+    a.bounds_head = bounds_head_stride;
+    a.bounds_seq = bounds_seq_stride;
+    a.block_size = block_size;
+    a.capacity = capacity;
+    a.n_new = n_new;
+    a.max_touched = (int)touched;
+    a.batch = batch;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.pos = pos;
+    a.status = status;
+    return lat::launch_block_bounds(a, dt == LAT_BF16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LAT_OK
+               : LAT_ERR_CUDA;
+}
+
+size_t lat_attn_select_blocks_workspace_size(int batch, int n_kv_heads, int block_size, int max_kv_len) {
+    if (batch < 0 || n_kv_heads <= 0 || max_kv_len < 0 || !block_size_ok(block_size) ||
+        max_blocks_of(max_kv_len, block_size) > lat::kSelectMaxBlocks)
+        return 0;
+    const size_t n = (size_t)batch * n_kv_heads * (size_t)max_blocks_of(max_kv_len, block_size);
+    return round256(n * sizeof(float2)) + round256(n * sizeof(uint64_t));
+}
+
+lat_status lat_attn_select_blocks(lat_dtype dt, const void *q, int64_t q_rs, const void *bounds, int64_t bounds_rs,
+                                  int64_t bounds_head_stride, int64_t bounds_seq_stride, int block_size,
+                                  const int32_t *kv_lens, int max_kv_len, int32_t *blocks, int n_sel, int n_first,
+                                  int n_last, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                  void *workspace, size_t workspace_bytes, int32_t *status, void *stream) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || max_kv_len < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 ||
+        !block_size_ok(block_size) || n_sel <= 0 || n_first < 0 || n_last < 0 || n_first > n_sel ||
+        n_last > n_sel - n_first)
+        return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0) return LAT_OK;
+    if (!q || !bounds || !kv_lens || !blocks) return LAT_ERR_INVALID_ARG;
+    const int64_t per16 = dt == LAT_BF16 ? 8 : 4;
+    if (!aligned16(q) || !aligned16(bounds) || q_rs < (int64_t)n_heads * head_dim || q_rs % per16 || bounds_rs <= 0 ||
+        bounds_head_stride <= 0 || bounds_seq_stride <= 0 || bounds_rs % per16 || bounds_head_stride % per16 ||
+        bounds_seq_stride % per16)
+        return LAT_ERR_INVALID_ARG;
+    const int64_t max_blocks = max_blocks_of(max_kv_len, block_size);
+    if (max_blocks > lat::kSelectMaxBlocks || (int64_t)batch > 0x7fffffffLL / n_kv_heads) return LAT_ERR_UNSUPPORTED;
+    const size_t need = lat_attn_select_blocks_workspace_size(batch, n_kv_heads, block_size, max_kv_len);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return LAT_ERR_WORKSPACE;
+    int sms = 0;
+    if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
+    lat::SelectArgs a{};
+    a.q = q;
+    a.q_rs = q_rs;
+    a.bounds = bounds;
+    a.bounds_rs = bounds_rs;
+    a.bounds_head = bounds_head_stride;
+    a.bounds_seq = bounds_seq_stride;
+    a.block_size = block_size;
+    a.kv_lens = kv_lens;
+    a.max_kv_len = max_kv_len;
+    a.blocks = blocks;
+    a.n_sel = n_sel;
+    a.n_first = n_first;
+    a.n_last = n_last;
+    a.batch = batch;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    const size_t n = (size_t)batch * n_kv_heads * (size_t)max_blocks;
+    a.scores = static_cast<float2 *>(workspace);
+    a.exact = reinterpret_cast<uint64_t *>(static_cast<unsigned char *>(workspace) + round256(n * sizeof(float2)));
+    a.max_blocks = (int)max_blocks;
+    a.status = status;
+    return lat::launch_select_blocks(a, dt == LAT_BF16, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LAT_OK
+               : LAT_ERR_CUDA;
+}
+
+size_t lat_attn_decode_blocks_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                             int block_size, int n_sel) {
+    if ((dt != LAT_F32 && dt != LAT_BF16) || batch < 0 || batch > 65535 || n_heads <= 0 || n_kv_heads <= 0 ||
+        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || !block_size_ok(block_size) || n_sel <= 0 ||
+        n_sel > lat::kSelectMaxBlocks)
+        return 0;
+    if (dt == LAT_BF16)
+        return lat_attn_decode_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim, n_sel * block_size);
+    int sms = 0;
+    if (!current_sm_count(&sms)) return 0;
+    const size_t rows = (size_t)batch * n_heads;
+    const size_t splits = lat::blocks_f32_splits(batch, n_heads, n_kv_heads, block_size, n_sel, sms);
+    return splits == 1 ? 256 : round256(rows * splits * head_dim * 4) + round256(rows * splits * 4) + round256(rows * 4);
+}
+
+lat_status lat_attn_decode_blocks(lat_dtype dt, const void *q, int64_t q_rs, const void *k_cache,
+                                  const void *v_cache, int64_t cache_rs, int64_t cache_head_stride,
+                                  int64_t cache_seq_stride, const int32_t *kv_lens, int max_kv_len,
+                                  int block_size, const int32_t *blocks, int n_sel, void *out, int64_t out_rs,
+                                  float *lse, int batch, int n_heads, int n_kv_heads, int head_dim, float scale,
+                                  float softcap, void *workspace, size_t workspace_bytes, int32_t *status,
+                                  void *stream) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (!block_size_ok(block_size) || n_sel <= 0) return LAT_ERR_INVALID_ARG;
+    if (n_sel > lat::kSelectMaxBlocks) return LAT_ERR_UNSUPPORTED;
+    if (batch > 0 && !blocks) return LAT_ERR_INVALID_ARG;
+    if (dt == LAT_BF16)
+        return decode_impl(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,
+                           max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim, 0, scale, softcap, 0,
+                           workspace, workspace_bytes, status, stream, kDefaultTimeoutNs, 0, blocks, n_sel,
+                           block_size);
+    if (!(softcap >= 0.f) || !isfinite(softcap) || !isfinite(scale)) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || max_kv_len < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0)
+        return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0) return LAT_OK;
+    if (!q || !k_cache || !v_cache || !kv_lens || !out) return LAT_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+        q_rs < (int64_t)n_heads * head_dim || out_rs < (int64_t)n_heads * head_dim || q_rs % 4 || out_rs % 4 ||
+        cache_rs <= 0 || cache_head_stride <= 0 || cache_seq_stride <= 0 || cache_rs % 4 || cache_head_stride % 4 ||
+        cache_seq_stride % 4)
+        return LAT_ERR_INVALID_ARG;
+    if (batch > 65535) return LAT_ERR_UNSUPPORTED;
+    const size_t need = lat_attn_decode_blocks_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim, block_size, n_sel);
+    if (need == 0) return LAT_ERR_CUDA;
+    if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return LAT_ERR_WORKSPACE;
+    int sms = 0;
+    if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
+    lat::BlocksF32Args a{};
+    a.q = static_cast<const float *>(q);
+    a.q_rs = q_rs;
+    a.k = static_cast<const float *>(k_cache);
+    a.v = static_cast<const float *>(v_cache);
+    a.cache_rs = cache_rs;
+    a.cache_head = cache_head_stride;
+    a.cache_seq = cache_seq_stride;
+    a.kv_lens = kv_lens;
+    a.max_kv_len = max_kv_len;
+    a.blocks = blocks;
+    a.n_sel = n_sel;
+    a.block_size = block_size;
+    a.out = static_cast<float *>(out);
+    a.out_rs = out_rs;
+    a.lse = lse;
+    a.batch = batch;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.scale_log2 = scale * kLog2e;
+    a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
+    a.raw_over_cap = softcap > 0.f ? scale / softcap : 0.f;
+    a.splits = lat::blocks_f32_splits(batch, n_heads, n_kv_heads, block_size, n_sel, sms);
+    const size_t rows = (size_t)batch * n_heads;
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_lse = reinterpret_cast<float *>(ws + round256(rows * a.splits * head_dim * 4));
+    a.piece_count = reinterpret_cast<int32_t *>(ws + round256(rows * a.splits * head_dim * 4) + round256(rows * a.splits * 4));
+    a.status = status;
+    return lat::launch_decode_blocks_f32(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK
+                                                                                                   : LAT_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -92,7 +92,7 @@ struct StageRec {
     int kq;             // piece number within this CTA (selects the query buffer)
     int slot, nseg;     // partial slot of the piece, pieces of the unit
     int end;            // no more tiles
-    int pad;
+    uint32_t rows;      // chosen blocks: valid rows of the tile's 16-row groups, a byte each
 };
 
 // byte offset of 16-byte chunk c of row r in a tile stored as 64-column, 128-byte
@@ -125,15 +125,20 @@ __device__ __forceinline__ SeqKeys seq_keys_of(const DecodeArgs &a, int kv_len) 
     s.n2 = s.n - s.n1;
     return s;
 }
-template <int T>
-__device__ __forceinline__ int seq_tiles(const SeqKeys &s) {  // tiles of one unit
+// tiles of one unit; over chosen blocks, 16-row groups of min(n_sel, blocks there are) blocks
+template <int T, bool kBlocks>
+__device__ __forceinline__ int seq_tiles(const DecodeArgs &a, const SeqKeys &s) {
+    if constexpr (kBlocks) {
+        const int slots = min(a.n_sel, (s.n + a.block_size - 1) / a.block_size);
+        return (slots * (a.block_size / 16) + T / 16 - 1) / (T / 16);
+    }
     return (s.n1 + T - 1) / T + (s.n2 + T - 1) / T;
 }
 __device__ __forceinline__ SeqKeys seq_keys(const DecodeArgs &a, int b) {
     return seq_keys_of(a, a.kv_lens[b]);
 }
 
-template <int D>
+template <int D, bool kBlocks>
 __global__ void __launch_bounds__(DecodeCfg<D>::kThreads, DecodeCfg<D>::kMinBlocks)
 decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
     using C = DecodeCfg<D>;
@@ -179,7 +184,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
     for (int b = b_lo; b < b_hi; ++b) {
         const int kv_len = a.kv_lens[b];
         const SeqKeys sk = seq_keys_of(a, kv_len);
-        my_sum += (long long)seq_tiles<T>(sk) * HU;
+        my_sum += (long long)seq_tiles<T, kBlocks>(a, sk) * HU;
         if (blockIdx.x == 0) {  // CTA 0 handles sequences with nothing to stream
             if (a.defer_merge && (kv_len < 0 || kv_len > a.max_kv_len || sk.n == 0))
                 for (int h = 0; h < a.n_heads; ++h)  // the merge kernel leaves them alone
@@ -217,7 +222,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
         long long p = my_start;
         for (int b = b_lo; b < b_hi; ++b) {
             const SeqKeys sk = seq_keys(a, b);
-            const long long w = (long long)seq_tiles<T>(sk) * HU;
+            const long long w = (long long)seq_tiles<T, kBlocks>(a, sk) * HU;
             if (r0 >= p && r0 < p + w) {
                 *start_b = b;
                 *start_p = p;
@@ -246,7 +251,134 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
     // a deferred merge kernel may be set up now; it waits for this grid before reading
     if (a.defer_merge) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (warp == C::kWarps) {
+    if (kBlocks && warp == C::kWarps) {
+        // ------------------------------------------------------------ producer over chosen
+        // blocks: the stream's walk as below, by the whole warp, which holds 32 entries of the
+        // unit's list at a time (lane i: the list's place base + i - 1); lane 0 issues.  A tile
+        // is kWarps groups of 16 rows, group after group of the listed blocks.
+        int tg = 0, kq = 0;
+        bool ok = true;
+        if (has_work && *start_b >= 0) {
+            int b = *start_b;
+            long long pb = *start_p, pos = r0;
+            const int per_block = a.block_size / 16;
+            while (pos < r1 && ok && b < a.batch) {
+                const SeqKeys sk = seq_keys(a, b);
+                const int nt = seq_tiles<T, kBlocks>(a, sk);
+                const long long w = (long long)nt * HU;
+                if (pos >= pb + w) {
+                    pb += w;
+                    ++b;
+                    continue;
+                }
+                const int idx = (int)((pos - pb) / nt);
+                const int hk = idx / HB, hb = idx % HB;
+                const long long ustart = pb + (long long)idx * nt;
+                const int t0 = (int)(pos - ustart), t1 = (int)min((long long)nt, r1 - ustart);
+                const long long first_cta = ustart / per_cta, last_cta = (ustart + nt - 1) / per_cta;
+                const int slots = min(a.n_sel, (sk.n + a.block_size - 1) / a.block_size);
+                const int32_t *list = a.blocks + ((int64_t)b * a.n_kv_heads + hk) * a.n_sel;
+                int base = t0 * C::kWarps / per_block;
+                int held = base + lane >= 1 && base + lane - 1 < slots ? list[base + lane - 1] : -1;
+                const int qs = kq & 1;
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait_bounded(&q_empty[qs], ((kq >> 1) & 1) ^ 1, abort_flag, deadline));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[qs], C::kQBytes);
+                    for (int c = 0; c < C::kCols64; ++c)
+                        tma_load_3d(sQ + qs * C::kQBytes + c * kHeadsPerBlock * 128, &a.tm_q, &q_full[qs], c * 64,
+                                    hk * G + hb * kHeadsPerBlock, b);
+                }
+                for (int t = t0; t < t1; ++t) {
+                    int row0[C::kWarps];
+                    uint32_t rows = 0;
+                    int boxes = 0;
+#pragma unroll
+                    for (int g = 0; g < C::kWarps; ++g) {
+                        const int at = t * C::kWarps + g, slot = at / per_block;
+                        if (slot - base > 30 && slot < slots) {  // the next entries of the list
+                            base = slot;
+                            held = base + lane >= 1 && base + lane - 1 < slots ? list[base + lane - 1] : -1;
+                        }
+                        const int place = slot < slots ? slot - base + 1 : 1;
+                        const int blk = slot < slots ? __shfl_sync(0xffffffffu, held, place) : -1;
+                        const int before = __shfl_sync(0xffffffffu, held, place - 1);
+                        // an entry lies below the blocks there are and above the one before it,
+                        // which is no padding; -1 is padding
+                        const bool fits = blk >= 0 && blk < (sk.n + a.block_size - 1) / a.block_size &&
+                                          (slot == 0 || (before >= 0 && before < blk));
+                        if (!fits && blk != -1 && lane == 0) report_status(a.status, kErrBounds);
+                        row0[g] = fits ? blk * a.block_size + 16 * (at % per_block) : 0;
+                        const int n = fits ? max(0, min(16, sk.n - row0[g])) : 0;
+                        rows |= (uint32_t)n << (8 * g);
+                        boxes += n > 0;
+                    }
+                    const int s = tg % C::kStages;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((tg / C::kStages) & 1) ^ 1,
+                                                                   abort_flag, deadline));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        StageRec r;
+                        r.b = b; r.hk = hk; r.hb = hb; r.key0 = 0; r.ke = 0;
+                        r.first = t == t0; r.last = t == t1 - 1;
+                        r.kq = kq; r.slot = (int)(blockIdx.x - first_cta);
+                        r.nseg = (int)(last_cta - first_cta + 1); r.end = 0; r.rows = rows;
+                        rec[s] = r;
+                        unsigned char *dk = sRing + s * C::kStageBytes;
+                        unsigned char *dv = dk + C::kTileBytes;
+                        // a tile within one block, all of it there, comes as a whole
+                        const bool whole = a.chunked && a.block_size % T == 0 &&
+                                           rows == (C::kWarps == 4 ? 0x10101010u : 0x00001010u);
+                        if (whole) {
+                            mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+                            tma_load_5d(dk, &a.tm_k, &full[s], 0, row0[0], 0, hk, b);
+                            tma_load_5d(dv, &a.tm_v, &full[s], 0, row0[0], 0, hk, b);
+                        } else if (boxes == 0) {
+                            mbar_arrive(&full[s]);
+                        } else {
+                            mbar_arrive_expect_tx(&full[s], 2 * C::kCols64 * boxes * 16 * 128);
+#pragma unroll
+                            for (int g = 0; g < C::kWarps; ++g)
+                                if ((rows >> (8 * g)) & 0xff)
+                                    for (int c = 0; c < C::kCols64; ++c) {
+                                        const uint32_t off = c * C::kTile * 128 + g * 16 * 128;
+                                        tma_load_4d(dk + off, &a.tm_k16, &full[s], c * 64, hk, row0[g], b);
+                                        tma_load_4d(dv + off, &a.tm_v16, &full[s], c * 64, hk, row0[g], b);
+                                    }
+                        }
+                    }
+                    ++tg;
+                }
+                ++kq;
+                pos = ustart + t1;
+            }
+        }
+        if (ok) {
+            const int s = tg % C::kStages;
+            if (__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((tg / C::kStages) & 1) ^ 1, abort_flag,
+                                                          deadline))) {
+                if (lane == 0) {
+                    rec[s].end = 1;
+                    mbar_arrive(&full[s]);
+                }
+                ++tg;
+            }
+        }
+        if (lane == 0) {  // drain, as below
+            const uint64_t drain_deadline = globaltimer_ns() + 100000000ull;
+            volatile int no_abort = 0;
+            for (int s = 0; s < min(C::kStages, tg); ++s) {
+                const int last = s + (tg - 1 - s) / C::kStages * C::kStages;
+                mbar_wait_bounded(&full[s], (last / C::kStages) & 1, &no_abort, drain_deadline);
+            }
+            for (int i = 0; i < min(2, kq); ++i) {
+                const int last = i + (kq - 1 - i) / 2 * 2;
+                mbar_wait_bounded(&q_full[i], (last >> 1) & 1, &no_abort, drain_deadline);
+            }
+        }
+        __syncwarp();
+    } else if (warp == C::kWarps) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             tma_prefetch_desc(&a.tm_k);
@@ -263,7 +395,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
                 SeqKeys sk = seq_keys(a, b);
                 int next_len = b + 1 < a.batch ? a.kv_lens[b + 1] : 0;  // fetched ahead
                 while (pos < r1 && ok) {
-                    const int nt = seq_tiles<T>(sk);
+                    const int nt = seq_tiles<T, kBlocks>(a, sk);
                     const long long w = (long long)nt * HU;
                     if (pos >= pb + w) {  // nothing (left) of this sequence in our share
                         pb += w;
@@ -306,7 +438,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
                         StageRec r;
                         r.b = b; r.hk = hk; r.hb = hb; r.key0 = key0; r.ke = kend;
                         r.first = t == t0; r.last = t == t1 - 1;
-                        r.kq = kq; r.slot = slot; r.nseg = nseg; r.end = 0; r.pad = 0;
+                        r.kq = kq; r.slot = slot; r.nseg = nseg; r.end = 0; r.rows = 0;
                         rec[s] = r;
                         if (a.test_skip_load && tg == 0) {  // test hook: never filled
                             ++tg;
@@ -421,7 +553,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
             unsigned char *tv = tk + C::kTileBytes;
             const unsigned char *tq = sQ + qs * C::kQBytes;
             // this warp's rows past the piece's end: zero their V (their K is masked below)
-            const int valid_rows = r.ke - (r.key0 + row0);
+            const int valid_rows = kBlocks ? (int)(r.rows >> (8 * warp)) & 0xff : r.ke - (r.key0 + row0);
             if (valid_rows < 16) {
                 for (int i = lane; i < 16 * C::kChunks; i += 32) {
                     const int rr = i / C::kChunks, c = i % C::kChunks;
@@ -461,8 +593,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[e] *= a.scale_log2;
             }
-            const int key_a = r.key0 + row0 + (lane >> 2);
-            const bool va = key_a < r.ke, vb = key_a + 8 < r.ke;
+            const bool va = (lane >> 2) < valid_rows, vb = (lane >> 2) + 8 < valid_rows;
             sc[0] = va ? sc[0] : -INFINITY;
             sc[1] = va ? sc[1] : -INFINITY;
             sc[2] = vb ? sc[2] : -INFINITY;
@@ -571,7 +702,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
                     f[w] = fast_exp2(ml[g] - mu);
                     l += ml[kHeadsPerBlock + g] * f[w];
                 }
-                const float rl = 1.f / l;
+                const float rl = l == 0.f ? 0.f : 1.f / l;  // 0: a piece whose blocks held no key
                 // element (g, x+k) sits in register j = 4*(x/16) + (g&1) + 2*((x/8)&1) of
                 // lane 4k + g/2 (the m16n8 accumulator layout with keys' D in M)
                 const int j = 4 * (x >> 4) + (g & 1) + 2 * ((x >> 3) & 1);
@@ -688,7 +819,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
                 }
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, off);
-                const float rz = 1.f / Z;
+                const float rz = Z == 0.f ? 0.f : 1.f / Z;
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
                     if (lane + 32 * k < nseg) wts[g * nseg + lane + 32 * k] = e[k] * rz;
@@ -732,13 +863,13 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
                     const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (rb + sp) * D + x));
                     const float mn = fmaxf(M, l);
                     const float c = M == -INFINITY ? 0.f : fast_exp2(M - mn);
-                    const float e = fast_exp2(l - mn);
+                    const float e = l == -INFINITY ? 0.f : fast_exp2(l - mn);
                     Z = Z * c + e;
                     o.x = o.x * c + e * v.x; o.y = o.y * c + e * v.y;
                     o.z = o.z * c + e * v.z; o.w = o.w * c + e * v.w;
                     M = mn;
                 }
-                const float rz = 1.f / Z;
+                const float rz = Z == 0.f ? 0.f : 1.f / Z;
                 *reinterpret_cast<uint2 *>(a.out + (int64_t)b * a.out_rs + (int64_t)(h_base + g) * D + x) =
                     make_uint2(pack_bf16x2(o.x * rz, o.y * rz), pack_bf16x2(o.z * rz, o.w * rz));
                 if (x == 0 && a.lse != nullptr)
@@ -828,7 +959,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
             o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
             zt += red_z[gg * w4];  // every column's threads saw the same weights
         }
-        const float rz = 1.f / zt;
+        const float rz = zt == 0.f ? 0.f : 1.f / zt;
         const int b = bh / a.n_heads, h = bh % a.n_heads;
         *reinterpret_cast<uint2 *>(a.out + (int64_t)b * a.out_rs + (int64_t)h * D + 4 * (v0 + tid)) =
             make_uint2(pack_bf16x2(o.x * rz, o.y * rz), pack_bf16x2(o.z * rz, o.w * rz));
@@ -836,13 +967,13 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
     }
 }
 
-template <int D>
+template <int D, bool kBlocks>
 cudaError_t launch_decode_d(const DecodeArgs &a, int grid, cudaStream_t s) {
     using C = DecodeCfg<D>;
-    cudaError_t e = cudaFuncSetAttribute(decode_bf16_kernel<D>,
+    cudaError_t e = cudaFuncSetAttribute(decode_bf16_kernel<D, kBlocks>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    decode_bf16_kernel<D><<<grid, C::kThreads, C::kSmem, s>>>(a);
+    decode_bf16_kernel<D, kBlocks><<<grid, C::kThreads, C::kSmem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.defer_merge) return e;
     // programmatic dependent launch: the merge grid is set up while the stream runs
     cudaLaunchConfig_t cfg = {};
@@ -864,9 +995,9 @@ template <int D>
 int ctas_per_sm() {  // resident CTAs per SM as the runtime sees them (smem and registers)
     using C = DecodeCfg<D>;
     int n = 0;
-    if (cudaFuncSetAttribute(decode_bf16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(decode_bf16_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_bf16_kernel<D>, C::kThreads,
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_bf16_kernel<D, false>, C::kThreads,
                                                       C::kSmem) != cudaSuccess)
         return 1;
     return std::max(1, n);
@@ -946,11 +1077,16 @@ bool plan_decode_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int 
 
 cudaError_t launch_decode_bf16(const DecodeArgs &a, int grid, cudaStream_t s) {
     switch (a.head_dim) {
-        case 64: return launch_decode_d<64>(a, grid, s);
-        case 80: return launch_decode_d<80>(a, grid, s);
-        case 128: return launch_decode_d<128>(a, grid, s);
-        case 256: return launch_decode_d<256>(a, grid, s);
-        case 512: return launch_decode_d<512>(a, grid, s);
+        case 64:
+            return a.blocks != nullptr ? launch_decode_d<64, true>(a, grid, s) : launch_decode_d<64, false>(a, grid, s);
+        case 80:
+            return a.blocks != nullptr ? launch_decode_d<80, true>(a, grid, s) : launch_decode_d<80, false>(a, grid, s);
+        case 128:
+            return a.blocks != nullptr ? launch_decode_d<128, true>(a, grid, s) : launch_decode_d<128, false>(a, grid, s);
+        case 256:
+            return a.blocks != nullptr ? launch_decode_d<256, true>(a, grid, s) : launch_decode_d<256, false>(a, grid, s);
+        case 512:
+            return a.blocks != nullptr ? launch_decode_d<512, true>(a, grid, s) : launch_decode_d<512, false>(a, grid, s);
         default: return cudaErrorInvalidValue;
     }
 }

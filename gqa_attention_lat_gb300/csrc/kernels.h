@@ -80,6 +80,8 @@ struct DecodeArgs {
     float *lse;
     int batch, n_heads, n_kv_heads, head_dim, window;
     int ring;           // > 0: ring cache of `ring` rows, key j in row j % ring (window <= ring)
+    const int32_t *blocks;  // non-null: only the listed blocks of block_size rows,
+    int n_sel, block_size;  // [batch, n_kv_heads, n_sel], ascending, -1 behind
     float scale_log2;   // scale * log2(e): scores are exponentiated with exp2
     float cap_log2, raw_over_cap;  // score cap, as in PrefillTcArgs (cap_log2 0: none)
     // split-KV scratch: partial outputs, partial lse and arrival counters
@@ -153,6 +155,61 @@ struct Q4Plan {
 bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,
                     Q4Plan *p);
 cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, int grid, cudaStream_t s);
+
+// ---------------------------------------------------------------- choice of cached blocks
+struct BoundsArgs {
+    const void *k_cache;
+    int64_t cache_rs, cache_head, cache_seq;  // elements
+    void *bounds;                             // row n: D maxima, D minima of block n
+    int64_t bounds_rs, bounds_head, bounds_seq;
+    int block_size, capacity, n_new, max_touched, batch, n_kv_heads, head_dim;
+    const int32_t *pos;
+    int32_t *status;
+};
+// batch * max_touched * n_kv_heads < 2^31
+cudaError_t launch_block_bounds(const BoundsArgs &a, bool bf16, cudaStream_t s);
+
+constexpr int kSelectMaxBlocks = 65536;  // a sequence's blocks, a bit each in shared memory
+struct SelectArgs {
+    const void *q;
+    int64_t q_rs;
+    const void *bounds;
+    int64_t bounds_rs, bounds_head, bounds_seq;
+    int block_size;
+    const int32_t *kv_lens;
+    int max_kv_len;
+    int32_t *blocks;  // [batch, n_kv_heads, n_sel]
+    int n_sel, n_first, n_last, batch, n_heads, n_kv_heads, head_dim;
+    float2 *scores;   // [batch, n_kv_heads, max_blocks]: the score, a bound of its error
+    uint64_t *exact;  // [batch, n_kv_heads, max_blocks]: ordered fp64 scores near the border
+    int max_blocks, keys_held;
+    int32_t *status;
+};
+cudaError_t launch_select_blocks(SelectArgs a, bool bf16, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- fp32 decode over blocks
+struct BlocksF32Args {
+    const float *q;
+    int64_t q_rs;
+    const float *k, *v;
+    int64_t cache_rs, cache_head, cache_seq;
+    const int32_t *kv_lens;
+    int max_kv_len;
+    const int32_t *blocks;
+    int n_sel, block_size;
+    float *out;
+    int64_t out_rs;
+    float *lse;
+    int batch, n_heads, n_kv_heads, head_dim;
+    float scale_log2, cap_log2, raw_over_cap;
+    float *part_o, *part_lse;
+    int32_t *piece_count;
+    int splits;  // pieces of a unit, all of them written
+    int32_t *status;
+};
+// pieces per (sequence, KV head, block of heads)
+int blocks_f32_splits(int batch, int n_heads, int n_kv_heads, int block_size, int n_sel, int num_sms);
+cudaError_t launch_decode_blocks_f32(const BlocksF32Args &a, cudaStream_t s);
 
 // ---------------------------------------------------------------- bf16 tensor-core prefill
 struct PrefillTcArgs {

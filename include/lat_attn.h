@@ -389,6 +389,97 @@ lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const v
                               float softcap, void *workspace, size_t workspace_bytes,
                               int32_t *status, void *stream);
 
+/*
+ * Attention over chosen blocks of a long cache: lat_kv_block_bounds, lat_attn_select_blocks
+ * and lat_attn_decode_blocks.  A decode step that reads a fixed number of blocks of
+ * block_size keys instead of the whole cache, chosen anew for each query by a bound of the
+ * scores that a block's keys can reach.  block_size is a multiple of 16 from 16 to 1024,
+ * else LAT_ERR_INVALID_ARG; block n of a sequence is its cache rows n*block_size ..
+ * (n+1)*block_size - 1.  In a step: append the new token (lat_kv_append), bring its block's
+ * bounds up to date, select, attend.
+ *
+ * lat_kv_block_bounds — the bounds of the blocks that the rows pos[b] .. pos[b] + n_new - 1
+ * of each sequence lie in, after they were appended to k_cache (caches as in
+ * lat_kv_append).  For block n and channel d, hi_d and lo_d are the largest and the
+ * smallest k over the block's rows up to the last new one; a NaN among them makes both NaN.
+ *   hi of (b,n,hk,d) at bounds[b*bounds_seq_stride + n*bounds_rs + hk*bounds_head_stride + d]
+ *   lo of (b,n,hk,d) head_dim elements behind it
+ * (type dt, exact).  Where the new rows begin inside a block, its stored bounds stand for
+ * the rows before them; a block that they begin is written anew.  So appending n rows in
+ * one call or one at a time gives the same bounds, and a sequence rolled back to the start
+ * of a block needs nothing else.  `bounds` holds ceil(capacity / block_size) rows per
+ * sequence and must not overlap the cache.  k_cache and bounds must be 16-byte aligned and
+ * all six strides positive multiples of 16 bytes, else LAT_ERR_INVALID_ARG.  A sequence
+ * whose rows would fall outside [0, capacity) is skipped whole and sets *status =
+ * LAT_ERR_BOUNDS.  batch * (blocks that n_new rows touch) * n_kv_heads < 2^31, else
+ * LAT_ERR_UNSUPPORTED.
+ */
+lat_status lat_kv_block_bounds(lat_dtype dt, const void *k_cache, int64_t cache_rs,
+                               int64_t cache_head_stride, int64_t cache_seq_stride, int capacity,
+                               void *bounds, int64_t bounds_rs, int64_t bounds_head_stride,
+                               int64_t bounds_seq_stride, int block_size, const int32_t *pos,
+                               int n_new, int batch, int n_kv_heads, int head_dim,
+                               int32_t *status, void *stream);
+
+/*
+ * lat_attn_select_blocks — the blocks that each KV head of each sequence keeps for one query
+ * token: of the ceil(kv_lens[b] / block_size) blocks there are, the first n_first, the last
+ * n_last and the best scored others, ties to the lowest, n_sel in all (all of them where
+ * there are no more).  The score of a block is the largest over the KV head's query heads of
+ *   sum_d max(q_d * hi_d, q_d * lo_d),
+ * which no key of the block can exceed (a positive scale or a score cap keeps the order).
+ * The choice is that of the exact scores, whatever the order of their sums; a score that is
+ * NaN goes before all others.
+ *   blocks: int32 [batch, n_kv_heads, n_sel], ascending, -1 behind.
+ * q as in lat_attn_decode; bounds as lat_kv_block_bounds leaves them; a length outside
+ * [0, max_kv_len] sets *status = LAT_ERR_BOUNDS and leaves that sequence's lists unwritten.
+ * n_sel >= 1, n_first and n_last >= 0, n_first + n_last <= n_sel, q and bounds 16-byte
+ * aligned with strides that are multiples of 16 bytes, else LAT_ERR_INVALID_ARG;
+ * ceil(max_kv_len / block_size) <= 65536 and batch * n_kv_heads < 2^31, else
+ * LAT_ERR_UNSUPPORTED.
+ * workspace: at least lat_attn_select_blocks_workspace_size(...) bytes, 256-byte aligned,
+ * else LAT_ERR_WORKSPACE; it needs no clearing, and calls sharing one must not overlap.
+ */
+size_t lat_attn_select_blocks_workspace_size(int batch, int n_kv_heads, int block_size,
+                                             int max_kv_len);
+lat_status lat_attn_select_blocks(lat_dtype dt, const void *q, int64_t q_rs, const void *bounds,
+                                  int64_t bounds_rs, int64_t bounds_head_stride,
+                                  int64_t bounds_seq_stride, int block_size,
+                                  const int32_t *kv_lens, int max_kv_len, int32_t *blocks,
+                                  int n_sel, int n_first, int n_last, int batch, int n_heads,
+                                  int n_kv_heads, int head_dim, void *workspace,
+                                  size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * lat_attn_decode_blocks — lat_attn_decode_softcap over the listed blocks alone: query head h
+ * of sequence b attends to the cached keys j < kv_lens[b] that lie in a block of
+ * blocks[b, h / (n_heads / n_kv_heads), :] (int32 [batch, n_kv_heads, n_sel], block numbers
+ * ascending, -1 behind, as lat_attn_select_blocks writes them).  An entry that is neither -1
+ * nor a block below ceil(kv_lens[b] / block_size), or that is not above the entry before it,
+ * sets *status = LAT_ERR_BOUNDS and leaves that KV head's output unspecified; only the first
+ * ceil(kv_lens[b] / block_size) entries are read.  A list that holds no key gives out = 0,
+ * lse = -inf.
+ * q, the caches, kv_lens, max_kv_len, out, lse and softcap as in lat_attn_decode_softcap, its
+ * alignment rules for LAT_BF16; for LAT_F32, q, out and the caches 16-byte aligned and all
+ * strides multiples of 4.  n_sel >= 1, else LAT_ERR_INVALID_ARG; n_sel <= 65536, batch <=
+ * 65535 and the size limits of lat_attn_decode, else LAT_ERR_UNSUPPORTED.
+ * workspace: at least lat_attn_decode_blocks_workspace_size(...) bytes for the same sizes and
+ * dt, 256-byte aligned, else LAT_ERR_WORKSPACE.  For LAT_BF16 the rules of lat_attn_decode's
+ * workspace hold (zero-filled before its first use, and again after LAT_ERR_TIMEOUT); for
+ * LAT_F32 it needs no clearing.  Calls sharing one must not overlap on the GPU.
+ */
+size_t lat_attn_decode_blocks_workspace_size(lat_dtype dt, int batch, int n_heads,
+                                             int n_kv_heads, int head_dim, int block_size,
+                                             int n_sel);
+lat_status lat_attn_decode_blocks(lat_dtype dt, const void *q, int64_t q_rs, const void *k_cache,
+                                  const void *v_cache, int64_t cache_rs,
+                                  int64_t cache_head_stride, int64_t cache_seq_stride,
+                                  const int32_t *kv_lens, int max_kv_len, int block_size,
+                                  const int32_t *blocks, int n_sel, void *out, int64_t out_rs,
+                                  float *lse, int batch, int n_heads, int n_kv_heads,
+                                  int head_dim, float scale, float softcap, void *workspace,
+                                  size_t workspace_bytes, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
