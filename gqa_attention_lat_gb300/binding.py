@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblat_attn.so")
@@ -91,6 +92,8 @@ _SIGNATURES = {
 def library(path: str = LIB_PATH) -> ctypes.CDLL:
     """The loaded CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -106,17 +109,18 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_initialized() else None
+        torch = sys.modules.get("torch")  # CUDA cannot be up in a torch that was never imported
+        if torch is None or not torch.cuda.is_initialized():
+            return None
+        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream

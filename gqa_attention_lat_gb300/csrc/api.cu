@@ -729,6 +729,8 @@ lat_status q4_store_impl(lat_dtype dt, void *cache, int64_t cache_rs, int64_t ca
     a.batch = batch;
     a.n_kv_heads = n_kv_heads;
     a.head_dim = head_dim;
+    a.by_heads = lat::FastDiv((uint32_t)n_kv_heads);
+    a.by_n = lat::FastDiv((uint32_t)n);
     a.status = status;
     return lat::launch_q4_store(a, dt == LAT_BF16, expand, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? LAT_OK

@@ -994,13 +994,8 @@ int tile_keys() { return DecodeCfg<D>::kTile; }
 template <int D>
 int ctas_per_sm() {  // resident CTAs per SM as the runtime sees them (smem and registers)
     using C = DecodeCfg<D>;
-    int n = 0;
-    if (cudaFuncSetAttribute(decode_bf16_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_bf16_kernel<D, false>, C::kThreads,
-                                                      C::kSmem) != cudaSuccess)
-        return 1;
-    return std::max(1, n);
+    static Occupancy occupancy;
+    return occupancy(decode_bf16_kernel<D, false>, C::kThreads, C::kSmem);
 }
 
 }  // namespace

@@ -61,7 +61,7 @@ struct Q4Cfg {
     static constexpr int kParkPitch = 16 * kRound + 4;
     static constexpr int kParkBytes = kWarps * kHeads * kParkPitch * 4;
     static constexpr int kMisc = 1024;
-    static constexpr int kSmem = 128 + kWarps * kStages * kStageBytes + kQBytes + kParkBytes + kMisc;
+    static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes + kParkBytes + kMisc;
     static_assert(kSmem <= 232448, "shared memory budget");
     static_assert(kStageBytes % 128 == 0, "TMA destinations");
 };
@@ -121,15 +121,6 @@ __device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
     return false;
 }
 
-__device__ __forceinline__ uint32_t hsub2_bf16(uint32_t x, uint32_t y) {
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&x), *reinterpret_cast<__nv_bfloat162 *>(&y));
-    return *reinterpret_cast<const uint32_t *>(&d);
-}
-// nibbles i (low halves) of a pair of 16-bit fields as bf16 c - z, bias = 128 + z
-__device__ __forceinline__ uint32_t codes2(uint32_t w, int i, uint32_t bias) {
-    return hsub2_bf16(((w >> (4 * i)) & 0x000f000fu) | 0x43004300u, bias);
-}
-
 // N consecutive 32-bit words of shared memory, in the widest loads their count allows
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const unsigned char *p) {
@@ -186,9 +177,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     using R = Q4Row<D>;
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int kTerms = C::kTerms, kSet = R::kSet, kSets = R::kGroups / R::kSet;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *smem = reinterpret_cast<unsigned char *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    extern __shared__ __align__(128) unsigned char smem[];  // (an aligned-up pointer would load as generic)
     unsigned char *ring = smem;                                              // [warp][stage]
     unsigned char *sQ = ring + C::kWarps * C::kStages * C::kStageBytes;      // [term][head] rows
     float *park = reinterpret_cast<float *>(sQ + C::kQBytes);                // [warp][head][channel]
@@ -411,10 +400,10 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     for (int j = 0; j < kSet; ++j) {
                         const uint32_t bx = q4_bias2(px[j]), by = q4_bias2(py[j]);
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        const uint32_t a0[4] = {codes2(wx[j], 0, bx), codes2(wy[j], 0, by), codes2(wx[j], 1, bx),
-                                                codes2(wy[j], 1, by)};
-                        const uint32_t a1[4] = {codes2(wx[j], 2, bx), codes2(wy[j], 2, by), codes2(wx[j], 3, bx),
-                                                codes2(wy[j], 3, by)};
+                        const uint32_t a0[4] = {q4_codes2(wx[j], 0, bx), q4_codes2(wy[j], 0, by), q4_codes2(wx[j], 1, bx),
+                                                q4_codes2(wy[j], 1, by)};
+                        const uint32_t a1[4] = {q4_codes2(wx[j], 2, bx), q4_codes2(wy[j], 2, by), q4_codes2(wx[j], 3, bx),
+                                                q4_codes2(wy[j], 3, by)};
 #pragma unroll
                         for (int k = kTerms - 1; k >= 0; --k) {
                             const uint32_t(&q)[4] = [&]() -> const uint32_t(&)[4] {
@@ -515,10 +504,10 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                         split2<kTerms>(w0, sc[u][0] * fx, sc[u][1] * fx);
                         split2<kTerms>(w1, sc[u][2] * fy, sc[u][3] * fy);
                         const uint32_t b01 = __byte_perm(q0[j], q1[j], 0x7632), b23 = __byte_perm(q2[j], q3[j], 0x7632);
-                        const uint32_t a0[4] = {codes2(ab[j], 0, b01), codes2(ab[j], 1, b01), codes2(cd[j], 0, b23),
-                                                codes2(cd[j], 1, b23)};
-                        const uint32_t a1[4] = {codes2(ab[j], 2, b01), codes2(ab[j], 3, b01), codes2(cd[j], 2, b23),
-                                                codes2(cd[j], 3, b23)};
+                        const uint32_t a0[4] = {q4_codes2(ab[j], 0, b01), q4_codes2(ab[j], 1, b01), q4_codes2(cd[j], 0, b23),
+                                                q4_codes2(cd[j], 1, b23)};
+                        const uint32_t a1[4] = {q4_codes2(ab[j], 2, b01), q4_codes2(ab[j], 3, b01), q4_codes2(cd[j], 2, b23),
+                                                q4_codes2(cd[j], 3, b23)};
 #pragma unroll
                         for (int k = kTerms - 1; k >= 0; --k) {
                             const uint32_t p0 = movmatrix_trans(w0[k]), p1 = movmatrix_trans(w1[k]);
@@ -642,10 +631,8 @@ void shape_of(int *keys, int *tile, int *occ) {
     using C = Q4Cfg<D, F32>;
     *keys = C::kKeys;
     *tile = C::kTileKeys;
-    if (cudaFuncSetAttribute(decode_q4_kernel<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(occ, decode_q4_kernel<D, F32>, C::kThreads, C::kSmem) != cudaSuccess)
-        *occ = 1;
-    *occ = std::max(1, *occ);
+    static Occupancy occupancy;
+    *occ = occupancy(decode_q4_kernel<D, F32>, C::kThreads, C::kSmem);
 }
 
 }  // namespace

@@ -8,7 +8,49 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
+
 namespace lat {
+
+// Resident CTAs per SM of a kernel as the runtime sees them (shared memory and registers), at
+// least 1.  It depends on the kernel and the device alone, so it is asked for once per device:
+// the question costs a call 1.4 us.  Sets the kernel's dynamic shared memory limit too.
+class Occupancy {
+  public:
+    template <typename Kernel>
+    int operator()(Kernel *k, int threads, int smem) {
+        int dev = -1, n = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+        std::atomic<int> *seen = dev >= 0 && dev < kDevices ? &seen_[dev] : nullptr;
+        if (seen != nullptr && (n = seen->load(std::memory_order_relaxed)) > 0) return n;
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k, threads, smem) != cudaSuccess)
+            return 1;
+        n = std::max(1, n);
+        if (seen != nullptr) seen->store(n, std::memory_order_relaxed);
+        return n;
+    }
+
+  private:
+    static constexpr int kDevices = 64;
+    std::atomic<int> seen_[kDevices] = {};
+};
+
+// Division of whole numbers below 2^31 by one fixed beforehand: n / d = (n + hi(n m)) >> s
+// (Granlund and Montgomery's round-up multiplier), a handful of instructions where the
+// hardware has no divide.
+struct FastDiv {
+    uint32_t m = 0, s = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t d) {
+        while (s < 31 && (1u << s) < d) ++s;
+        m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (n + __umulhi(n, m)) >> s; }
+#endif
+};
 
 // ---------------------------------------------------------------- KV-cache append
 struct AppendArgs {
@@ -125,6 +167,7 @@ struct Q4StoreArgs {
     int vec;                                  // 16-byte vectors on that side
     const int32_t *pos;
     int capacity, n, batch, n_kv_heads, head_dim;
+    FastDiv by_heads, by_n;                   // by n_kv_heads, by n
     int32_t *status;
 };
 // batch * n * n_kv_heads < 2^31

@@ -4,12 +4,14 @@
 // Expand: rows pos[b] + t read back as K and V rows.  Both move bytes: 4 bytes a channel of
 // bf16 K and V on one side, 1.25 on the other.
 //
-// How: a warp takes kRows head rows at once, so that their loads are in flight together.  A
-// lane works on 8 neighbouring channels (an octet: one 16-byte vector of bf16), four lanes
-// on a group.  K's octet is one word of the row; V's octet is one nibble of eight halves, so
-// the four lanes of a group OR their nibbles together.  Packed rows pass through shared
-// memory, so that the cache is read and written in 16-byte vectors.  Every step of the
-// quantisation is one fp32 operation rounded to nearest, the same on any machine.
+// How: a warp takes kRows head rows at once, so that their loads are in flight together, first
+// all their K, then all their V.  A lane works on 8 neighbouring channels (an octet: one 16-byte
+// vector of bf16), four lanes on a group.  K's octet is one word of the row.  V's octet is one
+// nibble of eight halves: the four lanes of a group OR their nibbles together, or hand each
+// other their halves.  Packed rows pass through shared memory, so that the cache is read and
+// written in 16-byte vectors.  Both are bound by instruction issue as much as by bytes, so:
+// codes leave a float through its own bits (an added 1.5 * 2^23 puts a whole number there),
+// eight of them gather by a multiply-add each, and a head row's place comes by multiplication.
 #include <math.h>
 
 #include "device_common.cuh"
@@ -22,92 +24,262 @@ namespace {
 
 constexpr int kStoreWarps = 4;
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, bool vec, float x[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float *p, bool vec, float x[8]) {
-    if (vec) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = p[k];
-    }
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
 }
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// an octet of new channels as it lies in memory, so that many can be in flight
+template <typename T>
+struct Octet;
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, bool vec, float x[8]) {
-    if (vec) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Octet<float> {
+    float x[8];
+    __device__ __forceinline__ void load(const float *p, bool vec) {
+        if (vec) {
+            const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+            x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = p[k];
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 0.f;
+    }
+    __device__ __forceinline__ void get(float (&y)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = x[k];
+    }
+    // the smallest and largest with zero among them; a NaN makes both NaN
+    __device__ __forceinline__ void ends(float &mn, float &mx) const {
+        mn = mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            mn = min_nan(mn, x[k]);
+            mx = max_nan(mx, x[k]);
+        }
+    }
+};
+template <>
+struct Octet<__nv_bfloat16> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool vec) {
+        if (vec) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(p);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = (uint32_t)reinterpret_cast<const uint16_t *>(p)[2 * k] |
+                       ((uint32_t)reinterpret_cast<const uint16_t *>(p)[2 * k + 1] << 16);
+        }
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+    __device__ __forceinline__ void get(float (&y)[8]) const {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            x[2 * k] = __uint_as_float(w[k] << 16);
-            x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            y[2 * k] = __uint_as_float(w[k] << 16);
+            y[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
         }
+    }
+    __device__ __forceinline__ void ends(float &mn, float &mx) const {
+        uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(w[k]));
+            asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(w[k]));
+        }
+        mn = min_nan(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
+        mx = max_nan(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+    }
+};
+
+// eight channels as bf16 pairs v of whole numbers times the scale s, rounded once
+__device__ __forceinline__ void save8(__nv_bfloat16 *p, bool vec, const uint32_t v[4], uint32_t s2) {
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 t = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v[k]),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&s2));
+        y[k] = *reinterpret_cast<const uint32_t *>(&t);
+    }
+    if (vec) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(y[0], y[1], y[2], y[3]);
     } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = __bfloat162float(p[k]);
+        for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint16_t *>(p)[k] = (uint16_t)(y[k / 2] >> (16 * (k & 1)));
+    }
+}
+__device__ __forceinline__ void save8(float *p, bool vec, const uint32_t v[4], uint32_t s2) {
+    const float s = __uint_as_float(s2 & 0xffff0000u);
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = s * __uint_as_float((k & 1) ? v[k / 2] & 0xffff0000u : v[k / 2] << 16);
+    if (vec) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = y[k];
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void save8(T *p, bool vec, const float x[8]);
-template <>
-__device__ __forceinline__ void save8<float>(float *p, bool vec, const float x[8]) {
-    if (vec) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[k] = x[k];
-    }
-}
-template <>
-__device__ __forceinline__ void save8<__nv_bfloat16>(__nv_bfloat16 *p, bool vec, const float x[8]) {
-    if (vec) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                   pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) p[k] = __float2bfloat16_rn(x[k]);
-    }
-}
+constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: the sum's low bits are the whole number
+constexpr uint32_t kWholeBits = 0x4b400000u;
 
-// The whole number nearest to x / s, ties to even, exactly: n = rint(x * (1 / s)) is within one
-// of it, and the remainder x - n s is exact in fp32 (s has 8 bits; for n = 0 it is x, and for
-// n != 0 it ends no lower than x's last place and stays below 2 s).
-__device__ __forceinline__ float round_quotient(float x, float s, float r) {
-    float n = rintf(x * r);
-    const float twice = 2.f * fmaf(-n, s, x);
-    const bool odd = ((int)n & 1) != 0;
-    if (twice > s || (twice == s && odd)) n += 1.f;
-    else if (twice < -s || (twice == -s && odd)) n -= 1.f;
-    return n;
+// Codes of N channels, channel k at nibble k: c = nearest(x / s) + z in 0 .. 15, where the
+// nearest whole number is that of the exact quotient, ties to even.  n = rint(x r) with r the
+// rounded 1 / s is within one of it, and the remainder x - n s is exact in fp32 (s has 8 bits;
+// for n = 0 it is x, and for n != 0 it ends no lower than x's last place and stays below 2 s).
+template <int N>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[N], float s, float r, float z) {
+    static_assert(N == 1 || N == 8, "the constants' sum");
+    const float half = 0.5f * s, z15 = z * (1.f / 15.f);
+    float n[N];
+    bool near = false;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        n[k] = fmaf(x[k], r, kWhole) - kWhole;
+        near |= !(fabsf(fmaf(-n[k], s, x[k])) < half);
+    }
+    if (near) {  // some quotient at a half, or rounded the wrong way
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float twice = 2.f * fmaf(-n[k], s, x[k]);
+            const bool odd = (__float_as_uint(n[k] + kWhole) & 1u) != 0;
+            if (twice > s || (twice == s && odd)) n[k] += 1.f;
+            else if (twice < -s || (twice == -s && odd)) n[k] -= 1.f;
+        }
+    }
+    uint32_t code = 0;
+#pragma unroll
+    for (int k = N - 1; k >= 0; --k)
+        // held in 0 .. 15 as a fraction of 15 in 0 .. 1, whose rounding error times 15 is no half
+        code = code * 16u + __float_as_uint(fmaf(__saturatef(fmaf(n[k], 1.f / 15.f, z15)), 15.f, kWhole));
+    // each of them brought kWholeBits with it, times 16^k
+    return code - kWholeBits * (N == 8 ? 0x11111111u : 1u);
 }
 
 template <int D>
 struct StoreCfg {
     using R = Q4Row<D>;
-    static constexpr int kRows = D <= 80 ? 4 : (D == 128 ? 4 : (D == 256 ? 2 : 1));  // a warp's head rows
-    static constexpr int kOcts = R::kPad / 4;       // octets of a head row, K's then V's
-    static constexpr int kSteps = kRows * kOcts / 32;
+    static constexpr int kRows = D == 80 ? 8 : D <= 128 ? 4 : D == 256 ? 2 : 1;  // a warp's head rows
+    static constexpr int kOcts = R::kPad / 8;             // octets of a row's K (or V)
+    static constexpr int kSteps = kRows * kOcts / 32;     // a lane's octets of K (or V)
     static_assert(kRows * kOcts % 32 == 0, "every lane has an octet in every step");
-    static constexpr int kChunks = kRows * R::kBytes / 16;  // 16-byte pieces of the packed rows
+    static constexpr int kPieces = R::kBytes / 16;
 };
 
-// head row `u` (of batch * n * n_kv_heads) -> its sequence, row and head; false when it is
-// past the end or its sequence does not fit the cache (reported once per sequence)
-__device__ __forceinline__ bool locate(const Q4StoreArgs &a, uint32_t u, uint32_t units, int64_t *slot) {
-    if (u >= units) return false;
-    const uint32_t r = u / a.n_kv_heads, hk = u - r * a.n_kv_heads;
-    const uint32_t b = r / a.n, t = r - b * a.n;
-    const int p = a.pos[b];
-    if (p < 0 || (int64_t)p + a.n > (int64_t)a.capacity) {
-        if (t == 0 && hk == 0) report_status(a.status, kErrBounds);
+// head row `u` (of batch * n * n_kv_heads) -> its sequence, new row and head
+struct Place {
+    uint32_t row, hk, b, t;  // row: b * n + t
+    __device__ __forceinline__ Place(const Q4StoreArgs &a, uint32_t u) {
+        row = a.by_heads.div(u);
+        hk = u - row * a.n_kv_heads;
+        b = a.by_n.div(row);
+        t = row - b * a.n;
+    }
+};
+__device__ __forceinline__ bool fits(const Q4StoreArgs &a, int p) {
+    return p >= 0 && (int64_t)p + a.n <= (int64_t)a.capacity;
+}
+// byte offset of a head row in the cache; false where its sequence does not fit (reported once)
+__device__ __forceinline__ bool locate(const Q4StoreArgs &a, uint32_t u, int64_t *at) {
+    const Place w(a, u);
+    const int p = a.pos[w.b];
+    if (!fits(a, p)) {
+        if (w.t == 0 && w.hk == 0) report_status(a.status, kErrBounds);
         return false;
     }
-    *slot = (int64_t)b * a.cache_seq + ((int64_t)p + t) * a.cache_rs + (int64_t)hk * a.cache_head;
+    *at = (int64_t)w.b * a.cache_seq + (int64_t)(p + (int)w.t) * a.cache_rs + (int64_t)w.hk * a.cache_head;
     return true;
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void fetch(const Q4StoreArgs &a, const void *src, uint32_t u0, uint32_t units,
+                                      Octet<T> (&x)[StoreCfg<D>::kSteps]) {
+    using C = StoreCfg<D>;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int st = 0; st < C::kSteps; ++st) {
+        const int it = st * 32 + lane, row = it / C::kOcts, d = 8 * (it % C::kOcts);
+        const uint32_t u = u0 + row;
+        x[st].zero();
+        if (u < units && d < D) {
+            const uint32_t ur = a.by_heads.div(u);
+            x[st].load(static_cast<const T *>(src) + (int64_t)ur * a.rs + (u - ur * a.n_kv_heads) * D + d, a.vec);
+        }
+    }
+}
+
+template <typename T, int D, bool kIsV>
+__device__ __forceinline__ void quantise(const Octet<T> (&oct)[StoreCfg<D>::kSteps], unsigned char *mine) {
+    using C = StoreCfg<D>;
+    using R = Q4Row<D>;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int st = 0; st < C::kSteps; ++st) {
+        const int it = st * 32 + lane, row = it / C::kOcts, o = it % C::kOcts, g = o / 4, col = o & 3;
+        float mn, mx, x[8];
+        oct[st].ends(mn, mx);
+        oct[st].get(x);
+#pragma unroll
+        for (int off = 1; off < 4; off <<= 1) {
+            mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+            mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        }
+        const float range = __fsub_rn(mx, mn);
+        // a NaN, an infinity or a range past the largest number has no grid: the scale is NaN
+        // and so is what the group reads back as
+        const bool bad = !(range <= 3.4028235e38f);
+        const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.f / 15.f));
+        const float s = __bfloat162float(sb);
+        float z = 0.f;
+        uint32_t code = 0;
+        if (!bad && s > 0.f) {
+            // (a scale whose reciprocal could overflow is taken 2^100 times as large, exactly)
+            const float up = s < 0x1p-100f ? 0x1p100f : 1.f, div = s * up, rcp = __frcp_rn(div);
+            if (up != 1.f)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] *= up;
+            const float zx[1] = {-mn * up};
+            z = (float)codes_of(zx, div, rcp, 0.f);
+            code = codes_of(x, div, rcp, z);
+        }
+        unsigned char *r = mine + row * R::kBytes;
+        if (!kIsV) {
+            uint32_t w = 0;  // nibble i holds channel 2 i, nibble i + 4 channel 2 i + 1
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w |= ((code >> (4 * i)) & (15u << (4 * i))) | ((code << (12 - 4 * i)) & (15u << (16 + 4 * i)));
+            reinterpret_cast<uint32_t *>(r)[(g / R::kSet * 4 + col) * R::kSet + g % R::kSet] = w;
+        } else {
+            // halves 2 col and 2 col + 1: byte `col` of the four lanes' codes, lane m's as nibble m
+            uint32_t keep = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t b = __shfl_sync(0xffffffffu, code, (lane & ~3) | m) >> (8 * col);
+                keep |= ((b & 15u) << (4 * m)) | ((b & 0xf0u) << (12 + 4 * m));
+            }
+            uint16_t *h = reinterpret_cast<uint16_t *>(r + R::kV) + (g / R::kSet * 8 + 2 * col) * R::kSet + g % R::kSet;
+            h[0] = (uint16_t)keep;
+            h[R::kSet] = (uint16_t)(keep >> 16);
+        }
+        if (col == 0) {
+            const uint32_t lo = bad ? 0x7fc0u : (uint32_t)__bfloat16_as_ushort(sb);
+            reinterpret_cast<uint32_t *>(r + (kIsV ? R::kParamV : R::kParamK))[g] =
+                lo | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(128.f + z)) << 16);
+        }
+    }
 }
 
 template <typename T, int D>
@@ -120,106 +292,54 @@ __global__ void __launch_bounds__(32 * kStoreWarps) append_q4_kernel(const Q4Sto
     const uint32_t u0 = (blockIdx.x * kStoreWarps + warp) * C::kRows;
     if (u0 >= units) return;
     unsigned char *mine = stage[warp];
-
-    int64_t slot[C::kRows];
-    bool live[C::kRows];
-#pragma unroll
-    for (int i = 0; i < C::kRows; ++i) live[i] = locate(a, u0 + i, units, &slot[i]);
-
-    float x[C::kSteps][8];
-#pragma unroll
-    for (int st = 0; st < C::kSteps; ++st) {
-        const int it = st * 32 + lane, row = it / C::kOcts, o = it % C::kOcts;
-        const int d = 8 * (o % (C::kOcts / 2));
-        const bool is_v = o >= C::kOcts / 2;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[st][k] = 0.f;
-        const uint32_t u = u0 + row, ur = u / a.n_kv_heads;
-        if (u < units && d < D) {
-            const T *src = static_cast<const T *>(is_v ? a.v : a.k) + (int64_t)ur * a.rs + (u - ur * a.n_kv_heads) * D + d;
-            load8<T>(src, a.vec, x[st]);
-        }
-    }
-    // the padding behind the parameters
-    if (R::kParamV + 4 * R::kGroups < R::kBytes)
-        for (int i = lane; i < C::kRows * ((R::kBytes - R::kParamV) / 4 - R::kGroups); i += 32) {
-            constexpr int kW = (R::kBytes - R::kParamV) / 4 - R::kGroups > 0
-                                   ? (R::kBytes - R::kParamV) / 4 - R::kGroups : 1;
-            *reinterpret_cast<uint32_t *>(mine + i / kW * R::kBytes + R::kParamV + 4 * R::kGroups + 4 * (i % kW)) = 0u;
-        }
-#pragma unroll
-    for (int st = 0; st < C::kSteps; ++st) {
-        const int it = st * 32 + lane, row = it / C::kOcts, o = it % C::kOcts;
-        const bool is_v = o >= C::kOcts / 2;
-        const int g = o % (C::kOcts / 2) / 4, col = o & 3;
-        float mn = 0.f, mx = 0.f;
-        bool bad = false;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            mn = fminf(mn, x[st][k]);
-            mx = fmaxf(mx, x[st][k]);
-            bad |= x[st][k] != x[st][k];
-        }
-#pragma unroll
-        for (int off = 1; off < 4; off <<= 1) {
-            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, off) != 0;
-        }
-        const float range = __fsub_rn(mx, mn);
-        // a NaN, an infinity or a range past the largest number has no grid: the scale is NaN
-        // and so is what the group reads back as
-        bad |= !(range <= 3.4028235e38f);
-        __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(range, 1.f / 15.f));
-        const float s = __bfloat162float(sb);
-        const bool flat = bad || !(s > 0.f);
-        // (a scale whose reciprocal could overflow is taken 2^100 times as large, exactly)
-        const float up = flat ? 0.f : (s < 0x1p-100f ? 0x1p100f : 1.f);
-        const float div = flat ? 1.f : s * up, rcp = __frcp_rn(div);
-        const float z = flat ? 0.f : fminf(fmaxf(round_quotient(-mn * up, div, rcp), 0.f), 15.f);
-        uint32_t code = 0;  // 8 codes, channel k at nibble k
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float c = flat ? 0.f : fminf(fmaxf(round_quotient(x[st][k] * up, div, rcp) + z, 0.f), 15.f);
-            code |= (uint32_t)c << (4 * k);
-        }
-        // V: halves 2m and 2m + 1 take this lane's codes 2m and 2m + 1 as nibble `col`
-        uint32_t vw[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            vw[m] = (((code >> (8 * m)) & 15u) << (4 * col)) | (((code >> (8 * m + 4)) & 15u) << (16 + 4 * col));
-            vw[m] |= __shfl_xor_sync(0xffffffffu, vw[m], 1);
-            vw[m] |= __shfl_xor_sync(0xffffffffu, vw[m], 2);
-        }
-        {
-            unsigned char *r = mine + row * R::kBytes;
-            const int off = (g / R::kSet * 4 + col) * R::kSet + g % R::kSet;
-            if (!is_v) {
-                uint32_t w = 0;  // nibble i holds channel 2 i, nibble i + 4 channel 2 i + 1
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w |= (((code >> (8 * i)) & 15u) << (4 * i)) | (((code >> (8 * i + 4)) & 15u) << (16 + 4 * i));
-                reinterpret_cast<uint32_t *>(r)[off] = w;
-            } else {
-                const uint32_t w = col == 0 ? vw[0] : col == 1 ? vw[1] : col == 2 ? vw[2] : vw[3];
-                uint16_t *h = reinterpret_cast<uint16_t *>(r + R::kV) + (g / R::kSet * 8 + 2 * col) * R::kSet + g % R::kSet;
-                h[0] = (uint16_t)w;
-                h[R::kSet] = (uint16_t)(w >> 16);
-            }
-            if (col == 0) {
-                const uint32_t lo = bad ? 0x7fc0u : (uint32_t)__bfloat16_as_ushort(sb);
-                reinterpret_cast<uint32_t *>(r + (is_v ? R::kParamV : R::kParamK))[g] =
-                    lo | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(128.f + z)) << 16);
-            }
-        }
-    }
+    constexpr int kTail = (R::kBytes - R::kParamV) / 4 - R::kGroups;  // words behind the parameters
+    if constexpr (kTail > 0)
+        for (int i = lane; i < C::kRows * kTail; i += 32)
+            *reinterpret_cast<uint32_t *>(mine + i / kTail * R::kBytes + R::kParamV + 4 * R::kGroups + 4 * (i % kTail)) = 0u;
+    Octet<T> k[C::kSteps], v[C::kSteps];
+    fetch<T, D>(a, a.k, u0, units, k);
+    fetch<T, D>(a, a.v, u0, units, v);
+    quantise<T, D, false>(k, mine);
+    quantise<T, D, true>(v, mine);
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < C::kRows; ++i)
-        if (live[i])
-            for (int c = lane; c < R::kBytes / 16; c += 32)
-                *reinterpret_cast<uint4 *>(a.cache + slot[i] + 16 * c) =
-                    *reinterpret_cast<const uint4 *>(mine + i * R::kBytes + 16 * c);
+    for (int p0 = 0; p0 < C::kRows * C::kPieces; p0 += 32) {
+        const int p = p0 + lane, row = p / C::kPieces;
+        int64_t at;
+        if (row < C::kRows && u0 + row < units && locate(a, u0 + row, &at))
+            *reinterpret_cast<uint4 *>(a.cache + at + 16 * (p % C::kPieces)) = *reinterpret_cast<const uint4 *>(mine + 16 * p);
+    }
+}
+
+template <typename T, int D, bool kIsV>
+__device__ __forceinline__ void read_back(const Q4StoreArgs &a, uint32_t u0, uint32_t units, const unsigned char *mine) {
+    using C = StoreCfg<D>;
+    using R = Q4Row<D>;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int st = 0; st < C::kSteps; ++st) {
+        const int it = st * 32 + lane, row = it / C::kOcts, o = it % C::kOcts, g = o / 4, col = o & 3, d = 8 * o;
+        const unsigned char *r = mine + row * R::kBytes;
+        const uint32_t pw = reinterpret_cast<const uint32_t *>(r + (kIsV ? R::kParamV : R::kParamK))[g];
+        const uint32_t bias = q4_bias2(pw), s2 = __byte_perm(pw, pw, 0x1010);
+        uint32_t v[4];  // channels 2 k and 2 k + 1 as c - z
+        if (!kIsV) {
+            const uint32_t w = reinterpret_cast<const uint32_t *>(r)[(g / R::kSet * 4 + col) * R::kSet + g % R::kSet];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = q4_codes2(w, k, bias);
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(r + R::kV) + (g / R::kSet * 8 + 2 * col) * R::kSet + g % R::kSet;
+            const uint32_t own = (uint32_t)h[0] | ((uint32_t)h[R::kSet] << 16);  // halves 2 col, 2 col + 1
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = q4_codes2(__shfl_sync(0xffffffffu, own, (lane & ~3) | k), col, bias);
+        }
+        const uint32_t u = u0 + row;
+        if (u >= units || d >= D) continue;
+        const Place w(a, u);
+        if (!fits(a, a.pos[w.b])) continue;  // rows left as they were
+        save8(static_cast<T *>(kIsV ? a.v_out : a.k_out) + (int64_t)w.row * a.rs + w.hk * D + d, a.vec, v, s2);
+    }
 }
 
 template <typename T, int D>
@@ -228,55 +348,26 @@ __global__ void __launch_bounds__(32 * kStoreWarps) expand_q4_kernel(const Q4Sto
     using R = Q4Row<D>;
     __shared__ __align__(16) unsigned char stage[kStoreWarps][C::kRows * R::kBytes];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t units = (uint32_t)a.batch * a.n * a.n_kv_heads;  // below 2^31
+    const uint32_t units = (uint32_t)a.batch * a.n * a.n_kv_heads;
     const uint32_t u0 = (blockIdx.x * kStoreWarps + warp) * C::kRows;
     if (u0 >= units) return;
     unsigned char *mine = stage[warp];
-    constexpr int kPieces = R::kBytes / 16, kLoads = (C::kChunks + 31) / 32;
+    constexpr int kLoads = (C::kRows * C::kPieces + 31) / 32;
     uint4 got[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-        const int p = lane + 32 * i, row = p / kPieces;
-        int64_t slot;
+        const int p = lane + 32 * i, row = p / C::kPieces;
+        int64_t at;
         got[i] = make_uint4(0, 0, 0, 0);
-        if (row < C::kRows && locate(a, u0 + row, units, &slot))
-            got[i] = *reinterpret_cast<const uint4 *>(a.cache + slot + 16 * (p % kPieces));
+        if (row < C::kRows && u0 + row < units && locate(a, u0 + row, &at))
+            got[i] = *reinterpret_cast<const uint4 *>(a.cache + at + 16 * (p % C::kPieces));
     }
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int p = lane + 32 * i;
-        if (p < C::kChunks) *reinterpret_cast<uint4 *>(mine + 16 * p) = got[i];
-    }
+    for (int i = 0; i < kLoads; ++i)
+        if (lane + 32 * i < C::kRows * C::kPieces) *reinterpret_cast<uint4 *>(mine + 16 * (lane + 32 * i)) = got[i];
     __syncwarp();
-#pragma unroll
-    for (int st = 0; st < C::kSteps; ++st) {
-        const int it = st * 32 + lane, row = it / C::kOcts, o = it % C::kOcts;
-        const bool is_v = o >= C::kOcts / 2;
-        const int g = o % (C::kOcts / 2) / 4, col = o & 3, d = 8 * (o % (C::kOcts / 2));
-        const uint32_t u = u0 + row, ur = u / a.n_kv_heads;
-        if (u >= units || d >= D) continue;
-        const int p0 = a.pos[ur / a.n];
-        if (p0 < 0 || (int64_t)p0 + a.n > (int64_t)a.capacity) continue;  // rows left as they were
-        const unsigned char *r = mine + row * R::kBytes;
-        uint32_t code = 0;  // channel k at nibble k
-        if (!is_v) {
-            const uint32_t w = reinterpret_cast<const uint32_t *>(r)[(g / R::kSet * 4 + col) * R::kSet + g % R::kSet];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                code |= (((w >> (4 * i)) & 15u) << (8 * i)) | (((w >> (16 + 4 * i)) & 15u) << (8 * i + 4));
-        } else {
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(r + R::kV) + g / R::kSet * 8 * R::kSet + g % R::kSet;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) code |= (((uint32_t)h[k * R::kSet] >> (4 * col)) & 15u) << (4 * k);
-        }
-        const uint32_t pw = reinterpret_cast<const uint32_t *>(r + (is_v ? R::kParamV : R::kParamK))[g];
-        const float s = q4_scale(pw), z = __uint_as_float(pw & 0xffff0000u) - 128.f;
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = s * ((float)((code >> (4 * k)) & 15u) - z);
-        T *dst = static_cast<T *>(is_v ? a.v_out : a.k_out) + (int64_t)ur * a.rs + (u - ur * a.n_kv_heads) * D + d;
-        save8<T>(dst, a.vec, x);
-    }
+    read_back<T, D, false>(a, u0, units, mine);
+    read_back<T, D, true>(a, u0, units, mine);
 }
 
 template <typename T, int D>
