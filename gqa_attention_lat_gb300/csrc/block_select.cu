@@ -10,8 +10,8 @@
 //
 // The choice is that of the exact scores.  The score kernel works in fp32 and bounds its own
 // error; the choosing kernel takes what lies further than that from the border as it is, and
-// what lies nearer is scored again in fp64 (products of bf16 or fp32 are exact there, and sums
-// of them good to 2^-45), so no rounding of a sum's order decides.
+// what lies nearer is scored again in pairs of floats (48 bits), so no rounding of a sum's order
+// decides.
 //
 // What bounds them: bytes.  bounds reads each new key once, score each block's 2 D numbers
 // once; the choice works on 4 bytes a block in shared memory and waits on barriers.
@@ -159,6 +159,12 @@ constexpr int kScoreWarps = 4;
 constexpr int kScoreRows = 16;  // blocks a warp scores at a time
 constexpr int kQHeads = 8;
 
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
 __device__ __forceinline__ int blocks_of(const SelectArgs &a, int b) {  // 0: nothing, or out of range
     const int len = a.kv_lens[b];
     return len <= 0 || len > a.max_kv_len ? 0 : (len - 1) / a.block_size + 1;
@@ -172,6 +178,7 @@ __device__ __forceinline__ int blocks_of(const SelectArgs &a, int b) {  // 0: no
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) block_score_bf16_kernel(const SelectArgs a) {
     constexpr int kW = 2 * D, kSteps = kW / 32, kPitch = kW + 32;
+    constexpr int kAhead = kSteps < 8 ? kSteps : 8;  // steps whose loads are in flight at once
     __shared__ __align__(16) __nv_bfloat16 sq[kQHeads][kPitch];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     const int unit = blockIdx.x, b = unit / a.n_kv_heads, hk = unit % a.n_kv_heads;
@@ -181,29 +188,40 @@ __global__ void __launch_bounds__(32 * kScoreWarps) block_score_bf16_kernel(cons
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)b * a.q_rs + (int64_t)hk * G * D;
     const __nv_bfloat16 *bd = static_cast<const __nv_bfloat16 *>(a.bounds) + (int64_t)b * a.bounds_seq + (int64_t)hk * a.bounds_head;
     for (int h0 = 0; h0 < G; h0 += kQHeads) {
-        if (h0 > 0) __syncthreads();
-        for (int i = tid; i < kQHeads * D; i += 32 * kScoreWarps) {
-            const int h = i / D, d = i % D;
-            const __nv_bfloat16 x = h0 + h < G ? q[(h0 + h) * D + d] : __float2bfloat16_rn(0.f);
-            const __nv_bfloat16 z = __float2bfloat16_rn(0.f);
-            const bool neg = __bfloat162float(x) < 0.f;  // (a NaN goes with the maxima)
-            sq[h][d] = neg ? z : x;
-            sq[h][D + d] = neg ? x : z;
-        }
-        __syncthreads();
+        bool staged = false;
         for (int chunk = blockIdx.y; chunk * kScoreWarps * kScoreRows < have; chunk += gridDim.y) {
             const int n0 = (chunk * kScoreWarps + warp) * kScoreRows;
-            if (n0 >= have) continue;
             const uint4 *x = reinterpret_cast<const uint4 *>(bd + (int64_t)min(n0 + r, have - 1) * a.bounds_rs) + c;
             const uint4 *y = reinterpret_cast<const uint4 *>(bd + (int64_t)min(n0 + r + 8, have - 1) * a.bounds_rs) + c;
+            uint4 vx[kAhead], vy[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) vx[i] = x[4 * i], vy[i] = y[4 * i];
+            if (!staged) {  // the queries, while the first rows are on their way
+                if (h0 > 0) __syncthreads();
+                for (int i = tid; i < kQHeads * D / 8; i += 32 * kScoreWarps) {
+                    const int h = i / (D / 8), d = 8 * (i % (D / 8));
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    const uint4 w = h0 + h < G ? *reinterpret_cast<const uint4 *>(q + (h0 + h) * D + d) : z;
+                    const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+                    uint32_t pos[4], neg[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // by the sign bit, channel by channel
+                        const uint32_t m = ((e[k] >> 15) & 0x00010001u) * 0xffffu;
+                        pos[k] = e[k] & ~m, neg[k] = e[k] & m;
+                    }
+                    *reinterpret_cast<uint4 *>(&sq[h][d]) = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+                    *reinterpret_cast<uint4 *>(&sq[h][D + d]) = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+                }
+                __syncthreads();
+                staged = true;
+            }
             float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
-            constexpr int kAhead = kSteps < 8 ? kSteps : 8;
 #pragma unroll
             for (int i0 = 0; i0 < kSteps; i0 += kAhead) {
-                uint4 vx[kAhead], vy[kAhead];
+                if (i0 > 0)
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-                    if (i0 + i < kSteps) vx[i] = x[4 * (i0 + i)], vy[i] = y[4 * (i0 + i)];
+                    for (int i = 0; i < kAhead; ++i)
+                        if (i0 + i < kSteps) vx[i] = x[4 * (i0 + i)], vy[i] = y[4 * (i0 + i)];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
                     if (i0 + i < kSteps) {
@@ -224,15 +242,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps) block_score_bf16_kernel(cons
             for (int half = 0; half < 2; ++half) {
                 float m = -INFINITY, e = 0.f;
                 if (l0) m = s[2 * half], e = t[2 * half];
-                if (l1) {
-                    m = s[2 * half + 1] != s[2 * half + 1] || m != m ? NAN : fmaxf(m, s[2 * half + 1]);
-                    e = fmaxf(e, t[2 * half + 1]);
-                }
+                if (l1) m = max_nan(m, s[2 * half + 1]), e = max_nan(e, t[2 * half + 1]);
 #pragma unroll
                 for (int off = 1; off < 4; off <<= 1) {
-                    const float o = __shfl_xor_sync(0xffffffffu, m, off);
-                    m = o != o || m != m ? NAN : fmaxf(m, o);
-                    e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, off));
+                    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+                    e = max_nan(e, __shfl_xor_sync(0xffffffffu, e, off));
                 }
                 const int n = n0 + r + 8 * half;
                 if (c == 0 && n < have) {
@@ -240,8 +254,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) block_score_bf16_kernel(cons
                     e *= (2.f * D / 16.f + 1.f) * 18.f * 0x1p-23f;
                     if (h0 > 0) {  // more than eight heads: with what the earlier ones left
                         const float2 was = *dst;
-                        m = was.x != was.x || m != m ? NAN : fmaxf(m, was.x);
-                        e = fmaxf(e, was.y);
+                        m = max_nan(m, was.x), e = max_nan(e, was.y);
                     }
                     *dst = make_float2(m, e);
                 }
@@ -250,80 +263,99 @@ __global__ void __launch_bounds__(32 * kScoreWarps) block_score_bf16_kernel(cons
     }
 }
 
-// fp32: a warp per block; a lane takes 4 neighbouring columns of every 128 and up to 8 heads'
-// sums.  The error bound: a sum of 2 D products, each addition off by at most 2^-24 of the sum
-// of magnitudes, taken over the heads' largest |q|.
+// fp32: a warp takes four blocks at a time, a lane 4 neighbouring columns of every 128; the 32
+// sums of four blocks and eight heads come out of the lanes by a butterfly that halves the
+// values at every step, one sum a lane.  The error bound: each addition is off by at most 2^-24
+// of the sum of magnitudes, taken over the heads' largest |q|.
+constexpr int kRowsF32 = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) block_score_f32_kernel(const SelectArgs a) {
-    constexpr int kW = 2 * D, kVecs = kW / 4;
+    constexpr int kW = 2 * D, kVecs = kW / 4, kSteps = (kVecs + 31) / 32;
     __shared__ __align__(16) float sq[kQHeads + 1][kW];  // the last: the largest |q| of the heads
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int unit = blockIdx.x, b = unit / a.n_kv_heads, hk = unit % a.n_kv_heads;
     const int have = blocks_of(a, b), G = a.n_heads / a.n_kv_heads;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (have <= a.n_sel || (int64_t)blockIdx.y * kScoreWarps * kScoreRows >= have) return;
+    if (have <= a.n_sel || (int64_t)blockIdx.y * kScoreWarps * kRowsF32 >= have) return;
     const float *q = static_cast<const float *>(a.q) + (int64_t)b * a.q_rs + (int64_t)hk * G * D;
     const float *bd = static_cast<const float *>(a.bounds) + (int64_t)b * a.bounds_seq + (int64_t)hk * a.bounds_head;
     for (int h0 = 0; h0 < G; h0 += kQHeads) {
         if (h0 > 0) __syncthreads();
         for (int d = tid; d < D; d += 32 * kScoreWarps) {
-            float hi = 0.f, lo = 0.f;
+            float hi = 0.f, lo = 0.f, x[kQHeads];
+#pragma unroll
+            for (int h = 0; h < kQHeads; ++h) x[h] = h0 + h < G ? q[(h0 + h) * D + d] : 0.f;
+#pragma unroll
             for (int h = 0; h < kQHeads; ++h) {
-                const float x = h0 + h < G ? q[(h0 + h) * D + d] : 0.f;
-                const bool neg = x < 0.f;
-                sq[h][d] = neg ? 0.f : x;
-                sq[h][D + d] = neg ? x : 0.f;
-                hi = fmaxf(hi, neg ? 0.f : x);
-                lo = fmaxf(lo, neg ? -x : 0.f);
+                const bool neg = x[h] < 0.f;  // (a NaN goes with the maxima)
+                sq[h][d] = neg ? 0.f : x[h];
+                sq[h][D + d] = neg ? x[h] : 0.f;
+                hi = fmaxf(hi, neg ? 0.f : x[h]);
+                lo = fmaxf(lo, neg ? -x[h] : 0.f);
             }
             sq[kQHeads][d] = hi;
             sq[kQHeads][D + d] = lo;
         }
         __syncthreads();
-        for (int chunk = blockIdx.y; chunk * kScoreWarps * kScoreRows < have; chunk += gridDim.y) {
-            const int n0 = (chunk * kScoreWarps + warp) * kScoreRows;
-            for (int n = n0; n < min(have, n0 + kScoreRows); ++n) {
-                const float4 *x = reinterpret_cast<const float4 *>(bd + (int64_t)n * a.bounds_rs);
-                float s[kQHeads + 1];
+        for (int chunk = blockIdx.y; chunk * kScoreWarps * kRowsF32 < have; chunk += gridDim.y) {
+            const int n0 = (chunk * kScoreWarps + warp) * kRowsF32;
+            float s[kRowsF32 * kQHeads], e[kRowsF32];
 #pragma unroll
-                for (int h = 0; h <= kQHeads; ++h) s[h] = 0.f;
+            for (int i = 0; i < kRowsF32 * kQHeads; ++i) s[i] = 0.f;
+#pragma unroll
+            for (int u = 0; u < kRowsF32; ++u) e[u] = 0.f;
 #pragma unroll 2
-                for (int v = 0; v < (kVecs + 31) / 32; ++v) {
-                    const int i = lane + 32 * v;
-                    if (i < kVecs) {
-                        const float4 w = x[i];
+            for (int v = 0; v < kSteps; ++v) {
+                const int i = lane + 32 * v;
+                if (i < kVecs) {
+                    float4 w[kRowsF32];
 #pragma unroll
-                        for (int h = 0; h < kQHeads; ++h) {
-                            const float4 y = *reinterpret_cast<const float4 *>(&sq[h][4 * i]);
-                            s[h] = fmaf(w.x, y.x, fmaf(w.y, y.y, fmaf(w.z, y.z, fmaf(w.w, y.w, s[h]))));
+                    for (int u = 0; u < kRowsF32; ++u)
+                        w[u] = reinterpret_cast<const float4 *>(bd + (int64_t)min(n0 + u, have - 1) * a.bounds_rs)[i];
+#pragma unroll
+                    for (int h = 0; h <= kQHeads; ++h) {
+                        const float4 y = *reinterpret_cast<const float4 *>(&sq[h][4 * i]);
+#pragma unroll
+                        for (int u = 0; u < kRowsF32; ++u) {
+                            if (h < kQHeads) {
+                                float &t = s[u * kQHeads + (h < kQHeads ? h : 0)];
+                                t = fmaf(w[u].x, y.x, fmaf(w[u].y, y.y, fmaf(w[u].z, y.z, fmaf(w[u].w, y.w, t))));
+                            } else {
+                                e[u] = fmaf(fabsf(w[u].x), y.x, fmaf(fabsf(w[u].y), y.y, fmaf(fabsf(w[u].z), y.z, fmaf(fabsf(w[u].w), y.w, e[u]))));
+                            }
                         }
-                        const float4 y = *reinterpret_cast<const float4 *>(&sq[kQHeads][4 * i]);
-                        s[kQHeads] += fabsf(w.x) * y.x + fabsf(w.y) * y.y + fabsf(w.z) * y.z + fabsf(w.w) * y.w;
                     }
                 }
+            }
+            int off = 16;
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
+            for (int half = kRowsF32 * kQHeads / 2; half >= 1; half /= 2, off /= 2) {
+                const bool up = lane & off;
 #pragma unroll
-                    for (int h = 0; h <= kQHeads; ++h) s[h] += __shfl_xor_sync(0xffffffffu, s[h], off);
-                float m = -INFINITY;
-                bool nan = false;
-#pragma unroll
-                for (int h = 0; h < kQHeads; ++h)
-                    if (h0 + h < G) {
-                        m = fmaxf(m, s[h]);
-                        nan |= s[h] != s[h];
-                    }
-                if (nan) m = NAN;
-                if (lane == 0) {
-                    float2 *dst = a.scores + (int64_t)unit * a.max_blocks + n;
-                    float e = s[kQHeads] * (kVecs / 8.f + 16.f) * 0x1p-23f;
-                    if (h0 > 0) {
-                        const float2 was = *dst;
-                        m = was.x != was.x || m != m ? NAN : fmaxf(m, was.x);
-                        e = fmaxf(e, was.y);
-                    }
-                    *dst = make_float2(m, e);
+                for (int i = 0; i < half; ++i) {
+                    const float keep = up ? s[i + half] : s[i], send = up ? s[i] : s[i + half];
+                    s[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
                 }
+            }
+            float err = 0.f;  // of this lane's block
+#pragma unroll
+            for (int u = 0; u < kRowsF32; ++u) {
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) e[u] += __shfl_xor_sync(0xffffffffu, e[u], k);
+                err = lane / kQHeads == u ? e[u] : err;
+            }
+            float m = h0 + lane % kQHeads < G ? s[0] : -INFINITY;
+#pragma unroll
+            for (int k = 1; k < kQHeads; k <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
+            const int n = n0 + lane / kQHeads;
+            if (lane % kQHeads == 0 && n < have) {
+                float2 *dst = a.scores + (int64_t)unit * a.max_blocks + n;
+                err *= (kVecs / 8.f + 16.f) * 0x1p-23f;
+                if (h0 > 0) {
+                    const float2 was = *dst;
+                    m = max_nan(m, was.x), err = max_nan(err, was.y);
+                }
+                *dst = make_float2(m, err);
             }
         }
     }
@@ -347,12 +379,19 @@ __device__ __forceinline__ uint64_t order64(double x) {
     return x != x ? ~0ull : (u >> 63) ? ~u : u | (1ull << 63);
 }
 
+constexpr int kBins = kPickThreads;  // of one pass over the keys
+constexpr int kFew = 512;            // candidates ranked in shared memory
+
 struct PickShared {
     uint32_t in[kPickWords];   // chosen blocks, a bit each
-    uint32_t tie[kPickWords];  // those equal to the last chosen one
+    uint32_t tie[kPickWords];  // those near the border, then those equal to the last chosen one
     int red[kPickWarps];
     uint32_t red2[2][kPickWarps];
-    int carry;
+    int bins[kBins];
+    int found, found_above, found_in;
+    int few;
+    int at[kFew];
+    uint64_t key[kFew];
 };
 
 __device__ __forceinline__ int block_sum(PickShared &sh, int x) {
@@ -375,29 +414,78 @@ __device__ __forceinline__ void block_minmax(PickShared &sh, uint32_t &mn, uint3
     for (int w = 0; w < kPickWarps; ++w) mn = min(mn, sh.red2[0][w]), mx = max(mx, sh.red2[1][w]);
 }
 
-// the block's score by fp64 sums of exact products, one lane of a warp per channel in turn
+// s + e = x + y exactly (Knuth's two-sum); the intrinsics keep the compiler from fusing
+__device__ __forceinline__ float two_sum(float x, float y, float &e) {
+    const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
+    e = __fadd_rn(__fsub_rn(x, __fsub_rn(s, t)), __fsub_rn(y, t));
+    return s;
+}
+
+// The block's score, to 2^-45 of its terms' magnitude or better, by a whole warp.  Products split
+// by a fused multiply-add and sums by two-sum, each an unevaluated pair of floats: 48 bits on the
+// fp32 pipes.  (fp64 runs at a 64th of their rate here: it cost 13 us a step, this 1.)  Where
+// the pair could overflow or lose small products, fp64 it is.
 template <typename T>
 __device__ double exact_score(const SelectArgs &a, int b, int hk, int n) {
     const int G = a.n_heads / a.n_kv_heads, D = a.head_dim, lane = threadIdx.x & 31;
     const T *q = static_cast<const T *>(a.q) + (int64_t)b * a.q_rs + (int64_t)hk * G * D;
     const T *x = static_cast<const T *>(a.bounds) + (int64_t)b * a.bounds_seq + (int64_t)hk * a.bounds_head + (int64_t)n * a.bounds_rs;
     double best = -INFINITY;
-    for (int h = 0; h < G; ++h) {
-        double s = 0.0;
+    for (int h0 = 0; h0 < G; h0 += 4) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
+        float top = 0.f;
+#pragma unroll 2
         for (int d = lane; d < D; d += 32) {
-            const double w = (double)(float)q[h * D + d];
-            s += w * (double)(float)x[w < 0.0 ? D + d : d];
-            if (w != w) s = w;
+            const float hi = (float)x[d], lo = (float)x[D + d];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = h0 + i < G ? (float)q[(h0 + i) * D + d] : 0.f, k = w < 0.f ? lo : hi;
+                const float p = __fmul_rn(w, k);
+                float e;
+                s[i] = two_sum(s[i], p, e);
+                c[i] = __fadd_rn(c[i], __fadd_rn(e, __fmaf_rn(w, k, -p)));
+                top = max_nan(top, fabsf(p));
+            }
         }
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        best = s != s || best != best ? (double)NAN : fmax(best, s);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float e;
+                const float c2 = __shfl_xor_sync(0xffffffffu, c[i], off);
+                s[i] = two_sum(s[i], __shfl_xor_sync(0xffffffffu, s[i], off), e);
+                c[i] = __fadd_rn(c[i], __fadd_rn(c2, e));
+            }
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
+        }
+        double v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = (double)s[i] + (double)c[i];
+        if (!(top > 0x1p-60f && top < 0x1p100f)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = 0.0;
+            for (int d = lane; d < D; d += 32) {
+                const float hi = (float)x[d], lo = (float)x[D + d];
+                for (int i = 0; i < 4 && h0 + i < G; ++i) {
+                    const float w = (float)q[(h0 + i) * D + d];
+                    v[i] = fma((double)w, (double)(w < 0.f ? lo : hi), v[i]);
+                }
+            }
+            for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (h0 + i < G) best = v[i] != v[i] || best != best ? (double)NAN : fmax(best, v[i]);
     }
     return best;
 }
 
-// One CTA per (sequence, KV head).  The k-th largest score is found by halving the range of the
-// ordered keys (each step counts the keys above the middle; it ends as soon as exactly k are),
-// with no histogram to contend for.
+// One CTA per (sequence, KV head).  The k-th largest score is found by counting the ordered keys
+// into 512 equal bins of the range that still holds it, two or three times (the scores of one
+// query lie within a few binades, so they spread over the bins); it ends as soon as exactly k
+// keys lie from some bin on.
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectArgs a) {
     extern __shared__ uint32_t keys[];  // [have - n_first - n_last] where they fit, else unused
@@ -438,15 +526,37 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
     // kth: the k-th largest key; next: the (k + 1)-th
     uint32_t kth = 0, next = 0;
     if (k > 0) {
-        uint32_t lo = low, hi = top;  // count(>= lo) >= k always; kth in [lo, hi]
-        int at_lo = n;
-        while (lo < hi && at_lo != k) {
-            const uint32_t mid = lo + (hi - lo) / 2 + 1;
-            int cnt = 0;
-            for (int i = tid; i < n; i += kPickThreads) cnt += key_at(i) >= mid;
-            cnt = block_sum(sh, cnt);
-            if (cnt >= k) lo = mid, at_lo = cnt;
-            else hi = mid - 1;
+        uint32_t lo = low;   // count(>= lo) is at_lo >= k; the k-th largest lies in the `width` keys from lo on
+        int at_lo = n, above_all = 0;  // keys above that range
+        uint32_t last = top - low;     // its width less one
+        while (at_lo != k && last > 0) {
+            const int shift = max(0, 32 - __clz(last) - 9);  // last >> shift < 512
+            sh.bins[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += kPickThreads) {
+                const uint32_t d = key_at(i) - lo;
+                if (d <= last) atomicAdd(&sh.bins[d >> shift], 1);
+            }
+            __syncthreads();
+            const int mine = sh.bins[tid];
+            int from = mine;  // keys of this and the higher bins of the warp
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_down_sync(0xffffffffu, from, off);
+                if (lane + off < 32) from += v;
+            }
+            if (lane == 0) sh.red[warp] = from;
+            __syncthreads();
+            int base = above_all;
+#pragma unroll
+            for (int w = 0; w < kPickWarps; ++w) base += w > warp ? sh.red[w] : 0;
+            from += base;
+            if (from >= k && from - mine < k) sh.found = tid, sh.found_above = from - mine, sh.found_in = from;
+            __syncthreads();
+            lo += (uint32_t)sh.found << shift;
+            above_all = sh.found_above;
+            at_lo = sh.found_in;
+            last = min(last - ((uint32_t)sh.found << shift), (1u << shift) - 1u);
         }
         uint32_t above = 0xffffffffu, below = 0;
         for (int i = tid; i < n; i += kPickThreads) {
@@ -490,7 +600,27 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
         if (need >= cand) {  // all of them (need is cand: no more than k are above the border)
             for (int w = tid; w < words; w += kPickThreads) sh.in[w] |= sh.tie[w], sh.tie[w] = 0;
         } else {
-            // exact scores of the candidates, as ordered keys beside the scores' place
+            // exact scores of the candidates.  A few (the usual case): each counts those ahead of it
+            if (cand <= kFew) {
+                if (tid == 0) sh.few = 0;
+                __syncthreads();
+                for (int w = tid; w < words; w += kPickThreads)
+                    for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) sh.at[atomicAdd(&sh.few, 1)] = w * 32 + __ffs(m) - 1;
+                __syncthreads();
+                for (int i = warp; i < cand; i += kPickWarps) {
+                    const double s = exact_score<T>(a, b, hk, sh.at[i]);
+                    if (lane == 0) sh.key[i] = order64(s);
+                }
+                __syncthreads();
+                if (tid < cand) {
+                    const uint64_t mine = sh.key[tid];
+                    const int at = sh.at[tid];
+                    int ahead = 0;
+                    for (int i = 0; i < cand; ++i) ahead += sh.key[i] > mine || (sh.key[i] == mine && sh.at[i] < at);
+                    if (ahead < need) atomicOr(&sh.in[at / 32], 1u << (at % 32));
+                }
+            } else {
+            // many: the border among their ordered keys by halving, kept beside the scores
             uint64_t *exact = a.exact + (int64_t)unit * a.max_blocks;
             for (int w = warp; w < words; w += kPickWarps)
                 for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) {
@@ -542,6 +672,7 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
                     if (w0 + lane < words) sh.in[w0 + lane] |= take;
                     got += all;
                 }
+            }
             }
         }
         __syncthreads();
@@ -599,7 +730,7 @@ cudaError_t launch_block_bounds(const BoundsArgs &a, bool bf16, cudaStream_t s) 
 cudaError_t launch_select_blocks(SelectArgs a, bool bf16, int num_sms, cudaStream_t s) {
     const int units = a.batch * a.n_kv_heads;
     if (a.max_blocks > a.n_sel) {
-        const int chunks = (a.max_blocks + kScoreWarps * kScoreRows - 1) / (kScoreWarps * kScoreRows);
+        const int per = kScoreWarps * (bf16 ? kScoreRows : kRowsF32), chunks = (a.max_blocks + per - 1) / per;
         // enough CTAs for every SM to hold its fill; a CTA goes on with further chunks
         const int want = std::max(1, (16 * num_sms + units - 1) / units);
         const dim3 grid(units, std::min(chunks, want));
@@ -614,9 +745,9 @@ cudaError_t launch_select_blocks(SelectArgs a, bool bf16, int num_sms, cudaStrea
         }
         if (e != cudaSuccess) return e;
     }
-    // the keys stay in shared memory up to 24 KB of them (beside the 16 KB of bits), which
+    // the keys stay in shared memory up to 16 KB of them (beside 16 KB of bits), which
     // needs no attribute; beyond, every step reads them again from L2
-    a.keys_held = std::min(a.max_blocks, 6144);
+    a.keys_held = std::min(a.max_blocks, 4096);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

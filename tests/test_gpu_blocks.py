@@ -207,6 +207,20 @@ def test_select_between_equal_and_nearly_equal_scores(dt):
     assert got[0, 0].tolist() == list(range(n_sel - 3)) + [nb - 3, nb - 2, nb - 1]
 
 
+@pytest.mark.parametrize("dt,nb,n_sel", [("bf16", 2000, 700), ("f32", 2000, 1), ("bf16", 9000, 4000)])
+def test_select_among_many_equal_scores(dt, nb, n_sel):
+    """Thousands of exact ties: the lowest, beside one block ahead and one behind."""
+    D, block = 64, 16
+    bd = torch.ones(1, nb, 1, 2 * D, dtype=W.torch_dtype(dt), device="cuda")
+    bd[0, nb - 7, 0, 3] = 1.5
+    bd[0, 5, 0, 9] = 0.5
+    q = torch.ones(1, D, dtype=W.torch_dtype(dt), device="cuda")
+    got, st = select(q, bd, [nb * block], block, 1, 1, D, dt, n_sel, 0, 0)
+    assert int(st.item()) == 0
+    want = sorted([nb - 7] + [n for n in range(nb) if n not in (5, nb - 7)][:n_sel - 1])
+    assert got[0, 0].tolist() == want
+
+
 @pytest.mark.parametrize("nb,n_sel", [(6200, 100), (65536, 2000)])
 def test_select_among_many_blocks(nb, n_sel):
     """More than the keys that shared memory holds, up to the most blocks a sequence may have."""
