@@ -690,7 +690,7 @@ bool make_q4_map(CUtensorMap *m, const void *base, int row_bytes, int heads, int
     const cuuint32_t box[4] = {(cuuint32_t)row_bytes / 4, 1, (cuuint32_t)box_rows, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -819,10 +819,11 @@ lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const v
     a.window = window < 0 ? 0 : window;
     a.scale_log2 = scale * kLog2e;
     a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
-    a.raw_over_cap = softcap > 0.f ? scale / softcap : 0.f;
+    a.over_cap_log2 = softcap > 0.f ? 1.f / (softcap * kLog2e) : 0.f;
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_lse = reinterpret_cast<float *>(ws + plan.part_o_bytes);
-    a.piece_count = reinterpret_cast<int32_t *>(ws + plan.part_o_bytes + plan.part_lse_bytes);
+    a.piece_count = a.counters = reinterpret_cast<int32_t *>(ws + plan.part_o_bytes + plan.part_lse_bytes);
+    a.defer_join = plan.defer_join;
     a.max_splits = plan.max_splits;
     a.min_tiles = plan.min_tiles;
     a.timeout_ns = kDefaultTimeoutNs;

@@ -11,22 +11,34 @@
 // How:
 //  * Work unit = one (sequence, KV head, block of <= 8 query heads).  All units' keys, laid
 //    end to end in tiles of kTileKeys, form one stream; CTA c takes the c-th equal share
-//    (never under min_tiles).  A unit cut across CTAs leaves one normalised partial and its
-//    log-sum-exp per piece, joined by a second kernel (a programmatic dependent).
+//    (to a tile, never under min_tiles).  A unit cut across CTAs leaves one normalised partial and its
+//    log-sum-exp per piece.  The CTA that finishes a unit's last piece (an atomic ticket) joins
+//    them after its stream; units of many pieces are joined by a second kernel instead (a
+//    programmatic dependent), which spreads a head's channels over CTAs.
 //  * Every warp is its own pipeline: it owns kKeys rows of each tile, which one TMA copy
 //    brings into its ring (a box over the cache's strides; the row is one run of bytes for
 //    K and V), and its first lane issues the copy for a stage as soon as the warp is done
 //    with it.  Warps meet only at the end of a piece.
-//  * mma m16n8k16 with keys in M: S^T[16 keys x 8 heads] = K Q^T by groups of 32 channels,
-//    O^T[16 channels x 8 heads] += V^T (P s)^T.  A word of codes becomes four bf16 pairs of
-//    128 + c by an AND-OR each (0x4300 is bf16 128, whose last place is 1), minus 128 + z,
-//    which is exact.  The rows' layout puts a lane's codes side by side.
-//  * LAT_F32: the query, and the weights p s, are split into three bf16 terms (24 bits, so
-//    nothing is lost); the codes are exact as they are, so three MMAs give fp32 products.
+//  * Scores on mma m16n8k16 in fp16, keys in M, heads in N, by groups of 32 channels: a nibble
+//    left where it lies in the low byte of a half is the subnormal c 2^-24 or 16 c 2^-24, so
+//    a word of codes is four operand registers for four ANDs and a shift, and the query's
+//    channels on the 16-fold codes are taken 16 times smaller.  A query is brought to
+//    [2^12, 2^13) by a power of two of its own; a bf16 one is then exact down to 2^-26 of its
+//    largest channel, an fp32 one is two fp16 terms (22 bits and a sign).  The zero point
+//    enters as z times the group's sum of the query.
+//  * O^T[16 channels x 8 heads] += V^T (P s)^T on mma m16n8k16 in bf16 (a weight needs bf16's
+//    range): a nibble becomes 128 + c by an AND-OR (0x4300 is bf16 128, whose last place is 1),
+//    minus 128 + z, exactly.  The rows' layout puts a lane's codes side by side.
+//  * LAT_F32: the weights p s are three bf16 terms (24 bits, so nothing is lost).
 //  * Waits are bounded; on expiry the CTA records LAT_ERR_TIMEOUT, drains its copies, quits.
+// What bounds it: the logic pipe.  A warp instruction takes it two cycles of an SM's four
+// schedulers (measured: LOP3, PRMT and conversions 2 a cycle and SM, fp16 and bf16 MMA 0.49; an
+// e4m3 MMA, which would take the codes as they are, is unpacked to fp16 by 12 conversions here).
 #include <math.h>
 
 #include <algorithm>
+
+#include <cuda_fp16.h>
 
 #include "device_common.cuh"
 #include "kernels.h"
@@ -41,25 +53,33 @@ constexpr int kHeads = 8;                  // N of the mma: query heads of a uni
 constexpr float kRescaleBy = 8.0f;         // log2 units the maximum may grow unnoticed
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kPieceRing = 8;              // pieces known ahead
+// What a unit costs beside its tiles (its queries made ready, the warps' states joined), in
+// tiles: counted in the shares, so that a CTA of many short units is not the last to finish (32
+// sequences of 1 to 4096 keys: not counted 36.8 us, as 2 tiles 30.5 us).
+constexpr int kUnitCost = 2;
 
 template <int D, bool F32>
 struct Q4Cfg {
     using R = Q4Row<D>;
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTerms = F32 ? 3 : 1;               // bf16 terms of q and of p s
+    static constexpr int kTerms = F32 ? 3 : 1;               // bf16 terms of p s
+    static constexpr int kQTerms = F32 ? 2 : 1;              // fp16 terms of q
     static constexpr int kSub = D == 512 ? 1 : 2;            // 16-key MMA tiles a warp takes at once
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kTileKeys = kKeys * kWarps;
-    static constexpr int kStages = 3;
+    static constexpr int kStages = 2;
     static constexpr int kStageBytes = kKeys * R::kBytes;
     static constexpr int kMt = D / 16;                       // 16-channel MMA tiles
-    static constexpr bool kQReg = R::kPad * kTerms <= 256;   // query fragments in registers
-    static constexpr int kQPitch = R::kPad + 32;             // bf16; rows 16 words apart in the banks
-    static constexpr int kQBytes = kQReg ? 0 : kTerms * kHeads * kQPitch * 2;
-    static constexpr int kRound = 4;                         // MMA tiles joined at once: 64 channels
+    static constexpr bool kQReg = R::kPad * kQTerms <= 256;  // query fragments in registers
+    // else in shared memory: [term][head] rows of 16 bytes an octet, 16 words apart in the banks,
+    // [group][head] sums, [head] factors
+    static constexpr int kQRow = 2 * R::kPad + 64;
+    static constexpr int kQBytes = kQReg ? 0 : kQTerms * kHeads * kQRow + (R::kGroups + 1) * kHeads * 4;
+    static constexpr int kRound = 8;                         // MMA tiles joined at once: 128 channels
     static constexpr int kParkPitch = 16 * kRound + 4;
     static constexpr int kParkBytes = kWarps * kHeads * kParkPitch * 4;
+    static constexpr int kMinBlocks = D == 64 ? 5 : D == 80 ? 4 : D == 128 ? 3 : D == 256 ? 2 : 1;  // CTAs per SM
     static constexpr int kMisc = 1024;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes + kParkBytes + kMisc;
     static_assert(kSmem <= 232448, "shared memory budget");
@@ -71,6 +91,10 @@ struct Piece {
     int key0, keys;    // first key, keys of the piece (the last tile may be partial)
     int slot, nseg;    // which piece of how many
     int end;           // no more pieces
+};
+
+struct Join {          // a unit cut across CTAs that this one may have to join
+    int b, h_base, g_cnt, nseg, unit, last;
 };
 
 struct KeyRange {
@@ -86,35 +110,48 @@ __device__ __forceinline__ KeyRange range_of(const Q4DecodeArgs &a, int len) {
 
 // thread 0's place in the stream
 struct Walk {
-    long long pos, end, pb, per_cta;  // pb: where sequence b's units begin
+    uint32_t pos, end, pb;  // pb: where sequence b's units begin
+    uint32_t total, parts;  // the stream and how many CTAs share it
     int b;
 };
+// CTA c takes tiles [total c / parts, total (c + 1) / parts); tile x is CTA ((x + 1) parts - 1) / total's
+__device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t total, uint32_t parts) {
+    return (uint32_t)((uint64_t)total * c / parts);
+}
+__device__ __forceinline__ uint32_t share_of(uint32_t x, uint32_t total, uint32_t parts) {
+    const uint64_t n = (uint64_t)(x + 1) * parts - 1;
+    return n >> 32 ? (uint32_t)(n / total) : (uint32_t)n / total;
+}
 
+// a unit of n keys in the stream: nothing, or its tiles and what it costs beside them
+template <int T>
+__device__ __forceinline__ uint32_t unit_cost(int n) {
+    return n > 0 ? (uint32_t)(n + T - 1) / T + kUnitCost : 0u;
+}
 template <int T>
 __device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
-    const int HU = a.n_kv_heads * HB;
+    const uint32_t HU = (uint32_t)(a.n_kv_heads * HB);
     while (w.pos < w.end && w.b < a.batch) {
         const KeyRange k = range_of(a, a.kv_lens[w.b]);
-        const int nt = (k.n + T - 1) / T;
-        const long long all = (long long)nt * HU;
+        const uint32_t cost = unit_cost<T>(k.n), nt = cost - kUnitCost, all = cost * HU;
         if (w.pos >= w.pb + all) {
             w.pb += all;
             ++w.b;
             continue;
         }
-        const int idx = (int)((w.pos - w.pb) / nt);
-        const long long ustart = w.pb + (long long)idx * nt;
-        const int t0 = (int)(w.pos - ustart), t1 = (int)min((long long)nt, w.end - ustart);
-        const long long first = ustart / w.per_cta, last = (ustart + nt - 1) / w.per_cta;
+        const uint32_t idx = (w.pos - w.pb) / cost, ustart = w.pb + idx * cost + kUnitCost;  // its first tile
+        const uint32_t t0 = w.pos > ustart ? w.pos - ustart : 0, t1 = w.end > ustart ? min(nt, w.end - ustart) : 0;
+        w.pos = min(w.end, ustart + nt);
+        if (t0 >= t1) continue;  // the share ends before the unit's first tile
+        const uint32_t first = share_of(ustart, w.total, w.parts), last = share_of(ustart + nt - 1, w.total, w.parts);
         p.b = w.b;
-        p.hk = idx / HB;
-        p.hb = idx % HB;
-        p.key0 = k.lo + t0 * T;
-        p.keys = min(k.n, t1 * T) - t0 * T;
+        p.hk = (int)(idx / HB);
+        p.hb = (int)(idx % HB);
+        p.key0 = k.lo + (int)t0 * T;
+        p.keys = min(k.n, (int)t1 * T) - (int)t0 * T;
         p.slot = (int)(blockIdx.x - first);
         p.nseg = (int)(last - first + 1);
         p.end = 0;
-        w.pos = ustart + t1;
         return true;
     }
     p.end = 1;
@@ -157,6 +194,45 @@ __device__ __forceinline__ void v_pairs(uint32_t (&u)[SET], const unsigned char 
     }
 }
 
+// an octet of a query as TERMS fp16 operands: channels 0, 1 and 4, 5 as they are, 2, 3 and 6, 7
+// a sixteenth, in the order of the two MMAs' B registers
+template <int TERMS>
+__device__ __forceinline__ void split_f16(uint32_t (&o)[TERMS][4], const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = x[2 * i], b = x[2 * i + 1];
+        if (i & 1) a *= 0.0625f, b *= 0.0625f;
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+            const __half2 h = __floats2half2_rn(a, b);
+            o[t][i] = *reinterpret_cast<const uint32_t *>(&h);
+            if (t + 1 < TERMS) {
+                const float2 f = __half22float2(h);
+                a -= f.x, b -= f.y;
+            }
+        }
+    }
+}
+// the power of two that brings m >= 0 to [2^12, 2^13); 1 for nothing, NaN for what is not finite
+__device__ __forceinline__ float to_f16_range(float m) {
+    const int e = (int)(__float_as_uint(m) >> 23);
+    if (e == 255) return NAN;
+    return m == 0.f ? 1.f : __uint_as_float((uint32_t)min(254, 127 + 12 + 127 - e) << 23);
+}
+__device__ __forceinline__ void mma_f16_16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ int add_acq_rel(int32_t *p, int x) {
+    int was;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(was) : "l"(p), "r"(x) : "memory");
+    return was;
+}
+
 // two floats as `TERMS` packed bf16 pairs whose sum is the pair (to 8 bits a term)
 template <int TERMS>
 __device__ __forceinline__ void split2(uint32_t (&o)[TERMS], float x, float y) {
@@ -171,12 +247,12 @@ __device__ __forceinline__ void split2(uint32_t (&o)[TERMS], float x, float y) {
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(Q4Cfg<D, F32>::kThreads)
+__global__ void __launch_bounds__(Q4Cfg<D, F32>::kThreads, Q4Cfg<D, F32>::kMinBlocks)
 decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     using C = Q4Cfg<D, F32>;
     using R = Q4Row<D>;
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-    constexpr int kTerms = C::kTerms, kSet = R::kSet, kSets = R::kGroups / R::kSet;
+    constexpr int kTerms = C::kTerms, kQTerms = C::kQTerms, kSet = R::kSet, kSets = R::kGroups / R::kSet;
     extern __shared__ __align__(128) unsigned char smem[];  // (an aligned-up pointer would load as generic)
     unsigned char *ring = smem;                                              // [warp][stage]
     unsigned char *sQ = ring + C::kWarps * C::kStages * C::kStageBytes;      // [term][head] rows
@@ -186,38 +262,39 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     Piece *pieces = reinterpret_cast<Piece *>(misc + 128);                   // [kPieceRing]
     float *sM = reinterpret_cast<float *>(misc + 384);                       // [warp][m[8], l[8]]
     Walk *walk = reinterpret_cast<Walk *>(misc + 640);
-    long long *scan = reinterpret_cast<long long *>(misc + 704);             // [warps]
+    uint32_t *scan = reinterpret_cast<uint32_t *>(misc + 704);               // [warps]
     volatile int *abort_flag = reinterpret_cast<int *>(misc + 768);
-    static_assert(sizeof(Piece) * kPieceRing <= 256 && sizeof(Walk) <= 64, "misc area");
+    Join *joins = reinterpret_cast<Join *>(misc + 784);                      // [2]
+    static_assert(sizeof(Piece) * kPieceRing <= 256 && sizeof(Walk) <= 64 && sizeof(Join) * 2 <= 64, "misc area");
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, HB = (G + kHeads - 1) / kHeads, HU = a.n_kv_heads * HB;
     constexpr int TK = C::kTileKeys;
 
-    // ---- the stream's length and this CTA's share: per-thread sums over a slice of the
-    // sequences, then a scan ------------------------------------------------------------
-    const int per_thread = (a.batch + C::kThreads - 1) / C::kThreads;
+    // ---- the stream's length in tiles and this CTA's share: per-thread sums over a slice of
+    // the sequences, then a scan --------------------------------------------------------
+        const int per_thread = (a.batch + C::kThreads - 1) / C::kThreads;
     const int b_lo = min(a.batch, tid * per_thread), b_hi = min(a.batch, b_lo + per_thread);
-    long long my_sum = 0;
+    uint32_t my_sum = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const int len = a.kv_lens[b];
         const KeyRange k = range_of(a, len);
-        my_sum += (long long)((k.n + TK - 1) / TK) * HU;
+        my_sum += unit_cost<TK>(k.n) * HU;
         if (blockIdx.x == 0 && k.n == 0) {  // nothing to stream
             const bool bad = len < 0 || len > a.max_kv_len;
             if (bad) report_status(a.status, kErrBounds);
             for (int h = 0; h < a.n_heads; ++h) {
-                a.piece_count[(int64_t)b * a.n_heads + h] = 0;
+                if (a.defer_join) a.piece_count[(int64_t)b * a.n_heads + h] = 0;
                 if (!bad && a.lse != nullptr) a.lse[(int64_t)b * a.n_heads + h] = -INFINITY;
             }
             if (!bad)
                 for (int i = 0; i < a.n_heads * D; ++i) static_cast<T *>(a.out)[(int64_t)b * a.out_rs + i] = T(0.f);
         }
     }
-    long long incl = my_sum;
+    uint32_t incl = my_sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += v;
     }
     if (lane == 31) scan[warp] = incl;
@@ -228,73 +305,64 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         for (int i = 0; i < C::kWarps * C::kStages; ++i) mbar_init(&full[i], 1);
         *abort_flag = 0;
         fence_mbarrier_init();
+        tma_prefetch_desc(&a.tm);
     }
     __syncthreads();
-    long long total = 0, my_start = incl - my_sum;
+    uint32_t total = 0, my_start = incl - my_sum;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-        const long long v = scan[w];
+        const uint32_t v = scan[w];
         if (w < warp) my_start += v;
         total += v;
     }
-    const long long per_cta = max((total + gridDim.x - 1) / gridDim.x, (long long)a.min_tiles);
-    const long long r0 = (long long)blockIdx.x * per_cta, r1 = min(total, r0 + per_cta);
-    if (r0 < r1 && r0 >= my_start && r0 < my_start + my_sum) {  // the share begins in this slice
-        long long p = my_start;
+    const uint32_t parts = max(1u, min(gridDim.x, total / (uint32_t)a.min_tiles));
+    const bool shares = blockIdx.x < parts;
+    const uint32_t r0 = shares ? share_begin(blockIdx.x, total, parts) : 0;
+    const uint32_t r1 = shares ? share_begin(blockIdx.x + 1, total, parts) : 0;
+    if (r0 < r1 && r0 >= my_start && r0 - my_start < my_sum) {  // the share begins in this slice
+        uint32_t p = my_start;
         int b = b_lo;
         for (; b < b_hi; ++b) {
-            const long long w = (long long)((range_of(a, a.kv_lens[b]).n + TK - 1) / TK) * HU;
+            const uint32_t w = unit_cost<TK>(range_of(a, a.kv_lens[b]).n) * HU;
             if (r0 < p + w) break;
             p += w;
         }
-        walk->pos = r0;
-        walk->end = r1;
-        walk->pb = p;
-        walk->b = b;
-        walk->per_cta = per_cta;
-    }
-    __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (r0 >= r1) return;
-    if (tid == 0) {
-        Walk w = *walk;
-        for (int i = 0; i < kPieceRing / 2; ++i)
+        Walk w{r0, r1, p, total, parts, b};
+        for (int i = 0; i < kPieceRing / 4; ++i)
             if (!next_piece<TK>(a, w, HB, pieces[i])) break;
         *walk = w;
-        tma_prefetch_desc(&a.tm);
     }
+    if (a.defer_join) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (r0 >= r1) return;
     __syncthreads();
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
 
     // ---- this warp's copies -------------------------------------------------------------
     unsigned char *my_ring = ring + warp * C::kStages * C::kStageBytes;
     uint64_t *my_full = full + warp * C::kStages;
-    int ip = 0, it = 0;            // next copy: piece, tile of the piece
-    unsigned issued = 0, used = 0; // copies issued, consumed
-    // Issues this warp's next copy, if one is known.  A piece whose last tile leaves this warp
-    // no row has no copy for that tile.  `limit`: pieces in the table.
+    int ip = 0, next = 0, keys = 0;               // pieces taken up; next row and rows of the last one
+    int from = 0, at_hk = 0, at_b = 0;            // its first key and place
+    unsigned issued = 0, used = 0;                // copies issued, consumed
+    // Issues this warp's next copy, if one is known.  `limit`: pieces in the table.
     auto issue = [&](int limit) {
-        while (ip < limit) {
+        while (next >= keys) {
+            if (ip >= limit) return;
             const Piece &p = pieces[ip % kPieceRing];
             if (p.end) return;
-            const int k0 = it * TK + warp * C::kKeys;
-            if (k0 >= p.keys) {  // (also where the piece is over)
-                if ((it + 1) * TK >= p.keys) ++ip, it = 0;
-                else ++it;
-                continue;
-            }
-            const unsigned s = issued % C::kStages;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&my_full[s], C::kStageBytes);
-                tma_load_4d(my_ring + s * C::kStageBytes, &a.tm, &my_full[s], 0, p.hk, p.key0 + k0, p.b);
-            }
-            ++issued;
-            if ((it + 1) * TK >= p.keys) ++ip, it = 0;
-            else ++it;
-            return;
+            ++ip;
+            next = warp * C::kKeys;
+            keys = p.keys, from = p.key0, at_hk = p.hk, at_b = p.b;
         }
+        if (lane == 0) {
+            const unsigned s = issued % C::kStages;
+            mbar_arrive_expect_tx(&my_full[s], C::kStageBytes);
+            tma_load_4d(my_ring + s * C::kStageBytes, &a.tm, &my_full[s], 0, at_hk, from + next, at_b);
+        }
+        ++issued;
+        next += TK;
     };
-    int known = kPieceRing / 2;  // table entries written (or behind an end mark)
+    int known = kPieceRing / 4;  // table entries written (or behind an end mark)
+    int n_joins = 0;             // (thread 0)
     for (int s = 0; s < C::kStages; ++s) issue(known);
 
     const int r = lane >> 2, c = lane & 3;
@@ -308,49 +376,114 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         if (p.end) break;
         const int h_base = p.hk * G + p.hb * kHeads, g_cnt = min(kHeads, G - p.hb * kHeads);
         // ---- the unit's queries: lane (r, c) holds head r's channels 32 g + 8 c .. + 7 -----
-        uint32_t qf[C::kQReg ? R::kGroups : 1][kTerms][4];
-        {
-            const T *qrow = static_cast<const T *>(a.q) + (int64_t)p.b * a.q_rs + (int64_t)h_base * D;
-            auto octet = [&](int head, int d, uint32_t (&o)[kTerms][4]) {  // 8 channels, in terms
-                const bool live = head < g_cnt && d < D;
-                if constexpr (F32) {
-                    const float4 *src = reinterpret_cast<const float4 *>(qrow + (int64_t)head * D + d);
-                    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4 x = live ? src[0] : z, y = live ? src[1] : z;
-                    uint32_t t[kTerms];
-                    split2<kTerms>(t, x.x, x.y);
+        // qz[g]: the sums of heads 2 c and 2 c + 1, in the units of the products; hs brings those
+        // heads' scores to the log2 domain.
+        uint32_t qf[C::kQReg ? R::kGroups : 1][kQTerms][4];
+        float qz[C::kQReg ? R::kGroups : 1][2];
+        float hs[2] = {a.scale_log2, a.scale_log2};
+        const T *qrow = static_cast<const T *>(a.q) + (int64_t)p.b * a.q_rs + (int64_t)h_base * D;
+        constexpr int kRaw = F32 ? 2 : 1;  // 16-byte words of an octet
+        auto load = [&](int head, int d, uint4 (&x)[kRaw]) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(qrow + (int64_t)head * D + d);
 #pragma unroll
-                    for (int k = 0; k < kTerms; ++k) o[k][0] = t[k];
-                    split2<kTerms>(t, x.z, x.w);
+            for (int k = 0; k < kRaw; ++k) x[k] = head < g_cnt && d < D ? src[k] : make_uint4(0, 0, 0, 0);
+        };
+        auto octet = [](const uint4 (&x)[kRaw], float (&v)[8]) {
+            if constexpr (F32) {
+                const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[kRaw - 1].x, x[kRaw - 1].y, x[kRaw - 1].z, x[kRaw - 1].w};
 #pragma unroll
-                    for (int k = 0; k < kTerms; ++k) o[k][1] = t[k];
-                    split2<kTerms>(t, y.x, y.y);
-#pragma unroll
-                    for (int k = 0; k < kTerms; ++k) o[k][2] = t[k];
-                    split2<kTerms>(t, y.z, y.w);
-#pragma unroll
-                    for (int k = 0; k < kTerms; ++k) o[k][3] = t[k];
-                } else {
-                    const uint4 x = live ? *reinterpret_cast<const uint4 *>(qrow + (int64_t)head * D + d)
-                                         : make_uint4(0, 0, 0, 0);
-                    o[0][0] = x.x, o[0][1] = x.y, o[0][2] = x.z, o[0][3] = x.w;
-                }
-            };
-            if constexpr (C::kQReg) {
-#pragma unroll
-                for (int g = 0; g < R::kGroups; ++g) octet(r, 32 * g + 8 * c, qf[g]);
+                for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
             } else {
-                for (int i = tid; i < kHeads * R::kPad / 8; i += C::kThreads) {
-                    const int head = i / (R::kPad / 8), d = 8 * (i % (R::kPad / 8));
-                    uint32_t o[kTerms][4];
-                    octet(head, d, o);
+                const uint32_t w[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
 #pragma unroll
-                    for (int k = 0; k < kTerms; ++k)
-                        *reinterpret_cast<uint4 *>(sQ + ((k * kHeads + head) * C::kQPitch + d) * 2) =
-                            make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
+                for (int k = 0; k < 4; ++k) {
+                    v[2 * k] = __uint_as_float(w[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
                 }
-                __syncthreads();
             }
+        };
+        auto larger = [](float x, float y) {  // of two magnitudes, by their bits: a NaN is above all
+            return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
+        };
+        auto scaled = [](float (&v)[8], float by) {  // returns the sum
+            float z = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) z += v[k] *= by;
+            return z;
+        };
+        if constexpr (C::kQReg) {
+            uint4 raw[R::kGroups][kRaw];
+            float m = 0.f;
+#pragma unroll
+            for (int g = 0; g < R::kGroups; ++g) load(r, 32 * g + 8 * c, raw[g]);
+#pragma unroll
+            for (int g = 0; g < R::kGroups; ++g) {
+                float v[8];
+                octet(raw[g], v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = larger(m, fabsf(v[k]));
+            }
+            m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = larger(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const float by = to_f16_range(m), back = 0x1p24f / by;
+            hs[0] *= __shfl_sync(0xffffffffu, back, 8 * c);  // lane 4 h holds head h
+            hs[1] *= __shfl_sync(0xffffffffu, back, 8 * c + 4);
+#pragma unroll
+            for (int g = 0; g < R::kGroups; ++g) {
+                float v[8];
+                octet(raw[g], v);
+                float z = scaled(v, by);
+                split_f16<kQTerms>(qf[g], v);
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                z += __shfl_xor_sync(0xffffffffu, z, 2);
+                z *= 0x1p-24f;
+                qz[g][0] = __shfl_sync(0xffffffffu, z, 8 * c);
+                qz[g][1] = __shfl_sync(0xffffffffu, z, 8 * c + 4);
+            }
+        } else {
+            constexpr int kOcts = R::kPad / 8;
+            float *sums = reinterpret_cast<float *>(sQ + kQTerms * kHeads * C::kQRow), *backs = sums + R::kGroups * kHeads;
+            for (int h = warp; h < kHeads; h += C::kWarps) {
+                float m = 0.f;
+                for (int o = lane; o < kOcts; o += 32) {
+                    uint4 x[kRaw];
+                    float v[8];
+                    load(h, 8 * o, x);
+                    octet(x, v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) m = larger(m, fabsf(v[k]));
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, off));
+                const float by = to_f16_range(m);
+                for (int o0 = 0; o0 < kOcts; o0 += 32) {
+                    const int o = min(o0 + lane, kOcts - 1);  // (a group's four lanes are all there or none)
+                    uint4 x[kRaw];
+                    float v[8];
+                    uint32_t t[kQTerms][4];
+                    load(h, 8 * o, x);  // (again, from L1)
+                    octet(x, v);
+                    float z = scaled(v, by);
+                    split_f16<kQTerms>(t, v);
+#pragma unroll
+                    for (int k = 0; k < kQTerms; ++k)
+                        *reinterpret_cast<uint4 *>(sQ + (k * kHeads + h) * C::kQRow + 16 * o) =
+                            make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
+                    z += __shfl_xor_sync(0xffffffffu, z, 1);
+                    z += __shfl_xor_sync(0xffffffffu, z, 2);
+                    if ((lane & 3) == 0 && o0 + lane < kOcts) sums[o / 4 * kHeads + h] = z * 0x1p-24f;
+                }
+                if (lane == 0) backs[h] = 0x1p24f / by;
+            }
+            __syncthreads();
+            hs[0] *= backs[2 * c];
+            hs[1] *= backs[2 * c + 1];
+        }
+        // one more piece for the table, while the first tile is on its way
+        if (tid == 0 && !pieces[(known - 1) % kPieceRing].end) {
+            Walk w = *walk;
+            next_piece<TK>(a, w, HB, pieces[known % kPieceRing]);
+            *walk = w;
         }
         float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
         float acc[C::kMt][4];
@@ -377,16 +510,20 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             for (int u = 0; u < C::kSub; ++u) sc[u][0] = sc[u][1] = sc[u][2] = sc[u][3] = 0.f;
 #pragma unroll
             for (int st = 0; st < kSets; ++st) {
-                uint32_t qs[C::kQReg ? 1 : kSet][kTerms][4];
+                uint32_t qs[C::kQReg ? 1 : kSet][kQTerms][4];
+                float zs[C::kQReg ? 1 : kSet][2];
                 if constexpr (!C::kQReg) {
 #pragma unroll
-                    for (int j = 0; j < kSet; ++j)
+                    for (int j = 0; j < kSet; ++j) {
+                        const int g = st * kSet + j;
 #pragma unroll
-                        for (int k = 0; k < kTerms; ++k) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(
-                                sQ + ((k * kHeads + r) * C::kQPitch + 32 * (st * kSet + j) + 8 * c) * 2);
+                        for (int k = 0; k < kQTerms; ++k) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(sQ + (k * kHeads + r) * C::kQRow + 16 * (4 * g + c));
                             qs[j][k][0] = v.x, qs[j][k][1] = v.y, qs[j][k][2] = v.z, qs[j][k][3] = v.w;
                         }
+                        const float2 z = *reinterpret_cast<const float2 *>(sQ + kQTerms * kHeads * C::kQRow + 4 * (g * kHeads + 2 * c));
+                        zs[j][0] = z.x, zs[j][1] = z.y;
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < C::kSub; ++u) {
@@ -398,43 +535,39 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     lds_words(py, y + R::kParamK + 4 * kSet * st);
 #pragma unroll
                     for (int j = 0; j < kSet; ++j) {
-                        const uint32_t bx = q4_bias2(px[j]), by = q4_bias2(py[j]);
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        const uint32_t a0[4] = {q4_codes2(wx[j], 0, bx), q4_codes2(wy[j], 0, by), q4_codes2(wx[j], 1, bx),
-                                                q4_codes2(wy[j], 1, by)};
-                        const uint32_t a1[4] = {q4_codes2(wx[j], 2, bx), q4_codes2(wy[j], 2, by), q4_codes2(wx[j], 3, bx),
-                                                q4_codes2(wy[j], 3, by)};
-#pragma unroll
-                        for (int k = kTerms - 1; k >= 0; --k) {
-                            const uint32_t(&q)[4] = [&]() -> const uint32_t(&)[4] {
-                                if constexpr (C::kQReg) return qf[st * kSet + j][k];
-                                else return qs[j][k];
-                            }();
-                            mma_bf16_16816(d, a0, q[0], q[1]);
-                            mma_bf16_16816(d, a1, q[2], q[3]);
-                        }
+                        const int g = st * kSet + j;
                         const float fx = q4_scale(px[j]), fy = q4_scale(py[j]);
-                        sc[u][0] = fmaf(fx, d[0], sc[u][0]);
-                        sc[u][1] = fmaf(fx, d[1], sc[u][1]);
-                        sc[u][2] = fmaf(fy, d[2], sc[u][2]);
-                        sc[u][3] = fmaf(fy, d[3], sc[u][3]);
+                        const float zx = __uint_as_float(px[j] & 0xffff0000u) - 128.f, zy = __uint_as_float(py[j] & 0xffff0000u) - 128.f;
+                        const uint32_t ux = wx[j] >> 8, uy = wy[j] >> 8;
+                        const uint32_t a0[4] = {wx[j] & 0x000f000fu, wy[j] & 0x000f000fu, wx[j] & 0x00f000f0u, wy[j] & 0x00f000f0u};
+                        const uint32_t a1[4] = {ux & 0x000f000fu, uy & 0x000f000fu, ux & 0x00f000f0u, uy & 0x00f000f0u};
+                        const float *z = C::kQReg ? qz[C::kQReg ? g : 0] : zs[C::kQReg ? 0 : j];
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = kQTerms - 1; k >= 0; --k) {
+                            const uint32_t *q = C::kQReg ? qf[C::kQReg ? g : 0][k] : qs[C::kQReg ? 0 : j][k];
+                            mma_f16_16816(d, a0, q[0], q[1]);
+                            mma_f16_16816(d, a1, q[2], q[3]);
+                        }
+                        sc[u][0] = fmaf(fx, fmaf(-zx, z[0], d[0]), sc[u][0]);
+                        sc[u][1] = fmaf(fx, fmaf(-zx, z[1], d[1]), sc[u][1]);
+                        sc[u][2] = fmaf(fy, fmaf(-zy, z[0], d[2]), sc[u][2]);
+                        sc[u][3] = fmaf(fy, fmaf(-zy, z[1], d[3]), sc[u][3]);
                     }
                 }
             }
             // ---- the log2 domain, the cap, the mask ------------------------------------------
+#pragma unroll
+            for (int u = 0; u < C::kSub; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[u][e] *= hs[e & 1];
             if (a.cap_log2 > 0.f) {
-                const float k2 = a.raw_over_cap * kTwoLog2e;
 #pragma unroll
                 for (int u = 0; u < C::kSub; ++u)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        sc[u][e] = F32 ? a.cap_log2 * tanhf(sc[u][e] * a.raw_over_cap)
-                                       : capped_score_log2(sc[u][e], k2, a.cap_log2);
-            } else {
-#pragma unroll
-                for (int u = 0; u < C::kSub; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[u][e] *= a.scale_log2;
+                        sc[u][e] = F32 ? a.cap_log2 * tanhf(sc[u][e] * a.over_cap_log2)
+                                       : capped_score_log2(sc[u][e], a.over_cap_log2 * kTwoLog2e, a.cap_log2);
             }
             if (valid < C::kKeys) {
 #pragma unroll
@@ -443,39 +576,43 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     if (16 * u + 8 + kr >= valid) sc[u][2] = sc[u][3] = -INFINITY;
                 }
             }
-            // ---- running maximum and sum ----------------------------------------------------
-            float corr[2];
-            bool refresh_any = false;
+            // ---- running reference and sum.  Any reference within 2^8 of the maximum serves; it
+            // moves (to the maximum) only when some score has outgrown it, which a vote tells --
+            float t[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float t = fmaxf(sc[0][e], sc[0][e + 2]);
+                t[e] = fmaxf(sc[0][e], sc[0][e + 2]);
 #pragma unroll
-                for (int u = 1; u < C::kSub; ++u) t = fmaxf(t, fmaxf(sc[u][e], sc[u][e + 2]));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                const bool refresh = t > m_ref[e] + kRescaleBy;
-                const float m_new = refresh ? t : m_ref[e];
-                const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                corr[e] = refresh ? fast_exp2(m_ref[e] - m_use) : 1.f;
-                float sum = 0.f;
-#pragma unroll
-                for (int u = 0; u < C::kSub; ++u) {
-                    sc[u][e] = fast_exp2(sc[u][e] - m_use);
-                    sc[u][e + 2] = fast_exp2(sc[u][e + 2] - m_use);
-                    sum += sc[u][e] + sc[u][e + 2];
-                }
-                l_run[e] = l_run[e] * corr[e] + sum;
-                m_ref[e] = m_new;
-                refresh_any |= refresh;
+                for (int u = 1; u < C::kSub; ++u) t[e] = fmaxf(t[e], fmaxf(sc[u][e], sc[u][e + 2]));
             }
-            if (__any_sync(0xffffffffu, refresh_any)) {
+            if (__any_sync(0xffffffffu, t[0] > m_ref[0] + kRescaleBy || t[1] > m_ref[1] + kRescaleBy)) {
+                float corr[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    t[e] = fmaxf(t[e], __shfl_xor_sync(0xffffffffu, t[e], 4));
+                    t[e] = fmaxf(t[e], __shfl_xor_sync(0xffffffffu, t[e], 8));
+                    t[e] = fmaxf(t[e], __shfl_xor_sync(0xffffffffu, t[e], 16));
+                    const float m_new = fmaxf(m_ref[e], t[e]);
+                    corr[e] = m_new == -INFINITY ? 1.f : fast_exp2(m_ref[e] - m_new);
+                    l_run[e] *= corr[e];
+                    m_ref[e] = m_new;
+                }
 #pragma unroll
                 for (int i = 0; i < C::kMt; ++i) {
                     acc[i][0] *= corr[0];
                     acc[i][1] *= corr[1];
                     acc[i][2] *= corr[0];
                     acc[i][3] *= corr[1];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float m_use = m_ref[e] == -INFINITY ? 0.f : m_ref[e];
+#pragma unroll
+                for (int u = 0; u < C::kSub; ++u) {
+                    sc[u][e] = fast_exp2(sc[u][e] - m_use);
+                    sc[u][e + 2] = fast_exp2(sc[u][e + 2] - m_use);
+                    l_run[e] += sc[u][e] + sc[u][e + 2];
                 }
             }
             // ---- O^T += V^T (P s)^T ----------------------------------------------------------
@@ -539,20 +676,27 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         }
         __syncthreads();
         if (*abort_flag) break;  // seen by every thread alike: no wait lies between here and the barrier
-        if (tid == 0) {          // one more piece for the table
-            Walk w = *walk;
-            if (known == 0 || !pieces[(known - 1) % kPieceRing].end) next_piece<TK>(a, w, HB, pieces[known % kPieceRing]);
-            *walk = w;
-        }
+        // this warp's share of heads 2 c and 2 c + 1: 2^(m - M) / sum over the warps of l 2^(m - M)
         float f[2];
+        const bool single = p.nseg == 1;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float M = -INFINITY;
+            float M = -INFINITY, l = 0.f;
 #pragma unroll
             for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, sM[w * 2 * kHeads + 2 * c + e]);
-            f[e] = fast_exp2(m_ref[e] - (M == -INFINITY ? 0.f : M));
+            const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int w = 0; w < C::kWarps; ++w)
+                l = fmaf(sM[w * 2 * kHeads + kHeads + 2 * c + e], fast_exp2(sM[w * 2 * kHeads + 2 * c + e] - base), l);
+            f[e] = fast_exp2(m_ref[e] - base) / l;  // a piece holds a key: l > 0
+            if (warp == 0 && r == 0 && 2 * c + e < g_cnt) {
+                const int64_t bh = (int64_t)p.b * a.n_heads + h_base + 2 * c + e;
+                const float lse2 = M + log2f(l);
+                if (a.defer_join && p.slot == 0) a.piece_count[bh] = p.nseg;
+                if (!single) a.part_lse[bh * a.max_splits + p.slot] = lse2;
+                else if (a.lse != nullptr) a.lse[bh] = lse2 * kLn2;
+            }
         }
-        const bool single = p.nseg == 1;
 #pragma unroll
         for (int i0 = 0; i0 < C::kMt; i0 += C::kRound) {
             if (i0 > 0) __syncthreads();
@@ -569,35 +713,27 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             for (int v = tid; v < kHeads * kV4; v += C::kThreads) {
                 const int h = v / kV4, x = 4 * (v % kV4), d = 16 * i0 + x;
                 if (h >= g_cnt || d >= D) continue;
-                float M = -INFINITY, l = 0.f;
-#pragma unroll
-                for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, sM[w * 2 * kHeads + h]);
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < C::kWarps; ++w) {
-                    l += sM[w * 2 * kHeads + kHeads + h] * fast_exp2(sM[w * 2 * kHeads + h] - (M == -INFINITY ? 0.f : M));
                     const float4 t = *reinterpret_cast<const float4 *>(park + (w * kHeads + h) * C::kParkPitch + x);
                     o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
                 }
-                const float rl = 1.f / l;  // a piece holds a key: l > 0
-                o.x *= rl; o.y *= rl; o.z *= rl; o.w *= rl;
-                const int64_t bh = (int64_t)p.b * a.n_heads + h_base + h;
-                const float lse2 = M + log2f(l);
-                if (d == 0 && p.slot == 0) a.piece_count[bh] = p.nseg;
                 if (single) {
                     T *dst = static_cast<T *>(a.out) + (int64_t)p.b * a.out_rs + (int64_t)(h_base + h) * D + d;
                     if constexpr (F32)
                         *reinterpret_cast<float4 *>(dst) = o;
                     else
                         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-                    if (d == 0 && a.lse != nullptr) a.lse[bh] = lse2 * kLn2;
                 } else {
+                    const int64_t bh = (int64_t)p.b * a.n_heads + h_base + h;
                     *reinterpret_cast<float4 *>(a.part_o + (bh * a.max_splits + p.slot) * D + d) = o;
-                    if (d == 0) a.part_lse[bh * a.max_splits + p.slot] = lse2;
                 }
             }
         }
         __syncthreads();  // the table has grown; sM, park and sQ are free
+        if (tid == 0 && !single && n_joins < 2)  // at most a CTA's first and last piece
+            joins[n_joins++] = Join{p.b, h_base, g_cnt, p.nseg, (p.b * a.n_kv_heads + p.hk) * HB + p.hb, 0};
         if (!pieces[(known - 1) % kPieceRing].end) ++known;
         while (issued - used < (unsigned)C::kStages) {  // copies that had to wait for the table
             const unsigned before = issued;
@@ -613,6 +749,64 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             mbar_wait_bounded(&my_full[used % C::kStages], (used / C::kStages) & 1, &no_abort, until);
         if (warp == 0 && *abort_flag) report_status(a.status, kErrTimeout);
     }
+    if (a.defer_join) return;
+    // ---- the units whose last piece was this CTA's: weights 2^{lse_c - lse} over their pieces ----
+    __syncthreads();  // every thread's partials are written
+    if (*abort_flag) return;
+    // (each thread's partials happen before the barrier, that before the ticket's release; a last
+    // ticket's acquire before the next barrier, that before the reads, which skip L1)
+    if (tid == 0) {
+        int t0 = -1, t1 = -1;
+        if (n_joins > 0) t0 = add_acq_rel(a.counters + joins[0].unit, 1);
+        if (n_joins > 1) t1 = add_acq_rel(a.counters + joins[1].unit, 1);
+        joins[0].last = n_joins > 0 && t0 == joins[0].nseg - 1;
+        joins[1].last = n_joins > 1 && t1 == joins[1].nseg - 1;
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        const Join j = joins[k];
+        if (!j.last) continue;
+        for (int v = tid; v < j.g_cnt * (D / 4); v += C::kThreads) {
+            const int h = j.h_base + v / (D / 4), d = 4 * (v % (D / 4));
+            const int64_t bh = (int64_t)j.b * a.n_heads + h;
+            const float *pl = a.part_lse + bh * a.max_splits;
+            const float *po = a.part_o + bh * a.max_splits * D + d;
+            float m = -INFINITY, z = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int kAhead = 8;  // pieces in flight
+            for (int s0 = 0; s0 < j.nseg; s0 += kAhead) {
+                float l[kAhead], mn = m;
+                float4 w[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const bool there = s0 + i < j.nseg;
+                    l[i] = there ? __ldcg(pl + s0 + i) : -INFINITY;
+                    w[i] = there ? __ldcg(reinterpret_cast<const float4 *>(po + (int64_t)(s0 + i) * D))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) mn = fmaxf(mn, l[i]);  // finite: pieces hold keys
+                const float cf = fast_exp2(m - mn);
+                z *= cf; o.x *= cf; o.y *= cf; o.z *= cf; o.w *= cf;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float e = fast_exp2(l[i] - mn);
+                    z += e;
+                    o.x = fmaf(e, w[i].x, o.x); o.y = fmaf(e, w[i].y, o.y);
+                    o.z = fmaf(e, w[i].z, o.z); o.w = fmaf(e, w[i].w, o.w);
+                }
+                m = mn;
+            }
+            const float rz = 1.f / z;
+            T *dst = static_cast<T *>(a.out) + (int64_t)j.b * a.out_rs + (int64_t)h * D + d;
+            if constexpr (F32)
+                *reinterpret_cast<float4 *>(dst) = make_float4(o.x * rz, o.y * rz, o.z * rz, o.w * rz);
+            else
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o.x * rz, o.y * rz), pack_bf16x2(o.z * rz, o.w * rz));
+            if (d == 0 && a.lse != nullptr) a.lse[bh] = (m + log2f(z)) * kLn2;
+        }
+        if (tid == 0) a.counters[j.unit] = 0;  // ready for the next call
+    }
 }
 
 template <int D, bool F32>
@@ -621,7 +815,7 @@ cudaError_t launch_q4_d(const Q4DecodeArgs &a, int grid, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     decode_q4_kernel<D, F32><<<grid, C::kThreads, C::kSmem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.defer_join) return e;
     const JoinArgs j{a.part_o, a.part_lse, a.piece_count, a.max_splits, a.n_heads, a.out, a.out_rs, a.lse};
     return launch_split_join<D, F32>(j, (int64_t)a.batch * a.n_heads, s);
 }
@@ -656,14 +850,19 @@ bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool b
     // A unit of n tiles falls into at most n / min_tiles + 2 pieces.  min_tiles keeps that count
     // near 64 or, with few units, near the number of CTAs that each unit must feed.
     const int64_t range = ((int64_t)std::max(max_kv_len, 1) + tile - 1) / tile;
+    if (units * (range + kUnitCost) > 0x7fffffffLL) return false;
     const int64_t target = std::max<int64_t>(64, (p->grid + std::max<int64_t>(units, 1) - 1) / std::max<int64_t>(units, 1));
     p->min_tiles = (int)std::max<int64_t>(1, (range + target - 1) / target);
     p->max_splits = (int)((range + p->min_tiles - 1) / p->min_tiles) + 2;
+    // With few units, cut finely, the CTA that joins one would read tens of partials after its
+    // stream; a second kernel takes them then.
+    p->defer_join = units * 8 < p->grid && p->max_splits > 16;
     auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t rows = (size_t)batch * n_heads;
     p->part_o_bytes = round256(rows * p->max_splits * head_dim * 4);
     p->part_lse_bytes = round256(rows * p->max_splits * 4);
-    p->total_bytes = p->part_o_bytes + p->part_lse_bytes + round256(rows * 4);
+    // pieces per (sequence, head), or tickets per unit
+    p->total_bytes = p->part_o_bytes + p->part_lse_bytes + round256((p->defer_join ? rows : (size_t)units) * 4);
     return true;
 }
 

@@ -183,16 +183,18 @@ struct Q4DecodeArgs {
     int64_t out_rs;
     float *lse;
     int batch, n_heads, n_kv_heads, head_dim, window;
-    float scale_log2, cap_log2, raw_over_cap;  // as in DecodeArgs
+    float scale_log2, cap_log2;  // as in DecodeArgs
+    float over_cap_log2;         // 1 / (softcap * log2(e)): a log2-domain score over the cap
     float *part_o;         // [batch, n_heads, max_splits, head_dim]
     float *part_lse;       // [batch, n_heads, max_splits], log2 domain
-    int32_t *piece_count;  // [batch, n_heads]
-    int max_splits, min_tiles;
+    int32_t *piece_count;  // defer_join: [batch, n_heads]
+    int32_t *counters;     // else: tickets [batch, n_kv_heads, blocks of heads], zero between calls
+    int max_splits, min_tiles, defer_join;
     uint64_t timeout_ns;
     int32_t *status;
 };
 struct Q4Plan {
-    int grid, min_tiles, max_splits, box_rows;
+    int grid, min_tiles, max_splits, box_rows, defer_join;
     size_t part_o_bytes, part_lse_bytes, total_bytes;
 };
 bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,

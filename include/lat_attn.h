@@ -373,9 +373,10 @@ lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs,
  * multiples of 16 bytes, else LAT_ERR_INVALID_ARG.  Every sequence's cache must hold at
  * least max_kv_len rows; rows at or past kv_lens[b] may hold any bytes.
  * workspace: at least lat_attn_decode_q4_workspace_size(...) bytes of device memory with the
- * same sizes (for either dt), 256-byte aligned, else LAT_ERR_WORKSPACE.  It needs no
- * clearing; calls sharing one must not overlap on the GPU.  Its size depends on the current
- * device's SM count.
+ * same sizes and dt, 256-byte aligned, else LAT_ERR_WORKSPACE; the rules of
+ * lat_attn_decode's workspace hold (zero-filled before its first use with a given layout,
+ * and again after LAT_ERR_TIMEOUT; calls sharing one must not overlap on the GPU; its size
+ * depends on the current device's SM count).
  * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, batch * n_heads * ceil(head_dim / 128)
  * < 2^31.
  */

@@ -184,8 +184,8 @@ def decode(c, q, lens, dt, Hq, window=0, softcap=0.0, scale=None, max_len=None, 
     mk = c.cap if max_len is None else max_len
     nb = binding.lat_attn_decode_q4_workspace_size(DT[dt], c.B, Hq, c.Hkv, D, mk)
     assert nb > 0
-    if ws is None:  # needs no clearing: start from anything
-        ws = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")
+    if ws is None:
+        ws = torch.zeros(nb, dtype=torch.uint8, device="cuda")
     if out is None:
         out = torch.full((c.B, Hq * D + out_pad), float("nan"), dtype=q.dtype, device="cuda")
     if lse is None:
@@ -328,7 +328,7 @@ def test_chunks_prefill_and_steps_together():
             assert np.abs(out.float().cpu().numpy().reshape(ref.shape) - ref).max() <= 2.0 ** -7 * vmax
         qs, lens = torch.empty(B, Hq * D, dtype=q.dtype, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
         nb = binding.lat_attn_decode_q4_workspace_size(binding.LAT_BF16, B, Hq, Hkv, D, cap)
-        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        ws = torch.zeros(nb, dtype=torch.uint8, device="cuda")
         out = torch.empty(B, Hq * D, dtype=q.dtype, device="cuda")
         lse = torch.empty(B, Hq, device="cuda")
         pos = torch.zeros(B, dtype=torch.int32, device="cuda")
