@@ -1,10 +1,11 @@
 """ctypes binding of the lat_attn C ABI (include/lat_attn.h).
 
 Argument marshalling only: every function forwards to the CUDA library under the same
-name and argument order.  Pointer arguments accept a torch tensor (its data_ptr), an int
-address or None (NULL); ``stream`` accepts a torch.cuda.Stream, an int handle or None
-(torch's current stream when CUDA is up, else the legacy default stream).  A non-OK
-status raises LatError.  There is no CPU fallback: if the library is not built, the
+name and argument order, by way of the C extension that the build writes out from the
+signatures below (sizes and names by ctypes).  Pointer arguments accept a torch tensor (its
+data_ptr), an int address or None (NULL); ``stream`` accepts a torch.cuda.Stream, an int
+handle or None (torch's current stream when CUDA is up, else the legacy default stream).
+A non-OK status raises LatError.  There is no CPU fallback: if the library is not built, the
 first call raises.
 """
 from __future__ import annotations
@@ -32,6 +33,7 @@ class LatError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_caller = None
 
 _P, _I64, _I32, _F32, _SZ, _U64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                    ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64)
@@ -108,10 +110,14 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
     return _lib
 
 
-def _ptr(x):
-    if x is None or isinstance(x, int):
-        return x
-    return x.data_ptr()
+def _calls():
+    """The calls that return a status, as the extension module's functions."""
+    global _caller
+    if _caller is None:
+        library()  # raises if nothing has been built
+        from . import _lat_call
+        _caller = _lat_call
+    return _caller
 
 
 def _stream(s):
@@ -138,71 +144,71 @@ def lat_status_string(status: int) -> str:
 def lat_attn_prefill(dt, q, q_rs, k, k_rs, v, v_rs, out, out_rs, lse, batch, seq_len, kv_len,
                      n_heads, n_kv_heads, head_dim, causal, window, scale, status=None,
                      stream=None):
-    _check(library().lat_attn_prefill(
-        dt, _ptr(q), q_rs, _ptr(k), k_rs, _ptr(v), v_rs, _ptr(out), out_rs, _ptr(lse), batch,
+    _check(_calls().lat_attn_prefill(
+        dt, q, q_rs, k, k_rs, v, v_rs, out, out_rs, lse, batch,
         seq_len, kv_len, n_heads, n_kv_heads, head_dim, int(bool(causal)), window, scale,
-        _ptr(status), _stream(stream)), "lat_attn_prefill")
+        status, _stream(stream)), "lat_attn_prefill")
 
 
 def lat_attn_prefill_softcap(dt, q, q_rs, k, k_rs, v, v_rs, out, out_rs, lse, batch, seq_len,
                              kv_len, n_heads, n_kv_heads, head_dim, causal, window, scale,
                              softcap, status=None, stream=None):
-    _check(library().lat_attn_prefill_softcap(
-        dt, _ptr(q), q_rs, _ptr(k), k_rs, _ptr(v), v_rs, _ptr(out), out_rs, _ptr(lse), batch,
+    _check(_calls().lat_attn_prefill_softcap(
+        dt, q, q_rs, k, k_rs, v, v_rs, out, out_rs, lse, batch,
         seq_len, kv_len, n_heads, n_kv_heads, head_dim, int(bool(causal)), window, scale,
-        softcap, _ptr(status), _stream(stream)), "lat_attn_prefill_softcap")
+        softcap, status, _stream(stream)), "lat_attn_prefill_softcap")
 
 
 def lat_attn_decode_softcap(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
                             cache_seq_stride, kv_lens, max_kv_len, out, out_rs, lse, batch,
                             n_heads, n_kv_heads, head_dim, window, scale, softcap, workspace,
                             workspace_bytes, status=None, stream=None):
-    _check(library().lat_attn_decode_softcap(
-        dt, _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
-        cache_seq_stride, _ptr(kv_lens), max_kv_len, _ptr(out), out_rs, _ptr(lse), batch,
-        n_heads, n_kv_heads, head_dim, window, scale, softcap, _ptr(workspace),
-        workspace_bytes, _ptr(status), _stream(stream)), "lat_attn_decode_softcap")
+    _check(_calls().lat_attn_decode_softcap(
+        dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+        cache_seq_stride, kv_lens, max_kv_len, out, out_rs, lse, batch,
+        n_heads, n_kv_heads, head_dim, window, scale, softcap, workspace,
+        workspace_bytes, status, _stream(stream)), "lat_attn_decode_softcap")
 
 
 def lat_attn_decode_ring(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
                          cache_seq_stride, ring_capacity, kv_lens, max_kv_len, out, out_rs, lse,
                          batch, n_heads, n_kv_heads, head_dim, window, scale, workspace,
                          workspace_bytes, status=None, stream=None):
-    _check(library().lat_attn_decode_ring(
-        dt, _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
-        cache_seq_stride, ring_capacity, _ptr(kv_lens), max_kv_len, _ptr(out), out_rs,
-        _ptr(lse), batch, n_heads, n_kv_heads, head_dim, window, scale, _ptr(workspace),
-        workspace_bytes, _ptr(status), _stream(stream)), "lat_attn_decode_ring")
+    _check(_calls().lat_attn_decode_ring(
+        dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+        cache_seq_stride, ring_capacity, kv_lens, max_kv_len, out, out_rs,
+        lse, batch, n_heads, n_kv_heads, head_dim, window, scale, workspace,
+        workspace_bytes, status, _stream(stream)), "lat_attn_decode_ring")
 
 
 def lat_kv_append_ring(dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride,
                        ring_capacity, k_new, v_new, new_rs, pos, n_new, batch, n_kv_heads,
                        head_dim, status=None, stream=None):
-    _check(library().lat_kv_append_ring(
-        dt, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride, cache_seq_stride,
-        ring_capacity, _ptr(k_new), _ptr(v_new), new_rs, _ptr(pos), n_new, batch, n_kv_heads,
-        head_dim, _ptr(status), _stream(stream)), "lat_kv_append_ring")
+    _check(_calls().lat_kv_append_ring(
+        dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride,
+        ring_capacity, k_new, v_new, new_rs, pos, n_new, batch, n_kv_heads,
+        head_dim, status, _stream(stream)), "lat_kv_append_ring")
 
 
 def lat_qkv_norm_rope_append(dt, qkv, qkv_rs, q_norm_w, k_norm_w, eps, rope_base, v_unit_norm,
                              q_out, q_out_rs, k_cache, v_cache, cache_rs, cache_head_stride,
                              cache_seq_stride, capacity, pos, n_new, batch, n_heads, n_kv_heads,
                              head_dim, status=None, stream=None):
-    _check(library().lat_qkv_norm_rope_append(
-        dt, _ptr(qkv), qkv_rs, _ptr(q_norm_w), _ptr(k_norm_w), eps, rope_base,
-        int(bool(v_unit_norm)), _ptr(q_out), q_out_rs, _ptr(k_cache), _ptr(v_cache), cache_rs,
-        cache_head_stride, cache_seq_stride, capacity, _ptr(pos), n_new, batch, n_heads,
-        n_kv_heads, head_dim, _ptr(status), _stream(stream)), "lat_qkv_norm_rope_append")
+    _check(_calls().lat_qkv_norm_rope_append(
+        dt, qkv, qkv_rs, q_norm_w, k_norm_w, eps, rope_base,
+        int(bool(v_unit_norm)), q_out, q_out_rs, k_cache, v_cache, cache_rs,
+        cache_head_stride, cache_seq_stride, capacity, pos, n_new, batch, n_heads,
+        n_kv_heads, head_dim, status, _stream(stream)), "lat_qkv_norm_rope_append")
 
 
 def lat_attn_prefill_cached(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
                             cache_seq_stride, out, out_rs, lse, batch, seq_len, kv_len, n_heads,
                             n_kv_heads, head_dim, causal, window, scale, status=None,
                             stream=None):
-    _check(library().lat_attn_prefill_cached(
-        dt, _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
-        cache_seq_stride, _ptr(out), out_rs, _ptr(lse), batch, seq_len, kv_len, n_heads,
-        n_kv_heads, head_dim, int(bool(causal)), window, scale, _ptr(status), _stream(stream)),
+    _check(_calls().lat_attn_prefill_cached(
+        dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+        cache_seq_stride, out, out_rs, lse, batch, seq_len, kv_len, n_heads,
+        n_kv_heads, head_dim, int(bool(causal)), window, scale, status, _stream(stream)),
         "lat_attn_prefill_cached")
 
 
@@ -215,11 +221,11 @@ def lat_attn_decode(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
                     cache_seq_stride, kv_lens, max_kv_len, out, out_rs, lse, batch, n_heads,
                     n_kv_heads, head_dim, window, scale, workspace, workspace_bytes,
                     status=None, stream=None):
-    _check(library().lat_attn_decode(
-        dt, _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
-        cache_seq_stride, _ptr(kv_lens), max_kv_len, _ptr(out), out_rs, _ptr(lse), batch,
-        n_heads, n_kv_heads, head_dim, window, scale, _ptr(workspace), workspace_bytes,
-        _ptr(status), _stream(stream)), "lat_attn_decode")
+    _check(_calls().lat_attn_decode(
+        dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+        cache_seq_stride, kv_lens, max_kv_len, out, out_rs, lse, batch,
+        n_heads, n_kv_heads, head_dim, window, scale, workspace, workspace_bytes,
+        status, _stream(stream)), "lat_attn_decode")
 
 
 def lat_attn_decode_static(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
@@ -227,20 +233,20 @@ def lat_attn_decode_static(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_s
                            n_heads, n_kv_heads, head_dim, window, scale, status=None,
                            stream=None):
     """lat_attn_decode with the library's own fixed device scratch (no workspace)."""
-    _check(library().lat_attn_decode_static(
-        dt, _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
-        cache_seq_stride, _ptr(kv_lens), max_kv_len, _ptr(out), out_rs, _ptr(lse), batch,
-        n_heads, n_kv_heads, head_dim, window, scale, _ptr(status), _stream(stream)),
+    _check(_calls().lat_attn_decode_static(
+        dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+        cache_seq_stride, kv_lens, max_kv_len, out, out_rs, lse, batch,
+        n_heads, n_kv_heads, head_dim, window, scale, status, _stream(stream)),
         "lat_attn_decode_static")
 
 
 def lat_kv_append(dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride,
                   capacity, k_new, v_new, new_rs, pos, n_new, batch, n_kv_heads, head_dim,
                   status=None, stream=None):
-    _check(library().lat_kv_append(
-        dt, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride, cache_seq_stride,
-        capacity, _ptr(k_new), _ptr(v_new), new_rs, _ptr(pos), n_new, batch, n_kv_heads,
-        head_dim, _ptr(status), _stream(stream)), "lat_kv_append")
+    _check(_calls().lat_kv_append(
+        dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride,
+        capacity, k_new, v_new, new_rs, pos, n_new, batch, n_kv_heads,
+        head_dim, status, _stream(stream)), "lat_kv_append")
 
 
 def lat_kv_q4_row_bytes(head_dim) -> int:
@@ -252,9 +258,9 @@ def lat_kv_append_q4(dt, cache, cache_rs, cache_head_stride, cache_seq_stride, c
                      v_new, new_rs, pos, n_new, batch, n_kv_heads, head_dim, status=None,
                      stream=None):
     """Quantise new K/V rows into a 4-bit cache (cache strides in bytes)."""
-    _check(library().lat_kv_append_q4(
-        dt, _ptr(cache), cache_rs, cache_head_stride, cache_seq_stride, capacity, _ptr(k_new),
-        _ptr(v_new), new_rs, _ptr(pos), n_new, batch, n_kv_heads, head_dim, _ptr(status),
+    _check(_calls().lat_kv_append_q4(
+        dt, cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, k_new,
+        v_new, new_rs, pos, n_new, batch, n_kv_heads, head_dim, status,
         _stream(stream)), "lat_kv_append_q4")
 
 
@@ -262,9 +268,9 @@ def lat_kv_expand_q4(dt, cache, cache_rs, cache_head_stride, cache_seq_stride, c
                      v_out, out_rs, pos, n_rows, batch, n_kv_heads, head_dim, status=None,
                      stream=None):
     """Read rows of a 4-bit cache back as K and V rows."""
-    _check(library().lat_kv_expand_q4(
-        dt, _ptr(cache), cache_rs, cache_head_stride, cache_seq_stride, capacity, _ptr(k_out),
-        _ptr(v_out), out_rs, _ptr(pos), n_rows, batch, n_kv_heads, head_dim, _ptr(status),
+    _check(_calls().lat_kv_expand_q4(
+        dt, cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, k_out,
+        v_out, out_rs, pos, n_rows, batch, n_kv_heads, head_dim, status,
         _stream(stream)), "lat_kv_expand_q4")
 
 
@@ -279,10 +285,10 @@ def lat_attn_decode_q4(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_se
                        head_dim, window, scale, softcap, workspace, workspace_bytes,
                        status=None, stream=None):
     """Decode over a 4-bit cache (cache strides in bytes)."""
-    _check(library().lat_attn_decode_q4(
-        dt, _ptr(q), q_rs, _ptr(cache), cache_rs, cache_head_stride, cache_seq_stride,
-        _ptr(kv_lens), max_kv_len, _ptr(out), out_rs, _ptr(lse), batch, n_heads, n_kv_heads,
-        head_dim, window, scale, softcap, _ptr(workspace), workspace_bytes, _ptr(status),
+    _check(_calls().lat_attn_decode_q4(
+        dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride,
+        kv_lens, max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads,
+        head_dim, window, scale, softcap, workspace, workspace_bytes, status,
         _stream(stream)), "lat_attn_decode_q4")
 
 
@@ -290,10 +296,10 @@ def lat_kv_block_bounds(dt, k_cache, cache_rs, cache_head_stride, cache_seq_stri
                         bounds, bounds_rs, bounds_head_stride, bounds_seq_stride, block_size,
                         pos, n_new, batch, n_kv_heads, head_dim, status=None, stream=None):
     """Bring the bounds of the blocks that hold the newly appended keys up to date."""
-    _check(library().lat_kv_block_bounds(
-        dt, _ptr(k_cache), cache_rs, cache_head_stride, cache_seq_stride, capacity, _ptr(bounds),
-        bounds_rs, bounds_head_stride, bounds_seq_stride, block_size, _ptr(pos), n_new, batch,
-        n_kv_heads, head_dim, _ptr(status), _stream(stream)), "lat_kv_block_bounds")
+    _check(_calls().lat_kv_block_bounds(
+        dt, k_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, bounds,
+        bounds_rs, bounds_head_stride, bounds_seq_stride, block_size, pos, n_new, batch,
+        n_kv_heads, head_dim, status, _stream(stream)), "lat_kv_block_bounds")
 
 
 def lat_attn_select_blocks_workspace_size(batch, n_kv_heads, block_size, max_kv_len) -> int:
@@ -306,10 +312,10 @@ def lat_attn_select_blocks(dt, q, q_rs, bounds, bounds_rs, bounds_head_stride,
                            n_first, n_last, batch, n_heads, n_kv_heads, head_dim, workspace,
                            workspace_bytes, status=None, stream=None):
     """Choose the blocks that each KV head keeps, into int32 blocks [batch, n_kv_heads, n_sel]."""
-    _check(library().lat_attn_select_blocks(
-        dt, _ptr(q), q_rs, _ptr(bounds), bounds_rs, bounds_head_stride, bounds_seq_stride,
-        block_size, _ptr(kv_lens), max_kv_len, _ptr(blocks), n_sel, n_first, n_last, batch,
-        n_heads, n_kv_heads, head_dim, _ptr(workspace), workspace_bytes, _ptr(status),
+    _check(_calls().lat_attn_select_blocks(
+        dt, q, q_rs, bounds, bounds_rs, bounds_head_stride, bounds_seq_stride,
+        block_size, kv_lens, max_kv_len, blocks, n_sel, n_first, n_last, batch,
+        n_heads, n_kv_heads, head_dim, workspace, workspace_bytes, status,
         _stream(stream)), "lat_attn_select_blocks")
 
 
@@ -324,19 +330,19 @@ def lat_attn_decode_blocks(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_s
                            out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim, scale,
                            softcap, workspace, workspace_bytes, status=None, stream=None):
     """Decode over the listed blocks of the cache alone."""
-    _check(library().lat_attn_decode_blocks(
-        dt, _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
-        cache_seq_stride, _ptr(kv_lens), max_kv_len, block_size, _ptr(blocks), n_sel, _ptr(out),
-        out_rs, _ptr(lse), batch, n_heads, n_kv_heads, head_dim, scale, softcap,
-        _ptr(workspace), workspace_bytes, _ptr(status), _stream(stream)),
+    _check(_calls().lat_attn_decode_blocks(
+        dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+        cache_seq_stride, kv_lens, max_kv_len, block_size, blocks, n_sel, out,
+        out_rs, lse, batch, n_heads, n_kv_heads, head_dim, scale, softcap,
+        workspace, workspace_bytes, status, _stream(stream)),
         "lat_attn_decode_blocks")
 
 
 def lat_test_prefill_timeout(q, q_rs, k, k_rs, v, v_rs, out, out_rs, batch, seq_len, n_heads,
                              n_kv_heads, head_dim, timeout_ns, status, stream=None):
-    _check(library().lat_test_prefill_timeout(
-        _ptr(q), q_rs, _ptr(k), k_rs, _ptr(v), v_rs, _ptr(out), out_rs, batch, seq_len,
-        n_heads, n_kv_heads, head_dim, timeout_ns, _ptr(status), _stream(stream)),
+    _check(_calls().lat_test_prefill_timeout(
+        q, q_rs, k, k_rs, v, v_rs, out, out_rs, batch, seq_len,
+        n_heads, n_kv_heads, head_dim, timeout_ns, status, _stream(stream)),
         "lat_test_prefill_timeout")
 
 
@@ -344,13 +350,13 @@ def lat_test_decode_timeout(q, q_rs, k_cache, v_cache, cache_rs, cache_head_stri
                             cache_seq_stride, kv_lens, max_kv_len, out, out_rs, batch, n_heads,
                             n_kv_heads, head_dim, workspace, workspace_bytes, timeout_ns, status,
                             stream=None):
-    _check(library().lat_test_decode_timeout(
-        _ptr(q), q_rs, _ptr(k_cache), _ptr(v_cache), cache_rs, cache_head_stride,
-        cache_seq_stride, _ptr(kv_lens), max_kv_len, _ptr(out), out_rs, batch, n_heads,
-        n_kv_heads, head_dim, _ptr(workspace), workspace_bytes, timeout_ns, _ptr(status),
+    _check(_calls().lat_test_decode_timeout(
+        q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+        cache_seq_stride, kv_lens, max_kv_len, out, out_rs, batch, n_heads,
+        n_kv_heads, head_dim, workspace, workspace_bytes, timeout_ns, status,
         _stream(stream)), "lat_test_decode_timeout")
 
 
 def lat_test_capped_scores(raw, n, scale, softcap, out, stream=None):
-    _check(library().lat_test_capped_scores(_ptr(raw), n, scale, softcap, _ptr(out),
+    _check(_calls().lat_test_capped_scores(raw, n, scale, softcap, out,
                                             _stream(stream)), "lat_test_capped_scores")

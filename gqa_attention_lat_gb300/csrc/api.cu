@@ -411,7 +411,8 @@ lat_status decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k_
     // over chosen blocks the stream is as long as the list at most
     const int range = blocks != nullptr ? n_sel * block_size : rows;
     lat::DecodePlan plan;
-    if (!lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, range, window, sms, &plan))
+    if (!lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, range, window, sms, &plan,
+                               blocks != nullptr ? lat::kBlocksLeastTiles : 4))
         return LAT_ERR_UNSUPPORTED;
     if (workspace == nullptr || workspace_bytes < plan.total_bytes ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
@@ -960,10 +961,14 @@ size_t lat_attn_decode_blocks_workspace_size(lat_dtype dt, int batch, int n_head
         n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || !block_size_ok(block_size) || n_sel <= 0 ||
         n_sel > lat::kSelectMaxBlocks)
         return 0;
-    if (dt == LAT_BF16)
-        return lat_attn_decode_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim, n_sel * block_size);
     int sms = 0;
     if (!current_sm_count(&sms)) return 0;
+    lat::DecodePlan plan;
+    if (dt == LAT_BF16)
+        return lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, n_sel * block_size, 0, sms, &plan,
+                                     lat::kBlocksLeastTiles)
+                   ? plan.total_bytes
+                   : 0;
     const size_t rows = (size_t)batch * n_heads;
     const size_t splits = lat::blocks_f32_splits(batch, n_heads, n_kv_heads, block_size, n_sel, sms);
     return splits == 1 ? 256 : round256(rows * splits * head_dim * 4) + round256(rows * splits * 4) + round256(rows * 4);

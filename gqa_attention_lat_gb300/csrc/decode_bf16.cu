@@ -1016,8 +1016,8 @@ int decode_bf16_tile_keys(int head_dim) {
 // near 64 (the scratch layout is sized for it).  Shapes with few units, where that would
 // leave CTAs idle, take the deferred-merge plan below instead.
 constexpr int64_t kDeferPieces = 8;
-static int min_seg_for(int range, int T) {
-    const int m = std::max(4 * T, (range + 63) / 64);
+static int min_seg_for(int range, int T, int least_tiles) {
+    const int m = std::max(least_tiles * T, (range + 63) / 64);
     return (m + T - 1) / T * T;
 }
 
@@ -1027,7 +1027,7 @@ int64_t decode_bf16_units(int batch, int n_heads, int n_kv_heads) {
 }
 
 bool plan_decode_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int max_kv_len,
-                      int window, int num_sms, DecodePlan *p) {
+                      int window, int num_sms, DecodePlan *p, int least_tiles) {
     if (decode_bf16_units(batch, n_heads, n_kv_heads) >= kDecodeMaxUnits) return false;
     int T, occ;
     switch (head_dim) {
@@ -1049,9 +1049,9 @@ bool plan_decode_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int 
     // so cut the stream that finely and merge in a second kernel
     const int64_t target = (grid + units - 1) / units;
     const bool defer = target > kDeferPieces;
-    int min_seg = min_seg_for(layout_range, T);
+    int min_seg = min_seg_for(layout_range, T, least_tiles);
     if (defer) {
-        const int64_t m = std::max<int64_t>(4 * T, (layout_range + target - 1) / target);
+        const int64_t m = std::max<int64_t>(least_tiles * T, (layout_range + target - 1) / target);
         min_seg = (int)((m + T - 1) / T * T);
     }
     const int layout_splits = (layout_range + min_seg - 1) / min_seg + 2;

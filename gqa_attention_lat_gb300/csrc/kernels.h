@@ -147,7 +147,11 @@ struct DecodePlan {
 };
 // Chooses the split size and the scratch layout; false when the shape is not built.
 bool plan_decode_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int max_kv_len,
-                      int window, int num_sms, DecodePlan *plan);
+                      int window, int num_sms, DecodePlan *plan, int least_tiles = 4);
+// Over chosen blocks a CTA's share may be one tile: with few keys in all, more CTAs at once are
+// worth more partials (one sequence, 8 KV heads, 64 blocks of 64 keys: 4 tiles 13.6 us, 1 tile
+// 11.2 us; eight sequences: the same).
+constexpr int kBlocksLeastTiles = 1;
 // work units of one decode launch (sequence x KV head x block of <= 8 query heads); the
 // split-KV merge tickets carry a unit index in 23 bits, so plans stop below kDecodeMaxUnits
 int64_t decode_bf16_units(int batch, int n_heads, int n_kv_heads);
