@@ -111,11 +111,13 @@ __global__ void __launch_bounds__(32 * kBoundWarps) block_bounds_kernel(const Bo
             e[v].lo[0] = y.x, e[v].lo[1] = y.y, e[v].lo[2] = y.z, e[v].lo[3] = y.w;
         }
     }
-    for (int j0 = lo; j0 < hi; j0 += kRows * kAhead) {
+    k += (int64_t)lo * a.cache_rs * (int64_t)sizeof(T);
+    const int n = hi - lo;
+    for (int j0 = 0; j0 < n; j0 += kRows * kAhead) {
         uint4 x[kAhead][kPer];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int j = min(j0 + i * kRows + row, hi - 1);  // past the end: the last row again
+            const int j = min(j0 + i * kRows + row, n - 1);  // past the end: the last row again
 #pragma unroll
             for (int v = 0; v < kPer; ++v)
                 x[i][v] = active ? *reinterpret_cast<const uint4 *>(k + (int64_t)j * a.cache_rs * (int64_t)sizeof(T) + 16 * kLanes * v)

@@ -75,7 +75,9 @@ struct Q4Cfg {
     // else in shared memory: [term][head] rows of 16 bytes an octet, 16 words apart in the banks,
     // [group][head] sums, [head] factors
     static constexpr int kQRow = 2 * R::kPad + 64;
-    static constexpr int kQBytes = kQReg ? 0 : kQTerms * kHeads * kQRow + (R::kGroups + 1) * kHeads * 4;
+    // (in registers: two units' queries as they are, this one's and the next's)
+    static constexpr int kRawRow = D * (F32 ? 4 : 2), kRawBytes = kHeads * kRawRow;
+    static constexpr int kQBytes = kQReg ? 2 * kRawBytes : kQTerms * kHeads * kQRow + (R::kGroups + 1) * kHeads * 4;
     static constexpr int kRound = 8;                         // MMA tiles joined at once: 128 channels
     static constexpr int kParkPitch = 16 * kRound + 4;
     static constexpr int kParkBytes = kWarps * kHeads * kParkPitch * 4;
@@ -126,7 +128,7 @@ __device__ __forceinline__ uint32_t share_of(uint32_t x, uint32_t total, uint32_
 // a unit of n keys in the stream: nothing, or its tiles and what it costs beside them
 template <int T>
 __device__ __forceinline__ uint32_t unit_cost(int n) {
-    return n > 0 ? (uint32_t)(n + T - 1) / T + kUnitCost : 0u;
+    return n > 0 ? ((uint32_t)n + (T - 1)) / T + kUnitCost : 0u;
 }
 template <int T>
 __device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
@@ -148,7 +150,7 @@ __device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
         p.hk = (int)(idx / HB);
         p.hb = (int)(idx % HB);
         p.key0 = k.lo + (int)t0 * T;
-        p.keys = min(k.n, (int)t1 * T) - (int)t0 * T;
+        p.keys = (int)(min((uint32_t)k.n, t1 * T) - t0 * T);
         p.slot = (int)(blockIdx.x - first);
         p.nseg = (int)(last - first + 1);
         p.end = 0;
@@ -363,7 +365,25 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     };
     int known = kPieceRing / 4;  // table entries written (or behind an end mark)
     int n_joins = 0;             // (thread 0)
+    // A unit's queries come a unit ahead: asked for after the copies of its rows, they would wait
+    // behind them (2.5 us where they take 1).
+    const T *q_all = static_cast<const T *>(a.q);
+    auto fetch_queries = [&](int i, int limit) {
+        if constexpr (C::kQReg) {
+            const Piece &n = pieces[i % kPieceRing];
+            if (i < limit && !n.end) {
+                const int h0 = n.hk * G + n.hb * kHeads, cnt = min(kHeads, G - n.hb * kHeads);
+                const unsigned char *src = reinterpret_cast<const unsigned char *>(q_all + (int64_t)n.b * a.q_rs + (int64_t)h0 * D);
+                for (int v = tid; v < cnt * (C::kRawRow / 16); v += C::kThreads)
+                    cp_async_16(sQ + (i & 1) * C::kRawBytes + 16 * v, src + 16 * v, true);
+            }
+            cp_async_commit();
+        }
+    };
+    fetch_queries(0, known);
     for (int s = 0; s < C::kStages; ++s) issue(known);
+    cp_async_wait<0>();
+    __syncthreads();
 
     const int r = lane >> 2, c = lane & 3;
     // MMA row r is the tile's key perm(r): the two low bits swapped, so that the eight lanes of
@@ -376,15 +396,21 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         if (p.end) break;
         const int h_base = p.hk * G + p.hb * kHeads, g_cnt = min(kHeads, G - p.hb * kHeads);
         // ---- the unit's queries: lane (r, c) holds head r's channels 32 g + 8 c .. + 7 -----
-        // qz[g]: the sums of heads 2 c and 2 c + 1, in the units of the products; hs brings those
-        // heads' scores to the log2 domain.
+        // qz[g]: the sums of heads 2 c and 2 c + 1, in the units of the products; pre and hs bring
+        // those heads' scores to the log2 domain (2^24 over the query's power of two, which can
+        // exceed a float, and the scale).
         uint32_t qf[C::kQReg ? R::kGroups : 1][kQTerms][4];
         float qz[C::kQReg ? R::kGroups : 1][2];
-        float hs[2] = {a.scale_log2, a.scale_log2};
-        const T *qrow = static_cast<const T *>(a.q) + (int64_t)p.b * a.q_rs + (int64_t)h_base * D;
+        float hs[2], pre[2];
+        auto undo = [&](int e, float by) {
+            pre[e] = by < 0x1p-100f ? 0x1p24f : 1.f;
+            hs[e] = (by < 0x1p-100f ? 1.f : 0x1p24f) / by * a.scale_log2;
+        };
+        const T *qrow = q_all + (int64_t)p.b * a.q_rs + (int64_t)h_base * D;
         constexpr int kRaw = F32 ? 2 : 1;  // 16-byte words of an octet
         auto load = [&](int head, int d, uint4 (&x)[kRaw]) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(qrow + (int64_t)head * D + d);
+            const uint4 *src = C::kQReg ? reinterpret_cast<const uint4 *>(sQ + (pi & 1) * C::kRawBytes + head * C::kRawRow + d * (int)sizeof(T))
+                                        : reinterpret_cast<const uint4 *>(qrow + (int64_t)head * D + d);
 #pragma unroll
             for (int k = 0; k < kRaw; ++k) x[k] = head < g_cnt && d < D ? src[k] : make_uint4(0, 0, 0, 0);
         };
@@ -416,33 +442,49 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             float m = 0.f;
 #pragma unroll
             for (int g = 0; g < R::kGroups; ++g) load(r, 32 * g + 8 * c, raw[g]);
+            if constexpr (F32) {
 #pragma unroll
-            for (int g = 0; g < R::kGroups; ++g) {
-                float v[8];
-                octet(raw[g], v);
+                for (int g = 0; g < R::kGroups; ++g) {
+                    float v[8];
+                    octet(raw[g], v);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) m = larger(m, fabsf(v[k]));
+                    for (int k = 0; k < 8; ++k) m = larger(m, fabsf(v[k]));
+                }
+            } else {  // magnitudes as whole numbers, two at a time
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int g = 0; g < R::kGroups; ++g) {
+                    const uint32_t w[4] = {raw[g][0].x, raw[g][0].y, raw[g][0].z, raw[g][0].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7fff7fffu);
+                }
+                m = larger(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
             }
             m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = larger(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const float by = to_f16_range(m), back = 0x1p24f / by;
-            hs[0] *= __shfl_sync(0xffffffffu, back, 8 * c);  // lane 4 h holds head h
-            hs[1] *= __shfl_sync(0xffffffffu, back, 8 * c + 4);
+            const float by = to_f16_range(m);
+            undo(0, __shfl_sync(0xffffffffu, by, 8 * c));  // lane 4 h holds head h
+            undo(1, __shfl_sync(0xffffffffu, by, 8 * c + 4));
+            // codes of 1 everywhere give the sums, where the scores will be
+            const uint32_t one0[4] = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};
 #pragma unroll
             for (int g = 0; g < R::kGroups; ++g) {
-                float v[8];
+                float v[8], d[4] = {0.f, 0.f, 0.f, 0.f};
                 octet(raw[g], v);
-                float z = scaled(v, by);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= by;
                 split_f16<kQTerms>(qf[g], v);
-                z += __shfl_xor_sync(0xffffffffu, z, 1);
-                z += __shfl_xor_sync(0xffffffffu, z, 2);
-                z *= 0x1p-24f;
-                qz[g][0] = __shfl_sync(0xffffffffu, z, 8 * c);
-                qz[g][1] = __shfl_sync(0xffffffffu, z, 8 * c + 4);
+#pragma unroll
+                for (int k = kQTerms - 1; k >= 0; --k) {
+                    mma_f16_16816(d, one0, qf[g][k][0], qf[g][k][1]);
+                    mma_f16_16816(d, one0, qf[g][k][2], qf[g][k][3]);
+                }
+                qz[g][0] = d[0];
+                qz[g][1] = d[1];
             }
         } else {
             constexpr int kOcts = R::kPad / 8;
-            float *sums = reinterpret_cast<float *>(sQ + kQTerms * kHeads * C::kQRow), *backs = sums + R::kGroups * kHeads;
+            float *sums = reinterpret_cast<float *>(sQ + kQTerms * kHeads * C::kQRow), *bys = sums + R::kGroups * kHeads;
             for (int h = warp; h < kHeads; h += C::kWarps) {
                 float m = 0.f;
                 for (int o = lane; o < kOcts; o += 32) {
@@ -473,12 +515,13 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     z += __shfl_xor_sync(0xffffffffu, z, 2);
                     if ((lane & 3) == 0 && o0 + lane < kOcts) sums[o / 4 * kHeads + h] = z * 0x1p-24f;
                 }
-                if (lane == 0) backs[h] = 0x1p24f / by;
+                if (lane == 0) bys[h] = by;
             }
             __syncthreads();
-            hs[0] *= backs[2 * c];
-            hs[1] *= backs[2 * c + 1];
+            undo(0, bys[2 * c]);
+            undo(1, bys[2 * c + 1]);
         }
+        fetch_queries(pi + 1, known);
         // one more piece for the table, while the first tile is on its way
         if (tid == 0 && !pieces[(known - 1) % kPieceRing].end) {
             Walk w = *walk;
@@ -560,7 +603,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
 #pragma unroll
             for (int u = 0; u < C::kSub; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[u][e] *= hs[e & 1];
+                for (int e = 0; e < 4; ++e) sc[u][e] = sc[u][e] * pre[e & 1] * hs[e & 1];
             if (a.cap_log2 > 0.f) {
 #pragma unroll
                 for (int u = 0; u < C::kSub; ++u)
@@ -731,7 +774,8 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 }
             }
         }
-        __syncthreads();  // the table has grown; sM, park and sQ are free
+        cp_async_wait<0>();  // the next unit's queries
+        __syncthreads();     // the table has grown; sM, park and sQ are free
         if (tid == 0 && !single && n_joins < 2)  // at most a CTA's first and last piece
             joins[n_joins++] = Join{p.b, h_base, g_cnt, p.nseg, (p.b * a.n_kv_heads + p.hk) * HB + p.hb, 0};
         if (!pieces[(known - 1) % kPieceRing].end) ++known;

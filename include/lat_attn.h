@@ -378,7 +378,9 @@ lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs,
  * and again after LAT_ERR_TIMEOUT; calls sharing one must not overlap on the GPU; its size
  * depends on the current device's SM count).
  * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, batch * n_heads * ceil(head_dim / 128)
- * < 2^31.
+ * < 2^31, and batch * n_kv_heads * ceil(n_heads / n_kv_heads / 8) work units of up to
+ * ceil(max_kv_len / 128) + 2 tiles (64 rows a tile at head_dim 512) < 2^31 in all.
+ * A query that holds a NaN or an infinity gives NaN.
  */
 size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads,
                                          int head_dim, int max_kv_len);
@@ -429,7 +431,8 @@ lat_status lat_kv_block_bounds(lat_dtype dt, const void *k_cache, int64_t cache_
  * there are no more).  The score of a block is the largest over the KV head's query heads of
  *   sum_d max(q_d * hi_d, q_d * lo_d),
  * which no key of the block can exceed (a positive scale or a score cap keeps the order).
- * The choice is that of the exact scores, whatever the order of their sums; a score that is
+ * Scores are compared to within 2^-45 of their terms' magnitude (bf16 ones, whose products
+ * and sums fit, exactly), so the choice does not hang on the order of a sum; a score that is
  * NaN goes before all others.
  *   blocks: int32 [batch, n_kv_heads, n_sel], ascending, -1 behind.
  * q as in lat_attn_decode; bounds as lat_kv_block_bounds leaves them; a length outside

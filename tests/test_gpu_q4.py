@@ -267,6 +267,62 @@ def test_every_length_around_a_tile(D, G):
     check_decode(out, lse, q, kh, vh, lens, "bf16", G, D, 0, 0.0, "D%d G%d" % (D, G))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_many_sequences_most_of_them_empty(dt):
+    """More sequences than a CTA has threads, zero to 70 keys each, over a capacity above
+    max_kv_len: the shares cross many short units."""
+    B, Hq, Hkv, D, cap = 700, 4, 2, 64, 96
+    g = torch.Generator().manual_seed(11)
+    lens = (torch.randint(0, 71, (B,), generator=g) * (torch.rand(B, generator=g) < 0.4)).tolist()
+    c = Cache(B, cap, Hkv, D)
+    k, v = rows(B, cap, Hkv, D, dt, 1, "k"), rows(B, cap, Hkv, D, dt, 1, "v")
+    c.append(k, v, [0] * B, cap, dt=dt)
+    q = W.normal((B, Hq * D), dtype=dt, device="cuda", seed=2, role="q")
+    out, lse, st = decode(c, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), dt, Hq, max_len=71)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check_decode(out, lse, q, held(k), held(v), lens, dt, Hq, D, 0, 0.0, "many")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("q_mul,k_mul,scale", [(1.0, 1.0, 0.0), (1.0, 1.0, -0.1), (2.0 ** 118, 2.0 ** -118, 0.1),
+                                               (2.0 ** -120, 2.0 ** 118, 0.4), (2.0 ** -9, 1.0, 50.0)])
+def test_scales_at_the_edges_of_the_numbers(dt, q_mul, k_mul, scale):
+    """Scale zero and below; queries and keys far from 1 whose products are not."""
+    B, Hq, Hkv, D, cap = 2, 4, 1, 128, 200
+    k, v = rows(B, cap, Hkv, D, "f32", 1, "k") * k_mul, rows(B, cap, Hkv, D, "f32", 1, "v")
+    q = W.normal((B, Hq * D), dtype="f32", device="cuda", seed=2, role="q") * q_mul
+    k, v, q = (x.to(W.torch_dtype(dt)) for x in (k, v, q))
+    c = Cache(B, cap, Hkv, D)
+    c.append(k, v, [0] * B, cap, dt=dt)
+    lens = [200, 3]
+    out, lse, st = decode(c, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), dt, Hq, scale=scale)
+    torch.cuda.synchronize()
+    kh, vh = held(k), held(v)
+    ref, ref_lse = oracle.decode(q.view(B, Hq, D), kh, vh, lens, window=0, scale=scale)
+    got = out.double().cpu().numpy().reshape(B, Hq, D)
+    assert np.isfinite(got).all()
+    # (a larger scale magnifies the scores' error: their magnitude stays below 2^7 here)
+    assert np.abs(got - ref).max() <= 2 * REL[dt] * np.abs(vh).max()
+    assert np.abs(lse.double().cpu().numpy() - ref_lse).max() <= 2e-4
+
+
+def test_nan_in_a_visible_row_and_in_the_query():
+    """A NaN value makes its group's 32 channels NaN and no others; a NaN key or query, the head."""
+    B, Hq, Hkv, D, cap = 3, 2, 1, 128, 64
+    k, v = rows(B, cap, Hkv, D, "bf16", 1, "k"), rows(B, cap, Hkv, D, "bf16", 1, "v")
+    v[0, 5, 0, 40] = float("nan")
+    k[1, 7, 0, 3] = float("inf")
+    q = W.normal((B, Hq * D), dtype="bf16", device="cuda", seed=2, role="q")
+    q[2, 3] = float("nan")  # head 0
+    c = Cache(B, cap, Hkv, D)
+    c.append(k, v, [0] * B, cap)
+    out, lse, st = decode(c, q, torch.full((B,), cap, dtype=torch.int32, device="cuda"), "bf16", Hq)
+    bad = torch.isnan(out.view(B, Hq, D))
+    assert bad[0, :, 32:64].all() and int(bad[0].sum()) == Hq * 32
+    assert bad[1].all() and bad[2, 0].all() and not bad[2, 1].any()
+
+
 def test_lengths_out_of_range_leave_their_rows_alone():
     B, Hq, Hkv, D, cap = 4, 4, 2, 128, 64
     lens = [64, 65, -1, 10]
