@@ -70,6 +70,9 @@ struct Q4Cfg {
     static constexpr int kTileKeys = kKeys * kWarps;
     static constexpr int kStages = 2;
     static constexpr int kStageBytes = kKeys * R::kBytes;
+    // Rows of 128 bytes (head_dim 80) would all begin in the same bank: their copies permute each
+    // row's 16-byte pieces by its number (the 128-byte swizzle: piece p of row j lies at p ^ (j % 8)).
+    static constexpr bool kSwizzle = R::kBytes == 128;
     static constexpr int kMt = D / 16;                       // 16-channel MMA tiles
     static constexpr bool kQReg = R::kPad * kQTerms <= 256;  // query fragments in registers
     // else in shared memory: [term][head] rows of 16 bytes an octet, 16 words apart in the banks,
@@ -160,39 +163,41 @@ __device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
     return false;
 }
 
-// N consecutive 32-bit words of shared memory, in the widest loads their count allows
+// N consecutive 32-bit words of a row of shared memory, in the widest loads their count allows.
+// `x`: the row's swizzle (see Q4Cfg::kSwizzle), 0 for none.
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const unsigned char *p) {
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const unsigned char *row, int off, int x) {
     if constexpr (N == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + off);
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        const uint2 v = *reinterpret_cast<const uint2 *>(row + off);
         w[0] = v.x, w[1] = v.y;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t *>(row + ((off + 4 * i) ^ x));
     }
 }
-// a lane's V halves of one set from two rows, paired: low halves from row x, high from row y
+// a lane's V halves of one set from two rows, paired: low halves from row r0, high from row r1
 template <int SET>
-__device__ __forceinline__ void v_pairs(uint32_t (&u)[SET], const unsigned char *x, const unsigned char *y) {
+__device__ __forceinline__ void v_pairs(uint32_t (&u)[SET], const unsigned char *r0, const unsigned char *r1, int off,
+                                        int x0, int x1) {
     if constexpr (SET % 2 == 0) {
         uint32_t wx[SET / 2], wy[SET / 2];
         if constexpr (SET == 4) {
-            lds_words(wx, x);
-            lds_words(wy, y);
+            lds_words(wx, r0, off, 0);
+            lds_words(wy, r1, off, 0);
         } else {
-            wx[0] = *reinterpret_cast<const uint32_t *>(x);
-            wy[0] = *reinterpret_cast<const uint32_t *>(y);
+            wx[0] = *reinterpret_cast<const uint32_t *>(r0 + off);
+            wy[0] = *reinterpret_cast<const uint32_t *>(r1 + off);
         }
 #pragma unroll
         for (int j = 0; j < SET; ++j) u[j] = __byte_perm(wx[j / 2], wy[j / 2], (j & 1) ? 0x7632 : 0x5410);
     } else {
 #pragma unroll
         for (int j = 0; j < SET; ++j)
-            u[j] = (uint32_t)reinterpret_cast<const uint16_t *>(x)[j] |
-                   ((uint32_t)reinterpret_cast<const uint16_t *>(y)[j] << 16);
+            u[j] = (uint32_t)*reinterpret_cast<const uint16_t *>(r0 + ((off + 2 * j) ^ x0)) |
+                   ((uint32_t)*reinterpret_cast<const uint16_t *>(r1 + ((off + 2 * j) ^ x1)) << 16);
     }
 }
 
@@ -255,7 +260,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     using R = Q4Row<D>;
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int kTerms = C::kTerms, kQTerms = C::kQTerms, kSet = R::kSet, kSets = R::kGroups / R::kSet;
-    extern __shared__ __align__(128) unsigned char smem[];  // (an aligned-up pointer would load as generic)
+    extern __shared__ __align__(1024) unsigned char smem[];  // (an aligned-up pointer would load as generic)
     unsigned char *ring = smem;                                              // [warp][stage]
     unsigned char *sQ = ring + C::kWarps * C::kStages * C::kStageBytes;      // [term][head] rows
     float *park = reinterpret_cast<float *>(sQ + C::kQBytes);                // [warp][head][channel]
@@ -390,6 +395,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     // a 16-byte shared-memory access fall into different banks at a 160-byte row
     const int kr = (r & 4) | ((r & 1) << 1) | ((r >> 1) & 1);
     const int kp = ((c & 2) << 1) | (c & 1);  // perm(2 c); perm(2 c + 1) is kp + 2
+    const int sw_r = C::kSwizzle ? kr << 4 : 0, sw_0 = C::kSwizzle ? kp << 4 : 0, sw_1 = C::kSwizzle ? (kp + 2) << 4 : 0;
 
     for (int pi = 0;; ++pi) {
         const Piece p = pieces[pi % kPieceRing];
@@ -543,8 +549,11 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 // rows past the end hold anything: their parameters become zeros, so that what
                 // they add is a finite number times a weight of zero
                 for (int i = lane; i < (C::kKeys - valid) * 2 * R::kGroups; i += 32)
-                    reinterpret_cast<uint32_t *>(tile + (valid + i / (2 * R::kGroups)) * R::kBytes +
-                                                 R::kParamK)[i % (2 * R::kGroups)] = 0u;
+                {
+                    const int row = valid + i / (2 * R::kGroups);
+                    *reinterpret_cast<uint32_t *>(tile + row * R::kBytes + ((R::kParamK + 4 * (i % (2 * R::kGroups))) ^
+                                                                           (C::kSwizzle ? (row & 7) << 4 : 0))) = 0u;
+                }
                 __syncwarp();
             }
             // ---- S^T: by groups, each scaled by its keys' scales -----------------------------
@@ -572,10 +581,10 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 for (int u = 0; u < C::kSub; ++u) {
                     const unsigned char *x = tile + (16 * u + kr) * R::kBytes, *y = x + 8 * R::kBytes;
                     uint32_t wx[kSet], wy[kSet], px[kSet], py[kSet];
-                    lds_words(wx, x + 4 * kSet * (4 * st + c));
-                    lds_words(wy, y + 4 * kSet * (4 * st + c));
-                    lds_words(px, x + R::kParamK + 4 * kSet * st);
-                    lds_words(py, y + R::kParamK + 4 * kSet * st);
+                    lds_words(wx, x, 4 * kSet * (4 * st + c), sw_r);
+                    lds_words(wy, y, 4 * kSet * (4 * st + c), sw_r);
+                    lds_words(px, x, R::kParamK + 4 * kSet * st, sw_r);
+                    lds_words(py, y, R::kParamK + 4 * kSet * st, sw_r);
 #pragma unroll
                     for (int j = 0; j < kSet; ++j) {
                         const int g = st * kSet + j;
@@ -667,15 +676,15 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     const unsigned char *x = rows + kr * R::kBytes, *y = x + 8 * R::kBytes;
                     const unsigned char *k0p = rows + kp * R::kBytes, *k1p = k0p + 2 * R::kBytes;
                     uint32_t px[kSet], py[kSet], q0[kSet], q1[kSet], q2[kSet], q3[kSet], ab[kSet], cd[kSet];
-                    lds_words(px, x + R::kParamV + 4 * kSet * st);
-                    lds_words(py, y + R::kParamV + 4 * kSet * st);
-                    lds_words(q0, k0p + R::kParamV + 4 * kSet * st);
-                    lds_words(q1, k1p + R::kParamV + 4 * kSet * st);
-                    lds_words(q2, k0p + 8 * R::kBytes + R::kParamV + 4 * kSet * st);
-                    lds_words(q3, k1p + 8 * R::kBytes + R::kParamV + 4 * kSet * st);
+                    lds_words(px, x, R::kParamV + 4 * kSet * st, sw_r);
+                    lds_words(py, y, R::kParamV + 4 * kSet * st, sw_r);
+                    lds_words(q0, k0p, R::kParamV + 4 * kSet * st, sw_0);
+                    lds_words(q1, k1p, R::kParamV + 4 * kSet * st, sw_1);
+                    lds_words(q2, k0p + 8 * R::kBytes, R::kParamV + 4 * kSet * st, sw_0);
+                    lds_words(q3, k1p + 8 * R::kBytes, R::kParamV + 4 * kSet * st, sw_1);
                     const int vo = R::kV + 2 * kSet * (8 * st + r);
-                    v_pairs<kSet>(ab, k0p + vo, k1p + vo);
-                    v_pairs<kSet>(cd, k0p + 8 * R::kBytes + vo, k1p + 8 * R::kBytes + vo);
+                    v_pairs<kSet>(ab, k0p, k1p, vo, sw_0, sw_1);
+                    v_pairs<kSet>(cd, k0p + 8 * R::kBytes, k1p + 8 * R::kBytes, vo, sw_0, sw_1);
 #pragma unroll
                     for (int j = 0; j < kSet; ++j) {
                         const int g = st * kSet + j;
