@@ -680,22 +680,30 @@ lat_status lat_kv_append_ring(lat_dtype dt, void *k_cache, void *v_cache, int64_
 
 namespace {
 
-// 4-D map of a 4-bit cache in 32-bit words: (word of the row, KV head, row < rows, sequence)
-// with a [row, 1, box_rows, 1] box; a warp's rows land one behind another, swizzled where a row is
-// 128 bytes.  L2 fetches 64 bytes at a time: a row of a token-major cache lies apart from the next
-// one of its head, and fetching 256 bytes about it cost 40 % (32 x 8192 keys, 8 KV heads of 128:
-// 113 us, by 64 bytes 81).
+// Map of a 4-bit cache in 32-bit words.  Rows of whole 128-byte pieces: 5-D, (word of the piece,
+// row < rows, piece, KV head, sequence) with a [32, box_rows, pieces, 1, 1] box and the 128-byte
+// swizzle; others 4-D, (word of the row, KV head, row, sequence) with a [row, 1, box_rows, 1] box.
+// L2 fetches 64 bytes at a time: a row of a token-major cache lies apart from the next one of its
+// head, and fetching 256 bytes about it cost 40 % (32 x 8192 keys, 8 KV heads of 128: 113 us, by
+// 64 bytes 81).
 bool make_q4_map(CUtensorMap *m, const void *base, int row_bytes, int heads, int rows, int batch,
                  int64_t row_stride, int64_t head_stride, int64_t seq_stride, int box_rows) {
     EncodeTiledFn fn = encode_tiled_fn();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)row_bytes / 4, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)batch};
-    const cuuint64_t strides[3] = {(cuuint64_t)head_stride, (cuuint64_t)row_stride, (cuuint64_t)seq_stride};
-    const cuuint32_t box[4] = {(cuuint32_t)row_bytes / 4, 1, (cuuint32_t)box_rows, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const cuuint64_t w = (cuuint64_t)row_bytes / 4, h = (cuuint64_t)heads, n = (cuuint64_t)rows, b = (cuuint64_t)batch;
+    const cuuint64_t rs = (cuuint64_t)row_stride, hs = (cuuint64_t)head_stride, ss = (cuuint64_t)seq_stride;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    if (row_bytes % 128 == 0) {
+        const cuuint64_t dims[5] = {32, n, w / 32, h, b}, strides[4] = {rs, 128, hs, ss};
+        const cuuint32_t box[5] = {32, (cuuint32_t)box_rows, (cuuint32_t)w / 32, 1, 1};
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 5, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    const cuuint64_t dims[4] = {w, h, n, b}, strides[3] = {hs, rs, ss};
+    const cuuint32_t box[4] = {(cuuint32_t)w, 1, (cuuint32_t)box_rows, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

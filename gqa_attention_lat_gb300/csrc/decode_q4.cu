@@ -70,9 +70,15 @@ struct Q4Cfg {
     static constexpr int kTileKeys = kKeys * kWarps;
     static constexpr int kStages = 2;
     static constexpr int kStageBytes = kKeys * R::kBytes;
-    // Rows of 128 bytes (head_dim 80) would all begin in the same bank: their copies permute each
-    // row's 16-byte pieces by its number (the 128-byte swizzle: piece p of row j lies at p ^ (j % 8)).
-    static constexpr bool kSwizzle = R::kBytes == 128;
+    // Rows of whole 128-byte pieces (head_dim 80: one, 512: five) would all begin in the same
+    // bank.  Their copies lay each piece of the kKeys rows behind the last and permute its 16-byte
+    // parts by the row's number (the 128-byte swizzle: part p of row j lies at p ^ (j % 8)).
+    static constexpr bool kSwizzle = R::kBytes % 128 == 0;
+    static constexpr int kPitch = kSwizzle ? 128 : R::kBytes;
+    // where byte `off` of a row lies from its first; x: 16 (row % 8)
+    static __device__ __forceinline__ int place(int off, int x) {
+        return kSwizzle ? (off >> 7) * (kKeys * 128) + ((off & 127) ^ x) : off;
+    }
     static constexpr int kMt = D / 16;                       // 16-channel MMA tiles
     static constexpr bool kQReg = R::kPad * kQTerms <= 256;  // query fragments in registers
     // else in shared memory: [term][head] rows of 16 bytes an octet, 16 words apart in the banks,
@@ -163,41 +169,35 @@ __device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
     return false;
 }
 
-// N consecutive 32-bit words of a row of shared memory, in the widest loads their count allows.
-// `x`: the row's swizzle (see Q4Cfg::kSwizzle), 0 for none.
-template <int N>
+// N consecutive 32-bit words at byte `off` of a row, in the widest loads their count allows
+template <typename C, int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const unsigned char *row, int off, int x) {
     if constexpr (N == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(row + off);
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + C::place(off, x));
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(row + off);
+        const uint2 v = *reinterpret_cast<const uint2 *>(row + C::place(off, x));
         w[0] = v.x, w[1] = v.y;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t *>(row + ((off + 4 * i) ^ x));
+        for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t *>(row + C::place(off + 4 * i, x));
     }
 }
 // a lane's V halves of one set from two rows, paired: low halves from row r0, high from row r1
-template <int SET>
+template <typename C, int SET>
 __device__ __forceinline__ void v_pairs(uint32_t (&u)[SET], const unsigned char *r0, const unsigned char *r1, int off,
                                         int x0, int x1) {
     if constexpr (SET % 2 == 0) {
         uint32_t wx[SET / 2], wy[SET / 2];
-        if constexpr (SET == 4) {
-            lds_words(wx, r0, off, 0);
-            lds_words(wy, r1, off, 0);
-        } else {
-            wx[0] = *reinterpret_cast<const uint32_t *>(r0 + off);
-            wy[0] = *reinterpret_cast<const uint32_t *>(r1 + off);
-        }
+        lds_words<C>(wx, r0, off, x0);
+        lds_words<C>(wy, r1, off, x1);
 #pragma unroll
         for (int j = 0; j < SET; ++j) u[j] = __byte_perm(wx[j / 2], wy[j / 2], (j & 1) ? 0x7632 : 0x5410);
     } else {
 #pragma unroll
         for (int j = 0; j < SET; ++j)
-            u[j] = (uint32_t)*reinterpret_cast<const uint16_t *>(r0 + ((off + 2 * j) ^ x0)) |
-                   ((uint32_t)*reinterpret_cast<const uint16_t *>(r1 + ((off + 2 * j) ^ x1)) << 16);
+            u[j] = (uint32_t)*reinterpret_cast<const uint16_t *>(r0 + C::place(off + 2 * j, x0)) |
+                   ((uint32_t)*reinterpret_cast<const uint16_t *>(r1 + C::place(off + 2 * j, x1)) << 16);
     }
 }
 
@@ -363,7 +363,10 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         if (lane == 0) {
             const unsigned s = issued % C::kStages;
             mbar_arrive_expect_tx(&my_full[s], C::kStageBytes);
-            tma_load_4d(my_ring + s * C::kStageBytes, &a.tm, &my_full[s], 0, at_hk, from + next, at_b);
+            if constexpr (C::kSwizzle)
+                tma_load_5d(my_ring + s * C::kStageBytes, &a.tm, &my_full[s], 0, from + next, 0, at_hk, at_b);
+            else
+                tma_load_4d(my_ring + s * C::kStageBytes, &a.tm, &my_full[s], 0, at_hk, from + next, at_b);
         }
         ++issued;
         next += TK;
@@ -395,7 +398,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     // a 16-byte shared-memory access fall into different banks at a 160-byte row
     const int kr = (r & 4) | ((r & 1) << 1) | ((r >> 1) & 1);
     const int kp = ((c & 2) << 1) | (c & 1);  // perm(2 c); perm(2 c + 1) is kp + 2
-    const int sw_r = C::kSwizzle ? kr << 4 : 0, sw_0 = C::kSwizzle ? kp << 4 : 0, sw_1 = C::kSwizzle ? (kp + 2) << 4 : 0;
+    const int sw_r = kr << 4, sw_0 = kp << 4, sw_1 = (kp + 2) << 4;  // those rows' swizzles
 
     for (int pi = 0;; ++pi) {
         const Piece p = pieces[pi % kPieceRing];
@@ -550,9 +553,8 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 // they add is a finite number times a weight of zero
                 for (int i = lane; i < (C::kKeys - valid) * 2 * R::kGroups; i += 32)
                 {
-                    const int row = valid + i / (2 * R::kGroups);
-                    *reinterpret_cast<uint32_t *>(tile + row * R::kBytes + ((R::kParamK + 4 * (i % (2 * R::kGroups))) ^
-                                                                           (C::kSwizzle ? (row & 7) << 4 : 0))) = 0u;
+                    const int row = valid + i / (2 * R::kGroups), off = R::kParamK + 4 * (i % (2 * R::kGroups));
+                    *reinterpret_cast<uint32_t *>(tile + row * C::kPitch + C::place(off, (row & 7) << 4)) = 0u;
                 }
                 __syncwarp();
             }
@@ -579,12 +581,12 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 }
 #pragma unroll
                 for (int u = 0; u < C::kSub; ++u) {
-                    const unsigned char *x = tile + (16 * u + kr) * R::kBytes, *y = x + 8 * R::kBytes;
+                    const unsigned char *x = tile + (16 * u + kr) * C::kPitch, *y = x + 8 * C::kPitch;
                     uint32_t wx[kSet], wy[kSet], px[kSet], py[kSet];
-                    lds_words(wx, x, 4 * kSet * (4 * st + c), sw_r);
-                    lds_words(wy, y, 4 * kSet * (4 * st + c), sw_r);
-                    lds_words(px, x, R::kParamK + 4 * kSet * st, sw_r);
-                    lds_words(py, y, R::kParamK + 4 * kSet * st, sw_r);
+                    lds_words<C>(wx, x, 4 * kSet * (4 * st + c), sw_r);
+                    lds_words<C>(wy, y, 4 * kSet * (4 * st + c), sw_r);
+                    lds_words<C>(px, x, R::kParamK + 4 * kSet * st, sw_r);
+                    lds_words<C>(py, y, R::kParamK + 4 * kSet * st, sw_r);
 #pragma unroll
                     for (int j = 0; j < kSet; ++j) {
                         const int g = st * kSet + j;
@@ -672,19 +674,19 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             for (int st = 0; st < kSets; ++st) {
 #pragma unroll
                 for (int u = 0; u < C::kSub; ++u) {
-                    const unsigned char *rows = tile + 16 * u * R::kBytes;
-                    const unsigned char *x = rows + kr * R::kBytes, *y = x + 8 * R::kBytes;
-                    const unsigned char *k0p = rows + kp * R::kBytes, *k1p = k0p + 2 * R::kBytes;
+                    const unsigned char *rows = tile + 16 * u * C::kPitch;
+                    const unsigned char *x = rows + kr * C::kPitch, *y = x + 8 * C::kPitch;
+                    const unsigned char *k0p = rows + kp * C::kPitch, *k1p = k0p + 2 * C::kPitch;
                     uint32_t px[kSet], py[kSet], q0[kSet], q1[kSet], q2[kSet], q3[kSet], ab[kSet], cd[kSet];
-                    lds_words(px, x, R::kParamV + 4 * kSet * st, sw_r);
-                    lds_words(py, y, R::kParamV + 4 * kSet * st, sw_r);
-                    lds_words(q0, k0p, R::kParamV + 4 * kSet * st, sw_0);
-                    lds_words(q1, k1p, R::kParamV + 4 * kSet * st, sw_1);
-                    lds_words(q2, k0p + 8 * R::kBytes, R::kParamV + 4 * kSet * st, sw_0);
-                    lds_words(q3, k1p + 8 * R::kBytes, R::kParamV + 4 * kSet * st, sw_1);
+                    lds_words<C>(px, x, R::kParamV + 4 * kSet * st, sw_r);
+                    lds_words<C>(py, y, R::kParamV + 4 * kSet * st, sw_r);
+                    lds_words<C>(q0, k0p, R::kParamV + 4 * kSet * st, sw_0);
+                    lds_words<C>(q1, k1p, R::kParamV + 4 * kSet * st, sw_1);
+                    lds_words<C>(q2, k0p + 8 * C::kPitch, R::kParamV + 4 * kSet * st, sw_0);
+                    lds_words<C>(q3, k1p + 8 * C::kPitch, R::kParamV + 4 * kSet * st, sw_1);
                     const int vo = R::kV + 2 * kSet * (8 * st + r);
-                    v_pairs<kSet>(ab, k0p, k1p, vo, sw_0, sw_1);
-                    v_pairs<kSet>(cd, k0p + 8 * R::kBytes, k1p + 8 * R::kBytes, vo, sw_0, sw_1);
+                    v_pairs<C>(ab, k0p, k1p, vo, sw_0, sw_1);
+                    v_pairs<C>(cd, k0p + 8 * C::kPitch, k1p + 8 * C::kPitch, vo, sw_0, sw_1);
 #pragma unroll
                     for (int j = 0; j < kSet; ++j) {
                         const int g = st * kSet + j;

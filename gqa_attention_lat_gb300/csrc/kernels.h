@@ -178,7 +178,7 @@ struct Q4StoreArgs {
 cudaError_t launch_q4_store(const Q4StoreArgs &a, bool bf16, bool expand, cudaStream_t s);
 
 struct Q4DecodeArgs {
-    CUtensorMap tm;  // 4-D map of 32-bit words (word, head, row < max_kv_len, sequence)
+    CUtensorMap tm;  // map of 32-bit words over the rows below max_kv_len
     const void *q;
     int64_t q_rs;
     const int32_t *kv_lens;
