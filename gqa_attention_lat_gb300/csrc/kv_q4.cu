@@ -144,20 +144,20 @@ template <int N>
 __device__ __forceinline__ uint32_t codes_of(const float (&x)[N], float s, float r, float z) {
     static_assert(N == 1 || N == 8, "the constants' sum");
     const float half = 0.5f * s, z15 = z * (1.f / 15.f);
-    float n[N];
+    float t[N], n[N], e[N];  // the whole number behind kWhole's bits, itself, the remainder
     bool near = false;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        n[k] = fmaf(x[k], r, kWhole) - kWhole;
-        near |= !(fabsf(fmaf(-n[k], s, x[k])) < half);
+        t[k] = fmaf(x[k], r, kWhole);
+        n[k] = t[k] - kWhole;
+        e[k] = fmaf(-n[k], s, x[k]);
+        near |= !(fabsf(e[k]) < half);
     }
-    if (near) {  // some quotient at a half, or rounded the wrong way
+    if (near) {  // some quotient at a half (the even one it is), or rounded the wrong way
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            const float twice = 2.f * fmaf(-n[k], s, x[k]);
-            const bool odd = (__float_as_uint(n[k] + kWhole) & 1u) != 0;
-            if (twice > s || (twice == s && odd)) n[k] += 1.f;
-            else if (twice < -s || (twice == -s && odd)) n[k] -= 1.f;
+            const bool odd = (__float_as_uint(t[k]) & 1u) != 0;
+            if (fabsf(e[k]) > half || (fabsf(e[k]) == half && odd)) n[k] += copysignf(1.f, e[k]);
         }
     }
     uint32_t code = 0;
@@ -179,45 +179,36 @@ struct StoreCfg {
     static constexpr int kPieces = R::kBytes / 16;
 };
 
-// head row `u` (of batch * n * n_kv_heads) -> its sequence, new row and head
-struct Place {
-    uint32_t row, hk, b, t;  // row: b * n + t
-    __device__ __forceinline__ Place(const Q4StoreArgs &a, uint32_t u) {
-        row = a.by_heads.div(u);
-        hk = u - row * a.n_kv_heads;
-        b = a.by_n.div(row);
-        t = row - b * a.n;
+// A warp's head rows: lane i < kRows finds row i's place, every lane asks for the row it works
+// on.  `cache`: byte offset in the cache; `rows`: element offset among the new (or output) rows;
+// -1 past the end, and in the cache where the sequence does not fit (reported once).
+struct Places {
+    int64_t cache, rows;
+    __device__ __forceinline__ Places(const Q4StoreArgs &a, uint32_t u, uint32_t units, bool mine) : cache(-1), rows(-1) {
+        if (!mine || u >= units) return;
+        const uint32_t row = a.by_heads.div(u), hk = u - row * a.n_kv_heads;  // row: b * n + t
+        const uint32_t b = a.by_n.div(row), t = row - b * a.n;
+        rows = (int64_t)row * a.rs + (int64_t)hk * a.head_dim;
+        const int p = a.pos[b];
+        if (p >= 0 && (int64_t)p + a.n <= (int64_t)a.capacity)
+            cache = (int64_t)b * a.cache_seq + ((int64_t)p + t) * a.cache_rs + (int64_t)hk * a.cache_head;
+        else if (t == 0 && hk == 0)
+            report_status(a.status, kErrBounds);
     }
+    __device__ __forceinline__ int64_t cache_of(int row) const { return __shfl_sync(0xffffffffu, cache, row); }
+    __device__ __forceinline__ int64_t rows_of(int row) const { return __shfl_sync(0xffffffffu, rows, row); }
 };
-__device__ __forceinline__ bool fits(const Q4StoreArgs &a, int p) {
-    return p >= 0 && (int64_t)p + a.n <= (int64_t)a.capacity;
-}
-// byte offset of a head row in the cache; false where its sequence does not fit (reported once)
-__device__ __forceinline__ bool locate(const Q4StoreArgs &a, uint32_t u, int64_t *at) {
-    const Place w(a, u);
-    const int p = a.pos[w.b];
-    if (!fits(a, p)) {
-        if (w.t == 0 && w.hk == 0) report_status(a.status, kErrBounds);
-        return false;
-    }
-    *at = (int64_t)w.b * a.cache_seq + (int64_t)(p + (int)w.t) * a.cache_rs + (int64_t)w.hk * a.cache_head;
-    return true;
-}
 
 template <typename T, int D>
-__device__ __forceinline__ void fetch(const Q4StoreArgs &a, const void *src, uint32_t u0, uint32_t units,
-                                      Octet<T> (&x)[StoreCfg<D>::kSteps]) {
+__device__ __forceinline__ void fetch(const Places &at, const void *src, bool vec, Octet<T> (&x)[StoreCfg<D>::kSteps]) {
     using C = StoreCfg<D>;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int st = 0; st < C::kSteps; ++st) {
-        const int it = st * 32 + lane, row = it / C::kOcts, d = 8 * (it % C::kOcts);
-        const uint32_t u = u0 + row;
+        const int it = st * 32 + lane, d = 8 * (it % C::kOcts);
+        const int64_t off = at.rows_of(it / C::kOcts);
         x[st].zero();
-        if (u < units && d < D) {
-            const uint32_t ur = a.by_heads.div(u);
-            x[st].load(static_cast<const T *>(src) + (int64_t)ur * a.rs + (u - ur * a.n_kv_heads) * D + d, a.vec);
-        }
+        if (off >= 0 && d < D) x[st].load(static_cast<const T *>(src) + off + d, vec);
     }
 }
 
@@ -296,23 +287,24 @@ __global__ void __launch_bounds__(32 * kStoreWarps) append_q4_kernel(const Q4Sto
     if constexpr (kTail > 0)
         for (int i = lane; i < C::kRows * kTail; i += 32)
             *reinterpret_cast<uint32_t *>(mine + i / kTail * R::kBytes + R::kParamV + 4 * R::kGroups + 4 * (i % kTail)) = 0u;
+    const Places at(a, u0 + lane, units, lane < C::kRows);
     Octet<T> k[C::kSteps], v[C::kSteps];
-    fetch<T, D>(a, a.k, u0, units, k);
-    fetch<T, D>(a, a.v, u0, units, v);
+    fetch<T, D>(at, a.k, a.vec, k);
+    fetch<T, D>(at, a.v, a.vec, v);
     quantise<T, D, false>(k, mine);
     quantise<T, D, true>(v, mine);
     __syncwarp();
 #pragma unroll
     for (int p0 = 0; p0 < C::kRows * C::kPieces; p0 += 32) {
         const int p = p0 + lane, row = p / C::kPieces;
-        int64_t at;
-        if (row < C::kRows && u0 + row < units && locate(a, u0 + row, &at))
-            *reinterpret_cast<uint4 *>(a.cache + at + 16 * (p % C::kPieces)) = *reinterpret_cast<const uint4 *>(mine + 16 * p);
+        const int64_t off = at.cache_of(min(row, C::kRows - 1));
+        if (row < C::kRows && off >= 0)
+            *reinterpret_cast<uint4 *>(a.cache + off + 16 * (p % C::kPieces)) = *reinterpret_cast<const uint4 *>(mine + 16 * p);
     }
 }
 
 template <typename T, int D, bool kIsV>
-__device__ __forceinline__ void read_back(const Q4StoreArgs &a, uint32_t u0, uint32_t units, const unsigned char *mine) {
+__device__ __forceinline__ void read_back(const Places &at, void *out, bool vec, const unsigned char *mine) {
     using C = StoreCfg<D>;
     using R = Q4Row<D>;
     const int lane = threadIdx.x & 31;
@@ -334,11 +326,8 @@ __device__ __forceinline__ void read_back(const Q4StoreArgs &a, uint32_t u0, uin
             for (int k = 0; k < 4; ++k)
                 v[k] = q4_codes2(__shfl_sync(0xffffffffu, own, (lane & ~3) | k), col, bias);
         }
-        const uint32_t u = u0 + row;
-        if (u >= units || d >= D) continue;
-        const Place w(a, u);
-        if (!fits(a, a.pos[w.b])) continue;  // rows left as they were
-        save8(static_cast<T *>(kIsV ? a.v_out : a.k_out) + (int64_t)w.row * a.rs + w.hk * D + d, a.vec, v, s2);
+        const int64_t off = at.rows_of(row);
+        if (off >= 0 && d < D) save8(static_cast<T *>(out) + off + d, vec, v, s2);
     }
 }
 
@@ -353,21 +342,22 @@ __global__ void __launch_bounds__(32 * kStoreWarps) expand_q4_kernel(const Q4Sto
     if (u0 >= units) return;
     unsigned char *mine = stage[warp];
     constexpr int kLoads = (C::kRows * C::kPieces + 31) / 32;
+    Places at(a, u0 + lane, units, lane < C::kRows);
+    if (at.cache < 0) at.rows = -1;  // rows left as they were
     uint4 got[kLoads];
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const int p = lane + 32 * i, row = p / C::kPieces;
-        int64_t at;
+        const int64_t off = at.cache_of(min(row, C::kRows - 1));
         got[i] = make_uint4(0, 0, 0, 0);
-        if (row < C::kRows && u0 + row < units && locate(a, u0 + row, &at))
-            got[i] = *reinterpret_cast<const uint4 *>(a.cache + at + 16 * (p % C::kPieces));
+        if (row < C::kRows && off >= 0) got[i] = *reinterpret_cast<const uint4 *>(a.cache + off + 16 * (p % C::kPieces));
     }
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
         if (lane + 32 * i < C::kRows * C::kPieces) *reinterpret_cast<uint4 *>(mine + 16 * (lane + 32 * i)) = got[i];
     __syncwarp();
-    read_back<T, D, false>(a, u0, units, mine);
-    read_back<T, D, true>(a, u0, units, mine);
+    read_back<T, D, false>(at, a.k_out, a.vec, mine);
+    read_back<T, D, true>(at, a.v_out, a.vec, mine);
 }
 
 template <typename T, int D>
