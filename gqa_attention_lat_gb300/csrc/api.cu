@@ -8,6 +8,7 @@
 
 #include <mutex>
 
+#include "cache_kernels.h"
 #include "kernels.h"
 #include "lat_attn.h"
 #include "lat_attn_testing.h"
@@ -408,17 +409,17 @@ lat_status decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k_
     // rows per sequence: the ring, or every position up to max_kv_len; the scratch layout
     // is sized by the same count (a ring's visible keys never exceed it)
     const int rows = ring > 0 ? ring : max_kv_len;
-    // over chosen blocks the stream is as long as the list at most
-    const int range = blocks != nullptr ? n_sel * block_size : rows;
+    // (over chosen blocks the stream is as long as the list at most)
     lat::DecodePlan plan;
-    if (!lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, range, window, sms, &plan,
-                               blocks != nullptr ? lat::kBlocksLeastTiles : 4))
+    if (!(blocks != nullptr
+              ? lat::plan_decode_blocks_bf16(batch, n_heads, n_kv_heads, head_dim, n_sel * block_size, sms, &plan)
+              : lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, rows, window, sms, &plan)))
         return LAT_ERR_UNSUPPORTED;
     if (workspace == nullptr || workspace_bytes < plan.total_bytes ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return LAT_ERR_WORKSPACE;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    lat::DecodeArgs a{};
+    lat::DecodeBlocksArgs a{};  // the dense decode's arguments are its first part
     if (max_kv_len > 0) {
         const int box = lat::decode_bf16_tile_keys(head_dim);
         // head dims of up to four whole 64-column chunks take each K (or V) tile in one
@@ -480,7 +481,10 @@ lat_status decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k_
     a.timeout_ns = timeout_ns;
     a.test_skip_load = skip_load;
     a.status = status;
-    return lat::launch_decode_bf16(a, plan.grid, s) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+    return (blocks != nullptr ? lat::launch_decode_blocks_bf16(a, plan.grid, s)
+                              : lat::launch_decode_bf16(a, plan.grid, s)) == cudaSuccess
+               ? LAT_OK
+               : LAT_ERR_CUDA;
 }
 
 }  // namespace
@@ -977,8 +981,7 @@ size_t lat_attn_decode_blocks_workspace_size(lat_dtype dt, int batch, int n_head
     if (!current_sm_count(&sms)) return 0;
     lat::DecodePlan plan;
     if (dt == LAT_BF16)
-        return lat::plan_decode_bf16(batch, n_heads, n_kv_heads, head_dim, n_sel * block_size, 0, sms, &plan,
-                                     lat::kBlocksLeastTiles)
+        return lat::plan_decode_blocks_bf16(batch, n_heads, n_kv_heads, head_dim, n_sel * block_size, sms, &plan)
                    ? plan.total_bytes
                    : 0;
     const size_t rows = (size_t)batch * n_heads;

@@ -19,8 +19,8 @@
 
 #include <algorithm>
 
+#include "cache_kernels.h"
 #include "device_common.cuh"
-#include "kernels.h"
 
 namespace lat {
 

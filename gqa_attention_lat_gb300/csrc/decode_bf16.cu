@@ -40,7 +40,9 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "cache_kernels.h"
 #include "device_common.cuh"
 #include "kernels.h"
 
@@ -126,9 +128,9 @@ __device__ __forceinline__ SeqKeys seq_keys_of(const DecodeArgs &a, int kv_len) 
     return s;
 }
 // tiles of one unit; over chosen blocks, 16-row groups of min(n_sel, blocks there are) blocks
-template <int T, bool kBlocks>
-__device__ __forceinline__ int seq_tiles(const DecodeArgs &a, const SeqKeys &s) {
-    if constexpr (kBlocks) {
+template <int T, typename Args>
+__device__ __forceinline__ int seq_tiles(const Args &a, const SeqKeys &s) {
+    if constexpr (std::is_same<Args, DecodeBlocksArgs>::value) {
         const int slots = min(a.n_sel, (s.n + a.block_size - 1) / a.block_size);
         return (slots * (a.block_size / 16) + T / 16 - 1) / (T / 16);
     }
@@ -138,9 +140,12 @@ __device__ __forceinline__ SeqKeys seq_keys(const DecodeArgs &a, int b) {
     return seq_keys_of(a, a.kv_lens[b]);
 }
 
+template <bool kBlocks>
+using DecodeArgsOf = typename std::conditional<kBlocks, DecodeBlocksArgs, DecodeArgs>::type;
+
 template <int D, bool kBlocks>
 __global__ void __launch_bounds__(DecodeCfg<D>::kThreads, DecodeCfg<D>::kMinBlocks)
-decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
+decode_bf16_kernel(const __grid_constant__ DecodeArgsOf<kBlocks> a) {
     using C = DecodeCfg<D>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -184,7 +189,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
     for (int b = b_lo; b < b_hi; ++b) {
         const int kv_len = a.kv_lens[b];
         const SeqKeys sk = seq_keys_of(a, kv_len);
-        my_sum += (long long)seq_tiles<T, kBlocks>(a, sk) * HU;
+        my_sum += (long long)seq_tiles<T>(a, sk) * HU;
         if (blockIdx.x == 0) {  // CTA 0 handles sequences with nothing to stream
             if (a.defer_merge && (kv_len < 0 || kv_len > a.max_kv_len || sk.n == 0))
                 for (int h = 0; h < a.n_heads; ++h)  // the merge kernel leaves them alone
@@ -222,7 +227,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
         long long p = my_start;
         for (int b = b_lo; b < b_hi; ++b) {
             const SeqKeys sk = seq_keys(a, b);
-            const long long w = (long long)seq_tiles<T, kBlocks>(a, sk) * HU;
+            const long long w = (long long)seq_tiles<T>(a, sk) * HU;
             if (r0 >= p && r0 < p + w) {
                 *start_b = b;
                 *start_p = p;
@@ -251,7 +256,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
     // a deferred merge kernel may be set up now; it waits for this grid before reading
     if (a.defer_merge) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (kBlocks && warp == C::kWarps) {
+    if constexpr (kBlocks) if (warp == C::kWarps) {
         // ------------------------------------------------------------ producer over chosen
         // blocks: the stream's walk as below, by the whole warp, which holds 32 entries of the
         // unit's list at a time (lane i: the list's place base + i - 1); lane 0 issues.  A tile
@@ -264,7 +269,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
             const int per_block = a.block_size / 16;
             while (pos < r1 && ok && b < a.batch) {
                 const SeqKeys sk = seq_keys(a, b);
-                const int nt = seq_tiles<T, kBlocks>(a, sk);
+                const int nt = seq_tiles<T>(a, sk);
                 const long long w = (long long)nt * HU;
                 if (pos >= pb + w) {
                     pb += w;
@@ -378,7 +383,8 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
             }
         }
         __syncwarp();
-    } else if (warp == C::kWarps) {
+    }
+    if (!kBlocks && warp == C::kWarps) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             tma_prefetch_desc(&a.tm_k);
@@ -395,7 +401,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
                 SeqKeys sk = seq_keys(a, b);
                 int next_len = b + 1 < a.batch ? a.kv_lens[b + 1] : 0;  // fetched ahead
                 while (pos < r1 && ok) {
-                    const int nt = seq_tiles<T, kBlocks>(a, sk);
+                    const int nt = seq_tiles<T>(a, sk);
                     const long long w = (long long)nt * HU;
                     if (pos >= pb + w) {  // nothing (left) of this sequence in our share
                         pb += w;
@@ -509,7 +515,8 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgs a) {
                 }
         }
         __syncwarp();
-    } else {
+    }
+    if (warp < C::kWarps) {
         // ------------------------------------------------------------ compute warps
         const int row0 = warp * 16;
         float m_ref[2] = {-INFINITY, -INFINITY};  // reference maxima (log2 domain, scaled)
@@ -968,7 +975,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
 }
 
 template <int D, bool kBlocks>
-cudaError_t launch_decode_d(const DecodeArgs &a, int grid, cudaStream_t s) {
+cudaError_t launch_decode_d(const DecodeArgsOf<kBlocks> &a, int grid, cudaStream_t s) {
     using C = DecodeCfg<D>;
     cudaError_t e = cudaFuncSetAttribute(decode_bf16_kernel<D, kBlocks>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -985,7 +992,7 @@ cudaError_t launch_decode_d(const DecodeArgs &a, int grid, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, decode_merge_kernel<D>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, decode_merge_kernel<D>, static_cast<const DecodeArgs &>(a))) != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
@@ -1026,8 +1033,8 @@ int64_t decode_bf16_units(int batch, int n_heads, int n_kv_heads) {
     return (int64_t)batch * n_kv_heads * ((G + kHeadsPerBlock - 1) / kHeadsPerBlock);
 }
 
-bool plan_decode_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int max_kv_len,
-                      int window, int num_sms, DecodePlan *p, int least_tiles) {
+static bool plan_of(int batch, int n_heads, int n_kv_heads, int head_dim, int max_kv_len, int num_sms,
+                    int least_tiles, DecodePlan *p) {
     if (decode_bf16_units(batch, n_heads, n_kv_heads) >= kDecodeMaxUnits) return false;
     int T, occ;
     switch (head_dim) {
@@ -1066,22 +1073,38 @@ bool plan_decode_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int 
     // merge counters per unit, or (deferred merge) piece counts per (sequence, head)
     p->counter_bytes = round256((size_t)(defer ? (int64_t)batch * n_heads : units) * 4);
     p->total_bytes = p->part_o_bytes + p->part_lse_bytes + p->counter_bytes;
-    (void)window;
     return true;
+}
+
+bool plan_decode_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int max_kv_len,
+                      int window, int num_sms, DecodePlan *p) {
+    (void)window;
+    return plan_of(batch, n_heads, n_kv_heads, head_dim, max_kv_len, num_sms, 4, p);
+}
+
+bool plan_decode_blocks_bf16(int batch, int n_heads, int n_kv_heads, int head_dim, int max_keys, int num_sms,
+                             DecodePlan *p) {
+    return plan_of(batch, n_heads, n_kv_heads, head_dim, max_keys, num_sms, 1, p);
 }
 
 cudaError_t launch_decode_bf16(const DecodeArgs &a, int grid, cudaStream_t s) {
     switch (a.head_dim) {
-        case 64:
-            return a.blocks != nullptr ? launch_decode_d<64, true>(a, grid, s) : launch_decode_d<64, false>(a, grid, s);
-        case 80:
-            return a.blocks != nullptr ? launch_decode_d<80, true>(a, grid, s) : launch_decode_d<80, false>(a, grid, s);
-        case 128:
-            return a.blocks != nullptr ? launch_decode_d<128, true>(a, grid, s) : launch_decode_d<128, false>(a, grid, s);
-        case 256:
-            return a.blocks != nullptr ? launch_decode_d<256, true>(a, grid, s) : launch_decode_d<256, false>(a, grid, s);
-        case 512:
-            return a.blocks != nullptr ? launch_decode_d<512, true>(a, grid, s) : launch_decode_d<512, false>(a, grid, s);
+        case 64: return launch_decode_d<64, false>(a, grid, s);
+        case 80: return launch_decode_d<80, false>(a, grid, s);
+        case 128: return launch_decode_d<128, false>(a, grid, s);
+        case 256: return launch_decode_d<256, false>(a, grid, s);
+        case 512: return launch_decode_d<512, false>(a, grid, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_decode_blocks_bf16(const DecodeBlocksArgs &a, int grid, cudaStream_t s) {
+    switch (a.head_dim) {
+        case 64: return launch_decode_d<64, true>(a, grid, s);
+        case 80: return launch_decode_d<80, true>(a, grid, s);
+        case 128: return launch_decode_d<128, true>(a, grid, s);
+        case 256: return launch_decode_d<256, true>(a, grid, s);
+        case 512: return launch_decode_d<512, true>(a, grid, s);
         default: return cudaErrorInvalidValue;
     }
 }

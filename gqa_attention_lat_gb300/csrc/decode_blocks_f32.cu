@@ -14,8 +14,8 @@
 
 #include <algorithm>
 
+#include "cache_kernels.h"
 #include "device_common.cuh"
-#include "kernels.h"
 #include "split_join.cuh"
 
 namespace lat {

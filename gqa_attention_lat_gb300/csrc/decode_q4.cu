@@ -24,12 +24,12 @@
 //    a word of codes is four operand registers for four ANDs and a shift, and the query's
 //    channels on the 16-fold codes are taken 16 times smaller.  A query is brought to
 //    [2^12, 2^13) by a power of two of its own; a bf16 one is then exact down to 2^-26 of its
-//    largest channel, an fp32 one is two fp16 terms (22 bits and a sign).  The zero point
-//    enters as z times the group's sum of the query.
+//    largest channel.  The zero point enters as z times the group's sum of the query.
 //  * O^T[16 channels x 8 heads] += V^T (P s)^T on mma m16n8k16 in bf16 (a weight needs bf16's
 //    range): a nibble becomes 128 + c by an AND-OR (0x4300 is bf16 128, whose last place is 1),
 //    minus 128 + z, exactly.  The rows' layout puts a lane's codes side by side.
-//  * LAT_F32: the weights p s are three bf16 terms (24 bits, so nothing is lost).
+//  * LAT_F32: the query is two fp16 terms (22 bits and their signs, 2^-24 of a channel), the
+//    codes lose their zero point before the product, and the weights p s are three bf16 terms.
 //  * Waits are bounded; on expiry the CTA records LAT_ERR_TIMEOUT, drains its copies, quits.
 // What bounds it: the logic pipe.  A warp instruction takes it two cycles of an SM's four
 // schedulers (measured: LOP3, PRMT and conversions 2 a cycle and SM, fp16 and bf16 MMA 0.49; an
@@ -40,8 +40,8 @@
 
 #include <cuda_fp16.h>
 
+#include "cache_kernels.h"
 #include "device_common.cuh"
-#include "kernels.h"
 #include "q4_row.cuh"
 #include "split_join.cuh"
 
@@ -225,6 +225,14 @@ __device__ __forceinline__ float to_f16_range(float m) {
     const int e = (int)(__float_as_uint(m) >> 23);
     if (e == 255) return NAN;
     return m == 0.f ? 1.f : __uint_as_float((uint32_t)min(254, 127 + 12 + 127 - e) << 23);
+}
+__device__ __forceinline__ uint32_t hsub2_f16(uint32_t x, uint32_t y) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+// a parameter word's z as fp16 1024 + (z << shift), twice
+__device__ __forceinline__ uint32_t f16_bias(uint32_t w, int shift) {
+    return ((((w >> 16) & 0xfu) * 0x00010001u) << shift) | 0x64006400u;
 }
 __device__ __forceinline__ void mma_f16_16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -591,11 +599,22 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     for (int j = 0; j < kSet; ++j) {
                         const int g = st * kSet + j;
                         const float fx = q4_scale(px[j]), fy = q4_scale(py[j]);
-                        const float zx = __uint_as_float(px[j] & 0xffff0000u) - 128.f, zy = __uint_as_float(py[j] & 0xffff0000u) - 128.f;
                         const uint32_t ux = wx[j] >> 8, uy = wy[j] >> 8;
-                        const uint32_t a0[4] = {wx[j] & 0x000f000fu, wy[j] & 0x000f000fu, wx[j] & 0x00f000f0u, wy[j] & 0x00f000f0u};
-                        const uint32_t a1[4] = {ux & 0x000f000fu, uy & 0x000f000fu, ux & 0x00f000f0u, uy & 0x00f000f0u};
-                        const float *z = C::kQReg ? qz[C::kQReg ? g : 0] : zs[C::kQReg ? 0 : j];
+                        uint32_t a0[4] = {wx[j] & 0x000f000fu, wy[j] & 0x000f000fu, wx[j] & 0x00f000f0u, wy[j] & 0x00f000f0u};
+                        uint32_t a1[4] = {ux & 0x000f000fu, uy & 0x000f000fu, ux & 0x00f000f0u, uy & 0x00f000f0u};
+                        if constexpr (F32) {
+                            // less the zero point before the sum, where taking it off after would cost
+                            // bits: fp16 1024 + c and 1024 + 16 c, minus the same of z, exactly
+                            const uint32_t bx[2] = {f16_bias(px[j], 0), f16_bias(px[j], 4)};
+                            const uint32_t by[2] = {f16_bias(py[j], 0), f16_bias(py[j], 4)};
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                a0[2 * i] = hsub2_f16(a0[2 * i] | 0x64006400u, bx[i]);
+                                a0[2 * i + 1] = hsub2_f16(a0[2 * i + 1] | 0x64006400u, by[i]);
+                                a1[2 * i] = hsub2_f16(a1[2 * i] | 0x64006400u, bx[i]);
+                                a1[2 * i + 1] = hsub2_f16(a1[2 * i + 1] | 0x64006400u, by[i]);
+                            }
+                        }
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int k = kQTerms - 1; k >= 0; --k) {
@@ -603,10 +622,20 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                             mma_f16_16816(d, a0, q[0], q[1]);
                             mma_f16_16816(d, a1, q[2], q[3]);
                         }
-                        sc[u][0] = fmaf(fx, fmaf(-zx, z[0], d[0]), sc[u][0]);
-                        sc[u][1] = fmaf(fx, fmaf(-zx, z[1], d[1]), sc[u][1]);
-                        sc[u][2] = fmaf(fy, fmaf(-zy, z[0], d[2]), sc[u][2]);
-                        sc[u][3] = fmaf(fy, fmaf(-zy, z[1], d[3]), sc[u][3]);
+                        if constexpr (F32) {  // (whole codes: in the other's units a large scale cannot overflow)
+                            sc[u][0] = fmaf(fx, d[0] * 0x1p-24f, sc[u][0]);
+                            sc[u][1] = fmaf(fx, d[1] * 0x1p-24f, sc[u][1]);
+                            sc[u][2] = fmaf(fy, d[2] * 0x1p-24f, sc[u][2]);
+                            sc[u][3] = fmaf(fy, d[3] * 0x1p-24f, sc[u][3]);
+                        } else {
+                            const float *z = C::kQReg ? qz[C::kQReg ? g : 0] : zs[C::kQReg ? 0 : j];
+                            const float zx = __uint_as_float(px[j] & 0xffff0000u) - 128.f;
+                            const float zy = __uint_as_float(py[j] & 0xffff0000u) - 128.f;
+                            sc[u][0] = fmaf(fx, fmaf(-zx, z[0], d[0]), sc[u][0]);
+                            sc[u][1] = fmaf(fx, fmaf(-zx, z[1], d[1]), sc[u][1]);
+                            sc[u][2] = fmaf(fy, fmaf(-zy, z[0], d[2]), sc[u][2]);
+                            sc[u][3] = fmaf(fy, fmaf(-zy, z[1], d[3]), sc[u][3]);
+                        }
                     }
                 }
             }

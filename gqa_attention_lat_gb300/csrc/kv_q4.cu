@@ -14,8 +14,8 @@
 // eight of them gather by a multiply-add each, and a head row's place comes by multiplication.
 #include <math.h>
 
+#include "cache_kernels.h"
 #include "device_common.cuh"
-#include "kernels.h"
 #include "q4_row.cuh"
 
 namespace lat {
