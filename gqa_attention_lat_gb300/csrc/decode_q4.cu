@@ -20,11 +20,16 @@
 //    K and V), and its first lane issues the copy for a stage as soon as the warp is done
 //    with it.  Warps meet only at the end of a piece.
 //  * Scores on mma m16n8k16 in fp16, keys in M, heads in N, by groups of 32 channels: a nibble
-//    left where it lies in the low byte of a half is the subnormal c 2^-24 or 16 c 2^-24, so
-//    a word of codes is four operand registers for four ANDs and a shift, and the query's
-//    channels on the 16-fold codes are taken 16 times smaller.  A query is brought to
-//    [2^12, 2^13) by a power of two of its own; a bf16 one is then exact down to 2^-26 of its
-//    largest channel.  The zero point enters as z times the group's sum of the query.
+//    left where it lies in the low byte of a half, ORed into fp16 2^-10, is 2^-20 times 1024 + c
+//    or 16 (64 + c); 2^-20 times 960 less brings the first to 64 + c too, exactly.  So a word of
+//    codes is four operand registers for four AND-ORs, a shift and two subtractions, and the
+//    query's channels on the 16-fold codes are taken 16 times smaller.  The zero point enters as
+//    (64 + z) times the group's sum of the query.  An MMA lines its products up by the exponents
+//    that the operands carry: the bare codes as fp16 subnormals need neither OR nor subtraction,
+//    but lost six bits (log-sum-exp 2e-6 off, against 1e-7 now).  Taking off 8 from every nibble
+//    instead gave 5e-8, for 280 instead of 273 us on 8 x 131072 keys at the time.  A query is
+//    brought to [2^8, 2^9) by a power of two of its own: channels above 2^-20 of its largest stay
+//    exact, smaller ones are within 2^-29 of it.
 //  * O^T[16 channels x 8 heads] += V^T (P s)^T on mma m16n8k16 in bf16 (a weight needs bf16's
 //    range): a nibble becomes 128 + c by an AND-OR (0x4300 is bf16 128, whose last place is 1),
 //    minus 128 + z, exactly.  The rows' layout puts a lane's codes side by side.
@@ -65,6 +70,8 @@ struct Q4Cfg {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTerms = F32 ? 3 : 1;               // bf16 terms of p s
     static constexpr int kQTerms = F32 ? 2 : 1;              // fp16 terms of q
+    static constexpr float kUnit = F32 ? 0x1p-24f : 0x1p-20f;  // of the scores' products
+    static constexpr int kQTo = F32 ? 12 : 8;                // its largest channel's exponent
     static constexpr int kSub = D == 512 ? 1 : 2;            // 16-key MMA tiles a warp takes at once
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kTileKeys = kKeys * kWarps;
@@ -220,15 +227,23 @@ __device__ __forceinline__ void split_f16(uint32_t (&o)[TERMS][4], const float (
         }
     }
 }
-// the power of two that brings m >= 0 to [2^12, 2^13); 1 for nothing, NaN for what is not finite
-__device__ __forceinline__ float to_f16_range(float m) {
+// the power of two that brings m >= 0 to [2^to, 2^(to + 1)), as near as floats have one; 1 for
+// nothing, NaN for what is not finite
+__device__ __forceinline__ float to_f16_range(float m, int to) {
     const int e = (int)(__float_as_uint(m) >> 23);
     if (e == 255) return NAN;
-    return m == 0.f ? 1.f : __uint_as_float((uint32_t)min(254, 127 + 12 + 127 - e) << 23);
+    return m == 0.f ? 1.f : __uint_as_float((uint32_t)max(1, min(254, 127 + to + 127 - e)) << 23);
 }
 __device__ __forceinline__ uint32_t hsub2_f16(uint32_t x, uint32_t y) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
     return *reinterpret_cast<const uint32_t *>(&d);
+}
+// nibbles at bits 0 or 4 (`shift`) of a word's halves in the last places of kOr, a pair of fp16,
+// less another (0 for none)
+template <uint32_t kOr>
+__device__ __forceinline__ uint32_t f16_codes(uint32_t w, int shift, uint32_t bias) {
+    const uint32_t x = and_or(w, 0x000f000fu << shift, kOr);
+    return bias ? hsub2_f16(x, bias) : x;
 }
 // a parameter word's z as fp16 1024 + (z << shift), twice
 __device__ __forceinline__ uint32_t f16_bias(uint32_t w, int shift) {
@@ -413,15 +428,15 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         if (p.end) break;
         const int h_base = p.hk * G + p.hb * kHeads, g_cnt = min(kHeads, G - p.hb * kHeads);
         // ---- the unit's queries: lane (r, c) holds head r's channels 32 g + 8 c .. + 7 -----
-        // qz[g]: the sums of heads 2 c and 2 c + 1, in the units of the products; pre and hs bring
-        // those heads' scores to the log2 domain (2^24 over the query's power of two, which can
-        // exceed a float, and the scale).
+        // qz[g]: the sums of heads 2 c and 2 c + 1, in units of kUnit (F32 has no use for them); pre
+        // and hs bring those heads' scores to the log2 domain: 1 / kUnit over the query's power of
+        // two, which can exceed a float, and the scale.
         uint32_t qf[C::kQReg ? R::kGroups : 1][kQTerms][4];
         float qz[C::kQReg ? R::kGroups : 1][2];
         float hs[2], pre[2];
         auto undo = [&](int e, float by) {
-            pre[e] = by < 0x1p-100f ? 0x1p24f : 1.f;
-            hs[e] = (by < 0x1p-100f ? 1.f : 0x1p24f) / by * a.scale_log2;
+            pre[e] = by < 0x1p-100f ? 1.f / C::kUnit : 1.f;
+            hs[e] = (by < 0x1p-100f ? 1.f : 1.f / C::kUnit) / by * a.scale_log2;
         };
         const T *qrow = q_all + (int64_t)p.b * a.q_rs + (int64_t)h_base * D;
         constexpr int kRaw = F32 ? 2 : 1;  // 16-byte words of an octet
@@ -479,11 +494,12 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             }
             m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = larger(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const float by = to_f16_range(m);
+            const float by = to_f16_range(m, C::kQTo);
             undo(0, __shfl_sync(0xffffffffu, by, 8 * c));  // lane 4 h holds head h
             undo(1, __shfl_sync(0xffffffffu, by, 8 * c + 4));
-            // codes of 1 everywhere give the sums, where the scores will be
-            const uint32_t one0[4] = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};
+            // 2^-10 (and 16 times it on the sixteenths) everywhere gives the sums, where the scores
+            // will be
+            const uint32_t ones[4] = {0x14001400u, 0x14001400u, 0x24002400u, 0x24002400u};
 #pragma unroll
             for (int g = 0; g < R::kGroups; ++g) {
                 float v[8], d[4] = {0.f, 0.f, 0.f, 0.f};
@@ -493,11 +509,11 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 split_f16<kQTerms>(qf[g], v);
 #pragma unroll
                 for (int k = kQTerms - 1; k >= 0; --k) {
-                    mma_f16_16816(d, one0, qf[g][k][0], qf[g][k][1]);
-                    mma_f16_16816(d, one0, qf[g][k][2], qf[g][k][3]);
+                    mma_f16_16816(d, ones, qf[g][k][0], qf[g][k][1]);
+                    mma_f16_16816(d, ones, qf[g][k][2], qf[g][k][3]);
                 }
-                qz[g][0] = d[0];
-                qz[g][1] = d[1];
+                qz[g][0] = d[0] * (C::kUnit * 0x1p10f);
+                qz[g][1] = d[1] * (C::kUnit * 0x1p10f);
             }
         } else {
             constexpr int kOcts = R::kPad / 8;
@@ -514,7 +530,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 }
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, off));
-                const float by = to_f16_range(m);
+                const float by = to_f16_range(m, C::kQTo);
                 for (int o0 = 0; o0 < kOcts; o0 += 32) {
                     const int o = min(o0 + lane, kOcts - 1);  // (a group's four lanes are all there or none)
                     uint4 x[kRaw];
@@ -530,7 +546,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                             make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
                     z += __shfl_xor_sync(0xffffffffu, z, 1);
                     z += __shfl_xor_sync(0xffffffffu, z, 2);
-                    if ((lane & 3) == 0 && o0 + lane < kOcts) sums[o / 4 * kHeads + h] = z * 0x1p-24f;
+                    if ((lane & 3) == 0 && o0 + lane < kOcts) sums[o / 4 * kHeads + h] = z * C::kUnit;
                 }
                 if (lane == 0) bys[h] = by;
             }
@@ -600,21 +616,14 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                         const int g = st * kSet + j;
                         const float fx = q4_scale(px[j]), fy = q4_scale(py[j]);
                         const uint32_t ux = wx[j] >> 8, uy = wy[j] >> 8;
-                        uint32_t a0[4] = {wx[j] & 0x000f000fu, wy[j] & 0x000f000fu, wx[j] & 0x00f000f0u, wy[j] & 0x00f000f0u};
-                        uint32_t a1[4] = {ux & 0x000f000fu, uy & 0x000f000fu, ux & 0x00f000f0u, uy & 0x00f000f0u};
-                        if constexpr (F32) {
-                            // less the zero point before the sum, where taking it off after would cost
-                            // bits: fp16 1024 + c and 1024 + 16 c, minus the same of z, exactly
-                            const uint32_t bx[2] = {f16_bias(px[j], 0), f16_bias(px[j], 4)};
-                            const uint32_t by[2] = {f16_bias(py[j], 0), f16_bias(py[j], 4)};
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                a0[2 * i] = hsub2_f16(a0[2 * i] | 0x64006400u, bx[i]);
-                                a0[2 * i + 1] = hsub2_f16(a0[2 * i + 1] | 0x64006400u, by[i]);
-                                a1[2 * i] = hsub2_f16(a1[2 * i] | 0x64006400u, bx[i]);
-                                a1[2 * i + 1] = hsub2_f16(a1[2 * i + 1] | 0x64006400u, by[i]);
-                            }
-                        }
+                        // 2^-20 (64 + c) and 16 times that, or (F32) c - z and 16 (c - z)
+                        constexpr uint32_t kOr = F32 ? 0x64006400u : 0x14001400u;
+                        const uint32_t bx[2] = {F32 ? f16_bias(px[j], 0) : 0x13801380u, F32 ? f16_bias(px[j], 4) : 0u};
+                        const uint32_t by[2] = {F32 ? f16_bias(py[j], 0) : 0x13801380u, F32 ? f16_bias(py[j], 4) : 0u};
+                        const uint32_t a0[4] = {f16_codes<kOr>(wx[j], 0, bx[0]), f16_codes<kOr>(wy[j], 0, by[0]),
+                                                f16_codes<kOr>(wx[j], 4, bx[1]), f16_codes<kOr>(wy[j], 4, by[1])};
+                        const uint32_t a1[4] = {f16_codes<kOr>(ux, 0, bx[0]), f16_codes<kOr>(uy, 0, by[0]), f16_codes<kOr>(ux, 4, bx[1]),
+                                                f16_codes<kOr>(uy, 4, by[1])};
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int k = kQTerms - 1; k >= 0; --k) {
@@ -622,15 +631,15 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                             mma_f16_16816(d, a0, q[0], q[1]);
                             mma_f16_16816(d, a1, q[2], q[3]);
                         }
-                        if constexpr (F32) {  // (whole codes: in the other's units a large scale cannot overflow)
-                            sc[u][0] = fmaf(fx, d[0] * 0x1p-24f, sc[u][0]);
-                            sc[u][1] = fmaf(fx, d[1] * 0x1p-24f, sc[u][1]);
-                            sc[u][2] = fmaf(fy, d[2] * 0x1p-24f, sc[u][2]);
-                            sc[u][3] = fmaf(fy, d[3] * 0x1p-24f, sc[u][3]);
+                        if constexpr (F32) {  // (the query is large: 2^-24 keeps a large scale from overflowing)
+                            sc[u][0] = fmaf(fx, d[0] * C::kUnit, sc[u][0]);
+                            sc[u][1] = fmaf(fx, d[1] * C::kUnit, sc[u][1]);
+                            sc[u][2] = fmaf(fy, d[2] * C::kUnit, sc[u][2]);
+                            sc[u][3] = fmaf(fy, d[3] * C::kUnit, sc[u][3]);
                         } else {
                             const float *z = C::kQReg ? qz[C::kQReg ? g : 0] : zs[C::kQReg ? 0 : j];
-                            const float zx = __uint_as_float(px[j] & 0xffff0000u) - 128.f;
-                            const float zy = __uint_as_float(py[j] & 0xffff0000u) - 128.f;
+                            const float zx = __uint_as_float(px[j] & 0xffff0000u) - 64.f;  // 64 + z
+                            const float zy = __uint_as_float(py[j] & 0xffff0000u) - 64.f;
                             sc[u][0] = fmaf(fx, fmaf(-zx, z[0], d[0]), sc[u][0]);
                             sc[u][1] = fmaf(fx, fmaf(-zx, z[1], d[1]), sc[u][1]);
                             sc[u][2] = fmaf(fy, fmaf(-zy, z[0], d[2]), sc[u][2]);
