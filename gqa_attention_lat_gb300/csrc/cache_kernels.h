@@ -88,12 +88,12 @@ struct Q4DecodeArgs {
     int32_t *status;
 };
 struct Q4Plan {
-    int grid, min_tiles, max_splits, box_rows, defer_join;
+    int grid, wide, min_tiles, max_splits, box_rows, defer_join;
     size_t part_o_bytes, part_lse_bytes, total_bytes;
 };
 bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,
                     Q4Plan *p);
-cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, int grid, cudaStream_t s);
+cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, const Q4Plan &p, cudaStream_t s);
 
 // ---------------------------------------------------------------- choice of cached blocks
 struct BoundsArgs {

@@ -63,7 +63,13 @@ constexpr int kPieceRing = 8;              // pieces known ahead
 // sequences of 1 to 4096 keys: not counted 36.8 us, as 2 tiles 30.5 us).
 constexpr int kUnitCost = 2;
 
+// The more keys a warp takes at once, the further a tile's fixed costs spread, until its registers
+// cost CTAs (8 x 131072 keys, 16 times kSub keys: head_dim 64 2 153 us, 4 134; 80 2 215, 3 190,
+// 4 197; 256 2 463, 3 660).  At head_dim 128 that comes with tiles too coarse for short units, so
+// there are two forms; kWideKeys says when.  (fp32 queries there: 392 us either way.)
 template <int D, bool F32>
+constexpr bool kHasWide = D == 128 && !F32;
+template <int D, bool F32, bool Wide>
 struct Q4Cfg {
     using R = Q4Row<D>;
     static constexpr int kWarps = 4;
@@ -72,7 +78,7 @@ struct Q4Cfg {
     static constexpr int kQTerms = F32 ? 2 : 1;              // fp16 terms of q
     static constexpr float kUnit = F32 ? 0x1p-24f : 0x1p-20f;  // of the scores' products
     static constexpr int kQTo = F32 ? 12 : 8;                // its largest channel's exponent
-    static constexpr int kSub = D == 512 ? 1 : 2;            // 16-key MMA tiles a warp takes at once
+    static constexpr int kSub = D == 64 || Wide ? 4 : D == 80 ? 3 : D == 512 ? 1 : 2;  // 16-key MMA tiles a warp takes at once
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kTileKeys = kKeys * kWarps;
     static constexpr int kStages = 2;
@@ -97,7 +103,7 @@ struct Q4Cfg {
     static constexpr int kRound = 8;                         // MMA tiles joined at once: 128 channels
     static constexpr int kParkPitch = 16 * kRound + 4;
     static constexpr int kParkBytes = kWarps * kHeads * kParkPitch * 4;
-    static constexpr int kMinBlocks = D == 64 ? 5 : D == 80 ? 4 : D == 128 ? 3 : D == 256 ? 2 : 1;  // CTAs per SM
+    static constexpr int kMinBlocks = D == 512 ? 1 : D == 256 || Wide || (D == 128 && F32) ? 2 : 3;  // CTAs per SM
     static constexpr int kMisc = 1024;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kQBytes + kParkBytes + kMisc;
     static_assert(kSmem <= 232448, "shared memory budget");
@@ -276,10 +282,10 @@ __device__ __forceinline__ void split2(uint32_t (&o)[TERMS], float x, float y) {
     }
 }
 
-template <int D, bool F32>
-__global__ void __launch_bounds__(Q4Cfg<D, F32>::kThreads, Q4Cfg<D, F32>::kMinBlocks)
+template <int D, bool F32, bool Wide>
+__global__ void __launch_bounds__(Q4Cfg<D, F32, Wide>::kThreads, Q4Cfg<D, F32, Wide>::kMinBlocks)
 decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
-    using C = Q4Cfg<D, F32>;
+    using C = Q4Cfg<D, F32, Wide>;
     using R = Q4Row<D>;
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int kTerms = C::kTerms, kQTerms = C::kQTerms, kSet = R::kSet, kSets = R::kGroups / R::kSet;
@@ -902,44 +908,78 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     }
 }
 
-template <int D, bool F32>
+template <int D, bool F32, bool Wide>
 cudaError_t launch_q4_d(const Q4DecodeArgs &a, int grid, cudaStream_t s) {
-    using C = Q4Cfg<D, F32>;
-    cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    using C = Q4Cfg<D, F32, Wide>;
+    cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, F32, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    decode_q4_kernel<D, F32><<<grid, C::kThreads, C::kSmem, s>>>(a);
+    decode_q4_kernel<D, F32, Wide><<<grid, C::kThreads, C::kSmem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.defer_join) return e;
     const JoinArgs j{a.part_o, a.part_lse, a.piece_count, a.max_splits, a.n_heads, a.out, a.out_rs, a.lse};
     return launch_split_join<D, F32>(j, (int64_t)a.batch * a.n_heads, s);
 }
 
-template <int D, bool F32>
-void shape_of(int *keys, int *tile, int *occ) {
-    using C = Q4Cfg<D, F32>;
-    *keys = C::kKeys;
-    *tile = C::kTileKeys;
+// Keys per CTA, were all units as long as they may be, from which the wide form is taken.  At 3449
+// 32 ragged sequences took 30.6 us wide and 28.9 narrow, 8 equally long ones 39.4 and 41.0; at 6898
+// 45.3 and 45.2, 68.3 and 71.9; at 13797 77.0 and 78.5, 124 and 131.
+constexpr int64_t kWideKeys = 6144;
+
+template <int D, bool F32, bool Wide>
+int occupancy_of() {
+    using C = Q4Cfg<D, F32, Wide>;
     static Occupancy occupancy;
-    *occ = occupancy(decode_q4_kernel<D, F32>, C::kThreads, C::kSmem);
+    return occupancy(decode_q4_kernel<D, F32, Wide>, C::kThreads, C::kSmem);
+}
+
+// grid, wide, box_rows, and the keys of a tile, for `units` units of up to `keys` keys
+template <int D, bool F32>
+int shape_of(Q4Plan *p, int sms, int64_t units, int64_t keys) {
+    using C = Q4Cfg<D, F32, false>;
+    p->wide = 0;
+    if constexpr (kHasWide<D, F32>) {
+        using W = Q4Cfg<D, F32, true>;
+        p->grid = sms * occupancy_of<D, F32, true>();
+        if (p->grid > 0 && units * keys / p->grid >= kWideKeys) {
+            p->wide = 1;
+            p->box_rows = W::kKeys;
+            return W::kTileKeys;
+        }
+    }
+    p->grid = sms * occupancy_of<D, F32, false>();
+    p->box_rows = C::kKeys;
+    return C::kTileKeys;
+}
+
+// calls f<D, F32> for a supported head_dim and type
+#define LAT_Q4_DISPATCH(head_dim, bf16, f, other, ...)                               \
+    switch (head_dim) {                                                              \
+        case 64: return bf16 ? f<64, false>(__VA_ARGS__) : f<64, true>(__VA_ARGS__);    \
+        case 80: return bf16 ? f<80, false>(__VA_ARGS__) : f<80, true>(__VA_ARGS__);    \
+        case 128: return bf16 ? f<128, false>(__VA_ARGS__) : f<128, true>(__VA_ARGS__); \
+        case 256: return bf16 ? f<256, false>(__VA_ARGS__) : f<256, true>(__VA_ARGS__); \
+        case 512: return bf16 ? f<512, false>(__VA_ARGS__) : f<512, true>(__VA_ARGS__); \
+        default: return other;                                                       \
+    }
+int shape(int head_dim, bool bf16, Q4Plan *p, int sms, int64_t units, int64_t keys) {
+    LAT_Q4_DISPATCH(head_dim, bf16, shape_of, 0, p, sms, units, keys)
+}
+template <int D, bool F32>
+cudaError_t launch_q4(const Q4DecodeArgs &a, int grid, bool wide, cudaStream_t s) {
+    if constexpr (kHasWide<D, F32>)
+        if (wide) return launch_q4_d<D, F32, true>(a, grid, s);
+    return launch_q4_d<D, F32, false>(a, grid, s);
 }
 
 }  // namespace
 
 bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,
                     Q4Plan *p) {
-    int tile = 0, occ = 0;
-    switch (head_dim) {
-        case 64: bf16 ? shape_of<64, false>(&p->box_rows, &tile, &occ) : shape_of<64, true>(&p->box_rows, &tile, &occ); break;
-        case 80: bf16 ? shape_of<80, false>(&p->box_rows, &tile, &occ) : shape_of<80, true>(&p->box_rows, &tile, &occ); break;
-        case 128: bf16 ? shape_of<128, false>(&p->box_rows, &tile, &occ) : shape_of<128, true>(&p->box_rows, &tile, &occ); break;
-        case 256: bf16 ? shape_of<256, false>(&p->box_rows, &tile, &occ) : shape_of<256, true>(&p->box_rows, &tile, &occ); break;
-        case 512: bf16 ? shape_of<512, false>(&p->box_rows, &tile, &occ) : shape_of<512, true>(&p->box_rows, &tile, &occ); break;
-        default: return false;
-    }
     const int G = n_heads / n_kv_heads, HB = (G + kHeads - 1) / kHeads;
     const int64_t units = (int64_t)batch * n_kv_heads * HB;
     // join grid: one CTA per (sequence, query head, up to 128 channels)
     if ((int64_t)batch * n_heads * ((head_dim + 127) / 128) > 0x7fffffffLL) return false;
-    p->grid = num_sms * occ;
+    const int tile = shape(head_dim, bf16, p, num_sms, units, max_kv_len);
+    if (tile == 0) return false;
     // A unit of n tiles falls into at most n / min_tiles + 2 pieces.  min_tiles keeps that count
     // near 64 or, with few units, near the number of CTAs that each unit must feed.
     const int64_t range = ((int64_t)std::max(max_kv_len, 1) + tile - 1) / tile;
@@ -959,15 +999,8 @@ bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool b
     return true;
 }
 
-cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, int grid, cudaStream_t s) {
-    switch (a.head_dim) {
-        case 64: return bf16 ? launch_q4_d<64, false>(a, grid, s) : launch_q4_d<64, true>(a, grid, s);
-        case 80: return bf16 ? launch_q4_d<80, false>(a, grid, s) : launch_q4_d<80, true>(a, grid, s);
-        case 128: return bf16 ? launch_q4_d<128, false>(a, grid, s) : launch_q4_d<128, true>(a, grid, s);
-        case 256: return bf16 ? launch_q4_d<256, false>(a, grid, s) : launch_q4_d<256, true>(a, grid, s);
-        case 512: return bf16 ? launch_q4_d<512, false>(a, grid, s) : launch_q4_d<512, true>(a, grid, s);
-        default: return cudaErrorInvalidValue;
-    }
+cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, const Q4Plan &p, cudaStream_t s) {
+    LAT_Q4_DISPATCH(a.head_dim, bf16, launch_q4, cudaErrorInvalidValue, a, p.grid, p.wide != 0, s)
 }
 
 }  // namespace lat

@@ -379,7 +379,8 @@ lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs,
  * depends on the current device's SM count).
  * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, batch * n_heads * ceil(head_dim / 128)
  * < 2^31, and batch * n_kv_heads * ceil(n_heads / n_kv_heads / 8) work units of up to
- * ceil(max_kv_len / 128) + 2 tiles (64 rows a tile at head_dim 512) < 2^31 in all.
+ * ceil(max_kv_len / 128) + 2 tiles (64 rows a tile at head_dim 512; more elsewhere, at
+ * times) < 2^31 in all.
  * A query that holds a NaN or an infinity gives NaN.
  */
 size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads,

@@ -267,6 +267,23 @@ def test_every_length_around_a_tile(D, G):
     check_decode(out, lse, q, kh, vh, lens, "bf16", G, D, 0, 0.0, "D%d G%d" % (D, G))
 
 
+@pytest.mark.parametrize("window,softcap", [(0, 0.0), (130, 20.0)])
+def test_short_sequences_in_long_caches(window, softcap):
+    """Caches long enough for the form of head_dim 128 that takes 64 keys a warp at once."""
+    lens = [0, 1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 63, 64, 65, 127, 128, 129, 191, 255, 256, 257, 511, 513, 600]
+    B, Hq, Hkv, D, cap, n = len(lens), 40, 8, 128, 10240, 600
+    c = Cache(B, cap, Hkv, D)
+    k, v = rows(B, n, Hkv, D, "bf16", 3, "k"), rows(B, n, Hkv, D, "bf16", 3, "v")
+    c.append(k, v, [0] * B, n)
+    q = W.normal((B, Hq * D), dtype="bf16", device="cuda", seed=4, role="q")
+    for b, x in enumerate(lens):
+        c.t[b, x:n] = 255
+    out, lse, st = decode(c, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), "bf16", Hq, window, softcap)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check_decode(out, lse, q, held(k), held(v), lens, "bf16", Hq, D, window, softcap, "long caches")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_many_sequences_most_of_them_empty(dt):
     """More sequences than a CTA has threads, zero to 70 keys each, over a capacity above
