@@ -169,6 +169,12 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[N], float s, float
     return code - kWholeBits * (N == 8 ? 0x11111111u : 1u);
 }
 
+// the nibbles of even number, then those of odd number
+__device__ __forceinline__ uint32_t evens_first(uint32_t x) {
+    const uint32_t t = (x ^ (x >> 4)) & 0x00f000f0u;  // nibbles 1 and 2 of each half change places
+    return __byte_perm(x ^ t ^ (t << 4), 0, 0x3120);
+}
+
 template <int D>
 struct StoreCfg {
     using R = Q4Row<D>;
@@ -248,19 +254,15 @@ __device__ __forceinline__ void quantise(const Octet<T> (&oct)[StoreCfg<D>::kSte
         }
         unsigned char *r = mine + row * R::kBytes;
         if (!kIsV) {
-            uint32_t w = 0;  // nibble i holds channel 2 i, nibble i + 4 channel 2 i + 1
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w |= ((code >> (4 * i)) & (15u << (4 * i))) | ((code << (12 - 4 * i)) & (15u << (16 + 4 * i)));
-            reinterpret_cast<uint32_t *>(r)[(g / R::kSet * 4 + col) * R::kSet + g % R::kSet] = w;
+            reinterpret_cast<uint32_t *>(r)[(g / R::kSet * 4 + col) * R::kSet + g % R::kSet] = evens_first(code);
         } else {
-            // halves 2 col and 2 col + 1: byte `col` of the four lanes' codes, lane m's as nibble m
-            uint32_t keep = 0;
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint32_t b = __shfl_sync(0xffffffffu, code, (lane & ~3) | m) >> (8 * col);
-                keep |= ((b & 15u) << (4 * m)) | ((b & 0xf0u) << (12 + 4 * m));
-            }
+            // halves 2 col and 2 col + 1: byte `col` of the four lanes' codes, lane m's as nibble m.
+            // A transpose of 4 x 4 bytes over the four lanes: with lane col ^ 2 the halves that hold
+            // the other's bytes, then with col ^ 1 single bytes.
+            const uint32_t far = __shfl_xor_sync(0xffffffffu, __byte_perm(code, 0, (col & 2) ? 0x3210 : 0x1032), 2);
+            const uint32_t two = __byte_perm(code, far, (col & 2) ? 0x3254 : 0x5410);
+            const uint32_t near = __shfl_xor_sync(0xffffffffu, two, 1);
+            const uint32_t keep = evens_first(__byte_perm(two, near, (col & 1) ? 0x3715 : 0x6240));
             uint16_t *h = reinterpret_cast<uint16_t *>(r + R::kV) + (g / R::kSet * 8 + 2 * col) * R::kSet + g % R::kSet;
             h[0] = (uint16_t)keep;
             h[R::kSet] = (uint16_t)(keep >> 16);
