@@ -256,133 +256,135 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgsOf<kBlocks> a) {
     // a deferred merge kernel may be set up now; it waits for this grid before reading
     if (a.defer_merge) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if constexpr (kBlocks) if (warp == C::kWarps) {
-        // ------------------------------------------------------------ producer over chosen
-        // blocks: the stream's walk as below, by the whole warp, which holds 32 entries of the
-        // unit's list at a time (lane i: the list's place base + i - 1); lane 0 issues.  A tile
-        // is kWarps groups of 16 rows, group after group of the listed blocks.
-        int tg = 0, kq = 0;
-        bool ok = true;
-        if (has_work && *start_b >= 0) {
-            int b = *start_b;
-            long long pb = *start_p, pos = r0;
-            const int per_block = a.block_size / 16;
-            while (pos < r1 && ok && b < a.batch) {
-                const SeqKeys sk = seq_keys(a, b);
-                const int nt = seq_tiles<T>(a, sk);
-                const long long w = (long long)nt * HU;
-                if (pos >= pb + w) {
-                    pb += w;
-                    ++b;
-                    continue;
-                }
-                const int idx = (int)((pos - pb) / nt);
-                const int hk = idx / HB, hb = idx % HB;
-                const long long ustart = pb + (long long)idx * nt;
-                const int t0 = (int)(pos - ustart), t1 = (int)min((long long)nt, r1 - ustart);
-                const long long first_cta = ustart / per_cta, last_cta = (ustart + nt - 1) / per_cta;
-                const int slots = min(a.n_sel, (sk.n + a.block_size - 1) / a.block_size);
-                const int32_t *list = a.blocks + ((int64_t)b * a.n_kv_heads + hk) * a.n_sel;
-                int base = t0 * C::kWarps / per_block;
-                int held = base + lane >= 1 && base + lane - 1 < slots ? list[base + lane - 1] : -1;
-                const int qs = kq & 1;
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait_bounded(&q_empty[qs], ((kq >> 1) & 1) ^ 1, abort_flag, deadline));
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[qs], C::kQBytes);
-                    for (int c = 0; c < C::kCols64; ++c)
-                        tma_load_3d(sQ + qs * C::kQBytes + c * kHeadsPerBlock * 128, &a.tm_q, &q_full[qs], c * 64,
-                                    hk * G + hb * kHeadsPerBlock, b);
-                }
-                for (int t = t0; t < t1; ++t) {
-                    int row0[C::kWarps];
-                    uint32_t rows = 0;
-                    int boxes = 0;
-#pragma unroll
-                    for (int g = 0; g < C::kWarps; ++g) {
-                        const int at = t * C::kWarps + g, slot = at / per_block;
-                        if (slot - base > 30 && slot < slots) {  // the next entries of the list
-                            base = slot;
-                            held = base + lane >= 1 && base + lane - 1 < slots ? list[base + lane - 1] : -1;
-                        }
-                        const int place = slot < slots ? slot - base + 1 : 1;
-                        const int blk = slot < slots ? __shfl_sync(0xffffffffu, held, place) : -1;
-                        const int before = __shfl_sync(0xffffffffu, held, place - 1);
-                        // an entry lies below the blocks there are and above the one before it,
-                        // which is no padding; -1 is padding
-                        const bool fits = blk >= 0 && blk < (sk.n + a.block_size - 1) / a.block_size &&
-                                          (slot == 0 || (before >= 0 && before < blk));
-                        if (!fits && blk != -1 && lane == 0) report_status(a.status, kErrBounds);
-                        row0[g] = fits ? blk * a.block_size + 16 * (at % per_block) : 0;
-                        const int n = fits ? max(0, min(16, sk.n - row0[g])) : 0;
-                        rows |= (uint32_t)n << (8 * g);
-                        boxes += n > 0;
+    if constexpr (kBlocks) {
+        if (warp == C::kWarps) {
+            // ------------------------------------------------------------ producer over chosen
+            // blocks: the stream's walk as below, by the whole warp, which holds 32 entries of the
+            // unit's list at a time (lane i: the list's place base + i - 1); lane 0 issues.  A tile
+            // is kWarps groups of 16 rows, group after group of the listed blocks.
+            int tg = 0, kq = 0;
+            bool ok = true;
+            if (has_work && *start_b >= 0) {
+                int b = *start_b;
+                long long pb = *start_p, pos = r0;
+                const int per_block = a.block_size / 16;
+                while (pos < r1 && ok && b < a.batch) {
+                    const SeqKeys sk = seq_keys(a, b);
+                    const int nt = seq_tiles<T>(a, sk);
+                    const long long w = (long long)nt * HU;
+                    if (pos >= pb + w) {
+                        pb += w;
+                        ++b;
+                        continue;
                     }
-                    const int s = tg % C::kStages;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((tg / C::kStages) & 1) ^ 1,
-                                                                   abort_flag, deadline));
+                    const int idx = (int)((pos - pb) / nt);
+                    const int hk = idx / HB, hb = idx % HB;
+                    const long long ustart = pb + (long long)idx * nt;
+                    const int t0 = (int)(pos - ustart), t1 = (int)min((long long)nt, r1 - ustart);
+                    const long long first_cta = ustart / per_cta, last_cta = (ustart + nt - 1) / per_cta;
+                    const int slots = min(a.n_sel, (sk.n + a.block_size - 1) / a.block_size);
+                    const int32_t *list = a.blocks + ((int64_t)b * a.n_kv_heads + hk) * a.n_sel;
+                    int base = t0 * C::kWarps / per_block;
+                    int held = base + lane >= 1 && base + lane - 1 < slots ? list[base + lane - 1] : -1;
+                    const int qs = kq & 1;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait_bounded(&q_empty[qs], ((kq >> 1) & 1) ^ 1, abort_flag, deadline));
                     if (!ok) break;
                     if (lane == 0) {
-                        StageRec r;
-                        r.b = b; r.hk = hk; r.hb = hb; r.key0 = 0; r.ke = 0;
-                        r.first = t == t0; r.last = t == t1 - 1;
-                        r.kq = kq; r.slot = (int)(blockIdx.x - first_cta);
-                        r.nseg = (int)(last_cta - first_cta + 1); r.end = 0; r.rows = rows;
-                        rec[s] = r;
-                        unsigned char *dk = sRing + s * C::kStageBytes;
-                        unsigned char *dv = dk + C::kTileBytes;
-                        // a tile within one block, all of it there, comes as a whole
-                        const bool whole = a.chunked && a.block_size % T == 0 &&
-                                           rows == (C::kWarps == 4 ? 0x10101010u : 0x00001010u);
-                        if (whole) {
-                            mbar_arrive_expect_tx(&full[s], C::kStageBytes);
-                            tma_load_5d(dk, &a.tm_k, &full[s], 0, row0[0], 0, hk, b);
-                            tma_load_5d(dv, &a.tm_v, &full[s], 0, row0[0], 0, hk, b);
-                        } else if (boxes == 0) {
-                            mbar_arrive(&full[s]);
-                        } else {
-                            mbar_arrive_expect_tx(&full[s], 2 * C::kCols64 * boxes * 16 * 128);
-#pragma unroll
-                            for (int g = 0; g < C::kWarps; ++g)
-                                if ((rows >> (8 * g)) & 0xff)
-                                    for (int c = 0; c < C::kCols64; ++c) {
-                                        const uint32_t off = c * C::kTile * 128 + g * 16 * 128;
-                                        tma_load_4d(dk + off, &a.tm_k16, &full[s], c * 64, hk, row0[g], b);
-                                        tma_load_4d(dv + off, &a.tm_v16, &full[s], c * 64, hk, row0[g], b);
-                                    }
+                        mbar_arrive_expect_tx(&q_full[qs], C::kQBytes);
+                        for (int c = 0; c < C::kCols64; ++c)
+                            tma_load_3d(sQ + qs * C::kQBytes + c * kHeadsPerBlock * 128, &a.tm_q, &q_full[qs], c * 64,
+                                        hk * G + hb * kHeadsPerBlock, b);
+                    }
+                    for (int t = t0; t < t1; ++t) {
+                        int row0[C::kWarps];
+                        uint32_t rows = 0;
+                        int boxes = 0;
+    #pragma unroll
+                        for (int g = 0; g < C::kWarps; ++g) {
+                            const int at = t * C::kWarps + g, slot = at / per_block;
+                            if (slot - base > 30 && slot < slots) {  // the next entries of the list
+                                base = slot;
+                                held = base + lane >= 1 && base + lane - 1 < slots ? list[base + lane - 1] : -1;
+                            }
+                            const int place = slot < slots ? slot - base + 1 : 1;
+                            const int blk = slot < slots ? __shfl_sync(0xffffffffu, held, place) : -1;
+                            const int before = __shfl_sync(0xffffffffu, held, place - 1);
+                            // an entry lies below the blocks there are and above the one before it,
+                            // which is no padding; -1 is padding
+                            const bool fits = blk >= 0 && blk < (sk.n + a.block_size - 1) / a.block_size &&
+                                              (slot == 0 || (before >= 0 && before < blk));
+                            if (!fits && blk != -1 && lane == 0) report_status(a.status, kErrBounds);
+                            row0[g] = fits ? blk * a.block_size + 16 * (at % per_block) : 0;
+                            const int n = fits ? max(0, min(16, sk.n - row0[g])) : 0;
+                            rows |= (uint32_t)n << (8 * g);
+                            boxes += n > 0;
                         }
+                        const int s = tg % C::kStages;
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((tg / C::kStages) & 1) ^ 1,
+                                                                       abort_flag, deadline));
+                        if (!ok) break;
+                        if (lane == 0) {
+                            StageRec r;
+                            r.b = b; r.hk = hk; r.hb = hb; r.key0 = 0; r.ke = 0;
+                            r.first = t == t0; r.last = t == t1 - 1;
+                            r.kq = kq; r.slot = (int)(blockIdx.x - first_cta);
+                            r.nseg = (int)(last_cta - first_cta + 1); r.end = 0; r.rows = rows;
+                            rec[s] = r;
+                            unsigned char *dk = sRing + s * C::kStageBytes;
+                            unsigned char *dv = dk + C::kTileBytes;
+                            // a tile within one block, all of it there, comes as a whole
+                            const bool whole = a.chunked && a.block_size % T == 0 &&
+                                               rows == (C::kWarps == 4 ? 0x10101010u : 0x00001010u);
+                            if (whole) {
+                                mbar_arrive_expect_tx(&full[s], C::kStageBytes);
+                                tma_load_5d(dk, &a.tm_k, &full[s], 0, row0[0], 0, hk, b);
+                                tma_load_5d(dv, &a.tm_v, &full[s], 0, row0[0], 0, hk, b);
+                            } else if (boxes == 0) {
+                                mbar_arrive(&full[s]);
+                            } else {
+                                mbar_arrive_expect_tx(&full[s], 2 * C::kCols64 * boxes * 16 * 128);
+    #pragma unroll
+                                for (int g = 0; g < C::kWarps; ++g)
+                                    if ((rows >> (8 * g)) & 0xff)
+                                        for (int c = 0; c < C::kCols64; ++c) {
+                                            const uint32_t off = c * C::kTile * 128 + g * 16 * 128;
+                                            tma_load_4d(dk + off, &a.tm_k16, &full[s], c * 64, hk, row0[g], b);
+                                            tma_load_4d(dv + off, &a.tm_v16, &full[s], c * 64, hk, row0[g], b);
+                                        }
+                            }
+                        }
+                        ++tg;
+                    }
+                    ++kq;
+                    pos = ustart + t1;
+                }
+            }
+            if (ok) {
+                const int s = tg % C::kStages;
+                if (__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((tg / C::kStages) & 1) ^ 1, abort_flag,
+                                                              deadline))) {
+                    if (lane == 0) {
+                        rec[s].end = 1;
+                        mbar_arrive(&full[s]);
                     }
                     ++tg;
                 }
-                ++kq;
-                pos = ustart + t1;
             }
-        }
-        if (ok) {
-            const int s = tg % C::kStages;
-            if (__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((tg / C::kStages) & 1) ^ 1, abort_flag,
-                                                          deadline))) {
-                if (lane == 0) {
-                    rec[s].end = 1;
-                    mbar_arrive(&full[s]);
+            if (lane == 0) {  // drain, as below
+                const uint64_t drain_deadline = globaltimer_ns() + 100000000ull;
+                volatile int no_abort = 0;
+                for (int s = 0; s < min(C::kStages, tg); ++s) {
+                    const int last = s + (tg - 1 - s) / C::kStages * C::kStages;
+                    mbar_wait_bounded(&full[s], (last / C::kStages) & 1, &no_abort, drain_deadline);
                 }
-                ++tg;
+                for (int i = 0; i < min(2, kq); ++i) {
+                    const int last = i + (kq - 1 - i) / 2 * 2;
+                    mbar_wait_bounded(&q_full[i], (last >> 1) & 1, &no_abort, drain_deadline);
+                }
             }
+            __syncwarp();
         }
-        if (lane == 0) {  // drain, as below
-            const uint64_t drain_deadline = globaltimer_ns() + 100000000ull;
-            volatile int no_abort = 0;
-            for (int s = 0; s < min(C::kStages, tg); ++s) {
-                const int last = s + (tg - 1 - s) / C::kStages * C::kStages;
-                mbar_wait_bounded(&full[s], (last / C::kStages) & 1, &no_abort, drain_deadline);
-            }
-            for (int i = 0; i < min(2, kq); ++i) {
-                const int last = i + (kq - 1 - i) / 2 * 2;
-                mbar_wait_bounded(&q_full[i], (last >> 1) & 1, &no_abort, drain_deadline);
-            }
-        }
-        __syncwarp();
     }
     if (!kBlocks && warp == C::kWarps) {
         // ------------------------------------------------------------ producer
@@ -709,7 +711,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgsOf<kBlocks> a) {
                     f[w] = fast_exp2(ml[g] - mu);
                     l += ml[kHeadsPerBlock + g] * f[w];
                 }
-                const float rl = l == 0.f ? 0.f : 1.f / l;  // 0: a piece whose blocks held no key
+                const float rl = kBlocks && l == 0.f ? 0.f : 1.f / l;  // 0: a piece whose blocks held no key
                 // element (g, x+k) sits in register j = 4*(x/16) + (g&1) + 2*((x/8)&1) of
                 // lane 4k + g/2 (the m16n8 accumulator layout with keys' D in M)
                 const int j = 4 * (x >> 4) + (g & 1) + 2 * ((x >> 3) & 1);

@@ -308,8 +308,8 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     constexpr int TK = C::kTileKeys;
 
     // ---- the stream's length in tiles and this CTA's share: per-thread sums over a slice of
-    // the sequences, then a scan --------------------------------------------------------
-        const int per_thread = (a.batch + C::kThreads - 1) / C::kThreads;
+    // the sequences, then a scan ----------------------------------------------------------
+    const int per_thread = (a.batch + C::kThreads - 1) / C::kThreads;
     const int b_lo = min(a.batch, tid * per_thread), b_hi = min(a.batch, b_lo + per_thread);
     uint32_t my_sum = 0;
     for (int b = b_lo; b < b_hi; ++b) {
@@ -786,7 +786,8 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
 #pragma unroll
             for (int w = 0; w < C::kWarps; ++w)
                 l = fmaf(sM[w * 2 * kHeads + kHeads + 2 * c + e], fast_exp2(sM[w * 2 * kHeads + 2 * c + e] - base), l);
-            f[e] = fast_exp2(m_ref[e] - base) / l;  // a piece holds a key: l > 0
+            // (a piece whose scores are all below the least float has weight zero, not 0 / 0)
+            f[e] = l == 0.f ? 0.f : fast_exp2(m_ref[e] - base) / l;
             if (warp == 0 && r == 0 && 2 * c + e < g_cnt) {
                 const int64_t bh = (int64_t)p.b * a.n_heads + h_base + 2 * c + e;
                 const float lse2 = M + log2f(l);
@@ -884,19 +885,19 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) mn = fmaxf(mn, l[i]);  // finite: pieces hold keys
-                const float cf = fast_exp2(m - mn);
+                for (int i = 0; i < kAhead; ++i) mn = fmaxf(mn, l[i]);
+                const float base = mn == -INFINITY ? 0.f : mn, cf = fast_exp2(m - base);
                 z *= cf; o.x *= cf; o.y *= cf; o.z *= cf; o.w *= cf;
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
-                    const float e = fast_exp2(l[i] - mn);
+                    const float e = fast_exp2(l[i] - base);
                     z += e;
                     o.x = fmaf(e, w[i].x, o.x); o.y = fmaf(e, w[i].y, o.y);
                     o.z = fmaf(e, w[i].z, o.z); o.w = fmaf(e, w[i].w, o.w);
                 }
                 m = mn;
             }
-            const float rz = 1.f / z;
+            const float rz = z == 0.f ? 0.f : 1.f / z;
             T *dst = static_cast<T *>(a.out) + (int64_t)j.b * a.out_rs + (int64_t)h * D + d;
             if constexpr (F32)
                 *reinterpret_cast<float4 *>(dst) = make_float4(o.x * rz, o.y * rz, o.z * rz, o.w * rz);

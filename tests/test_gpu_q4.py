@@ -340,6 +340,25 @@ def test_nan_in_a_visible_row_and_in_the_query():
     assert bad[1].all() and bad[2, 0].all() and not bad[2, 1].any()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cap", [300, 9000])
+def test_scores_below_the_least_float_weigh_nothing(dt, cap):
+    """Whole pieces of a sequence whose scores leave fp32's range on the low side."""
+    B, Hq, Hkv, D = 3, 4, 1, 128
+    k, v = rows(B, cap, Hkv, D, dt, 1, "k"), rows(B, cap, Hkv, D, dt, 1, "v")
+    k[0, :cap - 40] = -3e38
+    k[1, 40:] = -3e38
+    k[2, 100:cap - 100] = -3e38
+    q = W.normal((B, Hq * D), dtype=dt, device="cuda", seed=2, role="q").abs()  # sums of 128 terms near -3e38
+    c = Cache(B, cap, Hkv, D)
+    c.append(k, v, [0] * B, cap, dt=dt)
+    lens = [cap] * B
+    out, lse, st = decode(c, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), dt, Hq)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check_decode(out, lse, q, held(k), held(v), lens, dt, Hq, D, 0, 0.0, "low scores")
+
+
 def test_lengths_out_of_range_leave_their_rows_alone():
     B, Hq, Hkv, D, cap = 4, 4, 2, 128, 64
     lens = [64, 65, -1, 10]
