@@ -1016,7 +1016,9 @@ lat_status lat_attn_decode_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
         cache_rs <= 0 || cache_head_stride <= 0 || cache_seq_stride <= 0 || cache_rs % 4 || cache_head_stride % 4 ||
         cache_seq_stride % 4)
         return LAT_ERR_INVALID_ARG;
-    if (batch > 65535) return LAT_ERR_UNSUPPORTED;
+    // (a grid has one CTA per sequence, head and up to 128 channels at most, or six per SM)
+    if (batch > 65535 || (int64_t)batch * n_heads * ((head_dim + 127) / 128) > 0x7fffffffLL)
+        return LAT_ERR_UNSUPPORTED;
     const size_t need = lat_attn_decode_blocks_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim, block_size, n_sel);
     if (need == 0) return LAT_ERR_CUDA;
     if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

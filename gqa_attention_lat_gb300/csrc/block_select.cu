@@ -622,59 +622,59 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
                     if (ahead < need) atomicOr(&sh.in[at / 32], 1u << (at % 32));
                 }
             } else {
-            // many: the border among their ordered keys by halving, kept beside the scores
-            uint64_t *exact = a.exact + (int64_t)unit * a.max_blocks;
-            for (int w = warp; w < words; w += kPickWarps)
-                for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) {
-                    const int i = w * 32 + __ffs(m) - 1;
-                    const double s = exact_score<T>(a, b, hk, i);
-                    if (lane == 0) exact[i] = order64(s);
-                }
-            __syncthreads();
-            uint64_t lo = 0, hi = ~0ull;  // the need-th largest lies in [lo, hi]
-            int at_lo = cand;
-            while (lo < hi && at_lo != need) {
-                const uint64_t mid = lo + (hi - lo) / 2 + 1;
-                int cnt = 0;
-                for (int w = tid; w < words; w += kPickThreads)
-                    for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) cnt += exact[w * 32 + __ffs(m) - 1] >= mid;
-                cnt = block_sum(sh, cnt);
-                if (cnt >= need) lo = mid, at_lo = cnt;
-                else hi = mid - 1;
-            }
-            // above lo: in.  At lo: all when they are exactly as many, else the lowest first.
-            int over = 0;
-            for (int w = tid; w < words; w += kPickThreads) {
-                uint32_t in = 0, eq = 0;
-                for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) {
-                    const int bit = __ffs(m) - 1;
-                    const uint64_t x = exact[w * 32 + bit];
-                    if (x > lo || (x == lo && at_lo == need)) in |= 1u << bit;
-                    else if (x == lo) eq |= 1u << bit;
-                    over += x > lo || (x == lo && at_lo == need);
-                }
-                sh.in[w] |= in;
-                sh.tie[w] = eq;
-            }
-            const int left = need - block_sum(sh, over);
-            if (left > 0 && at_lo != need && warp == 0) {
-                int got = 0;
-                for (int w0 = 0; w0 < words && got < left; w0 += 32) {
-                    const uint32_t eq = w0 + lane < words ? sh.tie[w0 + lane] : 0u;
-                    int before = __popc(eq);
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const int v = __shfl_up_sync(0xffffffffu, before, off);
-                        if (lane >= off) before += v;
+                // many: the border among their ordered keys by halving, kept beside the scores
+                uint64_t *exact = a.exact + (int64_t)unit * a.max_blocks;
+                for (int w = warp; w < words; w += kPickWarps)
+                    for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) {
+                        const int i = w * 32 + __ffs(m) - 1;
+                        const double s = exact_score<T>(a, b, hk, i);
+                        if (lane == 0) exact[i] = order64(s);
                     }
-                    const int all = __shfl_sync(0xffffffffu, before, 31);
-                    int room = max(0, min(__popc(eq), left - got - (before - __popc(eq))));
-                    uint32_t m = eq, take = 0;
-                    for (; room > 0; --room, m &= m - 1) take |= m & (0u - m);
-                    if (w0 + lane < words) sh.in[w0 + lane] |= take;
-                    got += all;
+                __syncthreads();
+                uint64_t lo = 0, hi = ~0ull;  // the need-th largest lies in [lo, hi]
+                int at_lo = cand;
+                while (lo < hi && at_lo != need) {
+                    const uint64_t mid = lo + (hi - lo) / 2 + 1;
+                    int cnt = 0;
+                    for (int w = tid; w < words; w += kPickThreads)
+                        for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) cnt += exact[w * 32 + __ffs(m) - 1] >= mid;
+                    cnt = block_sum(sh, cnt);
+                    if (cnt >= need) lo = mid, at_lo = cnt;
+                    else hi = mid - 1;
                 }
-            }
+                // above lo: in.  At lo: all when they are exactly as many, else the lowest first.
+                int over = 0;
+                for (int w = tid; w < words; w += kPickThreads) {
+                    uint32_t in = 0, eq = 0;
+                    for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) {
+                        const int bit = __ffs(m) - 1;
+                        const uint64_t x = exact[w * 32 + bit];
+                        if (x > lo || (x == lo && at_lo == need)) in |= 1u << bit;
+                        else if (x == lo) eq |= 1u << bit;
+                        over += x > lo || (x == lo && at_lo == need);
+                    }
+                    sh.in[w] |= in;
+                    sh.tie[w] = eq;
+                }
+                const int left = need - block_sum(sh, over);
+                if (left > 0 && at_lo != need && warp == 0) {
+                    int got = 0;
+                    for (int w0 = 0; w0 < words && got < left; w0 += 32) {
+                        const uint32_t eq = w0 + lane < words ? sh.tie[w0 + lane] : 0u;
+                        int before = __popc(eq);
+    #pragma unroll
+                        for (int off = 1; off < 32; off <<= 1) {
+                            const int v = __shfl_up_sync(0xffffffffu, before, off);
+                            if (lane >= off) before += v;
+                        }
+                        const int all = __shfl_sync(0xffffffffu, before, 31);
+                        int room = max(0, min(__popc(eq), left - got - (before - __popc(eq))));
+                        uint32_t m = eq, take = 0;
+                        for (; room > 0; --room, m &= m - 1) take |= m & (0u - m);
+                        if (w0 + lane < words) sh.in[w0 + lane] |= take;
+                        got += all;
+                    }
+                }
             }
         }
         __syncthreads();

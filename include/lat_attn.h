@@ -467,7 +467,8 @@ lat_status lat_attn_select_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
  * q, the caches, kv_lens, max_kv_len, out, lse and softcap as in lat_attn_decode_softcap, its
  * alignment rules for LAT_BF16; for LAT_F32, q, out and the caches 16-byte aligned and all
  * strides multiples of 4.  n_sel >= 1, else LAT_ERR_INVALID_ARG; n_sel <= 65536, batch <=
- * 65535 and the size limits of lat_attn_decode, else LAT_ERR_UNSUPPORTED.
+ * 65535 and the size limits of lat_attn_decode (for LAT_F32 batch * n_heads * ceil(head_dim /
+ * 128) < 2^31), else LAT_ERR_UNSUPPORTED.
  * workspace: at least lat_attn_decode_blocks_workspace_size(...) bytes for the same sizes and
  * dt, 256-byte aligned, else LAT_ERR_WORKSPACE.  For LAT_BF16 the rules of lat_attn_decode's
  * workspace hold (zero-filled before its first use, and again after LAT_ERR_TIMEOUT); for

@@ -99,3 +99,8 @@ def test_decode_of_nothing_is_a_no_op():
     for dt in (binding.LAT_BF16, binding.LAT_F32):
         binding.lat_attn_decode_blocks(**dict(DECODE, dt=dt, batch=0, q=None, blocks=None))
     refused(binding.lat_attn_decode_blocks, DECODE, dict(dt=5), INVALID)
+
+
+def test_an_fp32_decode_of_too_many_heads_is_refused():
+    refused(binding.lat_attn_decode_blocks, DECODE,
+            dict(dt=binding.LAT_F32, batch=65535, n_heads=32768, q_rs=1 << 24, out_rs=1 << 24, head_dim=512), UNSUPPORTED)
