@@ -383,15 +383,16 @@ __device__ __forceinline__ uint64_t order64(double x) {
 
 constexpr int kBins = kPickThreads;  // of one pass over the keys
 constexpr int kFew = 512;            // candidates ranked in shared memory
+constexpr int kBand = 8;             // of a bin that are scored exactly rather than binned again
 
 struct PickShared {
     uint32_t in[kPickWords];   // chosen blocks, a bit each
     uint32_t tie[kPickWords];  // those near the border, then those equal to the last chosen one
     int red[kPickWarps];
-    uint32_t red2[2][kPickWarps];
+    uint32_t red2[3][kPickWarps];
     int bins[kBins];
     int found, found_above, found_in;
-    int few;
+    int few, sure;
     int at[kFew];
     uint64_t key[kFew];
 };
@@ -401,19 +402,24 @@ __device__ __forceinline__ int block_sum(PickShared &sh, int x) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh.red[threadIdx.x >> 5] = x;
     __syncthreads();
-    int t = 0;
-#pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) t += sh.red[w];
-    return t;
+    const int lane = threadIdx.x & 31;
+    return __reduce_add_sync(0xffffffffu, lane < kPickWarps ? sh.red[lane] : 0);
 }
-__device__ __forceinline__ void block_minmax(PickShared &sh, uint32_t &mn, uint32_t &mx) {
+// the least mn, and the largest mx and my
+__device__ __forceinline__ void block_ends(PickShared &sh, uint32_t &mn, uint32_t &mx, uint32_t &my) {
     mn = __reduce_min_sync(0xffffffffu, mn);
     mx = __reduce_max_sync(0xffffffffu, mx);
+    my = __reduce_max_sync(0xffffffffu, my);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.red2[0][threadIdx.x >> 5] = mn, sh.red2[1][threadIdx.x >> 5] = mx;
+    if ((threadIdx.x & 31) == 0) {
+        const int w = threadIdx.x >> 5;
+        sh.red2[0][w] = mn, sh.red2[1][w] = mx, sh.red2[2][w] = my;
+    }
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kPickWarps; ++w) mn = min(mn, sh.red2[0][w]), mx = max(mx, sh.red2[1][w]);
+    const int w = threadIdx.x % kPickWarps;
+    mn = __reduce_min_sync(0xffffffffu, sh.red2[0][w]);
+    mx = __reduce_max_sync(0xffffffffu, sh.red2[1][w]);
+    my = __reduce_max_sync(0xffffffffu, sh.red2[2][w]);
 }
 
 // s + e = x + y exactly (Knuth's two-sum); the intrinsics keep the compiler from fusing
@@ -423,16 +429,17 @@ __device__ __forceinline__ float two_sum(float x, float y, float &e) {
     return s;
 }
 
-// The block's score, to 2^-45 of its terms' magnitude or better, by a whole warp.  Products split
-// by a fused multiply-add and sums by two-sum, each an unevaluated pair of floats: 48 bits on the
-// fp32 pipes.  (fp64 runs at a 64th of their rate here: it cost 13 us a step, this 1.)  Where
-// the pair could overflow or lose small products, fp64 it is.
+// The block's score as a whole number in the scores' order, by a whole warp.  Products split by a
+// fused multiply-add and sums by two-sum, each an unevaluated pair of floats: 48 bits on the fp32
+// pipes, 2^-45 of the terms' magnitude or better.  `fits` is cleared where the pair could overflow
+// or lose small products; wide_score below is for those.  (fp64 runs at a 64th of fp32's rate
+// here: scores in fp64 cost 13 us a step, only the pairs' last sums and comparisons in it 4.)
 template <typename T>
-__device__ double exact_score(const SelectArgs &a, int b, int hk, int n) {
+__device__ uint64_t pair_score(const SelectArgs &a, int b, int hk, int n, bool &fits) {
     const int G = a.n_heads / a.n_kv_heads, D = a.head_dim, lane = threadIdx.x & 31;
     const T *q = static_cast<const T *>(a.q) + (int64_t)b * a.q_rs + (int64_t)hk * G * D;
     const T *x = static_cast<const T *>(a.bounds) + (int64_t)b * a.bounds_seq + (int64_t)hk * a.bounds_head + (int64_t)n * a.bounds_rs;
-    double best = -INFINITY;
+    uint64_t best = 0;
     for (int h0 = 0; h0 < G; h0 += 4) {
         float s[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
         float top = 0.f;
@@ -460,34 +467,43 @@ __device__ double exact_score(const SelectArgs &a, int b, int hk, int n) {
             }
             top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
         }
-        double v[4];
+        if (!(top > 0x1p-60f && top < 0x1p100f)) fits = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (double)s[i] + (double)c[i];
-        if (!(top > 0x1p-60f && top < 0x1p100f)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = 0.0;
-            for (int d = lane; d < D; d += 32) {
-                const float hi = (float)x[d], lo = (float)x[D + d];
-                for (int i = 0; i < 4 && h0 + i < G; ++i) {
-                    const float w = (float)q[(h0 + i) * D + d];
-                    v[i] = fma((double)w, (double)(w < 0.f ? lo : hi), v[i]);
-                }
-            }
-            for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+        for (int i = 0; i < 4; ++i) {  // the nearest float and the rest: the pairs' order is the sums'
+            float l;
+            const float h = two_sum(s[i], c[i], l);
+            const uint64_t key = (uint64_t)order32(h) << 32 | order32(l);
+            if (h0 + i < G && key > best) best = key;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (h0 + i < G) best = v[i] != v[i] || best != best ? (double)NAN : fmax(best, v[i]);
+    }
+    return best;
+}
+template <typename T>
+__device__ __noinline__ uint64_t wide_score(const SelectArgs &a, int b, int hk, int n) {
+    const int G = a.n_heads / a.n_kv_heads, D = a.head_dim, lane = threadIdx.x & 31;
+    const T *q = static_cast<const T *>(a.q) + (int64_t)b * a.q_rs + (int64_t)hk * G * D;
+    const T *x = static_cast<const T *>(a.bounds) + (int64_t)b * a.bounds_seq + (int64_t)hk * a.bounds_head + (int64_t)n * a.bounds_rs;
+    uint64_t best = 0;
+    for (int h = 0; h < G; ++h) {
+        double v = 0.0;
+        for (int d = lane; d < D; d += 32) {
+            const float w = (float)q[h * D + d];
+            v = fma((double)w, (double)(float)x[w < 0.f ? D + d : d], v);
+        }
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        const uint64_t key = order64(v);
+        best = key > best ? key : best;
     }
     return best;
 }
 
 // One CTA per (sequence, KV head).  The k-th largest score is found by counting the ordered keys
-// into 512 equal bins of the range that still holds it, two or three times (the scores of one
-// query lie within a few binades, so they spread over the bins); it ends as soon as exactly k
-// keys lie from some bin on.
+// into 512 equal bins of the range that still holds it (the scores of one query lie within a few
+// binades, so they spread over the bins).  It ends as soon as exactly k keys lie from some bin on,
+// or few share the bin: those are scored exactly, as a near border needs anyway.  Measured on 64
+// of up to 2048 blocks, 64 KV heads, score pass included: bins down to one key and sums ended in
+// fp64 19.7 us, in float pairs 19.0, the few of a bin scored 17.7, the warps' results joined by
+// one reduction instead of a loop 17.2.  What is left is barriers and first passes through code.
 template <typename T>
 __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectArgs a) {
     extern __shared__ uint32_t keys[];  // [have - n_first - n_last] where they fit, else unused
@@ -510,6 +526,7 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
     const int c0 = a.n_first, c1 = have - a.n_last, n = c1 - c0;  // the free choice
     const int k = a.n_sel - a.n_first - a.n_last;                 // how many of it; n > k
     const bool held = n <= a.keys_held;
+    if (tid == 0) sh.few = sh.sure = 0;
     float e_max = 0.f;
     uint32_t top = 0, low = 0xffffffffu;
     for (int i = tid; i < n; i += kPickThreads) {
@@ -521,12 +538,13 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
         e_max = s.y <= 3e38f ? fmaxf(e_max, s.y) : INFINITY;
     }
     uint32_t eu = __float_as_uint(e_max), unused = 0;
-    block_minmax(sh, unused, eu);
-    block_minmax(sh, low, top);
+    block_ends(sh, low, top, eu);
     e_max = __uint_as_float(eu);
     auto key_at = [&](int i) { return held ? keys[i] : order32(__ldcg(scores + c0 + i).x); };
-    // kth: the k-th largest key; next: the (k + 1)-th
+    // kth: the k-th largest key; next: the (k + 1)-th.  Where they share a bin with few others
+    // (band): the bin's first and last key, which hold the k-th largest between them
     uint32_t kth = 0, next = 0;
+    bool band = false;
     if (k > 0) {
         uint32_t lo = low;   // count(>= lo) is at_lo >= k; the k-th largest lies in the `width` keys from lo on
         int at_lo = n, above_all = 0;  // keys above that range
@@ -549,35 +567,38 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
             }
             if (lane == 0) sh.red[warp] = from;
             __syncthreads();
-            int base = above_all;
-#pragma unroll
-            for (int w = 0; w < kPickWarps; ++w) base += w > warp ? sh.red[w] : 0;
-            from += base;
+            from += above_all + __reduce_add_sync(0xffffffffu, lane > warp && lane < kPickWarps ? sh.red[lane] : 0);
             if (from >= k && from - mine < k) sh.found = tid, sh.found_above = from - mine, sh.found_in = from;
             __syncthreads();
             lo += (uint32_t)sh.found << shift;
             above_all = sh.found_above;
             at_lo = sh.found_in;
             last = min(last - ((uint32_t)sh.found << shift), (1u << shift) - 1u);
+            if (at_lo != k && at_lo - above_all <= kBand) {
+                kth = lo, next = lo + last, band = true;
+                break;
+            }
         }
-        uint32_t above = 0xffffffffu, below = 0;
-        for (int i = tid; i < n; i += kPickThreads) {
-            const uint32_t key = key_at(i);
-            if (key >= lo) above = min(above, key);
-            else below = max(below, key);
+        if (!band) {
+            uint32_t above = 0xffffffffu, below = 0;
+            for (int i = tid; i < n; i += kPickThreads) {
+                const uint32_t key = key_at(i);
+                if (key >= lo) above = min(above, key);
+                else below = max(below, key);
+            }
+            block_ends(sh, above, below, unused);
+            kth = above;
+            next = at_lo == k ? below : kth;  // more than k from lo on: they are equal to it
         }
-        block_minmax(sh, above, below);
-        kth = above;
-        next = at_lo == k ? below : kth;  // more than k from lo on: they are equal to it
     }
     // sure of its place: further than both errors from the other side of the border
     const float f_kth = value32(kth), f_next = value32(next);
     const float in_above = f_next + 2.f * e_max, out_below = f_kth - 2.f * e_max;
-    const bool clear = k == 0 || (next < kth && in_above < f_kth);
-    int sure = 0, cand = 0;
+    const bool clear = k == 0 || (!band && next < kth && in_above < f_kth);
+    int sures = 0;  // (of the warp)
     for (int w0 = warp; w0 * 32 < have; w0 += kPickWarps) {  // one word of 32 blocks
         const int i = w0 * 32 + lane, j = i - c0;
-        bool in = i < have && (j < 0 || i >= c1), maybe = false;
+        bool in = i < have && (j < 0 || i >= c1), sure = false, maybe = false;
         if (!in && i < have && k > 0) {
             const uint32_t key = key_at(j);
             if (clear) {
@@ -585,35 +606,44 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
             } else {
                 const float f = value32(key);
                 const bool nan = key == 0xffffffffu;
-                in = !nan && f > in_above && key > next;
+                in = sure = !nan && f > in_above && key > next;
                 maybe = !in && (nan || !(f < out_below));
-                sure += in;
-                cand += maybe;
             }
         }
-        const uint32_t bits = __ballot_sync(0xffffffffu, in), may = __ballot_sync(0xffffffffu, maybe);
-        if (lane == 0) sh.in[w0] = bits, sh.tie[w0] = may;
+        const uint32_t bits = __ballot_sync(0xffffffffu, in);
+        if (lane == 0) sh.in[w0] = bits;
+        if (!clear) {
+            sures += __popc(__ballot_sync(0xffffffffu, sure));
+            const uint32_t may = __ballot_sync(0xffffffffu, maybe);
+            if (lane == 0) sh.tie[w0] = may;
+            if (maybe) {  // the first of them also as a list
+                const int at = atomicAdd(&sh.few, 1);
+                if (at < kFew) sh.at[at] = i;
+            }
+        }
     }
+    if (lane == 0 && sures > 0) atomicAdd(&sh.sure, sures);
     __syncthreads();
     const int words = (have + 31) / 32;
     if (!clear) {
-        const int need = k - block_sum(sh, sure);
-        cand = block_sum(sh, cand);
+        const int need = k - sh.sure, cand = sh.few;
         if (need >= cand) {  // all of them (need is cand: no more than k are above the border)
             for (int w = tid; w < words; w += kPickThreads) sh.in[w] |= sh.tie[w], sh.tie[w] = 0;
         } else {
             // exact scores of the candidates.  A few (the usual case): each counts those ahead of it
             if (cand <= kFew) {
-                if (tid == 0) sh.few = 0;
-                __syncthreads();
-                for (int w = tid; w < words; w += kPickThreads)
-                    for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) sh.at[atomicAdd(&sh.few, 1)] = w * 32 + __ffs(m) - 1;
-                __syncthreads();
+                bool fits = true;
                 for (int i = warp; i < cand; i += kPickWarps) {
-                    const double s = exact_score<T>(a, b, hk, sh.at[i]);
-                    if (lane == 0) sh.key[i] = order64(s);
+                    const uint64_t s = pair_score<T>(a, b, hk, sh.at[i], fits);
+                    if (lane == 0) sh.key[i] = s;
                 }
-                __syncthreads();
+                if (__syncthreads_or(!fits)) {
+                    for (int i = warp; i < cand; i += kPickWarps) {
+                        const uint64_t s = wide_score<T>(a, b, hk, sh.at[i]);
+                        if (lane == 0) sh.key[i] = s;
+                    }
+                    __syncthreads();
+                }
                 if (tid < cand) {
                     const uint64_t mine = sh.key[tid];
                     const int at = sh.at[tid];
@@ -624,13 +654,22 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
             } else {
                 // many: the border among their ordered keys by halving, kept beside the scores
                 uint64_t *exact = a.exact + (int64_t)unit * a.max_blocks;
+                bool fits = true;
                 for (int w = warp; w < words; w += kPickWarps)
                     for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) {
                         const int i = w * 32 + __ffs(m) - 1;
-                        const double s = exact_score<T>(a, b, hk, i);
-                        if (lane == 0) exact[i] = order64(s);
+                        const uint64_t s = pair_score<T>(a, b, hk, i, fits);
+                        if (lane == 0) exact[i] = s;
                     }
-                __syncthreads();
+                if (__syncthreads_or(!fits)) {
+                    for (int w = warp; w < words; w += kPickWarps)
+                        for (uint32_t m = sh.tie[w]; m != 0; m &= m - 1) {
+                            const int i = w * 32 + __ffs(m) - 1;
+                            const uint64_t s = wide_score<T>(a, b, hk, i);
+                            if (lane == 0) exact[i] = s;
+                        }
+                    __syncthreads();
+                }
                 uint64_t lo = 0, hi = ~0ull;  // the need-th largest lies in [lo, hi]
                 int at_lo = cand;
                 while (lo < hi && at_lo != need) {

@@ -207,6 +207,31 @@ def test_select_between_equal_and_nearly_equal_scores(dt):
     assert got[0, 0].tolist() == list(range(n_sel - 3)) + [nb - 3, nb - 2, nb - 1]
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("nb", [300, 2000])
+@pytest.mark.parametrize("q_mul,k_mul", [(2.0 ** 60, 2.0 ** 50), (2.0 ** -40, 2.0 ** -30)])
+def test_select_between_near_scores_far_from_one(dt, nb, q_mul, k_mul):
+    """The same at the ends of the range, where a pair of floats cannot hold the sums: every sum
+    of these products is exact in fp64 (terms of 8 bits from 2^-30 to 2^3 of the scale)."""
+    D, n_sel, block = 128, 40, 16
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(D, generator=g).bfloat16().float()
+    x[-1] = 0.0
+    r = torch.empty(1, nb, 1, 2 * D)
+    for n in range(nb):
+        y = x[torch.cat([torch.randperm(D - 1, generator=g), torch.tensor([D - 1])])]
+        r[0, n, 0, :D], r[0, n, 0, D:] = y, y
+    for n in (nb - 1, 150, 31):
+        r[0, n, 0, D - 1] = r[0, n, 0, 2 * D - 1] = 2.0 ** -30
+    r[0, 7, 0, D - 1] = r[0, 7, 0, 2 * D - 1] = -2.0 ** -30
+    q = torch.full((2, D), q_mul, dtype=W.torch_dtype(dt), device="cuda")
+    q[1] = 1.0  # and a sequence whose scores lie elsewhere
+    rr = (r * k_mul).to(W.torch_dtype(dt)).cuda().expand(2, -1, -1, -1).contiguous()
+    got, st = select(q, rr, [nb * block] * 2, block, 1, 1, D, dt, n_sel, 0, 0)
+    want = sorted([31, 150, nb - 1] + [n for n in range(nb) if n not in (7, 31, 150, nb - 1)][:n_sel - 3])
+    assert got[0, 0].tolist() == want and got[1, 0].tolist() == want and int(st.item()) == 0
+
+
 @pytest.mark.parametrize("dt,nb,n_sel", [("bf16", 2000, 700), ("f32", 2000, 1), ("bf16", 9000, 4000)])
 def test_select_among_many_equal_scores(dt, nb, n_sel):
     """Thousands of exact ties: the lowest, beside one block ahead and one behind."""
