@@ -132,20 +132,21 @@ __device__ __forceinline__ KeyRange range_of(const Q4DecodeArgs &a, int len) {
     return k;
 }
 
+// The stream of `total` tiles in equal shares: the first `more` CTAs have each + 1, the others each
+struct Shares {
+    uint32_t each, more;
+    __device__ __forceinline__ uint32_t begin(uint32_t c) const { return each * c + min(c, more); }
+    __device__ __forceinline__ uint32_t of(uint32_t x) const {  // whose tile x is
+        const uint32_t b = more * (each + 1);
+        return x < b ? x / (each + 1) : more + (x - b) / each;
+    }
+};
 // thread 0's place in the stream
 struct Walk {
     uint32_t pos, end, pb;  // pb: where sequence b's units begin
-    uint32_t total, parts;  // the stream and how many CTAs share it
+    Shares shares;
     int b;
 };
-// CTA c takes tiles [total c / parts, total (c + 1) / parts); tile x is CTA ((x + 1) parts - 1) / total's
-__device__ __forceinline__ uint32_t share_begin(uint32_t c, uint32_t total, uint32_t parts) {
-    return (uint32_t)((uint64_t)total * c / parts);
-}
-__device__ __forceinline__ uint32_t share_of(uint32_t x, uint32_t total, uint32_t parts) {
-    const uint64_t n = (uint64_t)(x + 1) * parts - 1;
-    return n >> 32 ? (uint32_t)(n / total) : (uint32_t)n / total;
-}
 
 // a unit of n keys in the stream: nothing, or its tiles and what it costs beside them
 template <int T>
@@ -164,13 +165,15 @@ __device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
             continue;
         }
         const uint32_t idx = (w.pos - w.pb) / cost, ustart = w.pb + idx * cost + kUnitCost;  // its first tile
+        const uint32_t uend = ustart + nt;
         const uint32_t t0 = w.pos > ustart ? w.pos - ustart : 0, t1 = w.end > ustart ? min(nt, w.end - ustart) : 0;
-        w.pos = min(w.end, ustart + nt);
+        const bool cut = w.pos > ustart;  // (divisions only for units that leave this share)
+        w.pos = min(w.end, uend);
         if (t0 >= t1) continue;  // the share ends before the unit's first tile
-        const uint32_t first = share_of(ustart, w.total, w.parts), last = share_of(ustart + nt - 1, w.total, w.parts);
+        const uint32_t first = cut ? w.shares.of(ustart) : blockIdx.x, last = uend > w.end ? w.shares.of(uend - 1) : blockIdx.x;
         p.b = w.b;
-        p.hk = (int)(idx / HB);
-        p.hb = (int)(idx % HB);
+        p.hk = HB == 1 ? (int)idx : (int)(idx / HB);
+        p.hb = HB == 1 ? 0 : (int)(idx % HB);
         p.key0 = k.lo + (int)t0 * T;
         p.keys = (int)(min((uint32_t)k.n, t1 * T) - t0 * T);
         p.slot = (int)(blockIdx.x - first);
@@ -340,6 +343,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         walk->b = a.batch;
         for (int i = 0; i < C::kWarps * C::kStages; ++i) mbar_init(&full[i], 1);
         *abort_flag = 0;
+        joins[0].nseg = joins[1].nseg = joins[0].last = joins[1].last = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&a.tm);
     }
@@ -351,10 +355,10 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         if (w < warp) my_start += v;
         total += v;
     }
-    const uint32_t parts = max(1u, min(gridDim.x, total / (uint32_t)a.min_tiles));
-    const bool shares = blockIdx.x < parts;
-    const uint32_t r0 = shares ? share_begin(blockIdx.x, total, parts) : 0;
-    const uint32_t r1 = shares ? share_begin(blockIdx.x + 1, total, parts) : 0;
+    const uint32_t parts = max(1u, min(gridDim.x, total / (uint32_t)a.min_tiles)), each = total / parts;
+    const Shares shares{each, total - each * parts};
+    const uint32_t r0 = blockIdx.x < parts ? shares.begin(blockIdx.x) : 0;
+    const uint32_t r1 = blockIdx.x < parts ? shares.begin(blockIdx.x + 1) : 0;
     if (r0 < r1 && r0 >= my_start && r0 - my_start < my_sum) {  // the share begins in this slice
         uint32_t p = my_start;
         int b = b_lo;
@@ -363,9 +367,8 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             if (r0 < p + w) break;
             p += w;
         }
-        Walk w{r0, r1, p, total, parts, b};
-        for (int i = 0; i < kPieceRing / 4; ++i)
-            if (!next_piece<TK>(a, w, HB, pieces[i])) break;
+        Walk w{r0, r1, p, shares, b};
+        next_piece<TK>(a, w, HB, pieces[0]);
         *walk = w;
     }
     if (a.defer_join) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -400,7 +403,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         ++issued;
         next += TK;
     };
-    int known = kPieceRing / 4;  // table entries written (or behind an end mark)
+    int known = 1;               // table entries written (or behind an end mark)
     int n_joins = 0;             // (thread 0)
     // A unit's queries come a unit ahead: asked for after the copies of its rows, they would wait
     // behind them (2.5 us where they take 1).
@@ -419,8 +422,25 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     };
     fetch_queries(0, known);
     for (int s = 0; s < C::kStages; ++s) issue(known);
+    auto one_more = [&]() {  // another entry for the table, by thread 0
+        if (tid == 0 && !pieces[(known - 1) % kPieceRing].end) {
+            Walk w = *walk;
+            next_piece<TK>(a, w, HB, pieces[known % kPieceRing]);
+            *walk = w;
+        }
+    };
+    one_more();
     cp_async_wait<0>();
     __syncthreads();
+    if (!pieces[0].end) ++known;
+    auto issue_all = [&]() {  // what had to wait for the table
+        while (issued - used < (unsigned)C::kStages) {
+            const unsigned before = issued;
+            issue(known);
+            if (issued == before) break;
+        }
+    };
+    issue_all();
 
     const int r = lane >> 2, c = lane & 3;
     // MMA row r is the tile's key perm(r): the two low bits swapped, so that the eight lanes of
@@ -562,11 +582,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         }
         fetch_queries(pi + 1, known);
         // one more piece for the table, while the first tile is on its way
-        if (tid == 0 && !pieces[(known - 1) % kPieceRing].end) {
-            Walk w = *walk;
-            next_piece<TK>(a, w, HB, pieces[known % kPieceRing]);
-            *walk = w;
-        }
+        one_more();
         float m_ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
         float acc[C::kMt][4];
 #pragma unroll
@@ -835,11 +851,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         if (tid == 0 && !single && n_joins < 2)  // at most a CTA's first and last piece
             joins[n_joins++] = Join{p.b, h_base, g_cnt, p.nseg, (p.b * a.n_kv_heads + p.hk) * HB + p.hb, 0};
         if (!pieces[(known - 1) % kPieceRing].end) ++known;
-        while (issued - used < (unsigned)C::kStages) {  // copies that had to wait for the table
-            const unsigned before = issued;
-            issue(known);
-            if (issued == before) break;
-        }
+        issue_all();
     }
     // every copy lands before the CTA leaves
     if (lane == 0) {
@@ -855,13 +867,8 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     if (*abort_flag) return;
     // (each thread's partials happen before the barrier, that before the ticket's release; a last
     // ticket's acquire before the next barrier, that before the reads, which skip L1)
-    if (tid == 0) {
-        int t0 = -1, t1 = -1;
-        if (n_joins > 0) t0 = add_acq_rel(a.counters + joins[0].unit, 1);
-        if (n_joins > 1) t1 = add_acq_rel(a.counters + joins[1].unit, 1);
-        joins[0].last = n_joins > 0 && t0 == joins[0].nseg - 1;
-        joins[1].last = n_joins > 1 && t1 == joins[1].nseg - 1;
-    }
+    if (lane == 0 && warp < 2 && joins[warp].nseg > 0)  // a ticket a warp: they take a round trip each
+        joins[warp].last = add_acq_rel(a.counters + joins[warp].unit, 1) == joins[warp].nseg - 1;
     __syncthreads();
     for (int k = 0; k < 2; ++k) {
         const Join j = joins[k];
