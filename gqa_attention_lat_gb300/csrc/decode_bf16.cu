@@ -45,6 +45,7 @@
 #include "cache_kernels.h"
 #include "device_common.cuh"
 #include "kernels.h"
+#include "score_cap.cuh"
 
 namespace lat {
 
@@ -597,7 +598,9 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgsOf<kBlocks> a) {
             if (a.cap_log2 > 0.f) {
                 const float k2 = a.raw_over_cap * kTwoLog2e;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[e] = capped_score_log2(sc[e], k2, a.cap_log2);
+                for (int e = 0; e < 4; ++e)
+                    sc[e] = kBlocks ? capped_score_close(sc[e] * a.raw_over_cap, a.cap_log2)
+                                    : capped_score_log2(sc[e], k2, a.cap_log2);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[e] *= a.scale_log2;
@@ -637,8 +640,15 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgsOf<kBlocks> a) {
                 }
             }
             // P^T fragments: transpose the two 8x8 (key x head) quadrants
-            const uint32_t pb0 = movmatrix_trans(pack_bf16x2(p[0], p[1]));
-            const uint32_t pb1 = movmatrix_trans(pack_bf16x2(p[2], p[3]));
+            const uint32_t ph0 = pack_bf16x2(p[0], p[1]), ph1 = pack_bf16x2(p[2], p[3]);
+            const uint32_t pb0 = movmatrix_trans(ph0), pb1 = movmatrix_trans(ph1);
+            // Over chosen blocks what the rounding to bf16 left out goes through a second product:
+            // tiles wait for their copies, not for the tensor cores, so it costs nothing there.
+            uint32_t pl0 = 0, pl1 = 0;
+            if constexpr (kBlocks) {
+                pl0 = movmatrix_trans(pack_bf16x2(p[0] - __uint_as_float(ph0 << 16), p[1] - __uint_as_float(ph0 & 0xffff0000u)));
+                pl1 = movmatrix_trans(pack_bf16x2(p[2] - __uint_as_float(ph1 << 16), p[3] - __uint_as_float(ph1 & 0xffff0000u)));
+            }
             // O^T += V^T . P^T
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -646,6 +656,7 @@ decode_bf16_kernel(const __grid_constant__ DecodeArgsOf<kBlocks> a) {
                 const int rr = row0 + (lane & 7) + 8 * (lane >> 4);
                 const int c = 2 * i + ((lane >> 3) & 1);
                 ldmatrix_x4_trans(vf, tv + tile_off(rr, c, C::kTile));
+                if constexpr (kBlocks) mma_bf16_16816(acc[i], vf, pl0, pl1);
                 mma_bf16_16816(acc[i], vf, pb0, pb1);
             }
             // zeroed rows (generic writes) must precede the stage's next copy

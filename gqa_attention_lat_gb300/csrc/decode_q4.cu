@@ -48,6 +48,7 @@
 #include "cache_kernels.h"
 #include "device_common.cuh"
 #include "q4_row.cuh"
+#include "score_cap.cuh"
 #include "split_join.cuh"
 
 namespace lat {
@@ -681,7 +682,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         sc[u][e] = F32 ? a.cap_log2 * tanhf(sc[u][e] * a.over_cap_log2)
-                                       : capped_score_log2(sc[u][e], a.over_cap_log2 * kTwoLog2e, a.cap_log2);
+                                       : capped_score_close(sc[u][e] * a.over_cap_log2, a.cap_log2);
             }
             if (valid < C::kKeys) {
 #pragma unroll
@@ -928,8 +929,8 @@ cudaError_t launch_q4_d(const Q4DecodeArgs &a, int grid, cudaStream_t s) {
 }
 
 // Keys per CTA, were all units as long as they may be, from which the wide form is taken.  At 3449
-// 32 ragged sequences took 30.6 us wide and 28.9 narrow, 8 equally long ones 39.4 and 41.0; at 6898
-// 45.3 and 45.2, 68.3 and 71.9; at 13797 77.0 and 78.5, 124 and 131.
+// 32 ragged sequences take 28.9 us wide and 27.2 narrow, 8 equally long ones 39.4
+// and 41.0; at 6898 44.7 and 44.7, 68.3 and 71.9; at 13797 77.0 and 78.5, 124 and 131.
 constexpr int64_t kWideKeys = 6144;
 
 template <int D, bool F32, bool Wide>
