@@ -373,7 +373,7 @@ def test_lengths_out_of_range_leave_their_rows_alone():
 
 
 def test_a_long_cache_past_32_bit_offsets():
-    """Eight sequences whose bytes lie past 2^32; one is checked at its far end."""
+    """Two sequences of 2.2e9 bytes, written and read at their far ends."""
     B, Hq, Hkv, D, cap = 2, 8, 1, 512, 3_500_000  # 640 bytes a row: 2.2e9 bytes a sequence
     c = Cache(B, cap, Hkv, D)
     n, at = 300, cap - 300
