@@ -843,6 +843,7 @@ lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const v
     a.defer_join = plan.defer_join;
     a.max_splits = plan.max_splits;
     a.min_tiles = plan.min_tiles;
+    a.whole = plan.whole;
     a.timeout_ns = kDefaultTimeoutNs;
     a.status = status;
     return lat::launch_decode_q4(a, dt == LAT_BF16, plan, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess

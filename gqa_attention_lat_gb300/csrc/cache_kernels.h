@@ -83,12 +83,12 @@ struct Q4DecodeArgs {
     float *part_lse;       // [batch, n_heads, max_splits], log2 domain
     int32_t *piece_count;  // defer_join: [batch, n_heads]
     int32_t *counters;     // else: tickets [batch, n_kv_heads, blocks of heads], zero between calls
-    int max_splits, min_tiles, defer_join;
+    int max_splits, min_tiles, defer_join, whole;
     uint64_t timeout_ns;
     int32_t *status;
 };
 struct Q4Plan {
-    int grid, wide, min_tiles, max_splits, box_rows, defer_join;
+    int grid, wide, whole, min_tiles, max_splits, box_rows, defer_join;
     size_t part_o_bytes, part_lse_bytes, total_bytes;
 };
 bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,
