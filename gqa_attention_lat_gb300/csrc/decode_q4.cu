@@ -354,7 +354,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         *abort_flag = 0;
         joins[0].nseg = joins[1].nseg = joins[0].last = joins[1].last = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&a.tm);
+        if (a.max_kv_len > 0) tma_prefetch_desc(&a.tm);  // (else there is none)
     }
     __syncthreads();
     uint32_t total = 0, my_start = incl - my_sum;

@@ -495,3 +495,18 @@ def test_steps_together(dt):
                     assert np.array_equal(r[:, :D], hi) and np.array_equal(r[:, D:], lo)
             check_select(lists, qs, bd, [n] * B, block, Hq, H, D, n_sel, 1, 2)
             check_decode(out, lse, qs, k, v, [n] * B, block, lists.cpu().numpy(), Hq, D, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_nothing_cached_anywhere(dt):
+    """max_kv_len 0, and caches of every length 0: empty lists, zeros and -inf."""
+    B, Hq, H, D, cap, block, n_sel = 3, 4, 2, 64, 32, 16, 2
+    k = W.normal((B, cap, H, D), dtype=dt, device="cuda", seed=1, role="k")
+    bd = W.normal((B, cap // block, H, 2 * D), dtype=dt, device="cuda", seed=1, role="v")
+    q = W.normal((B, Hq * D), dtype=dt, device="cuda", seed=1, role="q")
+    for mk in (0, cap):
+        got, st = select(q, bd, [0] * B, block, Hq, H, D, dt, n_sel, 1, 1, max_len=mk)
+        out, lse, st2 = decode(q, k, k, [0] * B, block, got, Hq, D, dt, max_len=mk)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and int(st2.item()) == 0 and (got == -1).all()
+        assert (out == 0).all() and torch.isneginf(lse).all()

@@ -465,3 +465,16 @@ def test_two_streams_with_a_workspace_each():
             assert int(st.item()) == 0
             assert torch.equal(out, got[i][0][0]) and torch.equal(lse, got[i][0][1])  # no order of joins shows
         check_decode(got[i][0][0], got[i][0][1], qs[i], kh, vh, lens, "bf16", Hq, D, 0, 0.0, "stream %d" % i)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_nothing_cached_anywhere(dt):
+    """max_kv_len 0, and caches of every length 0: zeros and -inf, no read of the cache."""
+    B, Hq, Hkv, D, cap = 3, 4, 2, 64, 16
+    c = Cache(B, cap, Hkv, D)
+    q = W.normal((B, Hq * D), dtype=dt, device="cuda", seed=1, role="q")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for mk in (0, cap):
+        out, lse, st = decode(c, q, lens, dt, Hq, max_len=mk)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and (out == 0).all() and torch.isneginf(lse).all()
