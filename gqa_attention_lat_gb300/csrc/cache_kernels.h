@@ -88,7 +88,7 @@ struct Q4DecodeArgs {
     int32_t *status;
 };
 struct Q4Plan {
-    int grid, wide, whole, min_tiles, max_splits, box_rows, defer_join;
+    int grid, wide, twin, whole, min_tiles, max_splits, box_rows, defer_join;
     size_t part_o_bytes, part_lse_bytes, total_bytes;
 };
 bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,

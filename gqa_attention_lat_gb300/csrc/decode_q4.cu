@@ -5,8 +5,8 @@
 //   x_j = scale * sum_g s_jg sum_{d in g} q_d (c_jd - z_jg)      (then capped, if asked for)
 //   out = sum_j e^{x_j - m} v_j / sum_j e^{x_j - m}
 // The scale never meets the codes: a group's products are summed by the tensor cores and
-// scaled once per key, and V's scales multiply the softmax weights, p_j s_jg, before their
-// one rounding to bf16.
+// scaled once per key, and V's scales multiply the softmax weights, p_j s_jg, before
+// two bf16 terms are made of them.
 //
 // How:
 //  * Work unit = one (sequence, KV head, block of <= 8 query heads).  All units' keys, laid
@@ -32,10 +32,12 @@
 //    exact, smaller ones are within 2^-29 of it.
 //  * O^T[16 channels x 8 heads] += V^T (P s)^T on mma m16n8k16 in bf16 (a weight needs bf16's
 //    range): a nibble becomes 128 + c by an AND-OR (0x4300 is bf16 128, whose last place is 1),
-//    minus 128 + z, exactly.  The rows' layout puts a lane's codes side by side.  A weight has
-//    one bf16 term, whose rounding is as large as the bf16 output's own (2.2e-3 off in all where
-//    the output's alone is 1.6e-3); a second term takes that away and costs 281 instead of
-//    235 us on 8 x 131072 keys.
+//    minus 128 + z, exactly.  The rows' layout puts a lane's codes side by side.  A weight is
+//    two bf16 terms (16 bits): with one, its rounding was as large as the bf16 output's own
+//    (2.2e-3 off in all where the output's alone is 1.6e-3).  Units of up to 4 heads (Twin) have
+//    their heads twice in N, columns 0-3 with the first terms and 4-7 with the second, and add the
+//    two halves up at a piece's end; others take a second MMA (8 x 131072 keys, 4 heads a KV
+//    head: one term 234 us, twice in N 249, two MMAs 274; 8 heads a KV head: 275).
 //  * LAT_F32: the query is two fp16 terms (22 bits and their signs, 2^-24 of a channel), the
 //    codes lose their zero point before the product, and the weights p s are three bf16 terms.
 //  * Waits are bounded; on expiry the CTA records LAT_ERR_TIMEOUT, drains its copies, quits.
@@ -59,6 +61,7 @@ namespace lat {
 namespace {
 
 constexpr int kHeads = 8;                  // N of the mma: query heads of a unit
+constexpr int kTwinHeads = 4;              // heads of a unit that fill N twice
 constexpr float kRescaleBy = 8.0f;         // log2 units the maximum may grow unnoticed
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kPieceRing = 8;              // pieces known ahead
@@ -68,17 +71,17 @@ constexpr int kPieceRing = 8;              // pieces known ahead
 constexpr int kUnitCost = 2;
 
 // The more keys a warp takes at once, the further a tile's fixed costs spread, until its registers
-// cost CTAs (8 x 131072 keys, 16 times kSub keys: head_dim 64 2 153 us, 4 134; 80 2 215, 3 190,
-// 4 197; 256 2 463, 3 660).  At head_dim 128 that comes with tiles too coarse for short units, so
-// there are two forms; kWideKeys says when.  (fp32 queries there: 392 us either way.)
+// cost CTAs (8 x 131072 keys, 16 times kSub keys: head_dim 64 2 163 us, 3 152, 4 143; 80 2 209,
+// 3 198, 4 200; 256 2 479, 3 876).  At head_dim 128 that comes with tiles too coarse for short
+// units, so there are two forms; kWideKeys says when.  (fp32 queries there gain nothing.)
 template <int D, bool F32>
 constexpr bool kHasWide = D == 128 && !F32;
-template <int D, bool F32, bool Wide>
+template <int D, bool F32, bool Wide, bool Twin>
 struct Q4Cfg {
     using R = Q4Row<D>;
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTerms = F32 ? 3 : 1;               // bf16 terms of p s
+    static constexpr int kTerms = F32 ? 3 : Twin ? 1 : 2;    // bf16 terms of p s in MMAs of their own
     static constexpr int kQTerms = F32 ? 2 : 1;              // fp16 terms of q
     static constexpr float kUnit = F32 ? 0x1p-24f : 0x1p-20f;  // of the scores' products
     static constexpr int kQTo = F32 ? 12 : 8;                // its largest channel's exponent
@@ -281,23 +284,33 @@ __device__ __forceinline__ int add_acq_rel(int32_t *p, int x) {
     return was;
 }
 
+// x and y plus `by` (a bf16) times the halves of a bf16 pair, without unpacking it (the logic
+// pipe's work)
+__device__ __forceinline__ void add_pair(float &x, float &y, uint32_t pair, uint16_t by) {
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\n"
+        "fma.rn.f32.bf16 %0, l, %3, %0;\nfma.rn.f32.bf16 %1, h, %3, %1;\n}"
+        : "+f"(x), "+f"(y) : "r"(pair), "h"(by));
+}
+constexpr uint16_t kMinusOne = 0xbf80u;  // in bf16
 // two floats as `TERMS` packed bf16 pairs whose sum is the pair (to 8 bits a term)
 template <int TERMS>
 __device__ __forceinline__ void split2(uint32_t (&o)[TERMS], float x, float y) {
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
         o[t] = pack_bf16x2(x, y);
-        if (t + 1 < TERMS) {
-            x -= __uint_as_float(o[t] << 16);
-            y -= __uint_as_float(o[t] & 0xffff0000u);
-        }
+        if (t + 1 < TERMS) add_pair(x, y, o[t], kMinusOne);
     }
 }
+// the first term of both (by 0) or the second (by -1)
+__device__ __forceinline__ uint32_t term2(float x, float y, uint16_t by) {
+    add_pair(x, y, pack_bf16x2(x, y), by);
+    return pack_bf16x2(x, y);
+}
 
-template <int D, bool F32, bool Wide>
-__global__ void __launch_bounds__(Q4Cfg<D, F32, Wide>::kThreads, Q4Cfg<D, F32, Wide>::kMinBlocks)
+template <int D, bool F32, bool Wide, bool Twin>
+__global__ void __launch_bounds__(Q4Cfg<D, F32, Wide, Twin>::kThreads, Q4Cfg<D, F32, Wide, Twin>::kMinBlocks)
 decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
-    using C = Q4Cfg<D, F32, Wide>;
+    using C = Q4Cfg<D, F32, Wide, Twin>;
     using R = Q4Row<D>;
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
     constexpr int kTerms = C::kTerms, kQTerms = C::kQTerms, kSet = R::kSet, kSets = R::kGroups / R::kSet;
@@ -457,6 +470,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     const int kr = (r & 4) | ((r & 1) << 1) | ((r >> 1) & 1);
     const int kp = ((c & 2) << 1) | (c & 1);  // perm(2 c); perm(2 c + 1) is kp + 2
     const int sw_r = kr << 4, sw_0 = kp << 4, sw_1 = (kp + 2) << 4;  // those rows' swizzles
+    const uint16_t twin_by = c < 2 ? 0 : kMinusOne;                 // Twin: the term of this lane's columns
 
     for (int pi = 0;; ++pi) {
         const Piece p = pieces[pi % kPieceRing];
@@ -475,7 +489,8 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         };
         const T *qrow = q_all + (int64_t)p.b * a.q_rs + (int64_t)h_base * D;
         constexpr int kRaw = F32 ? 2 : 1;  // 16-byte words of an octet
-        auto load = [&](int head, int d, uint4 (&x)[kRaw]) {
+        auto load = [&](int column, int d, uint4 (&x)[kRaw]) {
+            const int head = Twin ? column % kTwinHeads : column;
             const uint4 *src = C::kQReg ? reinterpret_cast<const uint4 *>(sQ + (pi & 1) * C::kRawBytes + head * C::kRawRow + d * (int)sizeof(T))
                                         : reinterpret_cast<const uint4 *>(qrow + (int64_t)head * D + d);
 #pragma unroll
@@ -761,8 +776,13 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                         const int g = st * kSet + j;
                         const float fx = q4_scale(px[j]), fy = q4_scale(py[j]);
                         uint32_t w0[kTerms], w1[kTerms];
-                        split2<kTerms>(w0, sc[u][0] * fx, sc[u][1] * fx);
-                        split2<kTerms>(w1, sc[u][2] * fy, sc[u][3] * fy);
+                        if constexpr (Twin) {
+                            w0[0] = term2(sc[u][0] * fx, sc[u][1] * fx, twin_by);
+                            w1[0] = term2(sc[u][2] * fy, sc[u][3] * fy, twin_by);
+                        } else {
+                            split2<kTerms>(w0, sc[u][0] * fx, sc[u][1] * fx);
+                            split2<kTerms>(w1, sc[u][2] * fy, sc[u][3] * fy);
+                        }
                         const uint32_t b01 = __byte_perm(q0[j], q1[j], 0x7632), b23 = __byte_perm(q2[j], q3[j], 0x7632);
                         const uint32_t a0[4] = {q4_codes2(ab[j], 0, b01), q4_codes2(ab[j], 1, b01), q4_codes2(cd[j], 0, b23),
                                                 q4_codes2(cd[j], 1, b23)};
@@ -834,14 +854,16 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 }
             __syncthreads();
             constexpr int kV4 = 4 * C::kRound;  // 4-channel vectors of a head in this round
-            for (int v = tid; v < kHeads * kV4; v += C::kThreads) {
+            for (int v = tid; v < (Twin ? kTwinHeads : kHeads) * kV4; v += C::kThreads) {
                 const int h = v / kV4, x = 4 * (v % kV4), d = 16 * i0 + x;
                 if (h >= g_cnt || d >= D) continue;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < C::kWarps; ++w) {
-                    const float4 t = *reinterpret_cast<const float4 *>(park + (w * kHeads + h) * C::kParkPitch + x);
-                    o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
+                    for (int col = h; col < (Twin ? kHeads : h + 1); col += kTwinHeads) {
+                        const float4 t = *reinterpret_cast<const float4 *>(park + (w * kHeads + col) * C::kParkPitch + x);
+                        o.x += t.x; o.y += t.y; o.z += t.z; o.w += t.w;
+                    }
                 }
                 if (single) {
                     T *dst = static_cast<T *>(a.out) + (int64_t)p.b * a.out_rs + (int64_t)(h_base + h) * D + d;
@@ -925,66 +947,69 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     }
 }
 
-template <int D, bool F32, bool Wide>
+template <int D, bool F32, bool Wide, bool Twin>
 cudaError_t launch_q4_d(const Q4DecodeArgs &a, int grid, cudaStream_t s) {
-    using C = Q4Cfg<D, F32, Wide>;
-    cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, F32, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    using C = Q4Cfg<D, F32, Wide, Twin>;
+    cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D, F32, Wide, Twin>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    decode_q4_kernel<D, F32, Wide><<<grid, C::kThreads, C::kSmem, s>>>(a);
+    decode_q4_kernel<D, F32, Wide, Twin><<<grid, C::kThreads, C::kSmem, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess || !a.defer_join) return e;
     const JoinArgs j{a.part_o, a.part_lse, a.piece_count, a.max_splits, a.n_heads, a.out, a.out_rs, a.lse};
     return launch_split_join<D, F32>(j, (int64_t)a.batch * a.n_heads, s);
 }
 
 // Keys per CTA, were all units as long as they may be, from which the wide form is taken.  At 3449
-// 32 ragged sequences take 28.9 us wide and 27.2 narrow, 8 equally long ones 39.4
-// and 41.0; at 6898 44.7 and 44.7, 68.3 and 71.9; at 13797 77.0 and 78.5, 124 and 131.
+// 32 ragged sequences take 30.7 us wide and 28.6 narrow, 8 equally long ones 41.5 and 41.4; at
+// 6898 47.4 and 45.2, 71.0 and 73.4; at 13797 83.4 and 83.1, 131 and 136.
 constexpr int64_t kWideKeys = 6144;
 
-template <int D, bool F32, bool Wide>
+template <int D, bool F32, bool Wide, bool Twin>
 int occupancy_of() {
-    using C = Q4Cfg<D, F32, Wide>;
+    using C = Q4Cfg<D, F32, Wide, Twin>;
     static Occupancy occupancy;
-    return occupancy(decode_q4_kernel<D, F32, Wide>, C::kThreads, C::kSmem);
+    return occupancy(decode_q4_kernel<D, F32, Wide, Twin>, C::kThreads, C::kSmem);
 }
 
 // grid, wide, box_rows, and the keys of a tile, for `units` units of up to `keys` keys
-template <int D, bool F32>
+template <int D, bool F32, bool Twin>
 int shape_of(Q4Plan *p, int sms, int64_t units, int64_t keys) {
-    using C = Q4Cfg<D, F32, false>;
+    using C = Q4Cfg<D, F32, false, Twin>;
     p->wide = 0;
+    p->twin = Twin;
     if constexpr (kHasWide<D, F32>) {
-        using W = Q4Cfg<D, F32, true>;
-        p->grid = sms * occupancy_of<D, F32, true>();
+        using W = Q4Cfg<D, F32, true, Twin>;
+        p->grid = sms * occupancy_of<D, F32, true, Twin>();
         if (p->grid > 0 && units * keys / p->grid >= kWideKeys) {
             p->wide = 1;
             p->box_rows = W::kKeys;
             return W::kTileKeys;
         }
     }
-    p->grid = sms * occupancy_of<D, F32, false>();
+    p->grid = sms * occupancy_of<D, F32, false, Twin>();
     p->box_rows = C::kKeys;
     return C::kTileKeys;
 }
 
-// calls f<D, F32> for a supported head_dim and type
-#define LAT_Q4_DISPATCH(head_dim, bf16, f, other, ...)                               \
-    switch (head_dim) {                                                              \
-        case 64: return bf16 ? f<64, false>(__VA_ARGS__) : f<64, true>(__VA_ARGS__);    \
-        case 80: return bf16 ? f<80, false>(__VA_ARGS__) : f<80, true>(__VA_ARGS__);    \
-        case 128: return bf16 ? f<128, false>(__VA_ARGS__) : f<128, true>(__VA_ARGS__); \
-        case 256: return bf16 ? f<256, false>(__VA_ARGS__) : f<256, true>(__VA_ARGS__); \
-        case 512: return bf16 ? f<512, false>(__VA_ARGS__) : f<512, true>(__VA_ARGS__); \
-        default: return other;                                                       \
+// calls f<D, F32, Twin> for a supported head_dim and type (fp32 queries need their columns)
+#define LAT_Q4_CASE(D, bf16, twin, f, ...) \
+    case D: return !(bf16) ? f<D, true, false>(__VA_ARGS__) : (twin) ? f<D, false, true>(__VA_ARGS__) : f<D, false, false>(__VA_ARGS__);
+#define LAT_Q4_DISPATCH(head_dim, bf16, twin, f, other, ...) \
+    switch (head_dim) {                                      \
+        LAT_Q4_CASE(64, bf16, twin, f, __VA_ARGS__)          \
+        LAT_Q4_CASE(80, bf16, twin, f, __VA_ARGS__)          \
+        LAT_Q4_CASE(128, bf16, twin, f, __VA_ARGS__)         \
+        LAT_Q4_CASE(256, bf16, twin, f, __VA_ARGS__)         \
+        LAT_Q4_CASE(512, bf16, twin, f, __VA_ARGS__)         \
+        default: return other;                               \
     }
-int shape(int head_dim, bool bf16, Q4Plan *p, int sms, int64_t units, int64_t keys) {
-    LAT_Q4_DISPATCH(head_dim, bf16, shape_of, 0, p, sms, units, keys)
+int shape(int head_dim, bool bf16, bool twin, Q4Plan *p, int sms, int64_t units, int64_t keys) {
+    LAT_Q4_DISPATCH(head_dim, bf16, twin, shape_of, 0, p, sms, units, keys)
 }
-template <int D, bool F32>
+template <int D, bool F32, bool Twin>
 cudaError_t launch_q4(const Q4DecodeArgs &a, int grid, bool wide, cudaStream_t s) {
     if constexpr (kHasWide<D, F32>)
-        if (wide) return launch_q4_d<D, F32, true>(a, grid, s);
-    return launch_q4_d<D, F32, false>(a, grid, s);
+        if (wide) return launch_q4_d<D, F32, true, Twin>(a, grid, s);
+    return launch_q4_d<D, F32, false, Twin>(a, grid, s);
 }
 
 }  // namespace
@@ -995,7 +1020,7 @@ bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool b
     const int64_t units = (int64_t)batch * n_kv_heads * HB;
     // join grid: one CTA per (sequence, query head, up to 128 channels)
     if ((int64_t)batch * n_heads * ((head_dim + 127) / 128) > 0x7fffffffLL) return false;
-    const int tile = shape(head_dim, bf16, p, num_sms, units, max_kv_len);
+    const int tile = shape(head_dim, bf16, G <= kTwinHeads, p, num_sms, units, max_kv_len);
     if (tile == 0) return false;
     // A unit of n tiles falls into at most n / min_tiles + 2 pieces.  min_tiles keeps that count
     // near 64 or, with few units, near the number of CTAs that each unit must feed.
@@ -1004,8 +1029,8 @@ bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool b
     const int64_t target = std::max<int64_t>(64, (p->grid + std::max<int64_t>(units, 1) - 1) / std::max<int64_t>(units, 1));
     p->min_tiles = (int)std::max<int64_t>(1, (range + target - 1) / target);
     // Units of up to two tiles, no more than the CTAs: one each, and nothing to join (8 KV heads,
-    // head_dim 64: one sequence of 512 keys 7.1 instead of 7.5 us, 32 ragged ones of up to 512 8.2
-    // instead of 9.4; with three tiles it gains nothing).
+    // head_dim 64: one sequence of 512 keys 7.3 instead of 8.0 us, 32 ragged ones of up to 512 8.6
+    // instead of 10.2; with three tiles it gains nothing).
     p->whole = range <= 2 && units <= p->grid;
     if (p->whole) p->min_tiles = (int)range + kUnitCost;
     p->max_splits = (int)((range + p->min_tiles - 1) / p->min_tiles) + 2;
@@ -1022,7 +1047,7 @@ bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool b
 }
 
 cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, const Q4Plan &p, cudaStream_t s) {
-    LAT_Q4_DISPATCH(a.head_dim, bf16, launch_q4, cudaErrorInvalidValue, a, p.grid, p.wide != 0, s)
+    LAT_Q4_DISPATCH(a.head_dim, bf16, p.twin != 0, launch_q4, cudaErrorInvalidValue, a, p.grid, p.wide != 0, s)
 }
 
 }  // namespace lat
