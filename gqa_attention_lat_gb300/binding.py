@@ -87,6 +87,11 @@ _SIGNATURES = {
                                         _I32, _I32, _I32, _U64, _P, _P]),
     "lat_test_decode_timeout": (_I32, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _I64,
                                        _I32, _I32, _I32, _I32, _P, _SZ, _U64, _P, _P]),
+    "lat_test_decode_q4_timeout": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I32, _P, _I64,
+                                          _I32, _I32, _I32, _I32, _P, _SZ, _U64, _P, _P]),
+    "lat_test_decode_blocks_timeout": (_I32, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I32,
+                                              _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _SZ,
+                                              _U64, _P, _P]),
     "lat_test_capped_scores": (_I32, [_P, _I64, _F32, _F32, _P, _P]),
 }
 
@@ -355,6 +360,27 @@ def lat_test_decode_timeout(q, q_rs, k_cache, v_cache, cache_rs, cache_head_stri
         cache_seq_stride, kv_lens, max_kv_len, out, out_rs, batch, n_heads,
         n_kv_heads, head_dim, workspace, workspace_bytes, timeout_ns, status,
         _stream(stream)), "lat_test_decode_timeout")
+
+
+def lat_test_decode_q4_timeout(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride,
+                               kv_lens, max_kv_len, out, out_rs, batch, n_heads, n_kv_heads,
+                               head_dim, workspace, workspace_bytes, timeout_ns, status,
+                               stream=None):
+    _check(_calls().lat_test_decode_q4_timeout(
+        dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens, max_kv_len,
+        out, out_rs, batch, n_heads, n_kv_heads, head_dim, workspace, workspace_bytes,
+        timeout_ns, status, _stream(stream)), "lat_test_decode_q4_timeout")
+
+
+def lat_test_decode_blocks_timeout(q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,
+                                   cache_seq_stride, kv_lens, max_kv_len, block_size, blocks,
+                                   n_sel, out, out_rs, batch, n_heads, n_kv_heads, head_dim,
+                                   workspace, workspace_bytes, timeout_ns, status, stream=None):
+    _check(_calls().lat_test_decode_blocks_timeout(
+        q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,
+        max_kv_len, block_size, blocks, n_sel, out, out_rs, batch, n_heads, n_kv_heads, head_dim,
+        workspace, workspace_bytes, timeout_ns, status, _stream(stream)),
+        "lat_test_decode_blocks_timeout")
 
 
 def lat_test_capped_scores(raw, n, scale, softcap, out, stream=None):

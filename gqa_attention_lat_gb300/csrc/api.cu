@@ -754,47 +754,12 @@ lat_status q4_store_impl(lat_dtype dt, void *cache, int64_t cache_rs, int64_t ca
                : LAT_ERR_CUDA;
 }
 
-}  // namespace
-
-extern "C" {
-
-int lat_kv_q4_row_bytes(int head_dim) { return lat::q4_row_bytes(head_dim); }
-
-lat_status lat_kv_append_q4(lat_dtype dt, void *cache, int64_t cache_rs, int64_t cache_head_stride,
-                            int64_t cache_seq_stride, int capacity, const void *k_new, const void *v_new,
-                            int64_t new_rs, const int32_t *pos, int n_new, int batch, int n_kv_heads,
-                            int head_dim, int32_t *status, void *stream) {
-    return q4_store_impl(dt, cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, k_new, v_new, nullptr,
-                         nullptr, new_rs, pos, n_new, batch, n_kv_heads, head_dim, false, status, stream);
-}
-
-lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs, int64_t cache_head_stride,
-                            int64_t cache_seq_stride, int capacity, void *k_out, void *v_out, int64_t out_rs,
-                            const int32_t *pos, int n_rows, int batch, int n_kv_heads, int head_dim,
-                            int32_t *status, void *stream) {
-    return q4_store_impl(dt, const_cast<void *>(cache), cache_rs, cache_head_stride, cache_seq_stride, capacity,
-                         nullptr, nullptr, k_out, v_out, out_rs, pos, n_rows, batch, n_kv_heads, head_dim, true,
-                         status, stream);
-}
-
-size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads, int head_dim,
-                                         int max_kv_len) {
-    if ((dt != LAT_F32 && dt != LAT_BF16) || batch < 0 || batch > 65535 || n_heads <= 0 || n_kv_heads <= 0 ||
-        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || max_kv_len < 0)
-        return 0;
-    int sms = 0;
-    lat::Q4Plan plan;
-    if (!current_sm_count(&sms) ||
-        !lat::plan_decode_q4(batch, n_heads, n_kv_heads, head_dim, dt == LAT_BF16, max_kv_len, sms, &plan))
-        return 0;
-    return plan.total_bytes;
-}
-
-lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const void *cache, int64_t cache_rs,
-                              int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
-                              int max_kv_len, void *out, int64_t out_rs, float *lse, int batch, int n_heads,
-                              int n_kv_heads, int head_dim, int window, float scale, float softcap,
-                              void *workspace, size_t workspace_bytes, int32_t *status, void *stream) {
+lat_status q4_decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *cache, int64_t cache_rs,
+                          int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
+                          int max_kv_len, void *out, int64_t out_rs, float *lse, int batch, int n_heads,
+                          int n_kv_heads, int head_dim, int window, float scale, float softcap,
+                          void *workspace, size_t workspace_bytes, int32_t *status, void *stream,
+                          uint64_t timeout_ns, int skip_load) {
     if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
     if (!(softcap >= 0.f) || !isfinite(softcap) || !isfinite(scale)) return LAT_ERR_INVALID_ARG;
     if (batch < 0 || max_kv_len < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0)
@@ -844,11 +809,68 @@ lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const v
     a.max_splits = plan.max_splits;
     a.min_tiles = plan.min_tiles;
     a.whole = plan.whole;
-    a.timeout_ns = kDefaultTimeoutNs;
+    a.timeout_ns = timeout_ns;
+    a.test_skip_load = skip_load;
     a.status = status;
     return lat::launch_decode_q4(a, dt == LAT_BF16, plan, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? LAT_OK
                : LAT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lat_kv_q4_row_bytes(int head_dim) { return lat::q4_row_bytes(head_dim); }
+
+lat_status lat_kv_append_q4(lat_dtype dt, void *cache, int64_t cache_rs, int64_t cache_head_stride,
+                            int64_t cache_seq_stride, int capacity, const void *k_new, const void *v_new,
+                            int64_t new_rs, const int32_t *pos, int n_new, int batch, int n_kv_heads,
+                            int head_dim, int32_t *status, void *stream) {
+    return q4_store_impl(dt, cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, k_new, v_new, nullptr,
+                         nullptr, new_rs, pos, n_new, batch, n_kv_heads, head_dim, false, status, stream);
+}
+
+lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs, int64_t cache_head_stride,
+                            int64_t cache_seq_stride, int capacity, void *k_out, void *v_out, int64_t out_rs,
+                            const int32_t *pos, int n_rows, int batch, int n_kv_heads, int head_dim,
+                            int32_t *status, void *stream) {
+    return q4_store_impl(dt, const_cast<void *>(cache), cache_rs, cache_head_stride, cache_seq_stride, capacity,
+                         nullptr, nullptr, k_out, v_out, out_rs, pos, n_rows, batch, n_kv_heads, head_dim, true,
+                         status, stream);
+}
+
+size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                         int max_kv_len) {
+    if ((dt != LAT_F32 && dt != LAT_BF16) || batch < 0 || batch > 65535 || n_heads <= 0 || n_kv_heads <= 0 ||
+        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || max_kv_len < 0)
+        return 0;
+    int sms = 0;
+    lat::Q4Plan plan;
+    if (!current_sm_count(&sms) ||
+        !lat::plan_decode_q4(batch, n_heads, n_kv_heads, head_dim, dt == LAT_BF16, max_kv_len, sms, &plan))
+        return 0;
+    return plan.total_bytes;
+}
+
+lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const void *cache, int64_t cache_rs,
+                              int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
+                              int max_kv_len, void *out, int64_t out_rs, float *lse, int batch, int n_heads,
+                              int n_kv_heads, int head_dim, int window, float scale, float softcap,
+                              void *workspace, size_t workspace_bytes, int32_t *status, void *stream) {
+    return q4_decode_impl(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens, max_kv_len, out,
+                          out_rs, lse, batch, n_heads, n_kv_heads, head_dim, window, scale, softcap, workspace,
+                          workspace_bytes, status, stream, kDefaultTimeoutNs, 0);
+}
+
+lat_status lat_test_decode_q4_timeout(lat_dtype dt, const void *q, int64_t q_rs, const void *cache, int64_t cache_rs,
+                                      int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
+                                      int max_kv_len, void *out, int64_t out_rs, int batch, int n_heads,
+                                      int n_kv_heads, int head_dim, void *workspace, size_t workspace_bytes,
+                                      uint64_t timeout_ns, int32_t *status, void *stream) {
+    return q4_decode_impl(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens, max_kv_len, out,
+                          out_rs, nullptr, batch, n_heads, n_kv_heads, head_dim, 0, 0.125f, 0.f, workspace,
+                          workspace_bytes, status, stream, timeout_ns, 1);
 }
 
 }  // extern "C"
@@ -1058,6 +1080,20 @@ lat_status lat_attn_decode_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
     a.status = status;
     return lat::launch_decode_blocks_f32(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK
                                                                                                    : LAT_ERR_CUDA;
+}
+
+lat_status lat_test_decode_blocks_timeout(const void *q, int64_t q_rs, const void *k_cache, const void *v_cache,
+                                          int64_t cache_rs, int64_t cache_head_stride, int64_t cache_seq_stride,
+                                          const int32_t *kv_lens, int max_kv_len, int block_size,
+                                          const int32_t *blocks, int n_sel, void *out, int64_t out_rs, int batch,
+                                          int n_heads, int n_kv_heads, int head_dim, void *workspace,
+                                          size_t workspace_bytes, uint64_t timeout_ns, int32_t *status,
+                                          void *stream) {
+    if (!block_size_ok(block_size) || n_sel <= 0 || n_sel > lat::kSelectMaxBlocks || !blocks)
+        return LAT_ERR_INVALID_ARG;
+    return decode_impl(LAT_BF16, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,
+                       max_kv_len, out, out_rs, nullptr, batch, n_heads, n_kv_heads, head_dim, 0, 0.125f, 0.f, 0,
+                       workspace, workspace_bytes, status, stream, timeout_ns, 1, blocks, n_sel, block_size);
 }
 
 }  // extern "C"

@@ -85,6 +85,7 @@ struct Q4DecodeArgs {
     int32_t *counters;     // else: tickets [batch, n_kv_heads, blocks of heads], zero between calls
     int max_splits, min_tiles, defer_join, whole;
     uint64_t timeout_ns;
+    int test_skip_load;    // test hook: a warp's first copy of a CTA never comes (forces a timeout)
     int32_t *status;
 };
 struct Q4Plan {

@@ -404,8 +404,9 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     int ip = 0, next = 0, keys = 0;               // pieces taken up; next row and rows of the last one
     int from = 0, at_hk = 0, at_b = 0;            // its first key and place
     unsigned issued = 0, used = 0;                // copies issued, consumed
-    // Issues this warp's next copy, if one is known.  `limit`: pieces in the table.
-    auto issue = [&](int limit) {
+    // Issues this warp's next copy, if one is known.  `limit`: pieces in the table; `leave_out`:
+    // the copy counts as issued and never comes.
+    auto issue = [&](int limit, bool leave_out = false) {
         while (next >= keys) {
             if (ip >= limit) return;
             const Piece &p = pieces[ip % kPieceRing];
@@ -414,7 +415,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             next = warp * C::kKeys;
             keys = p.keys, from = p.key0, at_hk = p.hk, at_b = p.b;
         }
-        if (lane == 0) {
+        if (lane == 0 && !leave_out) {
             const unsigned s = issued % C::kStages;
             mbar_arrive_expect_tx(&my_full[s], C::kStageBytes);
             if constexpr (C::kSwizzle)
@@ -443,7 +444,9 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         }
     };
     fetch_queries(0, known);
-    for (int s = 0; s < C::kStages; ++s) issue(known);
+    issue(known, a.test_skip_load);
+    const bool missing = a.test_skip_load && issued > 0;  // test hook: the first copy is not there
+    for (int s = 1; s < C::kStages; ++s) issue(known);
     auto one_more = [&]() {  // another entry for the table, by thread 0
         if (tid == 0 && !pieces[(known - 1) % kPieceRing].end) {
             Walk w = *walk;
@@ -884,10 +887,12 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         if (!pieces[(known - 1) % kPieceRing].end) ++known;
         issue_all();
     }
-    // every copy lands before the CTA leaves
+    // every copy lands before the CTA leaves, a next unit's queries among them
+    cp_async_wait<0>();
     if (lane == 0) {
         volatile int no_abort = 0;
         const uint64_t until = globaltimer_ns() + 100000000ull;
+        if (missing && used == 0) ++used;
         for (; used < issued; ++used)
             mbar_wait_bounded(&my_full[used % C::kStages], (used / C::kStages) & 1, &no_abort, until);
         if (warp == 0 && *abort_flag) report_status(a.status, kErrTimeout);

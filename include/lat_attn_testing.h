@@ -18,6 +18,12 @@
  * workspace rules are those of lat_attn_decode; the output is unspecified, and the
  * workspace must be zero-filled again before its next use.
  *
+ * lat_test_decode_q4_timeout and lat_test_decode_blocks_timeout do the same to
+ * lat_attn_decode_q4 (dt its type; every warp's first copy of a CTA's share that is known when
+ * its stream begins never comes) and to the LAT_BF16 form of lat_attn_decode_blocks (the first
+ * K/V stage of every CTA is never filled): window 0, scale 1/8, no cap, no lse.  Arguments,
+ * layout and workspace rules are theirs.
+ *
  * lat_test_capped_scores evaluates the score cap of the bf16 kernels (the Gemma 2 softcap
  * of the larql "BLAS-Fused Attention" step 2, folded into the log2 domain) on n raw dot
  * products: out[i] = softcap * log2(e) * tanh(raw[i] * scale / softcap), formed exactly as
@@ -46,6 +52,21 @@ lat_status lat_test_decode_timeout(const void *q, int64_t q_rs, const void *k_ca
                                    int64_t out_rs, int batch, int n_heads, int n_kv_heads,
                                    int head_dim, void *workspace, size_t workspace_bytes,
                                    uint64_t timeout_ns, int32_t *status, void *stream);
+lat_status lat_test_decode_q4_timeout(lat_dtype dt, const void *q, int64_t q_rs,
+                                      const void *cache, int64_t cache_rs,
+                                      int64_t cache_head_stride, int64_t cache_seq_stride,
+                                      const int32_t *kv_lens, int max_kv_len, void *out,
+                                      int64_t out_rs, int batch, int n_heads, int n_kv_heads,
+                                      int head_dim, void *workspace, size_t workspace_bytes,
+                                      uint64_t timeout_ns, int32_t *status, void *stream);
+lat_status lat_test_decode_blocks_timeout(const void *q, int64_t q_rs, const void *k_cache,
+                                          const void *v_cache, int64_t cache_rs,
+                                          int64_t cache_head_stride, int64_t cache_seq_stride,
+                                          const int32_t *kv_lens, int max_kv_len, int block_size,
+                                          const int32_t *blocks, int n_sel, void *out,
+                                          int64_t out_rs, int batch, int n_heads, int n_kv_heads,
+                                          int head_dim, void *workspace, size_t workspace_bytes,
+                                          uint64_t timeout_ns, int32_t *status, void *stream);
 lat_status lat_test_capped_scores(const float *raw, int64_t n, float scale, float softcap,
                                   float *out, void *stream);
 
