@@ -2,20 +2,29 @@
 
 Argument marshalling only: every function forwards to the CUDA library under the same
 name and argument order, by way of the C extension that the build writes out from the
-signatures below (sizes and names by ctypes).  Pointer arguments accept a torch tensor (its
-data_ptr), an int address or None (NULL); ``stream`` accepts a torch.cuda.Stream, an int
-handle or None (torch's current stream when CUDA is up, else the legacy default stream).
-A non-OK status raises LatError.  There is no CPU fallback: if the library is not built, the
-first call raises.
+signatures below, or by ctypes where there is none or the library is not the one beside it
+(sizes and names always by ctypes).  Pointer arguments accept a torch tensor (its data_ptr),
+an int address or None (NULL); ``stream`` accepts a torch.cuda.Stream, an int handle or None
+(torch's current stream when CUDA is up, else the legacy default stream).  Either way a wrong
+type raises TypeError (AttributeError for a pointer), a whole number past its argument's range
+OverflowError, and a non-OK status LatError.  There is no CPU fallback: if the library is not
+built, the first call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import operator
 import os
 import sys
 import threading
+import types
 
-LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblat_attn.so")
+HERE = os.path.dirname(os.path.abspath(__file__))
+LIB_PATH = os.path.join(HERE, "liblat_attn.so")
+# (the suffix names the interpreter: an extension of another one is not taken for this one's)
+CALLER_PATH = os.path.join(HERE, "_lat_call" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 LAT_F32, LAT_BF16 = 0, 1
 STATUS_NAMES = {0: "LAT_OK", 1: "LAT_ERR_INVALID_ARG", 2: "LAT_ERR_UNSUPPORTED",
@@ -97,8 +106,9 @@ _SIGNATURES = {
 
 
 def library(path: str = LIB_PATH) -> ctypes.CDLL:
-    """The loaded CUDA library (raises if it has not been built)."""
-    global _lib
+    """The loaded CUDA library (raises if it has not been built).  The first call decides which
+    one that is, for sizes and launches alike."""
+    global _lib, _caller
     if _lib is not None:
         return _lib
     with _lock:
@@ -111,17 +121,62 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
+            # the extension is linked to the library beside it and to no other
+            ours = os.path.realpath(path) == os.path.realpath(LIB_PATH)
+            _caller = (_extension() if ours else None) or _ctypes_calls(lib)
             _lib = lib
     return _lib
 
 
+def _extension():
+    """The C extension's module; None where it was not built for this interpreter."""
+    spec = importlib.util.spec_from_file_location(__package__ + "._lat_call", CALLER_PATH)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:
+        return None
+    return module if all(hasattr(module, name) for name in _status_calls()) else None
+
+
+def _status_calls():
+    """The names of the calls that return a status (the others are not on a hot path)."""
+    return [name for name, (res, args) in _SIGNATURES.items() if res is _I32 and len(args) > 1]
+
+
+def _ptr(x):
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+_RANGES = {_I32: (-1 << 31, 1 << 31), _I64: (-1 << 63, 1 << 63), _SZ: (0, 1 << 64), _U64: (0, 1 << 64)}
+
+
+def _whole(x, t):  # (ctypes would take x modulo its argument's width)
+    x = operator.index(x)
+    lo, hi = _RANGES[t]
+    if not lo <= x < hi:
+        raise OverflowError("%d exceeds its argument" % x)
+    return x
+
+
+def _ctypes_call(name, fn, args):
+    def call(*values):
+        if len(values) != len(args):
+            raise TypeError("%s takes %d arguments, got %d" % (name, len(args), len(values)))
+        return fn(*[_ptr(v) if t is _P else _whole(v, t) if t in _RANGES else float(v)
+                    for v, t in zip(values, args)])
+    return call
+
+
+def _ctypes_calls(lib):
+    return types.SimpleNamespace(**{name: _ctypes_call(name, getattr(lib, name), _SIGNATURES[name][1])
+                                    for name in _status_calls()})
+
+
 def _calls():
-    """The calls that return a status, as the extension module's functions."""
-    global _caller
+    """The calls that return a status, by name."""
     if _caller is None:
         library()  # raises if nothing has been built
-        from . import _lat_call
-        _caller = _lat_call
     return _caller
 
 
@@ -130,8 +185,10 @@ def _stream(s):
         torch = sys.modules.get("torch")  # CUDA cannot be up in a torch that was never imported
         if torch is None or not torch.cuda.is_initialized():
             return None
-        # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        try:  # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:  # a torch that has no such functions
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -5,17 +5,22 @@
 
 Each CUDA translation unit compiles in parallel to ``_build/*.o``; the objects link into
 ``liblat_attn.so`` next to this file (CUDA runtime linked statically, so the library needs
-only the NVIDIA driver at run time).  ``_lat_call.so`` beside it is the same calls as functions
+only the NVIDIA driver at run time).  ``_lat_call.*.so`` beside it is the same calls as functions
 of a C extension, written out from the binding's signatures: it takes 0.8 us to hand 23
-arguments over where ctypes and Python take 4.
+arguments over where ctypes and Python take 4.  Where there is no C compiler or no Python.h it
+is left out, with a warning, and the binding calls by ctypes.
 """
 from __future__ import annotations
 
 import os
+import shlex
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
+
+from .binding import CALLER_PATH, _SIGNATURES, _status_calls
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -23,7 +28,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblat_attn.so")
-CALLER = os.path.join(HERE, "_lat_call.so")
 
 SOURCES = ["api.cu", "kv_append.cu", "row_attention_f32.cu", "decode_bf16.cu", "prefill_tc.cu",
            "decode_static.cu", "qkv_producer.cu", "kv_q4.cu", "decode_q4.cu",
@@ -43,15 +47,22 @@ def nvcc() -> str:
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    files += [os.path.abspath(__file__), os.path.join(HERE, "binding.py")]
+    files.append(os.path.abspath(__file__))
     return files
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLER):
+    if not os.path.exists(LIB):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLER))
+    t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _caller_is_stale() -> bool:
+    if not os.path.exists(CALLER_PATH):
+        return True
+    t = os.path.getmtime(CALLER_PATH)
+    return any(os.path.getmtime(f) > t for f in _inputs() + [os.path.join(HERE, "binding.py")])
 
 
 _CALLER_HEAD = """\
@@ -81,7 +92,11 @@ static int as_i32(PyObject *x, int *v) {
     return *v = (int)w, 1;
 }
 static int as_u64(PyObject *x, uint64_t *v) {
-    return *v = PyLong_AsUnsignedLongLong(x), *v != UINT64_MAX || !PyErr_Occurred();
+    PyObject *n = PyNumber_Index(x);  /* (the conversion below takes an int alone) */
+    if (n == NULL) return 0;
+    *v = PyLong_AsUnsignedLongLong(n);
+    Py_DECREF(n);
+    return *v != UINT64_MAX || !PyErr_Occurred();
 }
 static int as_f64(PyObject *x, double *v) { return *v = PyFloat_AsDouble(x), *v != -1.0 || !PyErr_Occurred(); }
 """
@@ -91,16 +106,13 @@ def _caller_source() -> str:
     """One function per call that returns a status: arguments by position, the status as an int."""
     import ctypes
 
-    from .binding import _SIGNATURES
-
     kinds = {ctypes.c_void_p: ("void *", "as_ptr", ""), ctypes.c_int64: ("int64_t ", "as_i64", ""),
              ctypes.c_int: ("int ", "as_i32", ""), ctypes.c_float: ("double ", "as_f64", "(float)"),
              ctypes.c_double: ("double ", "as_f64", ""), ctypes.c_size_t: ("uint64_t ", "as_u64", "(size_t)"),
              ctypes.c_uint64: ("uint64_t ", "as_u64", "")}
     out, table = [_CALLER_HEAD], []
-    for name, (res, args) in _SIGNATURES.items():
-        if res is not ctypes.c_int or len(args) < 2:  # sizes and names: not on a hot path
-            continue
+    for name in _status_calls():
+        args = _SIGNATURES[name][1]
         decl = " ".join("%sa%d;" % (kinds[t][0], i) for i, t in enumerate(args))
         take = " || ".join("!%s(v[%d], &a%d)" % (kinds[t][1], i, i) for i, t in enumerate(args))
         give = ", ".join("%sa%d" % (kinds[t][2], i) for i, t in enumerate(args))
@@ -132,22 +144,36 @@ PyMODINIT_FUNC PyInit__lat_call(void) {
 
 
 def _build_caller(verbose: bool) -> None:
+    os.makedirs(BUILD, exist_ok=True)
     src = os.path.join(BUILD, "lat_call.c")
     with open(src, "w") as f:
         f.write(_caller_source())
-    tmp = CALLER + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CC") or "gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
-           sysconfig.get_paths()["include"], src, "-o", tmp, "-L", HERE, "-l:liblat_attn.so",
-           "-Wl,-rpath,$ORIGIN"]
+    tmp = CALLER_PATH + ".tmp%d" % os.getpid()
+    cmd = shlex.split(os.environ.get("CC") or "gcc") + [
+        "-O2", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+        src, "-o", tmp, "-L", HERE, "-l:liblat_attn.so", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
-    os.replace(tmp, CALLER)
+    try:
+        subprocess.check_call(cmd)
+    except (OSError, subprocess.CalledProcessError) as e:  # no compiler, or no Python.h
+        if os.path.exists(CALLER_PATH):
+            os.remove(CALLER_PATH)  # not to be taken for the one that could not be built
+        warnings.warn("%s could not be built (%s): calls go by ctypes, 3 us longer each"
+                      % (os.path.basename(CALLER_PATH), e))
+        return
+    os.replace(tmp, CALLER_PATH)
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and not is_stale():
-        return LIB
+    if force or is_stale():
+        _build_cuda(verbose, extra_flags)
+    if force or _caller_is_stale():
+        _build_caller(verbose)
+    return LIB
+
+
+def _build_cuda(verbose: bool, extra_flags) -> None:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     procs = []
@@ -175,8 +201,6 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=()) ->
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
-    _build_caller(verbose)
-    return LIB
 
 
 if __name__ == "__main__":
