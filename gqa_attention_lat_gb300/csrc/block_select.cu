@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectAr
     }
     const int have = blocks_of(a, b);
     if (have <= a.n_sel) {  // all of them
-        for (int i = tid; i < a.n_sel; i += kPickThreads) out[i] = i < have ? i : -1;
+        // (whole numbers without a sign: n_sel may be the largest int)
+        for (uint32_t i = tid; i < (uint32_t)a.n_sel; i += kPickThreads) out[i] = i < (uint32_t)have ? (int)i : -1;
         return;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are complete
