@@ -711,6 +711,9 @@ bool make_q4_map(CUtensorMap *m, const void *base, int row_bytes, int heads, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// a query row's elements are counted in 32 bits by the decodes over reduced caches
+bool query_row_ok(int n_heads, int head_dim) { return (int64_t)n_heads * head_dim <= 0x7fffffffLL; }
+
 bool q4_strides_ok(int64_t row, int64_t head, int64_t seq) {
     return row > 0 && head > 0 && seq > 0 && row % 16 == 0 && head % 16 == 0 && seq % 16 == 0;
 }
@@ -772,7 +775,7 @@ lat_status q4_decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void 
         out_rs % per16 || !aligned16(q) || !aligned16(cache) || !aligned16(out) ||
         !q4_strides_ok(cache_rs, cache_head_stride, cache_seq_stride))
         return LAT_ERR_INVALID_ARG;
-    if (batch > 65535) return LAT_ERR_UNSUPPORTED;
+    if (batch > 65535 || !query_row_ok(n_heads, head_dim)) return LAT_ERR_UNSUPPORTED;
     int sms = 0;
     if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
     lat::Q4Plan plan;
@@ -843,7 +846,8 @@ lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs, i
 size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads, int head_dim,
                                          int max_kv_len) {
     if ((dt != LAT_F32 && dt != LAT_BF16) || batch < 0 || batch > 65535 || n_heads <= 0 || n_kv_heads <= 0 ||
-        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || max_kv_len < 0)
+        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || !query_row_ok(n_heads, head_dim) ||
+        max_kv_len < 0)
         return 0;
     int sms = 0;
     lat::Q4Plan plan;
@@ -960,7 +964,9 @@ lat_status lat_attn_select_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
         bounds_seq_stride % per16)
         return LAT_ERR_INVALID_ARG;
     const int64_t max_blocks = max_blocks_of(max_kv_len, block_size);
-    if (max_blocks > lat::kSelectMaxBlocks || (int64_t)batch > 0x7fffffffLL / n_kv_heads) return LAT_ERR_UNSUPPORTED;
+    if (max_blocks > lat::kSelectMaxBlocks || (int64_t)batch > 0x7fffffffLL / n_kv_heads ||
+        !query_row_ok(n_heads, head_dim))
+        return LAT_ERR_UNSUPPORTED;
     const size_t need = lat_attn_select_blocks_workspace_size(batch, n_kv_heads, block_size, max_kv_len);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
         return LAT_ERR_WORKSPACE;
@@ -997,8 +1003,8 @@ lat_status lat_attn_select_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
 size_t lat_attn_decode_blocks_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads, int head_dim,
                                              int block_size, int n_sel) {
     if ((dt != LAT_F32 && dt != LAT_BF16) || batch < 0 || batch > 65535 || n_heads <= 0 || n_kv_heads <= 0 ||
-        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || !block_size_ok(block_size) || n_sel <= 0 ||
-        n_sel > lat::kSelectMaxBlocks)
+        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || !query_row_ok(n_heads, head_dim) ||
+        !block_size_ok(block_size) || n_sel <= 0 || n_sel > lat::kSelectMaxBlocks)
         return 0;
     int sms = 0;
     if (!current_sm_count(&sms)) return 0;
@@ -1022,6 +1028,7 @@ lat_status lat_attn_decode_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
     if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
     if (!block_size_ok(block_size) || n_sel <= 0) return LAT_ERR_INVALID_ARG;
     if (n_sel > lat::kSelectMaxBlocks) return LAT_ERR_UNSUPPORTED;
+    if (n_heads > 0 && supported_head_dim(head_dim) && !query_row_ok(n_heads, head_dim)) return LAT_ERR_UNSUPPORTED;
     if (batch > 0 && !blocks) return LAT_ERR_INVALID_ARG;
     if (dt == LAT_BF16)
         return decode_impl(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,

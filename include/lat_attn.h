@@ -377,8 +377,8 @@ lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs,
  * lat_attn_decode's workspace hold (zero-filled before its first use with a given layout,
  * and again after LAT_ERR_TIMEOUT; calls sharing one must not overlap on the GPU; its size
  * depends on the current device's SM count).
- * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, batch * n_heads * ceil(head_dim / 128)
- * < 2^31, and batch * n_kv_heads * ceil(n_heads / n_kv_heads / 8) work units of up to
+ * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, n_heads * head_dim < 2^31, batch *
+ * n_heads * ceil(head_dim / 128) < 2^31, and batch * n_kv_heads * ceil(n_heads / n_kv_heads / 8) work units of up to
  * ceil(max_kv_len / 128) + 2 tiles (64 rows a tile at head_dim 512; more elsewhere, at
  * times) < 2^31 in all.
  * Sums, maxima and the joins are fp32.  A softmax weight is held to 16 bits for LAT_BF16 (2^-16
@@ -444,8 +444,8 @@ lat_status lat_kv_block_bounds(lat_dtype dt, const void *k_cache, int64_t cache_
  * [0, max_kv_len] sets *status = LAT_ERR_BOUNDS and leaves that sequence's lists unwritten.
  * n_sel >= 1, n_first and n_last >= 0, n_first + n_last <= n_sel, q and bounds 16-byte
  * aligned with strides that are multiples of 16 bytes, else LAT_ERR_INVALID_ARG;
- * ceil(max_kv_len / block_size) <= 65536 and batch * n_kv_heads < 2^31, else
- * LAT_ERR_UNSUPPORTED.
+ * ceil(max_kv_len / block_size) <= 65536, batch * n_kv_heads < 2^31 and n_heads * head_dim <
+ * 2^31, else LAT_ERR_UNSUPPORTED.
  * workspace: at least lat_attn_select_blocks_workspace_size(...) bytes, 256-byte aligned,
  * else LAT_ERR_WORKSPACE; it needs no clearing, and calls sharing one must not overlap.
  */
@@ -470,8 +470,8 @@ lat_status lat_attn_select_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
  * lse = -inf.
  * q, the caches, kv_lens, max_kv_len, out, lse and softcap as in lat_attn_decode_softcap, its
  * alignment rules for LAT_BF16; for LAT_F32, q, out and the caches 16-byte aligned and all
- * strides multiples of 4.  n_sel >= 1, else LAT_ERR_INVALID_ARG; n_sel <= 65536, batch <=
- * 65535 and the size limits of lat_attn_decode (for LAT_F32 batch * n_heads * ceil(head_dim /
+ * strides multiples of 4.  n_sel >= 1, else LAT_ERR_INVALID_ARG; n_sel <= 65536, n_heads *
+ * head_dim < 2^31, batch <= 65535 and the size limits of lat_attn_decode (for LAT_F32 batch * n_heads * ceil(head_dim /
  * 128) < 2^31), else LAT_ERR_UNSUPPORTED.
  * workspace: at least lat_attn_decode_blocks_workspace_size(...) bytes for the same sizes and
  * dt, 256-byte aligned, else LAT_ERR_WORKSPACE.  For LAT_BF16 the rules of lat_attn_decode's
