@@ -442,7 +442,7 @@ __device__ uint64_t pair_score(const SelectArgs &a, int b, int hk, int n, bool &
     uint64_t best = 0;
     for (int h0 = 0; h0 < G; h0 += 4) {
         float s[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
-        float top = 0.f;
+        float top = 0.f, other = 0.f;
 #pragma unroll 2
         for (int d = lane; d < D; d += 32) {
             const float hi = (float)x[d], lo = (float)x[D + d];
@@ -450,6 +450,7 @@ __device__ uint64_t pair_score(const SelectArgs &a, int b, int hk, int n, bool &
             for (int i = 0; i < 4; ++i) {
                 const float w = h0 + i < G ? (float)q[(h0 + i) * D + d] : 0.f, k = w < 0.f ? lo : hi;
                 const float p = __fmul_rn(w, k);
+                other = fmaf(w, w < 0.f ? hi : lo, other);
                 float e;
                 s[i] = two_sum(s[i], p, e);
                 c[i] = __fadd_rn(c[i], __fadd_rn(e, __fmaf_rn(w, k, -p)));
@@ -467,7 +468,8 @@ __device__ uint64_t pair_score(const SelectArgs &a, int b, int hk, int n, bool &
             }
             top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
         }
-        if (!(top > 0x1p-60f && top < 0x1p100f)) fits = false;
+        // (the products not taken count where they are no numbers: 0 times an infinite bound)
+        if (!(top > 0x1p-60f && top < 0x1p100f) || other != other) fits = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // the nearest float and the rest: the pairs' order is the sums'
             float l;
@@ -487,8 +489,9 @@ __device__ __noinline__ uint64_t wide_score(const SelectArgs &a, int b, int hk, 
     for (int h = 0; h < G; ++h) {
         double v = 0.0;
         for (int d = lane; d < D; d += 32) {
-            const float w = (float)q[h * D + d];
-            v = fma((double)w, (double)(float)x[w < 0.f ? D + d : d], v);
+            const double w = (double)(float)q[h * D + d], hi = w * (double)(float)x[d], lo = w * (double)(float)x[D + d];
+            const double other = w < 0.0 ? hi : lo;
+            v += other != other ? other : w < 0.0 ? lo : hi;  // (exact products: no fma needed)
         }
         for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
         const uint64_t key = order64(v);
