@@ -160,6 +160,9 @@ __global__ void __launch_bounds__(32 * kBoundWarps) block_bounds_kernel(const Bo
 constexpr int kScoreWarps = 4;
 constexpr int kScoreRows = 16;  // blocks a warp scores at a time
 constexpr int kQHeads = 8;
+// What the bounds of a score's error leave out: products and sums below the least normal number
+// lose up to 2^-126 each, and there are 2 D of either at most
+constexpr float kLeastError = 0x1p-115f;
 
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) block_score_bf16_kernel(cons
                 const int n = n0 + r + 8 * half;
                 if (c == 0 && n < have) {
                     float2 *dst = a.scores + (int64_t)unit * a.max_blocks + n;
-                    e *= (2.f * D / 16.f + 1.f) * 18.f * 0x1p-23f;
+                    e = fmaf(e, (2.f * D / 16.f + 1.f) * 18.f * 0x1p-23f, kLeastError);
                     if (h0 > 0) {  // more than eight heads: with what the earlier ones left
                         const float2 was = *dst;
                         m = max_nan(m, was.x), e = max_nan(e, was.y);
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) block_score_f32_kernel(const
             const int n = n0 + lane / kQHeads;
             if (lane % kQHeads == 0 && n < have) {
                 float2 *dst = a.scores + (int64_t)unit * a.max_blocks + n;
-                err *= (kVecs / 8.f + 16.f) * 0x1p-23f;
+                err = fmaf(err, (kVecs / 8.f + 16.f) * 0x1p-23f, kLeastError);
                 if (h0 > 0) {
                     const float2 was = *dst;
                     m = max_nan(m, was.x), err = max_nan(err, was.y);

@@ -74,3 +74,23 @@ def test_an_infinite_bound_of_a_channel_that_the_query_lacks(dt, G, nb):
         got, st = select(q, bd, [nb * block], block, G, 1, D, dt, n, 0, 0)
         assert int(st.item()) == 0
         assert got[0, 0].tolist() == kept(s, n), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("nb", [300, 1500])
+@pytest.mark.parametrize("q_exp,k_exp", [(-70, -70), (-72, -75), (-66, -64), (-60, -60)])
+def test_scores_down_to_the_least_floats(dt, nb, q_exp, k_exp):
+    """Products and sums among fp32's subnormal numbers, where a sum is off by parts of itself:
+    the choice is that of the exact scores (products of fp32 numbers are exact in fp64, and sums
+    of 64 of them are compared far above its rounding)."""
+    D, block, G, n_sel = 64, 16, 3, 40
+    mid = W.normal((nb, D), dtype="f32", device="cuda", seed=13, role="k")
+    half = W.normal((nb, D), dtype="f32", device="cuda", seed=14, role="k").abs()
+    bd = (torch.cat([mid + half, mid - half], 1) * 2.0 ** k_exp).to(W.torch_dtype(dt)).view(1, nb, 1, 2 * D)
+    q = (W.normal((1, G * D), dtype="f32", device="cuda", seed=15, role="q") * 2.0 ** q_exp).to(W.torch_dtype(dt))
+    s = by_definition(q[0], bd[0, :, 0], D)
+    gaps = sorted(s)
+    assert min(b - a for a, b in zip(gaps, gaps[1:])) > 2.0 ** (q_exp + k_exp - 40)
+    got, st = select(q, bd, [nb * block], block, G, 1, D, dt, n_sel, 0, 0)
+    assert int(st.item()) == 0
+    assert got[0, 0].tolist() == kept(s, n_sel)
