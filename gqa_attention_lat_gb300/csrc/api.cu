@@ -17,6 +17,10 @@ namespace {
 
 bool supported_head_dim(int d) { return d == 64 || d == 80 || d == 128 || d == 256 || d == 512; }
 
+// x / softcap for a score cap, kept where twice log2(e) times it is still a float: a cap so small
+// that this matters takes every score but 0 to its ends, and 0 must not meet an infinity
+float over_cap(float x, float softcap) { return fminf(fmaxf(x / softcap, -1e38f), 1e38f); }
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -247,7 +251,7 @@ lat_status prefill_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k
     a.window = window;
     a.scale_log2 = scale * kLog2e;
     a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
-    a.raw_over_cap = softcap > 0.f ? scale / softcap : 0.f;
+    a.raw_over_cap = softcap > 0.f ? over_cap(scale, softcap) : 0.f;
     a.status = status;
     a.timeout_ns = timeout_ns;
     a.test_skip_kv_load = skip_kv_load;
@@ -470,7 +474,7 @@ lat_status decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *k_
     a.block_size = block_size;
     a.scale_log2 = scale * kLog2e;
     a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
-    a.raw_over_cap = softcap > 0.f ? scale / softcap : 0.f;
+    a.raw_over_cap = softcap > 0.f ? over_cap(scale, softcap) : 0.f;
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_lse = reinterpret_cast<float *>(ws + plan.part_o_bytes);
     a.counters = reinterpret_cast<int32_t *>(ws + plan.part_o_bytes + plan.part_lse_bytes);
@@ -555,7 +559,7 @@ lat_status lat_test_capped_scores(const float *raw, int64_t n, float scale, floa
     if (n == 0) return LAT_OK;
     if (raw == nullptr || out == nullptr) return LAT_ERR_INVALID_ARG;
     // the same two factors the attention entry points hand their kernels
-    return lat::launch_capped_scores(raw, n, scale / softcap, softcap * kLog2e, out,
+    return lat::launch_capped_scores(raw, n, over_cap(scale, softcap), softcap * kLog2e, out,
                                      static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? LAT_OK
                : LAT_ERR_CUDA;
@@ -804,7 +808,7 @@ lat_status q4_decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void 
     a.window = window < 0 ? 0 : window;
     a.scale_log2 = scale * kLog2e;
     a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
-    a.over_cap_log2 = softcap > 0.f ? 1.f / (softcap * kLog2e) : 0.f;
+    a.over_cap_log2 = softcap > 0.f ? over_cap(1.f, softcap * kLog2e) : 0.f;
     a.part_o = reinterpret_cast<float *>(ws);
     a.part_lse = reinterpret_cast<float *>(ws + plan.part_o_bytes);
     a.piece_count = a.counters = reinterpret_cast<int32_t *>(ws + plan.part_o_bytes + plan.part_lse_bytes);
@@ -1077,7 +1081,7 @@ lat_status lat_attn_decode_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
     a.head_dim = head_dim;
     a.scale_log2 = scale * kLog2e;
     a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
-    a.raw_over_cap = softcap > 0.f ? scale / softcap : 0.f;
+    a.raw_over_cap = softcap > 0.f ? over_cap(scale, softcap) : 0.f;
     a.splits = lat::blocks_f32_splits(batch, n_heads, n_kv_heads, block_size, n_sel, sms);
     const size_t rows = (size_t)batch * n_heads;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
