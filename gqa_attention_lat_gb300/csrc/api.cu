@@ -718,6 +718,9 @@ bool make_q4_map(CUtensorMap *m, const void *base, int row_bytes, int heads, int
 // a query row's elements are counted in 32 bits by the decodes over reduced caches
 bool query_row_ok(int n_heads, int head_dim) { return (int64_t)n_heads * head_dim <= 0x7fffffffLL; }
 
+// a score cap whose products with log2(e) and 2 stay floats and whose reciprocal keeps its bits
+float cap_in_range(float softcap) { return fminf(softcap, 1e36f); }
+
 bool q4_strides_ok(int64_t row, int64_t head, int64_t seq) {
     return row > 0 && head > 0 && seq > 0 && row % 16 == 0 && head % 16 == 0 && seq % 16 == 0;
 }
@@ -807,6 +810,7 @@ lat_status q4_decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void 
     a.head_dim = head_dim;
     a.window = window < 0 ? 0 : window;
     a.scale_log2 = scale * kLog2e;
+    softcap = cap_in_range(softcap);
     a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
     a.over_cap_log2 = softcap > 0.f ? over_cap(1.f, softcap * kLog2e) : 0.f;
     a.part_o = reinterpret_cast<float *>(ws);
@@ -1034,6 +1038,7 @@ lat_status lat_attn_decode_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
     if (n_sel > lat::kSelectMaxBlocks) return LAT_ERR_UNSUPPORTED;
     if (n_heads > 0 && supported_head_dim(head_dim) && !query_row_ok(n_heads, head_dim)) return LAT_ERR_UNSUPPORTED;
     if (batch > 0 && !blocks) return LAT_ERR_INVALID_ARG;
+    if (isfinite(softcap)) softcap = cap_in_range(softcap);  // (others are refused below)
     if (dt == LAT_BF16)
         return decode_impl(dt, q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,
                            max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim, 0, scale, softcap, 0,

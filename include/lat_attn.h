@@ -367,7 +367,7 @@ lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs,
  * lat_attn_decode_q4 — lat_attn_decode_softcap over a 4-bit cache: one query token per
  * sequence, at position kv_lens[b] - 1, over the cached keys max(0, kv_lens[b] - window) ..
  * kv_lens[b] - 1 (all of them when window <= 0), keys and values as they read back; softcap
- * finite and >= 0, 0 = none.  dt is the type of q and out.
+ * finite and >= 0, 0 = none (one above 1e36 counts as 1e36).  dt is the type of q and out.
  * q, out, lse, kv_lens, max_kv_len and the status are lat_attn_decode's; a sequence of length
  * 0 gets out = 0, lse = -inf.  q and out must be 16-byte aligned and their row strides
  * multiples of 16 bytes, else LAT_ERR_INVALID_ARG.  Every sequence's cache must hold at
@@ -468,11 +468,12 @@ lat_status lat_attn_select_blocks(lat_dtype dt, const void *q, int64_t q_rs, con
  * sets *status = LAT_ERR_BOUNDS and leaves that KV head's output unspecified; only the first
  * ceil(kv_lens[b] / block_size) entries are read.  A list that holds no key gives out = 0,
  * lse = -inf.
- * q, the caches, kv_lens, max_kv_len, out, lse and softcap as in lat_attn_decode_softcap, its
- * alignment rules for LAT_BF16; for LAT_F32, q, out and the caches 16-byte aligned and all
- * strides multiples of 4.  n_sel >= 1, else LAT_ERR_INVALID_ARG; n_sel <= 65536, n_heads *
- * head_dim < 2^31, batch <= 65535 and the size limits of lat_attn_decode (for LAT_F32 batch * n_heads * ceil(head_dim /
- * 128) < 2^31), else LAT_ERR_UNSUPPORTED.
+ * q, the caches, kv_lens, max_kv_len, out, lse and softcap as in lat_attn_decode_softcap (a cap
+ * above 1e36 counts as 1e36), its alignment rules for LAT_BF16; for LAT_F32, q, out and the
+ * caches 16-byte aligned and all strides multiples of 4.  n_sel >= 1, else LAT_ERR_INVALID_ARG;
+ * n_sel <= 65536, n_heads * head_dim < 2^31, batch <= 65535 and the size limits of
+ * lat_attn_decode (for LAT_F32 batch * n_heads * ceil(head_dim / 128) < 2^31), else
+ * LAT_ERR_UNSUPPORTED.
  * workspace: at least lat_attn_decode_blocks_workspace_size(...) bytes for the same sizes and
  * dt, 256-byte aligned, else LAT_ERR_WORKSPACE.  For LAT_BF16 the rules of lat_attn_decode's
  * workspace hold (zero-filled before its first use, and again after LAT_ERR_TIMEOUT); for
