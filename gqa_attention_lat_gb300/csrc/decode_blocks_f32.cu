@@ -24,7 +24,9 @@ namespace {
 
 constexpr int kBWarps = 4;
 constexpr int kBHeads = 4;
-constexpr int kMinKeys = 64;  // keys a piece is worth
+// keys a piece is worth (one sequence, 2 KV heads of 8 query heads, head_dim 256: 2048 listed keys
+// 13.3 us at 16, 9.5 at 32, 9.3 at 64, 11.7 at 128; 256 of them 5.4, 6.0, 7.6, 10.9)
+constexpr int kMinKeys = 64;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kBWarps) decode_blocks_f32_kernel(const BlocksF32Args a) {

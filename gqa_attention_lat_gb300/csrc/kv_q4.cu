@@ -254,7 +254,7 @@ __device__ __forceinline__ void quantise(const Octet<T> (&oct)[StoreCfg<D>::kSte
         }
         unsigned char *r = mine + row * R::kBytes;
         if (!kIsV) {
-            reinterpret_cast<uint32_t *>(r)[(g / R::kSet * 4 + col) * R::kSet + g % R::kSet] = evens_first(code);
+            reinterpret_cast<uint32_t *>(r)[R::k_word(g, col)] = evens_first(code);
         } else {
             // halves 2 col and 2 col + 1: byte `col` of the four lanes' codes, lane m's as nibble m.
             // A transpose of 4 x 4 bytes over the four lanes: with lane col ^ 2 the halves that hold
@@ -263,7 +263,7 @@ __device__ __forceinline__ void quantise(const Octet<T> (&oct)[StoreCfg<D>::kSte
             const uint32_t two = __byte_perm(code, far, (col & 2) ? 0x3254 : 0x5410);
             const uint32_t near = __shfl_xor_sync(0xffffffffu, two, 1);
             const uint32_t keep = evens_first(__byte_perm(two, near, (col & 1) ? 0x3715 : 0x6240));
-            uint16_t *h = reinterpret_cast<uint16_t *>(r + R::kV) + (g / R::kSet * 8 + 2 * col) * R::kSet + g % R::kSet;
+            uint16_t *h = reinterpret_cast<uint16_t *>(r + R::kV) + R::v_half(g, 2 * col);
             h[0] = (uint16_t)keep;
             h[R::kSet] = (uint16_t)(keep >> 16);
         }
@@ -318,11 +318,11 @@ __device__ __forceinline__ void read_back(const Places &at, void *out, bool vec,
         const uint32_t bias = q4_bias2(pw), s2 = __byte_perm(pw, pw, 0x1010);
         uint32_t v[4];  // channels 2 k and 2 k + 1 as c - z
         if (!kIsV) {
-            const uint32_t w = reinterpret_cast<const uint32_t *>(r)[(g / R::kSet * 4 + col) * R::kSet + g % R::kSet];
+            const uint32_t w = reinterpret_cast<const uint32_t *>(r)[R::k_word(g, col)];
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = q4_codes2(w, k, bias);
         } else {
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(r + R::kV) + (g / R::kSet * 8 + 2 * col) * R::kSet + g % R::kSet;
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(r + R::kV) + R::v_half(g, 2 * col);
             const uint32_t own = (uint32_t)h[0] | ((uint32_t)h[R::kSet] << 16);  // halves 2 col, 2 col + 1
 #pragma unroll
             for (int k = 0; k < 4; ++k)

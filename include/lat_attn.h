@@ -330,7 +330,8 @@ lat_status lat_qkv_norm_rope_append(lat_dtype dt, const void *qkv, int64_t qkv_r
  *   s = bf16((mx - mn) * (1/15))  (difference, constant and product in fp32),
  *   z = nearest whole number to -mn / s,  c = nearest to x / s, plus z, each in 0 .. 15,
  * and the group reads back as s * (c - z): 0 is exact, a value is off by at most half a step
- * s (at the ends of the grid by up to one step more, where s or z was rounded).  A group
+ * s (at the ends of the grid by up to one step more, where s or z was rounded; a range below
+ * 2^-125 leaves s few bits and may be off by more, one below 2^-130 reads back as 0).  A group
  * that holds a NaN or an infinity, or spans more than the largest fp32, reads back as NaN.
  * The order of the codes within a row belongs to the library.
  */
@@ -436,7 +437,7 @@ lat_status lat_kv_block_bounds(lat_dtype dt, const void *k_cache, int64_t cache_
  * there are no more).  The score of a block is the largest over the KV head's query heads of
  *   sum_d max(q_d * hi_d, q_d * lo_d),
  * which no key of the block can exceed (a positive scale or a score cap keeps the order).
- * Scores are compared to within 2^-45 of their terms' magnitude (bf16 ones, whose products
+ * Scores are compared to within 2^-38 of their terms' magnitudes (bf16 ones, whose products
  * and sums fit, exactly), so the choice does not hang on the order of a sum; a score that is
  * NaN goes before all others.
  *   blocks: int32 [batch, n_kv_heads, n_sel], ascending, -1 behind.
