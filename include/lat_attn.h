@@ -383,9 +383,9 @@ lat_status lat_kv_expand_q4(lat_dtype dt, const void *cache, int64_t cache_rs,
  * ceil(max_kv_len / 128) + 2 tiles (64 rows a tile at head_dim 512; more elsewhere, at
  * times) < 2^31 in all.
  * Sums, maxima and the joins are fp32.  A softmax weight is held to 16 bits for LAT_BF16 (2^-16
- * of it; the output's own rounding to bf16 is the error that shows) and to 24 for LAT_F32; a
- * query's channels below 2^-20 of its largest (LAT_F32: all) are held to within 2^-29 (2^-24) of
- * that largest one.
+ * of it; the output's own rounding to bf16 is the error that shows) and to 24 for LAT_F32.  A
+ * query's channels are exact from 2^-20 of its largest on and within 2^-29 of that below
+ * (LAT_F32: within 2^-24 of themselves, or 2^-37 of the largest).
  * A query that holds a NaN or an infinity gives NaN.
  */
 size_t lat_attn_decode_q4_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads,

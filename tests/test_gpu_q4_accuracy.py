@@ -67,6 +67,18 @@ def test_weights_add_no_rounding_that_shows(D, G):
     check(c, queries(B, G * Hkv, D, G), lens, G * Hkv, kh, vh, 0, "D%d G%d" % (D, G))
 
 
+@pytest.mark.parametrize("D", [64, 128, 512])
+@pytest.mark.parametrize("G", [4, 6])
+@pytest.mark.parametrize("v_mul", [2.0 ** -110, 2.0 ** -60, 2.0 ** 100])
+def test_values_far_from_one(D, G, v_mul):
+    lens = [2, 3, 5, 17, 40, 130, 300]
+    B, Hkv, cap = len(lens), 2, 300
+    c = Cache(B, cap, Hkv, D)
+    k, v = rows(B, cap, Hkv, D, "bf16", 8, "k"), rows(B, cap, Hkv, D, "bf16", 8, "v") * v_mul
+    c.append(k, v, [0] * B, cap)
+    check(c, queries(B, G * Hkv, D, G), lens, G * Hkv, held(k), held(v), 0, "D%d G%d" % (D, G))
+
+
 @pytest.mark.parametrize("G", [2, 4, 7])
 def test_long_caches_too(G):
     """The form of head_dim 128 that takes 64 keys a warp at once, units cut and whole."""
