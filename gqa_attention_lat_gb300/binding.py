@@ -82,6 +82,15 @@ _SIGNATURES = {
     "lat_attn_decode_q4_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "lat_attn_decode_q4": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I32, _P, _I64, _P,
                                   _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P, _SZ, _P, _P]),
+    "lat_kv_q8_block_bytes": (_I64, [_I32, _I32]),
+    "lat_kv_append_q8": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _I64, _P, _I32,
+                                _I32, _I32, _I32, _P, _P]),
+    "lat_kv_expand_q8": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _I32, _P, _P, _I64, _P, _I32,
+                                _I32, _I32, _I32, _P, _P]),
+    "lat_attn_decode_q8_workspace_size": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "lat_attn_decode_q8": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _P, _I64,
+                                  _P, _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P, _SZ, _P,
+                                  _P]),
     "lat_kv_block_bounds": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64, _I32,
                                    _P, _I32, _I32, _I32, _I32, _P, _P]),
     "lat_attn_select_blocks_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
@@ -98,6 +107,8 @@ _SIGNATURES = {
                                        _I32, _I32, _I32, _I32, _P, _SZ, _U64, _P, _P]),
     "lat_test_decode_q4_timeout": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _P, _I32, _P, _I64,
                                           _I32, _I32, _I32, _I32, _P, _SZ, _U64, _P, _P]),
+    "lat_test_decode_q8_timeout": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _P,
+                                          _I64, _I32, _I32, _I32, _I32, _P, _SZ, _U64, _P, _P]),
     "lat_test_decode_blocks_timeout": (_I32, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I32,
                                               _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _SZ,
                                               _U64, _P, _P]),
@@ -354,6 +365,49 @@ def lat_attn_decode_q4(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_se
         _stream(stream)), "lat_attn_decode_q4")
 
 
+def lat_kv_q8_block_bytes(head_dim, block_size) -> int:
+    """Bytes of one 8-bit cache record (a block's K and V of one head); 0 if not built."""
+    return library().lat_kv_q8_block_bytes(head_dim, block_size)
+
+
+def lat_kv_append_q8(dt, cache, cache_block_stride, cache_head_stride, cache_seq_stride,
+                     block_size, capacity, k_new, v_new, new_rs, pos, n_new, batch, n_kv_heads,
+                     head_dim, status=None, stream=None):
+    """Quantise new K/V rows into an 8-bit cache (cache strides in bytes)."""
+    _check(_calls().lat_kv_append_q8(
+        dt, cache, cache_block_stride, cache_head_stride, cache_seq_stride, block_size, capacity,
+        k_new, v_new, new_rs, pos, n_new, batch, n_kv_heads, head_dim, status,
+        _stream(stream)), "lat_kv_append_q8")
+
+
+def lat_kv_expand_q8(dt, cache, cache_block_stride, cache_head_stride, cache_seq_stride,
+                     block_size, capacity, k_out, v_out, out_rs, pos, n_rows, batch, n_kv_heads,
+                     head_dim, status=None, stream=None):
+    """Read rows of an 8-bit cache back as K and V rows."""
+    _check(_calls().lat_kv_expand_q8(
+        dt, cache, cache_block_stride, cache_head_stride, cache_seq_stride, block_size, capacity,
+        k_out, v_out, out_rs, pos, n_rows, batch, n_kv_heads, head_dim, status,
+        _stream(stream)), "lat_kv_expand_q8")
+
+
+def lat_attn_decode_q8_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim,
+                                      max_kv_len) -> int:
+    return library().lat_attn_decode_q8_workspace_size(dt, batch, n_heads, n_kv_heads, head_dim,
+                                                       max_kv_len)
+
+
+def lat_attn_decode_q8(dt, q, q_rs, cache, cache_block_stride, cache_head_stride,
+                       cache_seq_stride, block_size, kv_lens, max_kv_len, out, out_rs, lse,
+                       batch, n_heads, n_kv_heads, head_dim, window, scale, softcap, workspace,
+                       workspace_bytes, status=None, stream=None):
+    """Decode over an 8-bit cache (cache strides in bytes)."""
+    _check(_calls().lat_attn_decode_q8(
+        dt, q, q_rs, cache, cache_block_stride, cache_head_stride, cache_seq_stride, block_size,
+        kv_lens, max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim, window,
+        scale, softcap, workspace, workspace_bytes, status, _stream(stream)),
+        "lat_attn_decode_q8")
+
+
 def lat_kv_block_bounds(dt, k_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity,
                         bounds, bounds_rs, bounds_head_stride, bounds_seq_stride, block_size,
                         pos, n_new, batch, n_kv_heads, head_dim, status=None, stream=None):
@@ -427,6 +481,16 @@ def lat_test_decode_q4_timeout(dt, q, q_rs, cache, cache_rs, cache_head_stride, 
         dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens, max_kv_len,
         out, out_rs, batch, n_heads, n_kv_heads, head_dim, workspace, workspace_bytes,
         timeout_ns, status, _stream(stream)), "lat_test_decode_q4_timeout")
+
+
+def lat_test_decode_q8_timeout(dt, q, q_rs, cache, cache_block_stride, cache_head_stride,
+                               cache_seq_stride, block_size, kv_lens, max_kv_len, out, out_rs,
+                               batch, n_heads, n_kv_heads, head_dim, workspace, workspace_bytes,
+                               timeout_ns, status, stream=None):
+    _check(_calls().lat_test_decode_q8_timeout(
+        dt, q, q_rs, cache, cache_block_stride, cache_head_stride, cache_seq_stride, block_size,
+        kv_lens, max_kv_len, out, out_rs, batch, n_heads, n_kv_heads, head_dim, workspace,
+        workspace_bytes, timeout_ns, status, _stream(stream)), "lat_test_decode_q8_timeout")
 
 
 def lat_test_decode_blocks_timeout(q, q_rs, k_cache, v_cache, cache_rs, cache_head_stride,

@@ -12,6 +12,7 @@
 #include "kernels.h"
 #include "lat_attn.h"
 #include "lat_attn_testing.h"
+#include "q8_block.cuh"
 
 namespace {
 
@@ -764,6 +765,40 @@ lat_status q4_store_impl(lat_dtype dt, void *cache, int64_t cache_rs, int64_t ca
                : LAT_ERR_CUDA;
 }
 
+// what the decodes over packed caches have in common; `workspace` holds plan.total_bytes
+void fill_split_args(lat::SplitDecodeArgs &a, const lat::SplitPlan &plan, const void *q, int64_t q_rs,
+                     const int32_t *kv_lens, int max_kv_len, void *out, int64_t out_rs, float *lse, int batch,
+                     int n_heads, int n_kv_heads, int head_dim, int window, float scale, float softcap,
+                     void *workspace, int32_t *status, uint64_t timeout_ns, int skip_load) {
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    a.q = q;
+    a.q_rs = q_rs;
+    a.kv_lens = kv_lens;
+    a.max_kv_len = max_kv_len;
+    a.out = out;
+    a.out_rs = out_rs;
+    a.lse = lse;
+    a.batch = batch;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.window = window < 0 ? 0 : window;
+    a.scale_log2 = scale * kLog2e;
+    softcap = cap_in_range(softcap);
+    a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
+    a.over_cap_log2 = softcap > 0.f ? over_cap(1.f, softcap * kLog2e) : 0.f;
+    a.part_o = reinterpret_cast<float *>(ws);
+    a.part_lse = reinterpret_cast<float *>(ws + plan.part_o_bytes);
+    a.piece_count = a.counters = reinterpret_cast<int32_t *>(ws + plan.part_o_bytes + plan.part_lse_bytes);
+    a.defer_join = plan.defer_join;
+    a.max_splits = plan.max_splits;
+    a.min_tiles = plan.min_tiles;
+    a.whole = plan.whole;
+    a.timeout_ns = timeout_ns;
+    a.test_skip_load = skip_load;
+    a.status = status;
+}
+
 lat_status q4_decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *cache, int64_t cache_rs,
                           int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
                           int max_kv_len, void *out, int64_t out_rs, float *lse, int batch, int n_heads,
@@ -796,33 +831,8 @@ lat_status q4_decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void 
         !make_q4_map(&a.tm, cache, lat::q4_row_bytes(head_dim), n_kv_heads, max_kv_len, batch, cache_rs,
                      cache_head_stride, cache_seq_stride, plan.box_rows))
         return LAT_ERR_CUDA;
-    unsigned char *ws = static_cast<unsigned char *>(workspace);
-    a.q = q;
-    a.q_rs = q_rs;
-    a.kv_lens = kv_lens;
-    a.max_kv_len = max_kv_len;
-    a.out = out;
-    a.out_rs = out_rs;
-    a.lse = lse;
-    a.batch = batch;
-    a.n_heads = n_heads;
-    a.n_kv_heads = n_kv_heads;
-    a.head_dim = head_dim;
-    a.window = window < 0 ? 0 : window;
-    a.scale_log2 = scale * kLog2e;
-    softcap = cap_in_range(softcap);
-    a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
-    a.over_cap_log2 = softcap > 0.f ? over_cap(1.f, softcap * kLog2e) : 0.f;
-    a.part_o = reinterpret_cast<float *>(ws);
-    a.part_lse = reinterpret_cast<float *>(ws + plan.part_o_bytes);
-    a.piece_count = a.counters = reinterpret_cast<int32_t *>(ws + plan.part_o_bytes + plan.part_lse_bytes);
-    a.defer_join = plan.defer_join;
-    a.max_splits = plan.max_splits;
-    a.min_tiles = plan.min_tiles;
-    a.whole = plan.whole;
-    a.timeout_ns = timeout_ns;
-    a.test_skip_load = skip_load;
-    a.status = status;
+    fill_split_args(a, plan, q, q_rs, kv_lens, max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim,
+                    window, scale, softcap, workspace, status, timeout_ns, skip_load);
     return lat::launch_decode_q4(a, dt == LAT_BF16, plan, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? LAT_OK
                : LAT_ERR_CUDA;
@@ -883,6 +893,161 @@ lat_status lat_test_decode_q4_timeout(lat_dtype dt, const void *q, int64_t q_rs,
     return q4_decode_impl(dt, q, q_rs, cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens, max_kv_len, out,
                           out_rs, nullptr, batch, n_heads, n_kv_heads, head_dim, 0, 0.125f, 0.f, workspace,
                           workspace_bytes, status, stream, timeout_ns, 1);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the 8-bit cache
+
+namespace {
+
+lat_status q8_store_impl(lat_dtype dt, void *cache, int64_t cache_block_stride, int64_t cache_head_stride,
+                         int64_t cache_seq_stride, int block_size, int capacity, const void *k, const void *v,
+                         void *k_out, void *v_out, int64_t rs, const int32_t *pos, int n, int batch, int n_kv_heads,
+                         int head_dim, bool expand, int32_t *status, void *stream) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || n < 0 || capacity < 0 || n_kv_heads <= 0 || !lat::q8_block_size_ok(block_size))
+        return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0 || n == 0) return LAT_OK;
+    if (!cache || !pos || (expand ? (!k_out || !v_out) : (!k || !v))) return LAT_ERR_INVALID_ARG;
+    if (!aligned16(cache) || !q4_strides_ok(cache_block_stride, cache_head_stride, cache_seq_stride) ||
+        rs < (int64_t)n_kv_heads * head_dim)
+        return LAT_ERR_INVALID_ARG;
+    const int64_t touched = ((int64_t)n + block_size - 2) / block_size + 1;
+    const int64_t per = expand ? n : 2 * touched;  // units of a sequence's head
+    if (per * batch > 0x7fffffffLL / n_kv_heads) return LAT_ERR_UNSUPPORTED;
+    lat::Q8StoreArgs a{};
+    a.cache = static_cast<unsigned char *>(cache);
+    a.cache_block = cache_block_stride;
+    a.cache_head = cache_head_stride;
+    a.cache_seq = cache_seq_stride;
+    while (1 << a.block_shift < block_size) ++a.block_shift;
+    a.k = k;
+    a.v = v;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.rs = rs;
+    const int64_t es = dt == LAT_BF16 ? 2 : 4;
+    a.vec = rs * es % 16 == 0 && (expand ? aligned16(k_out) && aligned16(v_out) : aligned16(k) && aligned16(v));
+    a.pos = pos;
+    a.capacity = capacity;
+    a.n = n;
+    a.batch = batch;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.touched = (int)touched;
+    a.units = per * batch * n_kv_heads;
+    a.by_heads = lat::FastDiv((uint32_t)n_kv_heads);
+    a.by_n = lat::FastDiv((uint32_t)n);
+    a.by_touched = lat::FastDiv((uint32_t)touched);
+    a.status = status;
+    return lat::launch_q8_store(a, dt == LAT_BF16, expand, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LAT_OK
+               : LAT_ERR_CUDA;
+}
+
+lat_status q8_decode_impl(lat_dtype dt, const void *q, int64_t q_rs, const void *cache, int64_t cache_block_stride,
+                          int64_t cache_head_stride, int64_t cache_seq_stride, int block_size,
+                          const int32_t *kv_lens, int max_kv_len, void *out, int64_t out_rs, float *lse, int batch,
+                          int n_heads, int n_kv_heads, int head_dim, int window, float scale, float softcap,
+                          void *workspace, size_t workspace_bytes, int32_t *status, void *stream,
+                          uint64_t timeout_ns, int skip_load) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (!(softcap >= 0.f) || !isfinite(softcap) || !isfinite(scale)) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || max_kv_len < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 ||
+        !lat::q8_block_size_ok(block_size))
+        return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0) return LAT_OK;
+    if (!q || !cache || !kv_lens || !out) return LAT_ERR_INVALID_ARG;
+    const int64_t per16 = dt == LAT_BF16 ? 8 : 4;  // elements in 16 bytes
+    if (q_rs < (int64_t)n_heads * head_dim || out_rs < (int64_t)n_heads * head_dim || q_rs % per16 ||
+        out_rs % per16 || !aligned16(q) || !aligned16(cache) || !aligned16(out) ||
+        !q4_strides_ok(cache_block_stride, cache_head_stride, cache_seq_stride))
+        return LAT_ERR_INVALID_ARG;
+    if (batch > 65535 || !query_row_ok(n_heads, head_dim)) return LAT_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
+    lat::SplitPlan plan;
+    if (!lat::plan_decode_q8(batch, n_heads, n_kv_heads, head_dim, dt == LAT_BF16, max_kv_len, sms, &plan))
+        return LAT_ERR_UNSUPPORTED;
+    if (workspace == nullptr || workspace_bytes < plan.total_bytes ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return LAT_ERR_WORKSPACE;
+    lat::Q8DecodeArgs a{};
+    fill_split_args(a, plan, q, q_rs, kv_lens, max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim,
+                    window, scale, softcap, workspace, status, timeout_ns, skip_load);
+    a.cache = static_cast<const unsigned char *>(cache);
+    a.cache_block = cache_block_stride;
+    a.cache_head = cache_head_stride;
+    a.cache_seq = cache_seq_stride;
+    while (1 << a.block_shift < block_size) ++a.block_shift;
+    return lat::launch_decode_q8(a, dt == LAT_BF16, plan, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? LAT_OK
+               : LAT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lat_kv_q8_block_bytes(int head_dim, int block_size) {
+    return supported_head_dim(head_dim) && lat::q8_block_size_ok(block_size) ? lat::q8_block_bytes(head_dim, block_size) : 0;
+}
+
+lat_status lat_kv_append_q8(lat_dtype dt, void *cache, int64_t cache_block_stride, int64_t cache_head_stride,
+                            int64_t cache_seq_stride, int block_size, int capacity, const void *k_new,
+                            const void *v_new, int64_t new_rs, const int32_t *pos, int n_new, int batch,
+                            int n_kv_heads, int head_dim, int32_t *status, void *stream) {
+    return q8_store_impl(dt, cache, cache_block_stride, cache_head_stride, cache_seq_stride, block_size, capacity,
+                         k_new, v_new, nullptr, nullptr, new_rs, pos, n_new, batch, n_kv_heads, head_dim, false,
+                         status, stream);
+}
+
+lat_status lat_kv_expand_q8(lat_dtype dt, const void *cache, int64_t cache_block_stride, int64_t cache_head_stride,
+                            int64_t cache_seq_stride, int block_size, int capacity, void *k_out, void *v_out,
+                            int64_t out_rs, const int32_t *pos, int n_rows, int batch, int n_kv_heads, int head_dim,
+                            int32_t *status, void *stream) {
+    return q8_store_impl(dt, const_cast<void *>(cache), cache_block_stride, cache_head_stride, cache_seq_stride,
+                         block_size, capacity, nullptr, nullptr, k_out, v_out, out_rs, pos, n_rows, batch, n_kv_heads,
+                         head_dim, true, status, stream);
+}
+
+size_t lat_attn_decode_q8_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                         int max_kv_len) {
+    if ((dt != LAT_F32 && dt != LAT_BF16) || batch < 0 || batch > 65535 || n_heads <= 0 || n_kv_heads <= 0 ||
+        n_heads % n_kv_heads != 0 || !supported_head_dim(head_dim) || !query_row_ok(n_heads, head_dim) ||
+        max_kv_len < 0)
+        return 0;
+    int sms = 0;
+    lat::SplitPlan plan;
+    if (!current_sm_count(&sms) ||
+        !lat::plan_decode_q8(batch, n_heads, n_kv_heads, head_dim, dt == LAT_BF16, max_kv_len, sms, &plan))
+        return 0;
+    return plan.total_bytes;
+}
+
+lat_status lat_attn_decode_q8(lat_dtype dt, const void *q, int64_t q_rs, const void *cache,
+                              int64_t cache_block_stride, int64_t cache_head_stride, int64_t cache_seq_stride,
+                              int block_size, const int32_t *kv_lens, int max_kv_len, void *out, int64_t out_rs,
+                              float *lse, int batch, int n_heads, int n_kv_heads, int head_dim, int window,
+                              float scale, float softcap, void *workspace, size_t workspace_bytes, int32_t *status,
+                              void *stream) {
+    return q8_decode_impl(dt, q, q_rs, cache, cache_block_stride, cache_head_stride, cache_seq_stride, block_size,
+                          kv_lens, max_kv_len, out, out_rs, lse, batch, n_heads, n_kv_heads, head_dim, window, scale,
+                          softcap, workspace, workspace_bytes, status, stream, kDefaultTimeoutNs, 0);
+}
+
+lat_status lat_test_decode_q8_timeout(lat_dtype dt, const void *q, int64_t q_rs, const void *cache,
+                                      int64_t cache_block_stride, int64_t cache_head_stride, int64_t cache_seq_stride,
+                                      int block_size, const int32_t *kv_lens, int max_kv_len, void *out,
+                                      int64_t out_rs, int batch, int n_heads, int n_kv_heads, int head_dim,
+                                      void *workspace, size_t workspace_bytes, uint64_t timeout_ns, int32_t *status,
+                                      void *stream) {
+    return q8_decode_impl(dt, q, q_rs, cache, cache_block_stride, cache_head_stride, cache_seq_stride, block_size,
+                          kv_lens, max_kv_len, out, out_rs, nullptr, batch, n_heads, n_kv_heads, head_dim, 0, 0.125f,
+                          0.f, workspace, workspace_bytes, status, stream, timeout_ns, 1);
 }
 
 }  // extern "C"

@@ -67,8 +67,8 @@ struct Q4StoreArgs {
 // batch * n * n_kv_heads < 2^31
 cudaError_t launch_q4_store(const Q4StoreArgs &a, bool bf16, bool expand, cudaStream_t s);
 
-struct Q4DecodeArgs {
-    CUtensorMap tm;  // map of 32-bit words over the rows below max_kv_len
+// a split-KV decode over a packed cache (unit_stream.cuh)
+struct SplitDecodeArgs {
     const void *q;
     int64_t q_rs;
     const int32_t *kv_lens;
@@ -88,13 +88,48 @@ struct Q4DecodeArgs {
     int test_skip_load;    // test hook: a warp's first copy of a CTA never comes (forces a timeout)
     int32_t *status;
 };
-struct Q4Plan {
-    int grid, wide, twin, whole, min_tiles, max_splits, box_rows, defer_join;
+struct SplitPlan {
+    int grid, whole, min_tiles, max_splits, defer_join;
     size_t part_o_bytes, part_lse_bytes, total_bytes;
+};
+
+struct Q4DecodeArgs : SplitDecodeArgs {
+    CUtensorMap tm;  // map of 32-bit words over the rows below max_kv_len
+};
+struct Q4Plan : SplitPlan {
+    int wide, twin, box_rows;
 };
 bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,
                     Q4Plan *p);
 cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, const Q4Plan &p, cudaStream_t s);
+
+// ---------------------------------------------------------------- 8-bit KV cache
+struct Q8StoreArgs {
+    unsigned char *cache;                        // records (q8_block.cuh); strides in bytes
+    int64_t cache_block, cache_head, cache_seq;
+    int block_shift;                             // log2 of block_size
+    const void *k, *v;                           // append: the new rows
+    void *k_out, *v_out;                         // expand: the rows read back
+    int64_t rs;                                  // their row stride in elements
+    int vec;                                     // 16-byte vectors on that side
+    const int32_t *pos;
+    int capacity, n, batch, n_kv_heads, head_dim;
+    int touched;                                 // append: blocks that n rows can lie in
+    int64_t units;                               // append: 2 * batch * touched * n_kv_heads; expand: batch * n * n_kv_heads
+    FastDiv by_heads, by_n, by_touched;
+    int32_t *status;
+};
+// units < 2^31
+cudaError_t launch_q8_store(const Q8StoreArgs &a, bool bf16, bool expand, cudaStream_t s);
+
+struct Q8DecodeArgs : SplitDecodeArgs {
+    const unsigned char *cache;
+    int64_t cache_block, cache_head, cache_seq;  // bytes
+    int block_shift;
+};
+bool plan_decode_q8(int batch, int n_heads, int n_kv_heads, int head_dim, bool bf16, int max_kv_len, int num_sms,
+                    SplitPlan *p);
+cudaError_t launch_decode_q8(const Q8DecodeArgs &a, bool bf16, const SplitPlan &p, cudaStream_t s);
 
 // ---------------------------------------------------------------- choice of cached blocks
 struct BoundsArgs {

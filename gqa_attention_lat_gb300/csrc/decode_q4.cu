@@ -55,21 +55,13 @@
 #include "q4_row.cuh"
 #include "score_cap.cuh"
 #include "split_join.cuh"
+#include "unit_stream.cuh"
 
 namespace lat {
 
 namespace {
 
-constexpr int kHeads = 8;                  // N of the mma: query heads of a unit
 constexpr int kTwinHeads = 4;              // heads of a unit that fill N twice
-constexpr float kRescaleBy = 8.0f;         // log2 units the maximum may grow unnoticed
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kPieceRing = 8;              // pieces known ahead
-// What a unit costs beside its tiles (its queries made ready, the warps' states joined), in
-// tiles: counted in the shares, so that a CTA of many short units is not the last to finish (32
-// sequences of 1 to 4096 keys: not counted 36.8 us, as 2 tiles 30.5 us).
-constexpr int kUnitCost = 2;
-
 // The more keys a warp takes at once, the further a tile's fixed costs spread, until its registers
 // cost CTAs (8 x 131072 keys, 16 times kSub keys: head_dim 64 2 163 us, 3 152, 4 143; 80 2 209,
 // 3 198, 4 200; 256 2 479, 3 876).  At head_dim 128 that comes with tiles too coarse for short
@@ -116,86 +108,6 @@ struct Q4Cfg {
     static_assert(kSmem <= 232448, "shared memory budget");
     static_assert(kStageBytes % 128 == 0, "TMA destinations");
 };
-
-struct Piece {
-    int b, hk, hb;     // unit
-    int key0, keys;    // first key, keys of the piece (the last tile may be partial)
-    int slot, nseg;    // which piece of how many
-    int end;           // no more pieces
-};
-
-struct Join {          // a unit cut across CTAs that this one may have to join
-    int b, h_base, g_cnt, nseg, unit, last;
-};
-
-struct KeyRange {
-    int lo, n;
-};
-__device__ __forceinline__ KeyRange range_of(const Q4DecodeArgs &a, int len) {
-    KeyRange k{0, 0};
-    if (len < 0 || len > a.max_kv_len) return k;  // reported once, by CTA 0
-    k.lo = a.window > 0 ? max(0, len - a.window) : 0;
-    k.n = len - k.lo;
-    return k;
-}
-
-// The stream of `total` tiles in equal shares: the first `more` CTAs have each + 1, the others each
-struct Shares {
-    uint32_t each, more;
-    __device__ __forceinline__ uint32_t begin(uint32_t c) const { return each * c + min(c, more); }
-    __device__ __forceinline__ uint32_t of(uint32_t x) const {  // whose tile x is
-        const uint32_t b = more * (each + 1);
-        return x < b ? x / (each + 1) : more + (x - b) / each;
-    }
-};
-// thread 0's place in the stream
-struct Walk {
-    uint32_t pos, end, pb;  // pb: where sequence b's units begin
-    Shares shares;
-    int b;
-};
-
-// a unit of n keys in the stream: nothing, or its tiles and what it costs beside them; where no
-// unit is to be cut (a.whole), as much as the longest
-template <int T>
-__device__ __forceinline__ uint32_t tiles_of(int n) {
-    return ((uint32_t)n + (T - 1)) / T;
-}
-template <int T>
-__device__ __forceinline__ uint32_t unit_cost(const Q4DecodeArgs &a, int n) {
-    return n <= 0 ? 0u : a.whole ? (uint32_t)a.min_tiles : tiles_of<T>(n) + kUnitCost;
-}
-template <int T>
-__device__ bool next_piece(const Q4DecodeArgs &a, Walk &w, int HB, Piece &p) {
-    const uint32_t HU = (uint32_t)(a.n_kv_heads * HB);
-    while (w.pos < w.end && w.b < a.batch) {
-        const KeyRange k = range_of(a, a.kv_lens[w.b]);
-        const uint32_t cost = unit_cost<T>(a, k.n), nt = tiles_of<T>(k.n), all = cost * HU;
-        if (w.pos >= w.pb + all) {
-            w.pb += all;
-            ++w.b;
-            continue;
-        }
-        const uint32_t idx = (w.pos - w.pb) / cost, ustart = w.pb + idx * cost + kUnitCost;  // its first tile
-        const uint32_t uend = ustart + nt;                                                       // behind its last
-        const uint32_t t0 = w.pos > ustart ? w.pos - ustart : 0, t1 = w.end > ustart ? min(nt, w.end - ustart) : 0;
-        const bool cut = w.pos > ustart;  // (divisions only for units that leave this share)
-        w.pos = min(w.end, w.pb + (idx + 1) * cost);
-        if (t0 >= t1) continue;  // the share ends before the unit's first tile
-        const uint32_t first = cut ? w.shares.of(ustart) : blockIdx.x, last = uend > w.end ? w.shares.of(uend - 1) : blockIdx.x;
-        p.b = w.b;
-        p.hk = HB == 1 ? (int)idx : (int)(idx / HB);
-        p.hb = HB == 1 ? 0 : (int)(idx % HB);
-        p.key0 = k.lo + (int)t0 * T;
-        p.keys = (int)(min((uint32_t)k.n, t1 * T) - t0 * T);
-        p.slot = (int)(blockIdx.x - first);
-        p.nseg = (int)(last - first + 1);
-        p.end = 0;
-        return true;
-    }
-    p.end = 1;
-    return false;
-}
 
 // N consecutive 32-bit words at byte `off` of a row, in the widest loads their count allows
 template <typename C, int N>
@@ -248,13 +160,6 @@ __device__ __forceinline__ void split_f16(uint32_t (&o)[TERMS][4], const float (
         }
     }
 }
-// the power of two that brings m >= 0 to [2^to, 2^(to + 1)), as near as floats have one; 1 for
-// nothing, NaN for what is not finite
-__device__ __forceinline__ float to_f16_range(float m, int to) {
-    const int e = (int)(__float_as_uint(m) >> 23);
-    if (e == 255) return NAN;
-    return m == 0.f ? 1.f : __uint_as_float((uint32_t)max(1, min(254, 127 + to + 127 - e)) << 23);
-}
 __device__ __forceinline__ uint32_t hsub2_f16(uint32_t x, uint32_t y) {
     const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
     return *reinterpret_cast<const uint32_t *>(&d);
@@ -270,20 +175,6 @@ __device__ __forceinline__ uint32_t f16_codes(uint32_t w, int shift, uint32_t bi
 __device__ __forceinline__ uint32_t f16_bias(uint32_t w, int shift) {
     return ((((w >> 16) & 0xfu) * 0x00010001u) << shift) | 0x64006400u;
 }
-__device__ __forceinline__ void mma_f16_16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ int add_acq_rel(int32_t *p, int x) {
-    int was;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(was) : "l"(p), "r"(x) : "memory");
-    return was;
-}
-
 // x and y plus `by` (a bf16) times the halves of a bf16 pair, without unpacking it (the logic
 // pipe's work)
 __device__ __forceinline__ void add_pair(float &x, float &y, uint32_t pair, uint16_t by) {
@@ -320,82 +211,22 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     float *park = reinterpret_cast<float *>(sQ + C::kQBytes);                // [warp][head][channel]
     unsigned char *misc = reinterpret_cast<unsigned char *>(park) + C::kParkBytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(misc);                     // [warp][stage]
-    Piece *pieces = reinterpret_cast<Piece *>(misc + 128);                   // [kPieceRing]
-    float *sM = reinterpret_cast<float *>(misc + 384);                       // [warp][m[8], l[8]]
-    Walk *walk = reinterpret_cast<Walk *>(misc + 640);
-    uint32_t *scan = reinterpret_cast<uint32_t *>(misc + 704);               // [warps]
-    volatile int *abort_flag = reinterpret_cast<int *>(misc + 768);
-    Join *joins = reinterpret_cast<Join *>(misc + 784);                      // [2]
-    static_assert(sizeof(Piece) * kPieceRing <= 256 && sizeof(Walk) <= 64 && sizeof(Join) * 2 <= 64, "misc area");
+    float *sM = reinterpret_cast<float *>(misc + 128);                       // [warp][m[8], l[8]]
+    StreamState &st = *reinterpret_cast<StreamState *>(misc + 384);
+    Piece *pieces = st.pieces;
+    volatile int *abort_flag = &st.abort_flag;
+    static_assert(sizeof(StreamState) <= C::kMisc - 384, "misc area");
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = a.n_heads / a.n_kv_heads, HB = (G + kHeads - 1) / kHeads, HU = a.n_kv_heads * HB;
+    const int G = a.n_heads / a.n_kv_heads, HB = (G + kHeads - 1) / kHeads;
     constexpr int TK = C::kTileKeys;
 
-    // ---- the stream's length in tiles and this CTA's share: per-thread sums over a slice of
-    // the sequences, then a scan ----------------------------------------------------------
-    const int per_thread = (a.batch + C::kThreads - 1) / C::kThreads;
-    const int b_lo = min(a.batch, tid * per_thread), b_hi = min(a.batch, b_lo + per_thread);
-    uint32_t my_sum = 0;
-    for (int b = b_lo; b < b_hi; ++b) {
-        const int len = a.kv_lens[b];
-        const KeyRange k = range_of(a, len);
-        my_sum += unit_cost<TK>(a, k.n) * HU;
-        if (blockIdx.x == 0 && k.n == 0) {  // nothing to stream
-            const bool bad = len < 0 || len > a.max_kv_len;
-            if (bad) report_status(a.status, kErrBounds);
-            for (int h = 0; h < a.n_heads; ++h) {
-                if (a.defer_join) a.piece_count[(int64_t)b * a.n_heads + h] = 0;
-                if (!bad && a.lse != nullptr) a.lse[(int64_t)b * a.n_heads + h] = -INFINITY;
-            }
-            if (!bad)
-                for (int i = 0; i < a.n_heads * D; ++i) static_cast<T *>(a.out)[(int64_t)b * a.out_rs + i] = T(0.f);
-        }
-    }
-    uint32_t incl = my_sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
-    }
-    if (lane == 31) scan[warp] = incl;
     if (tid == 0) {
-        walk->pos = 0;
-        walk->end = 0;
-        walk->b = a.batch;
         for (int i = 0; i < C::kWarps * C::kStages; ++i) mbar_init(&full[i], 1);
-        *abort_flag = 0;
-        joins[0].nseg = joins[1].nseg = joins[0].last = joins[1].last = 0;
         fence_mbarrier_init();
         if (a.max_kv_len > 0) tma_prefetch_desc(&a.tm);  // (else there is none)
     }
-    __syncthreads();
-    uint32_t total = 0, my_start = incl - my_sum;
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-        const uint32_t v = scan[w];
-        if (w < warp) my_start += v;
-        total += v;
-    }
-    const uint32_t parts = max(1u, min(gridDim.x, total / (uint32_t)a.min_tiles)), each = total / parts;
-    const Shares shares{each, total - each * parts};
-    const uint32_t r0 = blockIdx.x < parts ? shares.begin(blockIdx.x) : 0;
-    const uint32_t r1 = blockIdx.x < parts ? shares.begin(blockIdx.x + 1) : 0;
-    if (r0 < r1 && r0 >= my_start && r0 - my_start < my_sum) {  // the share begins in this slice
-        uint32_t p = my_start;
-        int b = b_lo;
-        for (; b < b_hi; ++b) {
-            const uint32_t w = unit_cost<TK>(a, range_of(a, a.kv_lens[b]).n) * HU;
-            if (r0 < p + w) break;
-            p += w;
-        }
-        Walk w{r0, r1, p, shares, b};
-        next_piece<TK>(a, w, HB, pieces[0]);
-        *walk = w;
-    }
-    if (a.defer_join) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (r0 >= r1) return;
-    __syncthreads();
+    if (!stream_begin<TK, 1, C::kWarps, T>(a, HB, D, st)) return;
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
 
     // ---- this warp's copies -------------------------------------------------------------
@@ -449,9 +280,9 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     for (int s = 1; s < C::kStages; ++s) issue(known);
     auto one_more = [&]() {  // another entry for the table, by thread 0
         if (tid == 0 && !pieces[(known - 1) % kPieceRing].end) {
-            Walk w = *walk;
-            next_piece<TK>(a, w, HB, pieces[known % kPieceRing]);
-            *walk = w;
+            Walk w = st.walk;
+            next_piece<TK, 1>(a, w, HB, pieces[known % kPieceRing]);
+            st.walk = w;
         }
     };
     one_more();
@@ -513,9 +344,6 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                 }
             }
         };
-        auto larger = [](float x, float y) {  // of two magnitudes, by their bits: a NaN is above all
-            return __uint_as_float(max(__float_as_uint(x), __float_as_uint(y)));
-        };
         auto scaled = [](float (&v)[8], float by) {  // returns the sum
             float z = 0.f;
 #pragma unroll
@@ -533,7 +361,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     float v[8];
                     octet(raw[g], v);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) m = larger(m, fabsf(v[k]));
+                    for (int k = 0; k < 8; ++k) m = larger_magnitude(m, fabsf(v[k]));
                 }
             } else {  // magnitudes as whole numbers, two at a time
                 uint32_t m2 = 0;
@@ -543,10 +371,10 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) m2 = __vmaxu2(m2, w[k] & 0x7fff7fffu);
                 }
-                m = larger(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+                m = larger_magnitude(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
             }
-            m = larger(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = larger(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = larger_magnitude(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = larger_magnitude(m, __shfl_xor_sync(0xffffffffu, m, 2));
             const float by = to_f16_range(m, C::kQTo);
             undo(0, __shfl_sync(0xffffffffu, by, 8 * c));  // lane 4 h holds head h
             undo(1, __shfl_sync(0xffffffffu, by, 8 * c + 4));
@@ -579,10 +407,10 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
                     load(h, 8 * o, x);
                     octet(x, v);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) m = larger(m, fabsf(v[k]));
+                    for (int k = 0; k < 8; ++k) m = larger_magnitude(m, fabsf(v[k]));
                 }
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, off));
+                for (int off = 16; off > 0; off >>= 1) m = larger_magnitude(m, __shfl_xor_sync(0xffffffffu, m, off));
                 const float by = to_f16_range(m, C::kQTo);
                 for (int o0 = 0; o0 < kOcts; o0 += 32) {
                     const int o = min(o0 + lane, kOcts - 1);  // (a group's four lanes are all there or none)
@@ -883,7 +711,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
         cp_async_wait<0>();  // the next unit's queries
         __syncthreads();     // the table has grown; sM, park and sQ are free
         if (tid == 0 && !single && n_joins < 2)  // at most a CTA's first and last piece
-            joins[n_joins++] = Join{p.b, h_base, g_cnt, p.nseg, (p.b * a.n_kv_heads + p.hk) * HB + p.hb, 0};
+            st.joins[n_joins++] = Join{p.b, h_base, g_cnt, p.nseg, (p.b * a.n_kv_heads + p.hk) * HB + p.hb, 0};
         if (!pieces[(known - 1) % kPieceRing].end) ++known;
         issue_all();
     }
@@ -897,59 +725,7 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
             mbar_wait_bounded(&my_full[used % C::kStages], (used / C::kStages) & 1, &no_abort, until);
         if (warp == 0 && *abort_flag) report_status(a.status, kErrTimeout);
     }
-    if (a.defer_join) return;
-    // ---- the units whose last piece was this CTA's: weights 2^{lse_c - lse} over their pieces ----
-    __syncthreads();  // every thread's partials are written
-    if (*abort_flag) return;
-    // (each thread's partials happen before the barrier, that before the ticket's release; a last
-    // ticket's acquire before the next barrier, that before the reads, which skip L1)
-    if (lane == 0 && warp < 2 && joins[warp].nseg > 0)  // a ticket a warp: they take a round trip each
-        joins[warp].last = add_acq_rel(a.counters + joins[warp].unit, 1) == joins[warp].nseg - 1;
-    __syncthreads();
-    for (int k = 0; k < 2; ++k) {
-        const Join j = joins[k];
-        if (!j.last) continue;
-        for (int v = tid; v < j.g_cnt * (D / 4); v += C::kThreads) {
-            const int h = j.h_base + v / (D / 4), d = 4 * (v % (D / 4));
-            const int64_t bh = (int64_t)j.b * a.n_heads + h;
-            const float *pl = a.part_lse + bh * a.max_splits;
-            const float *po = a.part_o + bh * a.max_splits * D + d;
-            float m = -INFINITY, z = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAhead = 8;  // pieces in flight
-            for (int s0 = 0; s0 < j.nseg; s0 += kAhead) {
-                float l[kAhead], mn = m;
-                float4 w[kAhead];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const bool there = s0 + i < j.nseg;
-                    l[i] = there ? __ldcg(pl + s0 + i) : -INFINITY;
-                    w[i] = there ? __ldcg(reinterpret_cast<const float4 *>(po + (int64_t)(s0 + i) * D))
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) mn = fmaxf(mn, l[i]);
-                const float base = mn == -INFINITY ? 0.f : mn, cf = fast_exp2(m - base);
-                z *= cf; o.x *= cf; o.y *= cf; o.z *= cf; o.w *= cf;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const float e = fast_exp2(l[i] - base);
-                    z += e;
-                    o.x = fmaf(e, w[i].x, o.x); o.y = fmaf(e, w[i].y, o.y);
-                    o.z = fmaf(e, w[i].z, o.z); o.w = fmaf(e, w[i].w, o.w);
-                }
-                m = mn;
-            }
-            const float rz = z == 0.f ? 0.f : 1.f / z;
-            T *dst = static_cast<T *>(a.out) + (int64_t)j.b * a.out_rs + (int64_t)h * D + d;
-            if constexpr (F32)
-                *reinterpret_cast<float4 *>(dst) = make_float4(o.x * rz, o.y * rz, o.z * rz, o.w * rz);
-            else
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(o.x * rz, o.y * rz), pack_bf16x2(o.z * rz, o.w * rz));
-            if (d == 0 && a.lse != nullptr) a.lse[bh] = (m + log2f(z)) * kLn2;
-        }
-        if (tid == 0) a.counters[j.unit] = 0;  // ready for the next call
-    }
+    stream_join<D, F32, C::kThreads>(a, st);
 }
 
 template <int D, bool F32, bool Wide, bool Twin>
@@ -1023,32 +799,9 @@ bool plan_decode_q4(int batch, int n_heads, int n_kv_heads, int head_dim, bool b
                     Q4Plan *p) {
     const int G = n_heads / n_kv_heads, HB = (G + kHeads - 1) / kHeads;
     const int64_t units = (int64_t)batch * n_kv_heads * HB;
-    // join grid: one CTA per (sequence, query head, up to 128 channels)
-    if ((int64_t)batch * n_heads * ((head_dim + 127) / 128) > 0x7fffffffLL) return false;
     const int tile = shape(head_dim, bf16, G <= kTwinHeads, p, num_sms, units, max_kv_len);
     if (tile == 0) return false;
-    // A unit of n tiles falls into at most n / min_tiles + 2 pieces.  min_tiles keeps that count
-    // near 64 or, with few units, near the number of CTAs that each unit must feed.
-    const int64_t range = ((int64_t)std::max(max_kv_len, 1) + tile - 1) / tile;
-    if (units * (range + kUnitCost) > 0x7fffffffLL) return false;
-    const int64_t target = std::max<int64_t>(64, (p->grid + std::max<int64_t>(units, 1) - 1) / std::max<int64_t>(units, 1));
-    p->min_tiles = (int)std::max<int64_t>(1, (range + target - 1) / target);
-    // Units of up to two tiles, no more than the CTAs: one each, and nothing to join (8 KV heads,
-    // head_dim 64: one sequence of 512 keys 7.3 instead of 8.0 us, 32 ragged ones of up to 512 8.6
-    // instead of 10.2; with three tiles it gains nothing).
-    p->whole = range <= 2 && units <= p->grid;
-    if (p->whole) p->min_tiles = (int)range + kUnitCost;
-    p->max_splits = (int)((range + p->min_tiles - 1) / p->min_tiles) + 2;
-    // With few units, cut finely, the CTA that joins one would read tens of partials after its
-    // stream; a second kernel takes them then.
-    p->defer_join = units * 8 < p->grid && p->max_splits > 16;
-    auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
-    const size_t rows = (size_t)batch * n_heads;
-    p->part_o_bytes = round256(rows * p->max_splits * head_dim * 4);
-    p->part_lse_bytes = round256(rows * p->max_splits * 4);
-    // pieces per (sequence, head), or tickets per unit
-    p->total_bytes = p->part_o_bytes + p->part_lse_bytes + round256((p->defer_join ? rows : (size_t)units) * 4);
-    return true;
+    return plan_units(p, units, ((int64_t)std::max(max_kv_len, 1) + tile - 1) / tile, (int64_t)batch * n_heads, head_dim);
 }
 
 cudaError_t launch_decode_q4(const Q4DecodeArgs &a, bool bf16, const Q4Plan &p, cudaStream_t s) {

@@ -399,6 +399,92 @@ lat_status lat_attn_decode_q4(lat_dtype dt, const void *q, int64_t q_rs, const v
                               int32_t *status, void *stream);
 
 /*
+ * The 8-bit KV cache: lat_kv_q8_block_bytes, lat_kv_append_q8, lat_kv_expand_q8 and
+ * lat_attn_decode_q8.  Half of a 16-bit cache's bytes, with one scale for K and one for V per
+ * block of block_size tokens (16, 32, 64 or 128, else LAT_ERR_INVALID_ARG) and KV head.
+ *
+ * One record holds one block of one KV head: lat_kv_q8_block_bytes(head_dim, block_size) bytes
+ * (block_size * 2 * head_dim of codes, the two scales, padding to 128; 0 for sizes not built).
+ * Block n of sequence b and KV head hk (cache rows n*block_size .. (n+1)*block_size - 1) is at byte
+ * b*cache_seq_stride + n*cache_block_stride + hk*cache_head_stride of `cache`: these three
+ * strides are positive multiples of 16, and the cache is 16-byte aligned, else
+ * LAT_ERR_INVALID_ARG (multiples of 128 read a little fewer lines).  A cache of `capacity` rows
+ * has ceil(capacity / block_size) blocks, each whole.
+ *
+ * A code is an e4m3 number (4 bits of exponent, 3 of mantissa) and stands for code * 2^e, e in
+ * -100 .. 119 the block's: the least with which its largest finite magnitude is at most 448 * 2^e.
+ * A value is off by at most 2^-4 of itself, or by 2^(e - 10) where it is smaller than 2^(e - 6);
+ * what reads back is exact in bf16.  Magnitudes above 448 * 2^119 (2.98e38) read back as that; an
+ * infinity or a NaN reads back as NaN, and no other value of the block is touched by it.
+ */
+int64_t lat_kv_q8_block_bytes(int head_dim, int block_size);
+
+/*
+ * lat_kv_append_q8 — lat_kv_append into an 8-bit cache: row pos[b] + t of sequence b takes new row
+ * t, for t < n_new.  New rows as in lat_kv_append (element (b,t,hk,d) at k_new[(b*n_new +
+ * t)*new_rs + hk*head_dim + d]); dt is their type.  A block that the new rows begin takes its
+ * scale from them.  Where they go on in a block begun earlier, its scale grows if they need it, and
+ * the codes of the rows before them are rounded to the new scale (exactly, but for values below
+ * 2^(e - 6) of the new e); rows behind the new ones keep their bytes.  So whole blocks in one
+ * call are rounded once; a token at a time, small values may be rounded more than once.
+ * A sequence whose rows would fall outside [0, capacity) is skipped whole and sets *status =
+ * LAT_ERR_BOUNDS.  2 * batch * n_kv_heads * (blocks that n_new rows can touch) < 2^31, else
+ * LAT_ERR_UNSUPPORTED.
+ */
+lat_status lat_kv_append_q8(lat_dtype dt, void *cache, int64_t cache_block_stride,
+                            int64_t cache_head_stride, int64_t cache_seq_stride, int block_size,
+                            int capacity, const void *k_new, const void *v_new, int64_t new_rs,
+                            const int32_t *pos, int n_new, int batch, int n_kv_heads,
+                            int head_dim, int32_t *status, void *stream);
+
+/*
+ * lat_kv_expand_q8 — the reverse: rows pos[b] .. pos[b] + n_rows - 1 of sequence b read back as
+ * K and V rows of type dt (element (b,t,hk,d) at k_out[(b*n_rows + t)*out_rs + hk*head_dim + d],
+ * v_out alike), the layout that lat_attn_prefill takes.  Other rules as in lat_kv_append_q8
+ * (batch * n_rows * n_kv_heads < 2^31); a sequence out of range leaves its output rows as they
+ * were.
+ */
+lat_status lat_kv_expand_q8(lat_dtype dt, const void *cache, int64_t cache_block_stride,
+                            int64_t cache_head_stride, int64_t cache_seq_stride, int block_size,
+                            int capacity, void *k_out, void *v_out, int64_t out_rs,
+                            const int32_t *pos, int n_rows, int batch, int n_kv_heads,
+                            int head_dim, int32_t *status, void *stream);
+
+/*
+ * lat_attn_decode_q8 — lat_attn_decode_softcap over an 8-bit cache: one query token per sequence,
+ * at position kv_lens[b] - 1, over the cached keys max(0, kv_lens[b] - window) .. kv_lens[b] - 1
+ * (all of them when window <= 0), keys and values as they read back; softcap finite and >= 0, 0 =
+ * none (one above 1e36 counts as 1e36).  dt is the type of q and out.  q, out, lse, kv_lens,
+ * max_kv_len and the status are lat_attn_decode's; a sequence of length 0 gets out = 0, lse =
+ * -inf.  q and out must be 16-byte aligned and their row strides multiples of 16 bytes, else
+ * LAT_ERR_INVALID_ARG.  Every sequence's cache must hold at least ceil(max_kv_len / block_size)
+ * blocks; rows outside the visible ones may hold any bytes.
+ * workspace: at least lat_attn_decode_q8_workspace_size(...) bytes of device memory with the same
+ * sizes and dt, 256-byte aligned, else LAT_ERR_WORKSPACE; the rules of lat_attn_decode's
+ * workspace hold (zero-filled before its first use with a given layout, and again after
+ * LAT_ERR_TIMEOUT; calls sharing one must not overlap on the GPU; its size depends on the current
+ * device's SM count).
+ * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, n_heads * head_dim < 2^31, batch * n_heads *
+ * ceil(head_dim / 128) < 2^31, and batch * n_kv_heads * ceil(n_heads / n_kv_heads / 8) work units of
+ * up to ceil(max_kv_len / 64) + 2 tiles < 2^31 in all.
+ * Sums, maxima and the joins are fp32.  A softmax weight that meets the values is held to 11 bits
+ * for LAT_BF16 (2^-12 of it; the output's own rounding to bf16 is the error that shows) and to 22
+ * for LAT_F32, and below 2^-21 of the largest weight (times its block's scale) to 2^-32 of that;
+ * the log-sum-exp has none of this.  A query's channels are exact from 2^-22 of its largest on
+ * (LAT_F32: within 2^-23 of themselves, or 2^-33 of the largest).
+ * A query that holds a NaN or an infinity gives NaN, as does a visible key that holds a NaN.
+ */
+size_t lat_attn_decode_q8_workspace_size(lat_dtype dt, int batch, int n_heads, int n_kv_heads,
+                                         int head_dim, int max_kv_len);
+lat_status lat_attn_decode_q8(lat_dtype dt, const void *q, int64_t q_rs, const void *cache,
+                              int64_t cache_block_stride, int64_t cache_head_stride,
+                              int64_t cache_seq_stride, int block_size, const int32_t *kv_lens,
+                              int max_kv_len, void *out, int64_t out_rs, float *lse, int batch,
+                              int n_heads, int n_kv_heads, int head_dim, int window, float scale,
+                              float softcap, void *workspace, size_t workspace_bytes,
+                              int32_t *status, void *stream);
+
+/*
  * Attention over chosen blocks of a long cache: lat_kv_block_bounds, lat_attn_select_blocks
  * and lat_attn_decode_blocks.  A decode step that reads a fixed number of blocks of
  * block_size keys instead of the whole cache, chosen anew for each query by a bound of the

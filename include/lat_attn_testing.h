@@ -59,6 +59,14 @@ lat_status lat_test_decode_q4_timeout(lat_dtype dt, const void *q, int64_t q_rs,
                                       int64_t out_rs, int batch, int n_heads, int n_kv_heads,
                                       int head_dim, void *workspace, size_t workspace_bytes,
                                       uint64_t timeout_ns, int32_t *status, void *stream);
+lat_status lat_test_decode_q8_timeout(lat_dtype dt, const void *q, int64_t q_rs,
+                                      const void *cache, int64_t cache_block_stride,
+                                      int64_t cache_head_stride, int64_t cache_seq_stride,
+                                      int block_size, const int32_t *kv_lens, int max_kv_len,
+                                      void *out, int64_t out_rs, int batch, int n_heads,
+                                      int n_kv_heads, int head_dim, void *workspace,
+                                      size_t workspace_bytes, uint64_t timeout_ns,
+                                      int32_t *status, void *stream);
 lat_status lat_test_decode_blocks_timeout(const void *q, int64_t q_rs, const void *k_cache,
                                           const void *v_cache, int64_t cache_rs,
                                           int64_t cache_head_stride, int64_t cache_seq_stride,
