@@ -91,6 +91,13 @@ _SIGNATURES = {
     "lat_attn_decode_q8": (_I32, [_I32, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I32, _P, _I64,
                                   _P, _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P, _SZ, _P,
                                   _P]),
+    "lat_attn_key_weights": (_I32, [_I32, _P, _I64, _I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P,
+                                    _I64, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _F32, _P,
+                                    _P]),
+    "lat_kv_evict_choose": (_I32, [_P, _I64, _I64, _P, _I32, _P, _I32, _I32, _I32, _P, _I64, _I64,
+                                   _P, _I32, _I32, _P, _P]),
+    "lat_kv_evict_rows": (_I32, [_I32, _P, _P, _I64, _I64, _I64, _I32, _P, _I32, _I32, _I32, _I32,
+                                 _P, _P]),
     "lat_kv_block_bounds": (_I32, [_I32, _P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64, _I32,
                                    _P, _I32, _I32, _I32, _I32, _P, _P]),
     "lat_attn_select_blocks_workspace_size": (_SZ, [_I32, _I32, _I32, _I32]),
@@ -112,6 +119,8 @@ _SIGNATURES = {
     "lat_test_decode_blocks_timeout": (_I32, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _I32,
                                               _P, _I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _SZ,
                                               _U64, _P, _P]),
+    "lat_test_key_weights_timeout": (_I32, [_P, _I64, _I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P,
+                                            _I64, _I64, _I32, _I32, _I32, _I32, _U64, _P, _P]),
     "lat_test_capped_scores": (_I32, [_P, _I64, _F32, _F32, _P, _P]),
 }
 
@@ -408,6 +417,37 @@ def lat_attn_decode_q8(dt, q, q_rs, cache, cache_block_stride, cache_head_stride
         "lat_attn_decode_q8")
 
 
+def lat_attn_key_weights(dt, q, q_rs, n_q, k_cache, cache_rs, cache_head_stride,
+                         cache_seq_stride, kv_lens, max_kv_len, lse, weights,
+                         weights_head_stride, weights_seq_stride, batch, n_heads, n_kv_heads,
+                         head_dim, causal, window, scale, softcap, status=None, stream=None):
+    """Add what the last n_q query rows gave each cached key onto fp32 weights."""
+    _check(_calls().lat_attn_key_weights(
+        dt, q, q_rs, n_q, k_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,
+        max_kv_len, lse, weights, weights_head_stride, weights_seq_stride, batch, n_heads,
+        n_kv_heads, head_dim, int(bool(causal)), window, scale, softcap, status,
+        _stream(stream)), "lat_attn_key_weights")
+
+
+def lat_kv_evict_choose(weights, weights_head_stride, weights_seq_stride, kv_lens, max_kv_len,
+                        kept, n_keep, n_first, n_last, weights_out, out_head_stride,
+                        out_seq_stride, new_lens, batch, n_kv_heads, status=None, stream=None):
+    """Choose the keys that stay, into int32 kept [batch, n_kv_heads, n_keep] and new_lens."""
+    _check(_calls().lat_kv_evict_choose(
+        weights, weights_head_stride, weights_seq_stride, kv_lens, max_kv_len, kept, n_keep,
+        n_first, n_last, weights_out, out_head_stride, out_seq_stride, new_lens, batch,
+        n_kv_heads, status, _stream(stream)), "lat_kv_evict_choose")
+
+
+def lat_kv_evict_rows(dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride,
+                      capacity, kept, n_keep, batch, n_kv_heads, head_dim, status=None,
+                      stream=None):
+    """Move the rows of the keys that stay up, in place."""
+    _check(_calls().lat_kv_evict_rows(
+        dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, kept,
+        n_keep, batch, n_kv_heads, head_dim, status, _stream(stream)), "lat_kv_evict_rows")
+
+
 def lat_kv_block_bounds(dt, k_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity,
                         bounds, bounds_rs, bounds_head_stride, bounds_seq_stride, block_size,
                         pos, n_new, batch, n_kv_heads, head_dim, status=None, stream=None):
@@ -502,6 +542,16 @@ def lat_test_decode_blocks_timeout(q, q_rs, k_cache, v_cache, cache_rs, cache_he
         max_kv_len, block_size, blocks, n_sel, out, out_rs, batch, n_heads, n_kv_heads, head_dim,
         workspace, workspace_bytes, timeout_ns, status, _stream(stream)),
         "lat_test_decode_blocks_timeout")
+
+
+def lat_test_key_weights_timeout(q, q_rs, n_q, k_cache, cache_rs, cache_head_stride,
+                                 cache_seq_stride, kv_lens, max_kv_len, lse, weights,
+                                 weights_head_stride, weights_seq_stride, batch, n_heads,
+                                 n_kv_heads, head_dim, timeout_ns, status, stream=None):
+    _check(_calls().lat_test_key_weights_timeout(
+        q, q_rs, n_q, k_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens, max_kv_len,
+        lse, weights, weights_head_stride, weights_seq_stride, batch, n_heads, n_kv_heads,
+        head_dim, timeout_ns, status, _stream(stream)), "lat_test_key_weights_timeout")
 
 
 def lat_test_capped_scores(raw, n, scale, softcap, out, stream=None):

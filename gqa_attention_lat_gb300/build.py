@@ -31,7 +31,7 @@ LIB = os.path.join(HERE, "liblat_attn.so")
 
 SOURCES = ["api.cu", "kv_append.cu", "row_attention_f32.cu", "decode_bf16.cu", "prefill_tc.cu",
            "decode_static.cu", "qkv_producer.cu", "kv_q4.cu", "decode_q4.cu", "kv_q8.cu",
-           "decode_q8.cu",
+           "decode_q8.cu", "key_weights.cu", "evict.cu",
            "block_select.cu", "decode_blocks_f32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -1052,6 +1052,201 @@ lat_status lat_test_decode_q8_timeout(lat_dtype dt, const void *q, int64_t q_rs,
 
 }  // extern "C"
 
+// ---------------------------------------------------------------- weights of cached keys
+
+namespace {
+
+// 4-D bf16 map over query rows: (head-dim d, query head, row, sequence), boxes of box_heads heads of
+// box_rows rows, 128-byte swizzle
+bool make_columns_map(CUtensorMap *m, const void *base, int head_dim, int heads, int rows, int batch,
+                      int64_t row_stride, int box_heads, int box_rows) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows, (cuuint64_t)batch};
+    const cuuint64_t strides[3] = {(cuuint64_t)head_dim * 2, (cuuint64_t)row_stride * 2,
+                                   (cuuint64_t)row_stride * 2 * (cuuint64_t)rows};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+lat_status key_weights_impl(lat_dtype dt, const void *q, int64_t q_rs, int n_q, const void *k_cache, int64_t cache_rs,
+                            int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
+                            int max_kv_len, const float *lse, float *weights, int64_t weights_head_stride,
+                            int64_t weights_seq_stride, int batch, int n_heads, int n_kv_heads, int head_dim,
+                            int causal, int window, float scale, float softcap, int32_t *status, void *stream,
+                            uint64_t timeout_ns, int skip_load) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (!(softcap >= 0.f) || !isfinite(softcap) || !isfinite(scale)) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || n_q < 0 || max_kv_len < 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0)
+        return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0 || n_q == 0) return LAT_OK;
+    if (!q || !k_cache || !kv_lens || !lse || !weights) return LAT_ERR_INVALID_ARG;
+    if (q_rs < (int64_t)n_heads * head_dim || cache_rs <= 0 || cache_head_stride <= 0 || cache_seq_stride <= 0 ||
+        weights_head_stride < max_kv_len || weights_seq_stride < max_kv_len)
+        return LAT_ERR_INVALID_ARG;
+    if (dt == LAT_BF16 && (!aligned16(q) || !aligned16(k_cache) || q_rs % 8 || cache_rs % 8 || cache_head_stride % 8 ||
+                           cache_seq_stride % 8))
+        return LAT_ERR_INVALID_ARG;
+    if (batch > 65535 || !query_row_ok(n_heads, head_dim) || (int64_t)batch * n_q > 0x7fffffffLL ||
+        ((int64_t)max_kv_len + 127) / 128 * n_kv_heads > 0x7fffffffLL / batch)
+        return LAT_ERR_UNSUPPORTED;
+    lat::KeyWeightsArgs a{};
+    a.q = q;
+    a.k = k_cache;
+    a.q_rs = q_rs;
+    a.k_row = cache_rs;
+    a.k_head = cache_head_stride;
+    a.k_seq = cache_seq_stride;
+    a.kv_lens = kv_lens;
+    a.max_kv_len = max_kv_len;
+    a.lse = lse;
+    a.weights = weights;
+    a.w_seq = weights_seq_stride;
+    a.w_head = weights_head_stride;
+    a.batch = batch;
+    a.n_q = n_q;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.causal = causal != 0;
+    a.window = window > 0 && window < max_kv_len ? window : 0;  // (a wider one hides nothing)
+    a.scale_log2 = scale * kLog2e;
+    softcap = cap_in_range(softcap);
+    a.cap_log2 = softcap > 0.f ? softcap * kLog2e : 0.f;
+    a.raw_over_cap = softcap > 0.f ? over_cap(scale, softcap) : 0.f;
+    a.timeout_ns = timeout_ns;
+    a.test_skip_load = skip_load;
+    a.status = status;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dt == LAT_F32) {
+        if ((int64_t)batch * n_kv_heads > 65535) return LAT_ERR_UNSUPPORTED;
+        return lat::launch_key_weights_f32(a, s) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+    }
+    int sms = 0;
+    if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
+    lat::KeyWeightsPlan plan;
+    if (!lat::plan_key_weights(batch, n_q, n_heads, n_kv_heads, head_dim, max_kv_len, sms, &plan))
+        return LAT_ERR_UNSUPPORTED;
+    a.keys_held = plan.keys_held;
+    a.heads_per = plan.heads_per;
+    a.rows_per = plan.rows_per;
+    a.head_blocks = plan.head_blocks;
+    a.n_cols = plan.n_cols;
+    a.slots = plan.slots;
+    if (max_kv_len > 0 &&
+        (!make_columns_map(&a.tm_q, q, head_dim, n_heads, n_q, batch, q_rs, plan.heads_per, plan.rows_per) ||
+         !make_cache_map(&a.tm_k, k_cache, head_dim, n_kv_heads, max_kv_len, batch, cache_rs, cache_head_stride,
+                         cache_seq_stride, 128)))
+        return LAT_ERR_CUDA;
+    return lat::launch_key_weights(a, plan.grid, s) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+lat_status lat_attn_key_weights(lat_dtype dt, const void *q, int64_t q_rs, int n_q, const void *k_cache,
+                                int64_t cache_rs, int64_t cache_head_stride, int64_t cache_seq_stride,
+                                const int32_t *kv_lens, int max_kv_len, const float *lse, float *weights,
+                                int64_t weights_head_stride, int64_t weights_seq_stride, int batch, int n_heads,
+                                int n_kv_heads, int head_dim, int causal, int window, float scale, float softcap,
+                                int32_t *status, void *stream) {
+    return key_weights_impl(dt, q, q_rs, n_q, k_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,
+                            max_kv_len, lse, weights, weights_head_stride, weights_seq_stride, batch, n_heads,
+                            n_kv_heads, head_dim, causal, window, scale, softcap, status, stream, kDefaultTimeoutNs, 0);
+}
+
+lat_status lat_test_key_weights_timeout(const void *q, int64_t q_rs, int n_q, const void *k_cache, int64_t cache_rs,
+                                        int64_t cache_head_stride, int64_t cache_seq_stride, const int32_t *kv_lens,
+                                        int max_kv_len, const float *lse, float *weights, int64_t weights_head_stride,
+                                        int64_t weights_seq_stride, int batch, int n_heads, int n_kv_heads,
+                                        int head_dim, uint64_t timeout_ns, int32_t *status, void *stream) {
+    return key_weights_impl(LAT_BF16, q, q_rs, n_q, k_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens,
+                            max_kv_len, lse, weights, weights_head_stride, weights_seq_stride, batch, n_heads,
+                            n_kv_heads, head_dim, 1, 0, 0.125f, 0.f, status, stream, timeout_ns, 1);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- eviction
+
+extern "C" {
+
+lat_status lat_kv_evict_choose(const float *weights, int64_t weights_head_stride, int64_t weights_seq_stride,
+                               const int32_t *kv_lens, int max_kv_len, int32_t *kept, int n_keep, int n_first,
+                               int n_last, float *weights_out, int64_t out_head_stride, int64_t out_seq_stride,
+                               int32_t *new_lens, int batch, int n_kv_heads, int32_t *status, void *stream) {
+    if (batch < 0 || max_kv_len < 0 || n_kv_heads <= 0 || n_keep < 1 || n_first < 0 || n_last < 0 ||
+        (int64_t)n_first + n_last > n_keep)
+        return LAT_ERR_INVALID_ARG;
+    if (batch == 0) return LAT_OK;
+    if (!weights || !kv_lens || !kept || !new_lens || new_lens == kv_lens || weights_head_stride < max_kv_len ||
+        weights_seq_stride < max_kv_len)
+        return LAT_ERR_INVALID_ARG;
+    // one layout where the weights are written over, or rows would meet other rows' entries
+    if (weights_out != nullptr &&
+        (out_head_stride < max_kv_len || out_seq_stride < max_kv_len ||
+         (weights_out == weights && (out_head_stride != weights_head_stride || out_seq_stride != weights_seq_stride))))
+        return LAT_ERR_INVALID_ARG;
+    if (max_kv_len > lat::kEvictMaxKeys || (int64_t)batch * n_kv_heads > 0x7fffffffLL / lat::kEvictCluster)
+        return LAT_ERR_UNSUPPORTED;
+    lat::EvictChooseArgs a{};
+    a.weights = weights;
+    a.w_seq = weights_seq_stride;
+    a.w_head = weights_head_stride;
+    a.kv_lens = kv_lens;
+    a.max_kv_len = max_kv_len;
+    a.kept = kept;
+    a.n_keep = n_keep;
+    a.n_first = n_first;
+    a.n_last = n_last;
+    a.out = weights_out;
+    a.out_seq = out_seq_stride;
+    a.out_head = out_head_stride;
+    a.new_lens = new_lens;
+    a.batch = batch;
+    a.n_kv_heads = n_kv_heads;
+    a.status = status;
+    return lat::launch_evict_choose(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+}
+
+lat_status lat_kv_evict_rows(lat_dtype dt, void *k_cache, void *v_cache, int64_t cache_rs, int64_t cache_head_stride,
+                             int64_t cache_seq_stride, int capacity, const int32_t *kept, int n_keep, int batch,
+                             int n_kv_heads, int head_dim, int32_t *status, void *stream) {
+    if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
+    if (batch < 0 || capacity < 0 || n_keep < 1 || n_kv_heads <= 0) return LAT_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
+    if (batch == 0) return LAT_OK;
+    const int es = dt == LAT_BF16 ? 2 : 4;
+    constexpr int64_t kMost = INT64_MAX / 4;  // elements whose bytes are still counted
+    if (cache_rs > kMost || cache_head_stride > kMost || cache_seq_stride > kMost || !k_cache || !v_cache || !kept || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !q4_strides_ok(cache_rs * es, cache_head_stride * es, cache_seq_stride * es))
+        return LAT_ERR_INVALID_ARG;
+    if ((int64_t)batch * n_kv_heads > 0x7fffffffLL / 16) return LAT_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
+    lat::EvictRowsArgs a{};
+    a.k = k_cache;
+    a.v = v_cache;
+    a.cache_rs = cache_rs * es;
+    a.cache_head = cache_head_stride * es;
+    a.cache_seq = cache_seq_stride * es;
+    a.row_bytes = head_dim * es;
+    a.capacity = capacity;
+    a.kept = kept;
+    a.n_keep = n_keep;
+    a.batch = batch;
+    a.n_kv_heads = n_kv_heads;
+    a.status = status;
+    return lat::launch_evict_rows(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+}
+
+}  // extern "C"
+
 // ---------------------------------------------------------------- choice of cached blocks
 
 namespace {

@@ -131,6 +131,66 @@ bool plan_decode_q8(int batch, int n_heads, int n_kv_heads, int head_dim, bool b
                     SplitPlan *p);
 cudaError_t launch_decode_q8(const Q8DecodeArgs &a, bool bf16, const SplitPlan &p, cudaStream_t s);
 
+// ---------------------------------------------------------------- weights of cached keys
+struct KeyWeightsArgs {
+    CUtensorMap tm_q, tm_k;  // bf16: (channel, head, row, sequence), boxes of the plan's columns and of 128 keys
+    const void *q, *k;       // fp32
+    int64_t q_rs, k_row, k_head, k_seq;  // elements
+    const int32_t *kv_lens;
+    int max_kv_len;
+    const float *lse;        // [batch * n_q, n_heads]
+    float *weights;          // key j of (b, hk) at b * w_seq + hk * w_head + j
+    int64_t w_seq, w_head;
+    int batch, n_q, n_heads, n_kv_heads, head_dim, causal, window;  // window 0: none, else < max_kv_len
+    float scale_log2, cap_log2, raw_over_cap;  // as in DecodeArgs
+    int keys_held, heads_per, rows_per, head_blocks, n_cols;  // the plan's
+    int64_t slots;
+    uint64_t timeout_ns;
+    int test_skip_load;      // test hook: the first stage never comes
+    int32_t *status;
+};
+// A tile of columns is rows_per query rows of heads_per heads (of head_blocks blocks a KV head),
+// n_cols of them rounded up to 16.  All columns in one tile: queries held, else keys.
+struct KeyWeightsPlan {
+    int keys_held, heads_per, rows_per, head_blocks, n_cols, grid;
+    int64_t slots;           // key tiles of all sequences, were they as long as they may be
+};
+bool plan_key_weights(int batch, int n_q, int n_heads, int n_kv_heads, int head_dim, int max_kv_len, int num_sms,
+                      KeyWeightsPlan *p);
+cudaError_t launch_key_weights(const KeyWeightsArgs &a, int grid, cudaStream_t s);
+// batch * n_kv_heads <= 65535
+cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, cudaStream_t s);
+
+// ---------------------------------------------------------------- eviction
+constexpr int kEvictCluster = 8, kEvictMaxSlice = 53248;  // CTAs of a head, keys of one in shared memory
+constexpr int64_t kEvictMaxKeys = (int64_t)kEvictCluster * kEvictMaxSlice;
+struct EvictChooseArgs {
+    const float *weights;    // key j of (b, hk) at b * w_seq + hk * w_head + j
+    int64_t w_seq, w_head;
+    const int32_t *kv_lens;
+    int max_kv_len;          // <= kEvictMaxKeys
+    int32_t *kept;           // [batch, n_kv_heads, n_keep]
+    int n_keep, n_first, n_last;
+    float *out;              // nullable; may be weights
+    int64_t out_seq, out_head;
+    int32_t *new_lens;
+    int batch, n_kv_heads, cluster;  // cluster: the launcher's
+    int32_t *status;
+};
+// batch * n_kv_heads * kEvictCluster < 2^31
+cudaError_t launch_evict_choose(EvictChooseArgs a, cudaStream_t s);
+
+struct EvictRowsArgs {
+    void *k, *v;
+    int64_t cache_rs, cache_head, cache_seq;  // bytes
+    int row_bytes, capacity;
+    const int32_t *kept;                      // [batch, n_kv_heads, n_keep]
+    int n_keep, batch, n_kv_heads;
+    int32_t *status;
+};
+// batch * n_kv_heads * 16 < 2^31
+cudaError_t launch_evict_rows(const EvictRowsArgs &a, int num_sms, cudaStream_t s);
+
 // ---------------------------------------------------------------- choice of cached blocks
 struct BoundsArgs {
     const void *k_cache;

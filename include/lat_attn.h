@@ -485,6 +485,83 @@ lat_status lat_attn_decode_q8(lat_dtype dt, const void *q, int64_t q_rs, const v
                               int32_t *status, void *stream);
 
 /*
+ * Which cached keys matter: lat_attn_key_weights sums up what attention gave each key,
+ * lat_kv_evict_choose picks the keys of each KV head that stay, lat_kv_evict_rows moves their
+ * rows up.  In a decode step: append, attend (with its log-sum-exp), sum up; when the cache is full,
+ * choose and move.  For a prompt: prefill, sum up over its last rows or all of them, choose and move,
+ * then decode from (or lat_kv_append_q8) what is left.
+ *
+ * lat_attn_key_weights — onto a running sum per key, the softmax weights that the last n_q query
+ * rows of each sequence gave it:
+ *   weights[b,hk,j] += sum over i < n_q and the KV head's query heads h of exp(s_bihj - lse_bih)
+ * for every key j < kv_lens[b] that row i sees; row i of sequence b is at position p =
+ * kv_lens[b] - n_q + i and sees the keys that the attention calls let it see: j <= p (causal != 0;
+ * else all), p - j < window (window > 0).  s is their score, scale and softcap (0 = none) included, and
+ * lse the log-sum-exp that they left for it (of a lat_attn_prefill* over the sequence's last n_q
+ * rows, or with n_q = 1 of a lat_attn_decode*).  A row at a position below 0, or whose lse is
+ * -inf, sees nothing.
+ *   q   element (b,i,h,d) at q[(b*n_q + i)*q_rs + h*head_dim + d]
+ *   lse fp32 at lse[(b*n_q + i)*n_heads + h]
+ *   weights fp32 at weights[b*weights_seq_stride + hk*weights_head_stride + j], strides at least
+ *     max_kv_len; entries of keys that no row sees keep their value
+ * k_cache, its strides, kv_lens and max_kv_len as in lat_attn_decode (the cache holds max_kv_len rows
+ * per sequence; those at or past kv_lens[b] may hold anything).  A length outside [0, max_kv_len]
+ * sets *status = LAT_ERR_BOUNDS and leaves that sequence's weights as they were.  Products and sums are
+ * fp32, and no sum's order depends on the launch: the same call gives the same bits.
+ * For LAT_BF16, q and k_cache must be 16-byte aligned and q_rs and the cache strides multiples of
+ * 8; softcap and scale finite, softcap >= 0, else LAT_ERR_INVALID_ARG (a cap above 1e36 counts
+ * as 1e36).  batch <= 65535 (LAT_F32: batch * n_kv_heads), batch * n_q < 2^31, n_heads *
+ * head_dim < 2^31 and batch * n_kv_heads * ceil(max_kv_len / 128) < 2^31, else
+ * LAT_ERR_UNSUPPORTED.  After LAT_ERR_TIMEOUT the weights are unspecified.
+ */
+lat_status lat_attn_key_weights(lat_dtype dt, const void *q, int64_t q_rs, int n_q,
+                                const void *k_cache, int64_t cache_rs,
+                                int64_t cache_head_stride, int64_t cache_seq_stride,
+                                const int32_t *kv_lens, int max_kv_len, const float *lse,
+                                float *weights, int64_t weights_head_stride,
+                                int64_t weights_seq_stride, int batch, int n_heads,
+                                int n_kv_heads, int head_dim, int causal, int window,
+                                float scale, float softcap, int32_t *status, void *stream);
+
+/*
+ * lat_kv_evict_choose — the n_keep keys of each KV head that stay, of the kv_lens[b] it has: the
+ * first n_first, the last n_last, and of the others those with the largest weights (ties to the
+ * lowest; a NaN goes before all others).  A sequence of at most n_keep keys keeps them all.
+ *   weights as in lat_attn_key_weights
+ *   kept: int32 [batch, n_kv_heads, n_keep], ascending, -1 behind
+ *   weights_out (nullable; it may be `weights`, with the same strides, but overlap it in no other
+ *     way): entry i takes the weight of key kept[i], entries from there to kv_lens[b] become 0
+ *   new_lens: int32 [batch], min(kv_lens[b], n_keep); it must not overlap kv_lens
+ * A length outside [0, max_kv_len] sets *status = LAT_ERR_BOUNDS and leaves that sequence's outputs
+ * unwritten.  n_keep >= 1, n_first and n_last >= 0, n_first + n_last <= n_keep, strides at least
+ * max_kv_len, else LAT_ERR_INVALID_ARG; max_kv_len <= 425984 and 8 * batch * n_kv_heads < 2^31,
+ * else LAT_ERR_UNSUPPORTED.
+ */
+lat_status lat_kv_evict_choose(const float *weights, int64_t weights_head_stride,
+                               int64_t weights_seq_stride, const int32_t *kv_lens,
+                               int max_kv_len, int32_t *kept, int n_keep, int n_first,
+                               int n_last, float *weights_out, int64_t out_head_stride,
+                               int64_t out_seq_stride, int32_t *new_lens, int batch,
+                               int n_kv_heads, int32_t *status, void *stream);
+
+/*
+ * lat_kv_evict_rows — moves the rows of the keys that stay up, in place: for each sequence and KV
+ * head, cache row i takes row kept[b,hk,i] as it was before the call, for i < n_keep up to the first
+ * -1 (lists as lat_kv_evict_choose writes them).  Rows behind keep their values, as do all other
+ * bytes.  Keys keep the rotation of the position they were appended at; positions of keys in
+ * the cache are no longer those of their tokens, so a window counts kept keys from then on.
+ * An entry that is not above the one before it, or not below `capacity`, sets *status =
+ * LAT_ERR_BOUNDS, is not moved, and leaves that head's rows unspecified.
+ * The caches must be 16-byte aligned, must not overlap each other, and their strides positive
+ * multiples of 16 bytes, n_keep >= 1, else LAT_ERR_INVALID_ARG; 16 * batch * n_kv_heads < 2^31, else
+ * LAT_ERR_UNSUPPORTED.
+ */
+lat_status lat_kv_evict_rows(lat_dtype dt, void *k_cache, void *v_cache, int64_t cache_rs,
+                             int64_t cache_head_stride, int64_t cache_seq_stride, int capacity,
+                             const int32_t *kept, int n_keep, int batch, int n_kv_heads,
+                             int head_dim, int32_t *status, void *stream);
+
+/*
  * Attention over chosen blocks of a long cache: lat_kv_block_bounds, lat_attn_select_blocks
  * and lat_attn_decode_blocks.  A decode step that reads a fixed number of blocks of
  * block_size keys instead of the whole cache, chosen anew for each query by a bound of the

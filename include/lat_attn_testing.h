@@ -75,6 +75,15 @@ lat_status lat_test_decode_blocks_timeout(const void *q, int64_t q_rs, const voi
                                           int64_t out_rs, int batch, int n_heads, int n_kv_heads,
                                           int head_dim, void *workspace, size_t workspace_bytes,
                                           uint64_t timeout_ns, int32_t *status, void *stream);
+lat_status lat_test_key_weights_timeout(const void *q, int64_t q_rs, int n_q,
+                                        const void *k_cache, int64_t cache_rs,
+                                        int64_t cache_head_stride, int64_t cache_seq_stride,
+                                        const int32_t *kv_lens, int max_kv_len,
+                                        const float *lse, float *weights,
+                                        int64_t weights_head_stride,
+                                        int64_t weights_seq_stride, int batch, int n_heads,
+                                        int n_kv_heads, int head_dim, uint64_t timeout_ns,
+                                        int32_t *status, void *stream);
 lat_status lat_test_capped_scores(const float *raw, int64_t n, float scale, float softcap,
                                   float *out, void *stream);
 
