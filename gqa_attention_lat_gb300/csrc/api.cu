@@ -1133,6 +1133,7 @@ lat_status key_weights_impl(lat_dtype dt, const void *q, int64_t q_rs, int n_q, 
         return LAT_ERR_UNSUPPORTED;
     a.keys_held = plan.keys_held;
     a.heads_per = plan.heads_per;
+    a.by_heads_per = lat::FastDiv((uint32_t)plan.heads_per);
     a.rows_per = plan.rows_per;
     a.head_blocks = plan.head_blocks;
     a.n_cols = plan.n_cols;

@@ -144,6 +144,7 @@ struct KeyWeightsArgs {
     int batch, n_q, n_heads, n_kv_heads, head_dim, causal, window;  // window 0: none, else < max_kv_len
     float scale_log2, cap_log2, raw_over_cap;  // as in DecodeArgs
     int keys_held, heads_per, rows_per, head_blocks, n_cols;  // the plan's
+    FastDiv by_heads_per;
     int64_t slots;
     uint64_t timeout_ns;
     int test_skip_load;      // test hook: the first stage never comes

@@ -18,11 +18,18 @@
 //    More columns (a chunk, a prompt): a key tile stays while its tiles of queries stream by, and
 //    items (key tiles) are dealt heaviest first, forwards and backwards in turn.
 //    Either way every key has one owner, so sums are in a fixed order and nothing is atomic.
-//  * Roles: warps 0-3 and 4-7 are two epilogues that take every other tile of S (two buffers in
-//    tensor memory), warp 8 issues the copies, warp 9 the MMAs, warp 10 prepares each column's
-//    log-sum-exp and range of keys.  Where a range cuts a tile, pairs are masked one by one.
-//  * A thread adds a tile's columns in four sums and those to its total with a compensation, so
-//    prompts of many thousand rows lose nothing.
+//  * Roles: epilogue warps in quartets (a warp can read the quarter of tensor memory's lanes that
+//    its number says), a warp that issues the copies, one that issues the MMAs, two that prepare
+//    the columns' log-sum-exps and ranges of keys.  S has two to four buffers in tensor memory.
+//    Queries held, a tile of up to 128 columns goes to one quartet, the next to another; otherwise a
+//    tile's columns are cut in four, and the quartets' sums meet in shared memory at a key tile's
+//    end.  Where a range cuts a tile, pairs are masked one by one.
+//  * What a role does for every tile is kept short (a wait that need not wait costs a thread 100
+//    to 200 cycles): walks go by runs of tiles, tables come with the tile of S they belong to, and
+//    a key's sum goes to memory as a reduction that nothing waits for.
+//  * A pair costs half an FMA and half an addition (f32x2) and one exponential.  A thread adds a
+//    tile's columns in four sums and those to its total with a compensation, so prompts of many
+//    thousand rows lose nothing.
 //  * Waits are bounded; on expiry the CTA records LAT_ERR_TIMEOUT, drains and quits.
 // What bounds it: HBM (keys once) for few columns; for many the tensor pipe and the exponentials,
 // 128 N D 2 flops against 128 N of them.
@@ -43,10 +50,14 @@ namespace lat {
 namespace {
 
 constexpr int kKeysTile = 128;
-constexpr int kTcThreads = 352;
-constexpr int kEpilogueWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kTableWarp = 10;
 constexpr int kMaxCols = 256, kStreamCols = 128;  // columns of a tile: at most, and where they stream
-constexpr uint32_t kTmemCols = 512;               // two tiles of S
+constexpr int kNarrowCols = 64;                   // queries held, up to so many: two quartets are enough
+constexpr int kMaxQuartets = 4;
+constexpr int kMoreWarps = 4;                     // behind them: copies, MMAs, two of tables
+constexpr int kMaxThreads = 128 * kMaxQuartets + 32 * kMoreWarps;
+constexpr int kTables = 4;
+constexpr int kPlaces = 8;                        // items whose sums can be under way at once
+constexpr uint32_t kTmemCols = 512;               // tiles of S, 128 columns apart (256 where they are wider)
 
 template <int D>
 struct KwCfg {
@@ -59,24 +70,25 @@ struct KwCfg {
     // the operand that stays: up to 256 (head_dim 256, 512: 128) columns, or 128 keys
     static constexpr int kHeldBytes = D == 512 ? 131072 : 65536;
     static constexpr int kHeldCols = kHeldBytes / (kChunks * 128) < kMaxCols ? kHeldBytes / (kChunks * 128) : kMaxCols;
-    static constexpr int kTableBytes = 2 * (3 * kMaxCols + 4) * 4;
-    static constexpr int kBarBytes = 512;
-    static constexpr int kSmem = 1024 + kHeldBytes + kStages * kStageBytes + kTableBytes + kKeysTile * 4 + kBarBytes;
+    static constexpr int kTableBytes = kTables * (3 * kMaxCols + 4) * 4;
+    static constexpr int kPassed = kPlaces * kMaxQuartets * kKeysTile * 4;          // [item % kPlaces][quartet][key] sums
+    static constexpr int kBarBytes = 1024;
+    static constexpr int kSmem = kHeldBytes + kStages * kStageBytes + kTableBytes + kPassed + kBarBytes;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
 // the columns of a tile: e^{s - lse} = 2^(s' - lse2), and the keys lo < j <= hi that a column sees
 struct Table {
-    float lse2[kMaxCols];
+    float minus_lse2[kMaxCols];
     int hi[kMaxCols], lo[kMaxCols];
     int min_hi, max_lo, count, pad;  // over the columns there are
 };
 
-struct Item {
-    int b, hk, t;        // key tile
-    int len;
-    int64_t col0, col1;  // its tiles of columns
-    bool fresh;          // another sequence or head than the item before
+// tiles one after another that share the operand that stays
+struct Run {
+    int b, hk, len;
+    int t, n;   // queries held: key tiles t .. t + n - 1; keys held: key tile t and n tiles of columns,
+    int64_t x;  // x .. x + n - 1
 };
 
 __device__ __forceinline__ int length_of(const KeyWeightsArgs &a, int b) {
@@ -90,164 +102,199 @@ __device__ __forceinline__ int2 tiles_seen(const KeyWeightsArgs &a, int len) {
     return make_int2(lo / kKeysTile, (int)(((int64_t)len + kKeysTile - 1) / kKeysTile));
 }
 
-// The CTA's items.  Queries held: a share of the sequence of (b, hk, t); keys held: every grid-th
-// of (t, b, hk), forwards and backwards in turn.
+// The CTA's runs.  Queries held: a share of all (b, hk, t) in this order; keys held: every grid-th
+// of all (t, b, hk), forwards and backwards in turn.
 struct Walker {
     const KeyWeightsArgs &a;
-    int64_t pos, end;   // next item, and behind the last; or the round
-    int64_t base;       // queries held: where sequence b's items begin
-    int b, hk, t, t1, len;
+    int64_t pos, end;  // next tile, and behind the last; or the round
+    int64_t base;      // queries held: where sequence b's tiles begin
+    int b;
 
-    __device__ Walker(const KeyWeightsArgs &a_, int64_t pos_, int64_t end_, int64_t base_, int b_)
-        : a(a_), pos(pos_), end(end_), base(base_), b(b_), hk(-1), t(0), t1(0), len(0) {}
-
-    __device__ bool next(Item &it) {
-        return a.keys_held ? next_dealt(it) : next_shared(it);
-    }
-    __device__ bool next_shared(Item &it) {
+    __device__ bool next(Run &r) { return a.keys_held ? next_dealt(r) : next_shared(r); }
+    __device__ bool next_shared(Run &r) {
         if (pos >= end) return false;
-        it.fresh = true;
-        if (hk >= 0 && t + 1 < t1) {
-            ++t;
-            it.fresh = false;
-        } else {
-            for (;;) {  // another head, or sequence
-                len = length_of(a, b);
-                const int2 seen = tiles_seen(a, len);
-                const int64_t n = seen.y - seen.x;
-                if (pos >= base + n * a.n_kv_heads) {
-                    base += n * a.n_kv_heads;
-                    ++b;
-                    continue;
-                }
-                hk = (int)((pos - base) / n);
-                t = seen.x + (int)((pos - base) % n);
-                t1 = seen.y;
-                break;
+        for (;; ++b) {
+            r.len = length_of(a, b);
+            const int2 seen = tiles_seen(a, r.len);
+            const int n = seen.y - seen.x;
+            const int64_t all = (int64_t)n * a.n_kv_heads;
+            if (pos >= base + all) {
+                base += all;
+                continue;
             }
+            const uint32_t at = (uint32_t)(pos - base);  // (items are fewer than 2^31)
+            r.b = b;
+            r.hk = (int)(at / (uint32_t)n);
+            r.t = seen.x + (int)(at % (uint32_t)n);
+            r.n = (int)min((int64_t)(seen.y - r.t), end - pos);
+            r.x = 0;
+            pos += r.n;
+            return true;
         }
-        ++pos;
-        it.b = b, it.hk = hk, it.t = t, it.len = len, it.col0 = 0, it.col1 = 1;
-        return true;
     }
-    __device__ bool next_dealt(Item &it) {
+    __device__ bool next_dealt(Run &r) {
         const int64_t per = (int64_t)a.batch * a.n_kv_heads;
         for (;; ++pos) {
             const int64_t x = pos * gridDim.x + ((pos & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             if (pos * gridDim.x >= end) return false;
             if (x >= end) continue;
-            it.t = (int)(x / per);
-            const int rem = (int)(x - it.t * per);
-            it.b = rem / a.n_kv_heads;
-            it.hk = rem - it.b * a.n_kv_heads;
-            it.len = length_of(a, it.b);
-            const int2 seen = tiles_seen(a, it.len);
-            if (it.t < seen.x || it.t >= seen.y) continue;
+            r.t = (int)(x / per);
+            const int rem = (int)(x - r.t * per);
+            r.b = rem / a.n_kv_heads;
+            r.hk = rem - r.b * a.n_kv_heads;
+            r.len = length_of(a, r.b);
+            const int2 seen = tiles_seen(a, r.len);
+            if (r.t < seen.x || r.t >= seen.y) continue;
             // rows that see a key of the tile
-            const int64_t off = (int64_t)it.len - a.n_q, first = (int64_t)it.t * kKeysTile;
-            const int64_t last = min(first + kKeysTile, (int64_t)it.len) - 1;
+            const int64_t off = (int64_t)r.len - a.n_q, first = (int64_t)r.t * kKeysTile;
+            const int64_t last = min(first + kKeysTile, (int64_t)r.len) - 1;
             int64_t i0 = max((int64_t)0, -off), i1 = a.n_q - 1;
             if (a.causal) i0 = max(i0, first - off);
             if (a.window > 0) i1 = min(i1, last + a.window - 1 - off);
             if (i0 > i1) continue;
-            it.col0 = i0 / a.rows_per * a.head_blocks;
-            it.col1 = (i1 / a.rows_per + 1) * a.head_blocks;
-            it.fresh = true;
+            r.x = i0 / a.rows_per * a.head_blocks;
+            r.n = (int)((i1 / a.rows_per + 1) * a.head_blocks - r.x);
             ++pos;
             return true;
         }
     }
 };
 
-// sum over 16 columns of 2^(s' - lse2), the scores as they came out of the MMA
+// pairs of floats
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 halves_of(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t twice(float x) { return pair_of(x, x); }
+
+// sums over 16 columns (the table's from n on) of 2^(s' - lse2), the scores as they came out of the
+// MMA; two a sum
 template <bool CAP, bool MASK>
-__device__ __forceinline__ void add_columns(float (&sum)[4], const uint32_t (&r)[16], const Table &tab, int n0, int j,
+__device__ __forceinline__ void add_columns(uint64_t (&sum)[2], const uint32_t (&r)[16], const Table &tab, int n, int j,
                                             const KeyWeightsArgs &a) {
-    float x[16];
+    uint64_t x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = pair_of(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
     if constexpr (CAP) {
         float most = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            x[k] = __uint_as_float(r[k]) * a.raw_over_cap;
-            most = fmaxf(most, fabsf(x[k]));
+        for (int k = 0; k < 8; ++k) {
+            x[k] = mul2(x[k], twice(a.raw_over_cap));
+            const float2 y = halves_of(x[k]);
+            most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
         }
         // scores well below the cap (tanh's Taylor series, as in capped_score_close) are most
         if (__any_sync(0xffffffffu, !(most < 0.3f))) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = capped_score_close(x[k], a.cap_log2);
+            for (int k = 0; k < 8; ++k) {
+                const float2 y = halves_of(x[k]);
+                x[k] = pair_of(capped_score_close(y.x, a.cap_log2), capped_score_close(y.y, a.cap_log2));
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const float z = x[k] * x[k];
-                const float t = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
-                x[k] = a.cap_log2 * x[k] * t;
+            for (int k = 0; k < 8; ++k) {
+                const uint64_t z = mul2(x[k], x[k]);
+                uint64_t t = fma2(z, twice(62.f / 2835.f), twice(-17.f / 315.f));
+                t = fma2(z, t, twice(2.f / 15.f));
+                t = fma2(z, t, twice(-1.f / 3.f));
+                t = fma2(z, t, twice(1.f));
+                x[k] = mul2(mul2(x[k], twice(a.cap_log2)), t);
             }
         }
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const float4 l = *reinterpret_cast<const float4 *>(tab.lse2 + n0 + 4 * q);
-        const float ls[4] = {l.x, l.y, l.z, l.w};
-        int hi[4], lo[4];
-        if constexpr (MASK) {
-            const int4 h = *reinterpret_cast<const int4 *>(tab.hi + n0 + 4 * q);
-            const int4 o = *reinterpret_cast<const int4 *>(tab.lo + n0 + 4 * q);
-            hi[0] = h.x, hi[1] = h.y, hi[2] = h.z, hi[3] = h.w;
-            lo[0] = o.x, lo[1] = o.y, lo[2] = o.z, lo[3] = o.w;
-        }
+        const float4 l = *reinterpret_cast<const float4 *>(tab.minus_lse2 + n + 4 * q);
+        const uint64_t ls[2] = {pair_of(l.x, l.y), pair_of(l.z, l.w)};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float p = fast_exp2(CAP ? x[4 * q + k] - ls[k] : fmaf(__uint_as_float(r[4 * q + k]), a.scale_log2, -ls[k]));
-            sum[k] += !MASK || (j <= hi[k] && j > lo[k]) ? p : 0.f;
+        for (int k = 0; k < 2; ++k) {
+            const uint64_t y = CAP ? add2(x[2 * q + k], ls[k]) : fma2(x[2 * q + k], twice(a.scale_log2), ls[k]);
+            float2 p = halves_of(y);
+            p.x = fast_exp2(p.x), p.y = fast_exp2(p.y);
+            if constexpr (MASK) {
+                const int2 hi = *reinterpret_cast<const int2 *>(tab.hi + n + 4 * q + 2 * k);
+                const int2 lo = *reinterpret_cast<const int2 *>(tab.lo + n + 4 * q + 2 * k);
+                p.x = j <= hi.x && j > lo.x ? p.x : 0.f;
+                p.y = j <= hi.y && j > lo.y ? p.y : 0.f;
+            }
+            sum[k] = add2(sum[k], pair_of(p.x, p.y));
         }
     }
 }
 
 template <int D, bool CAP>
-__global__ void __launch_bounds__(kTcThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsArgs a) {
     using C = KwCfg<D>;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char smem[];      // (an aligned-up pointer would load as generic)
     unsigned char *held = smem;                                  // one or two operands that stay
     unsigned char *ring = held + C::kHeldBytes;                  // [kStages]
-    Table *tables = reinterpret_cast<Table *>(ring + C::kStages * C::kStageBytes);  // [2]
-    float *passed = reinterpret_cast<float *>(tables + 2);       // [128] the second epilogue's totals
-    uint64_t *bars = reinterpret_cast<uint64_t *>(passed + kKeysTile);
+    Table *tables = reinterpret_cast<Table *>(ring + C::kStages * C::kStageBytes);  // [kTables]
+    float *passed = reinterpret_cast<float *>(tables + kTables);                    // [item % kPlaces][quartet][key]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(passed + kPlaces * kMaxQuartets * kKeysTile);
     uint64_t *ring_full = bars, *ring_empty = bars + 8;          // [kStages]
     uint64_t *held_full = bars + 16, *held_empty = bars + 18;    // [2]
-    uint64_t *s_full = bars + 20, *s_empty = bars + 22;          // [2]
-    uint64_t *tab_full = bars + 24, *tab_empty = bars + 26;      // [2]
-    uint64_t *x_full = bars + 28, *x_empty = bars + 32;          // [4] by quarter of the lanes
-    uint64_t *bar_done = bars + 36;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 37);
+    uint64_t *s_full = bars + 20, *s_empty = bars + 24;          // [4]
+    uint64_t *tab_full = bars + 28, *tab_empty = tab_full + kTables;
+    uint64_t *x_full = tab_empty + kTables;                      // [item % kPlaces][quarter of the lanes]
+    uint64_t *bar_done = x_full + 4 * kPlaces;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *scan = reinterpret_cast<int *>(tmem_slot + 2);          // [11] warps
-    int64_t *start = reinterpret_cast<int64_t *>(bars + 44);     // share: base, b
-    static_assert(sizeof(Table) * 2 == C::kTableBytes && C::kStages <= 8, "shared memory layout");
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int64_t *start = reinterpret_cast<int64_t *>(bar_done + 2);  // share: base, b
+    int *scan = reinterpret_cast<int *>(bar_done + 4);           // a warp each
+    static_assert(sizeof(Table) * kTables == C::kTableBytes && C::kStages <= 8 && kTables >= 4 &&
+                      (32 + 2 * kTables + 4 * kPlaces) * 8 + kMaxThreads / 32 * 4 <= C::kBarBytes,
+                  "shared memory layout");
+    if (smem_u32(smem) & 1023) {  // (swizzled operands need it; it is where dynamic shared memory begins)
+        if (threadIdx.x == 0) report_status(a.status, kErrCuda);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_threads = blockDim.x;
+    const int n_epilogue = n_threads / 32 - kMoreWarps, quartets = n_epilogue / 4;
+    const bool alone = !a.keys_held && a.n_cols <= 128;          // a quartet takes a tile of S alone
+    const unsigned s_stride = a.n_cols <= 128 ? 128 : 256, s_bufs = kTmemCols / s_stride;  // a power of two
+    const unsigned s_shift = a.n_cols <= 128 ? 2 : 1;            // log2 of s_bufs
     const int G = a.n_heads / a.n_kv_heads;
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) mbar_init(&ring_full[i], 1), mbar_init(&ring_empty[i], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&held_full[i], 1), mbar_init(&held_empty[i], 1);
-            mbar_init(&s_full[i], 1), mbar_init(&s_empty[i], 4);
-            mbar_init(&tab_full[i], 1), mbar_init(&tab_empty[i], kEpilogueWarps);
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&held_full[i], 1), mbar_init(&held_empty[i], 1);
+        // keys held: a tile of S is full when its MMAs are done and its table is there
+        for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], a.keys_held ? 2 : 1), mbar_init(&s_empty[i], alone ? 4 : n_epilogue);
+        for (int i = 0; i < kTables; ++i) mbar_init(&tab_full[i], 1), mbar_init(&tab_empty[i], n_epilogue);
+        for (int i = 0; i < 4 * kPlaces; ++i) mbar_init(&x_full[i], quartets);
         mbar_init(bar_done, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
         start[0] = 0, start[1] = a.batch;
     }
-    if (warp == kMmaWarp) {
+    if (warp == n_epilogue + 1) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
     // ---- this CTA's share: per-thread sums over a slice of the sequences, then a scan ----------
     // (item counts stay below 2^31)
-    const int per_thread = (a.batch + kTcThreads - 1) / kTcThreads;
+    const int per_thread = (a.batch + n_threads - 1) / n_threads;
     const int b_lo = min(a.batch, tid * per_thread), b_hi = min(a.batch, b_lo + per_thread);
     int mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
@@ -268,7 +315,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) key_weights_kernel(const __grid
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     int total = 0, before = incl - mine;
-    for (int w = 0; w < kTcThreads / 32; ++w) {
+    for (int w = 0; w < n_threads / 32; ++w) {
         const int v = scan[w];
         if (w < warp) before += v;
         total += v;
@@ -291,49 +338,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) key_weights_kernel(const __grid
         }
         __syncthreads();
     }
-    Walker walk(a, r0, r1, start[0], (int)start[1]);
+    Walker walk{a, r0, r1, start[0], (int)start[1]};
     // bytes of a chunk of the tile of queries and of keys; how many operands there is room to hold
     const int q_rows = a.rows_per * a.heads_per;                 // columns that a copy brings
     const int q_chunk = a.keys_held ? 16384 : a.n_cols * 128;    // where its chunks lie apart
     const int held_bytes = C::kChunks * (a.keys_held ? 16384 : q_chunk);
-    const int n_held = 2 * held_bytes <= C::kHeldBytes ? 2 : 1;
+    const unsigned n_held = 2 * held_bytes <= C::kHeldBytes ? 2 : 1;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag, deadline); };
 
-    if (warp == kCopyWarp) {
+    if (warp == n_epilogue) {
         if (lane == 0) {
             if (a.max_kv_len > 0) tma_prefetch_desc(&a.tm_q), tma_prefetch_desc(&a.tm_k);  // (else there are none)
             unsigned g = 0, h = 0;  // ring stages and held operands issued
             bool ok = true;
-            // chunks [c0, c1) of a tile of keys or of queries (column tile x)
-            auto keys = [&](unsigned char *to, uint64_t *bar, const Item &it, int c0, int c1) {
+            // chunks [c0, c1) of key tile t, and of the columns of row block rb and head block hb
+            auto keys = [&](unsigned char *to, uint64_t *bar, const Run &r, int t, int c0, int c1) {
                 for (int c = c0; c < c1; ++c)
-                    tma_load_4d(to + (c - c0) * 16384, &a.tm_k, bar, c * 64, it.hk, it.t * kKeysTile, it.b);
+                    tma_load_4d(to + (c - c0) * 16384, &a.tm_k, bar, c * 64, r.hk, t * kKeysTile, r.b);
             };
-            auto queries = [&](unsigned char *to, uint64_t *bar, const Item &it, int64_t x, int c0, int c1) {
-                const int rb = (int)(x / a.head_blocks), hb = (int)(x % a.head_blocks);
+            auto queries = [&](unsigned char *to, uint64_t *bar, const Run &r, int rb, int hb, int c0, int c1) {
                 for (int c = c0; c < c1; ++c)
-                    tma_load_4d(to + (c - c0) * q_chunk, &a.tm_q, bar, c * 64, it.hk * G + hb * a.heads_per,
-                                rb * a.rows_per, it.b);
+                    tma_load_4d(to + (c - c0) * q_chunk, &a.tm_q, bar, c * 64, r.hk * G + hb * a.heads_per, rb * a.rows_per, r.b);
             };
-            for (Item it; ok && walk.next(it);) {
-                if (it.fresh) {
-                    const unsigned x = h % n_held;
-                    if (!(ok = wait(&held_empty[x], ((h / n_held) & 1) ^ 1))) break;
-                    mbar_arrive_expect_tx(&held_full[x], C::kChunks * (a.keys_held ? 16384 : q_rows * 128));
-                    if (a.keys_held) keys(held + x * held_bytes, &held_full[x], it, 0, C::kChunks);
-                    else queries(held + x * held_bytes, &held_full[x], it, 0, 0, C::kChunks);
-                    ++h;
-                }
-                for (int64_t x = it.col0; ok && x < it.col1; ++x)
+            for (Run r; ok && walk.next(r); ++h) {
+                const unsigned y = h & (n_held - 1);
+                if (!(ok = wait(&held_empty[y], ((h >> (n_held - 1)) & 1) ^ 1))) break;
+                mbar_arrive_expect_tx(&held_full[y], C::kChunks * (a.keys_held ? 16384 : q_rows * 128));
+                if (a.keys_held) keys(held + y * held_bytes, &held_full[y], r, r.t, 0, C::kChunks);
+                else queries(held + y * held_bytes, &held_full[y], r, 0, 0, 0, C::kChunks);
+                int rb = (int)(r.x / a.head_blocks), hb = (int)(r.x - (int64_t)rb * a.head_blocks);
+                for (int i = 0; ok && i < r.n; ++i) {
                     for (int p = 0; p < C::kStagesPerTile; ++p, ++g) {
                         const unsigned s = g % C::kStages;
                         if (!(ok = wait(&ring_empty[s], ((g / C::kStages) & 1) ^ 1))) break;
                         if (a.test_skip_load && g == 0) continue;  // test hook: never comes
                         const int c0 = p * C::kStageChunks;
                         mbar_arrive_expect_tx(&ring_full[s], C::kStageChunks * (a.keys_held ? q_rows * 128 : 16384));
-                        if (a.keys_held) queries(ring + s * C::kStageBytes, &ring_full[s], it, x, c0, c0 + C::kStageChunks);
-                        else keys(ring + s * C::kStageBytes, &ring_full[s], it, c0, c0 + C::kStageChunks);
+                        if (a.keys_held) queries(ring + s * C::kStageBytes, &ring_full[s], r, rb, hb, c0, c0 + C::kStageChunks);
+                        else keys(ring + s * C::kStageBytes, &ring_full[s], r, r.t + i, c0, c0 + C::kStageChunks);
                     }
+                    if (++hb == a.head_blocks) hb = 0, ++rb;
+                }
             }
             // every copy lands before the CTA leaves: slot s last held the largest fill s + k * slots
             const uint64_t until = globaltimer_ns() + 100000000ull;
@@ -342,46 +387,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) key_weights_kernel(const __grid
                 const unsigned last = s + (g - 1 - s) / C::kStages * C::kStages;
                 if (!(a.test_skip_load && last == 0)) mbar_wait_bounded(&ring_full[s], (last / C::kStages) & 1, &no_abort, until);
             }
-            for (unsigned s = 0; s < (unsigned)n_held && s < h; ++s) {
+            for (unsigned s = 0; s < n_held && s < h; ++s) {
                 const unsigned last = s + (h - 1 - s) / n_held * n_held;
                 mbar_wait_bounded(&held_full[s], (last / n_held) & 1, &no_abort, until);
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == n_epilogue + 1) {
         if (lane == 0) {
             const uint32_t idesc = instr_desc(kKeysTile, a.n_cols, false);
+            const uint64_t d_ring = sw128_desc(smem_u32(ring)), d_held = sw128_desc(smem_u32(held));
+            // a chunk of keys is 16 KB wherever it lies
+            const uint64_t q_step = q_chunk >> 4, part = C::kStageChunks * (a.keys_held ? 1024 : q_step);
             unsigned g = 0, h = 0, step = 0;  // ring stages, held operands, tiles of S
             bool ok = true;
-            for (Item it; ok && walk.next(it);) {
-                if (it.fresh) {
-                    if (h > 0) tc_commit(&held_empty[(h - 1) % n_held]);
-                    if (!(ok = wait(&held_full[h % n_held], (h / n_held) & 1))) break;
-                    ++h;
-                }
-                const uint32_t kept = smem_u32(held + (h - 1) % n_held * held_bytes);
-                for (int64_t x = it.col0; ok && x < it.col1; ++x, ++step) {
-                    if (!(ok = wait(&s_empty[step & 1], ((step >> 1) & 1) ^ 1))) break;
-                    const uint32_t d = tmem + (step & 1) * kMaxCols;
+            for (Run r; ok && walk.next(r); ++h) {
+                const unsigned y = h & (n_held - 1);
+                if (!(ok = wait(&held_full[y], (h >> (n_held - 1)) & 1))) break;
+                const uint64_t kept = d_held + (uint64_t)((y * held_bytes) >> 4);
+                for (int i = 0; ok && i < r.n; ++i, ++step) {
+                    const unsigned buf = step & (s_bufs - 1);
+                    if (step >= s_bufs && !(ok = wait(&s_empty[buf], ((step >> s_shift) & 1) ^ 1))) break;
+                    const uint32_t d = tmem + buf * s_stride;
                     for (int p = 0; p < C::kStagesPerTile; ++p, ++g) {
                         const unsigned s = g % C::kStages;
                         if (!(ok = wait(&ring_full[s], (g / C::kStages) & 1))) break;
                         tc_fence_after();
-                        const uint32_t here = smem_u32(ring + s * C::kStageBytes);
-                        // a chunk of keys is 16 KB wherever it lies
-                        const uint64_t dk = sw128_desc(a.keys_held ? kept + p * C::kStageChunks * 16384 : here);
-                        const uint64_t dq = sw128_desc(a.keys_held ? here : kept + p * C::kStageChunks * q_chunk);
+                        const uint64_t here = d_ring + (uint64_t)((s * C::kStageBytes) >> 4), there = kept + p * part;
+                        const uint64_t dk = a.keys_held ? there : here, dq = a.keys_held ? here : there;
 #pragma unroll
                         for (int c = 0; c < C::kStageChunks; ++c)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 if (D % 64 == 0 || c * 4 + k < C::kSteps)
-                                    tc_mma_ss(d, dk + (uint64_t)((c * 16384 + k * 32) >> 4),
-                                              dq + (uint64_t)((c * q_chunk + k * 32) >> 4), idesc, p > 0 || c > 0 || k > 0);
+                                    tc_mma_ss(d, dk + (uint64_t)((c * 16384 + k * 32) >> 4), dq + c * q_step + (uint64_t)(k * 32 >> 4),
+                                              idesc, p > 0 || c > 0 || k > 0);
                         tc_commit(&ring_empty[s]);
                     }
-                    if (ok) tc_commit(&s_full[step & 1]);
+                    if (ok) tc_commit(&s_full[buf]);
                 }
+                tc_commit(&held_empty[y]);
             }
             // all MMAs finish before tensor memory is freed
             tc_commit(bar_done);
@@ -389,117 +434,190 @@ __global__ void __launch_bounds__(kTcThreads, 1) key_weights_kernel(const __grid
             mbar_wait_bounded(bar_done, 0, &no_abort, globaltimer_ns() + 100000000ull);
         }
         __syncwarp();
-    } else if (warp == kTableWarp) {
-        unsigned n = 0;  // tables made
-        for (Item it; walk.next(it);) {
-            if (!a.keys_held && !it.fresh) continue;
-            bool ok = true;
-            for (int64_t x = it.col0; x < it.col1; ++x, ++n) {
-                ok = __all_sync(0xffffffffu, wait(&tab_empty[n & 1], ((n >> 1) & 1) ^ 1));
-                if (!ok) break;
-                Table &tab = tables[n & 1];
-                const int rb = (int)(x / a.head_blocks), hb = (int)(x % a.head_blocks);
-                const int rows = min(a.rows_per, a.n_q - rb * a.rows_per), heads = min(a.heads_per, G - hb * a.heads_per);
-                // (one block of heads, or one row a tile: the columns there are come first)
-                const int count = a.head_blocks == 1 ? rows * heads : heads;
-                int min_hi = 0x7fffffff, max_lo = -1;
-                for (int i = lane; i < a.n_cols; i += 32) {
-                    int hi = -1, lo = -1;
-                    float l = INFINITY;
-                    if (i < count) {
-                        const int row = rb * a.rows_per + i / a.heads_per, pos = it.len - a.n_q + row;
-                        l = a.lse[((int64_t)it.b * a.n_q + row) * a.n_heads + it.hk * G + hb * a.heads_per + i % a.heads_per];
-                        if (pos >= 0 && l != -INFINITY) {  // (else the row sees nothing)
-                            hi = a.causal ? pos : 0x7fffffff;
-                            lo = a.window > 0 ? pos - a.window : -1;
-                        }
-                        l = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-                        min_hi = min(min_hi, hi);
-                        max_lo = max(max_lo, lo);
-                    }
-                    tab.lse2[i] = l, tab.hi[i] = hi, tab.lo[i] = lo;
-                }
-                min_hi = __reduce_min_sync(0xffffffffu, min_hi);
-                max_lo = __reduce_max_sync(0xffffffffu, max_lo);
-                if (lane == 0) tab.min_hi = min_hi, tab.max_lo = max_lo, tab.count = count;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tab_full[n & 1]);
+    } else if (warp >= n_epilogue + 2) {
+        // ---- tables.  Queries held: one a run, the warps in turn.  Keys held: one a tile of columns,
+        // the warps in turn, in the place of its tile of S; the next one's log-sum-exps are on their way
+        // while one is filled.  Lane i has columns i, i + 32, ...: rows and heads that do not change.
+        constexpr int kMine = kMaxCols / 32;
+        const int odd = warp - n_epilogue - 2;
+        int col_row[kMine], col_at[kMine];
+#pragma unroll
+        for (int e = 0; e < kMine; ++e) {
+            const uint32_t i = lane + 32 * e;
+            col_row[e] = (int)a.by_heads_per.div(i);
+            col_at[e] = col_row[e] * a.n_heads + (int)i - col_row[e] * a.heads_per;
+        }
+        struct Place {
+            int rb, hb, count;
+        };
+        auto place_of = [&](int64_t x) {  // (one block of heads, or one row a tile: the columns there are come first)
+            Place p;
+            p.rb = (int)(x / a.head_blocks), p.hb = (int)(x - (int64_t)p.rb * a.head_blocks);
+            p.count = min(a.rows_per, a.n_q - p.rb * a.rows_per) * min(a.heads_per, G - p.hb * a.heads_per);
+            return p;
+        };
+        float l[kMine];
+        auto ask = [&](const Run &r, const Place &p) {
+            const float *src = a.lse + ((int64_t)r.b * a.n_q + p.rb * a.rows_per) * a.n_heads + r.hk * G + p.hb * a.heads_per;
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                if (32 * e >= a.n_cols) break;
+                l[e] = lane + 32 * e < p.count ? __ldg(src + col_at[e]) : -INFINITY;
             }
-            if (!ok) break;
+        };
+        auto fill = [&](Table &tab, const Run &r, const Place &p) {
+            const int pos0 = r.len - a.n_q + p.rb * a.rows_per;
+            int min_hi = 0x7fffffff, max_lo = -1;
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+                const int i = lane + 32 * e, pos = pos0 + col_row[e];
+                if (32 * e >= a.n_cols) break;
+                int hi = -1, lo = -1;
+                if (i < p.count) {
+                    if (pos >= 0 && l[e] != -INFINITY) {  // (else the row sees nothing)
+                        hi = a.causal ? pos : 0x7fffffff;
+                        lo = a.window > 0 ? pos - a.window : -1;
+                    }
+                    min_hi = min(min_hi, hi);
+                    max_lo = max(max_lo, lo);
+                }
+                tab.minus_lse2[i] = l[e] == -INFINITY ? -INFINITY : l[e] * -1.4426950408889634f;
+                tab.hi[i] = hi, tab.lo[i] = lo;
+            }
+            min_hi = __reduce_min_sync(0xffffffffu, min_hi);
+            max_lo = __reduce_max_sync(0xffffffffu, max_lo);
+            if (lane == 0) tab.min_hi = min_hi, tab.max_lo = max_lo, tab.count = p.count;
+            __syncwarp();
+        };
+        auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+        unsigned n = 0;  // tables before this run's
+        bool ok = true;
+        for (Run r; ok && walk.next(r);) {
+            if (!a.keys_held) {
+                if ((n & 1) == (unsigned)odd) {
+                    const unsigned u = n % kTables;
+                    const Place p = place_of(0);
+                    ask(r, p);
+                    if (!(ok = wait_warp(&tab_empty[u], ((n / kTables) & 1) ^ 1))) break;
+                    fill(tables[u], r, p);
+                    if (lane == 0) mbar_arrive(&tab_full[u]);
+                }
+                ++n;
+                continue;
+            }
+            int i = (n & 1) == (unsigned)odd ? 0 : 1;  // this warp's first of the run
+            Place p = place_of(r.x + i);
+            if (i < r.n) ask(r, p);
+            for (; i < r.n; i += 2) {
+                const unsigned k = n + i, u = k & (s_bufs - 1);
+                if (k >= s_bufs && !(ok = wait_warp(&s_empty[u], ((k >> s_shift) & 1) ^ 1))) break;
+                fill(tables[u], r, p);
+                if (lane == 0) mbar_arrive(&s_full[u]);
+                if (i + 2 < r.n) {
+                    p = place_of(r.x + i + 2);
+                    ask(r, p);
+                }
+            }
+            n += r.n;
         }
     } else {
         // ---- epilogues: thread = key ----------------------------------------------------------
-        const unsigned group = warp >> 2, quarter = warp & 3;
-        const int row = quarter * 32 + lane;
+        const int quartet = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-        unsigned step = 0, tabs = 0, items = 0;  // tiles of S, tables, items before this one
-        bool ok = true;
-        for (Item it; ok && walk.next(it); ++items) {
-            const int first = it.t * kKeysTile, j = first + row, last = min(first + kKeysTile, it.len) - 1;
-            // keys held: the first epilogue has the last word on every item
-            const bool writes = a.keys_held ? group == 0 : (step & 1) == group;
-            float *dst = a.weights + (int64_t)it.b * a.w_seq + (int64_t)it.hk * a.w_head + j;
-            const float was = writes && j < it.len ? *dst : 0.f;
-            float sum = 0.f, lost = 0.f;
-            for (int64_t x = it.col0; x < it.col1; ++x, ++step) {
-                if (a.keys_held || it.fresh) {  // another table: every warp lets the last go, and has seen
-                    if (tabs > 0) {             // each one full before it lets that go
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tab_empty[(tabs - 1) & 1]);
-                    }
-                    if (!(ok = wait_warp(&tab_full[tabs & 1], (tabs >> 1) & 1))) break;
-                    ++tabs;
-                }
-                if ((step & 1) != group) continue;
-                if (!(ok = wait_warp(&s_full[group], (step >> 1) & 1))) break;
-                tc_fence_after();
-                const Table &tab = tables[(tabs - 1) & 1];
-                const int count = tab.count, whole = count / 16 * 16;
-                const bool mask = tab.min_hi < last || tab.max_lo >= first;
-                const uint32_t src = lanes + group * kMaxCols;
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
-                uint32_t r[2][16];
-                tmem_ld16(src, r[0]);
-                for (int n = 0; n < count; n += 32) {
-                    tc_wait_ld();
-                    if (n + 16 < count) tmem_ld16(src + n + 16, r[1]);
-                    if (mask || n >= whole) add_columns<CAP, true>(part, r[0], tab, n, j, a);
-                    else add_columns<CAP, false>(part, r[0], tab, n, j, a);
-                    if (n + 16 >= count) break;
-                    tc_wait_ld();
-                    if (n + 32 < count) tmem_ld16(src + n + 32, r[0]);
-                    if (mask || n + 16 >= whole) add_columns<CAP, true>(part, r[1], tab, n + 16, j, a);
-                    else add_columns<CAP, false>(part, r[1], tab, n + 16, j, a);
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[group]);
-                // sum + lost += part (a sum with its rounding error kept)
-                const float more = (part[0] + part[1]) + (part[2] + part[3]) + lost, now = sum + more;
-                lost = more - (now - sum);
-                sum = now;
-            }
-            if (!ok) break;
-            if (a.keys_held) {  // the second epilogue's share of the item, through shared memory
-                if (group == 1) {
-                    if (!(ok = wait_warp(&x_empty[quarter], (items & 1) ^ 1))) break;
-                    passed[row] = sum + lost;
+        // this warp's columns of the tile of S of that number, summed over; false: a wait ran out
+        auto take = [&](unsigned step, const Table &tab, int first, int last, float &total) {
+            const unsigned buf = step & (s_bufs - 1);
+            if (!wait_warp(&s_full[buf], (step >> s_shift) & 1)) return false;
+            tc_fence_after();
+            const int count = tab.count, per = alone ? count : (count + 63) / 64 * 16, j = first + row;
+            const int n0 = alone ? 0 : quartet * per, n1 = min(count, n0 + per);
+            const bool mask = tab.min_hi < last || tab.max_lo >= first;
+            const uint32_t src = lanes + buf * s_stride;
+            uint64_t part[2] = {0, 0};
+            for (int n = n0; n < n1; n += 32) {
+                uint32_t r0[16], r1[16];
+                const bool two = n + 16 < n1;
+                tmem_ld16(src + n, r0);
+                if (two) tmem_ld16(src + n + 16, r1);
+                tc_wait_ld();
+                if (n + 32 >= n1) {  // the last of them: S may be written again
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&x_full[quarter]);
+                    if (!a.keys_held && lane == 0) mbar_arrive(&s_empty[buf]);
+                }
+                if (mask || n + (two ? 32 : 16) > n1) {
+                    add_columns<CAP, true>(part, r0, tab, n, j, a);
+                    if (two) add_columns<CAP, true>(part, r1, tab, n + 16, j, a);
                 } else {
-                    if (!(ok = wait_warp(&x_full[quarter], items & 1))) break;
-                    sum += passed[row] + lost;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&x_empty[quarter]);
+                    add_columns<CAP, false>(part, r0, tab, n, j, a);
+                    if (two) add_columns<CAP, false>(part, r1, tab, n + 16, j, a);
                 }
             }
-            if (writes && j < it.len) *dst = was + sum;
+            if (a.keys_held || n0 >= n1) {  // (the table goes with its tile)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[buf]);
+            }
+            const float2 p0 = halves_of(part[0]), p1 = halves_of(part[1]);
+            total = (p0.x + p0.y) + (p1.x + p1.y);
+            return true;
+        };
+        // the quartets' sums of item number `item` meet at one of them, which has its turn.  While one
+        // warp is still at an item's sums, its tiles of S let go, the others get through the next four
+        // items at most (one more waits for that warp's share of a tile): their places are not this
+        // one's.
+        auto meet = [&](unsigned item, float &sum, bool turn) {
+            const unsigned slot = item % kPlaces;
+            float *place = passed + slot * kMaxQuartets * kKeysTile;
+            place[quartet * kKeysTile + row] = sum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x_full[slot * 4 + quarter]);
+            if (!turn) return true;
+            if (!wait_warp(&x_full[slot * 4 + quarter], (item / kPlaces) & 1)) return false;
+            sum = (place[row] + place[kKeysTile + row]) + (place[2 * kKeysTile + row] + place[3 * kKeysTile + row]);
+            return true;
+        };
+        // (this thread alone has the key: no order of additions comes into it)
+        auto give = [&](const Run &r, int t, float sum) {
+            const int j = t * kKeysTile + row;
+            if (j < r.len) atomicAdd(a.weights + (int64_t)r.b * a.w_seq + (int64_t)r.hk * a.w_head + j, sum);
+        };
+        unsigned step = 0, runs = 0;  // tiles of S, runs before this one
+        bool ok = true;
+        for (Run r; ok && walk.next(r); ++runs, step += r.n) {
+            if (a.keys_held) {  // one key tile
+                const int first = r.t * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
+                const bool turn = (int)(runs % quartets) == quartet;
+                float sum = 0.f, lost = 0.f, part;
+                for (int i = 0; i < r.n; ++i) {
+                    if (!(ok = take(step + i, tables[(step + i) & (s_bufs - 1)], first, last, part))) break;
+                    // sum + lost += part (a sum with its rounding error kept)
+                    const float more = part + lost, now = sum + more;
+                    lost = more - (now - sum);
+                    sum = now;
+                }
+                sum += lost;
+                if (!ok || !(ok = meet(runs, sum, turn))) break;
+                if (turn) give(r, r.t, sum);
+                continue;
+            }
+            const Table &tab = tables[runs % kTables];
+            if (!(ok = wait_warp(&tab_full[runs % kTables], (runs / kTables) & 1))) break;
+            for (int i = alone ? (int)((unsigned)(quartet - (int)step) & (quartets - 1)) : 0; i < r.n; i += alone ? quartets : 1) {
+                const int first = (r.t + i) * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
+                const bool turn = alone || (int)((step + i) % quartets) == quartet;
+                float sum;
+                if (!(ok = take(step + i, tab, first, last, sum))) break;
+                if (!alone && !(ok = meet(step + i, sum, turn))) break;
+                if (turn) give(r, r.t + i, sum);
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&tab_empty[runs % kTables]);
         }
     }
     __syncthreads();
     if (tid == 0 && *abort_flag) report_status(a.status, kErrTimeout);
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == n_epilogue + 1) tmem_dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------------- fp32
@@ -609,7 +727,8 @@ cudaError_t launch_tc(const KeyWeightsArgs &a, int grid, cudaStream_t s) {
     using C = KwCfg<D>;
     const cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    key_weights_kernel<D, CAP><<<grid, kTcThreads, C::kSmem, s>>>(a);
+    const int threads = 128 * (!a.keys_held && a.n_cols <= kNarrowCols ? 2 : kMaxQuartets) + 32 * kMoreWarps;
+    key_weights_kernel<D, CAP><<<grid, threads, C::kSmem, s>>>(a);
     return cudaGetLastError();
 }
 template <int D>
