@@ -20,10 +20,10 @@
 //    Either way every key has one owner, so sums are in a fixed order and nothing is atomic.
 //  * Roles: epilogue warps in quartets (a warp can read the quarter of tensor memory's lanes that
 //    its number says), a warp that issues the copies, one that issues the MMAs, two that prepare
-//    the columns' log-sum-exps and ranges of keys.  S has two to four buffers in tensor memory.
-//    Queries held, a tile of up to 128 columns goes to one quartet, the next to another; otherwise a
-//    tile's columns are cut in four, and the quartets' sums meet in shared memory at a key tile's
-//    end.  Where a range cuts a tile, pairs are masked one by one.
+//    the columns' log-sum-exps and ranges of keys.  S has four buffers of 128 columns in tensor
+//    memory; every quartet takes every fourth tile of S (two quartets where a tile is small, every
+//    other) whole, so that its waits are few.  Where a key tile has several tiles of S, the quartets'
+//    sums meet in shared memory at its end.  Where a range cuts a tile, pairs are masked one by one.
 //  * What a role does for every tile is kept short (a wait that need not wait costs a thread 100
 //    to 200 cycles): walks go by runs of tiles, tables come with the tile of S they belong to, and
 //    a key's sum goes to memory as a reduction that nothing waits for.
@@ -56,8 +56,10 @@ constexpr int kMaxQuartets = 4;
 constexpr int kMoreWarps = 4;                     // behind them: copies, MMAs, two of tables
 constexpr int kMaxThreads = 128 * kMaxQuartets + 32 * kMoreWarps;
 constexpr int kTables = 4;
-constexpr int kPlaces = 8;                        // items whose sums can be under way at once
-constexpr uint32_t kTmemCols = 512;               // tiles of S, 128 columns apart (256 where they are wider)
+constexpr int kPlaces = 8;                        // key tiles whose sums can be under way at once
+constexpr int kSBufs = 4, kSCols = 128;           // tiles of S in tensor memory
+constexpr uint32_t kTmemCols = kSBufs * kSCols;
+constexpr int kMaxStages = 8;
 
 template <int D>
 struct KwCfg {
@@ -66,14 +68,15 @@ struct KwCfg {
     static constexpr int kStageChunks = D == 64 ? 1 : 2;    // chunks of a ring stage, 16 KB each
     static constexpr int kStagesPerTile = kChunks / kStageChunks;
     static constexpr int kStageBytes = kStageChunks * 16384;
-    static constexpr int kStages = D == 512 ? 2 : D == 64 ? 8 : 4;
-    // the operand that stays: up to 256 (head_dim 256, 512: 128) columns, or 128 keys
+    // The operand that stays has up to 64 KB (head_dim 512: 128 KB): up to 256 (head_dim 256, 512: 128)
+    // columns, or 128 keys.  What it leaves of kTiles is the ring's.
     static constexpr int kHeldBytes = D == 512 ? 131072 : 65536;
     static constexpr int kHeldCols = kHeldBytes / (kChunks * 128) < kMaxCols ? kHeldBytes / (kChunks * 128) : kMaxCols;
+    static constexpr int kTiles = 196608;
     static constexpr int kTableBytes = kTables * (3 * kMaxCols + 4) * 4;
-    static constexpr int kPassed = kPlaces * kMaxQuartets * kKeysTile * 4;          // [item % kPlaces][quartet][key] sums
+    static constexpr int kPassed = kPlaces * kMaxQuartets * kKeysTile * 4;          // [key tile % kPlaces][quartet][key] sums
     static constexpr int kBarBytes = 1024;
-    static constexpr int kSmem = kHeldBytes + kStages * kStageBytes + kTableBytes + kPassed + kBarBytes;
+    static constexpr int kSmem = kTiles + kTableBytes + kPassed + kBarBytes;
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
@@ -247,22 +250,20 @@ template <int D, bool CAP>
 __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsArgs a) {
     using C = KwCfg<D>;
     extern __shared__ __align__(1024) unsigned char smem[];      // (an aligned-up pointer would load as generic)
-    unsigned char *held = smem;                                  // one or two operands that stay
-    unsigned char *ring = held + C::kHeldBytes;                  // [kStages]
-    Table *tables = reinterpret_cast<Table *>(ring + C::kStages * C::kStageBytes);  // [kTables]
-    float *passed = reinterpret_cast<float *>(tables + kTables);                    // [item % kPlaces][quartet][key]
+    Table *tables = reinterpret_cast<Table *>(smem + C::kTiles);  // [kTables]
+    float *passed = reinterpret_cast<float *>(tables + kTables);  // [key tile % kPlaces][quartet][key]
     uint64_t *bars = reinterpret_cast<uint64_t *>(passed + kPlaces * kMaxQuartets * kKeysTile);
-    uint64_t *ring_full = bars, *ring_empty = bars + 8;          // [kStages]
+    uint64_t *ring_full = bars, *ring_empty = bars + 8;          // [n_stages]
     uint64_t *held_full = bars + 16, *held_empty = bars + 18;    // [2]
     uint64_t *s_full = bars + 20, *s_empty = bars + 24;          // [4]
     uint64_t *tab_full = bars + 28, *tab_empty = tab_full + kTables;
-    uint64_t *x_full = tab_empty + kTables;                      // [item % kPlaces][quarter of the lanes]
+    uint64_t *x_full = tab_empty + kTables;                      // [key tile % kPlaces][quarter of the lanes]
     uint64_t *bar_done = x_full + 4 * kPlaces;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int64_t *start = reinterpret_cast<int64_t *>(bar_done + 2);  // share: base, b
     int *scan = reinterpret_cast<int *>(bar_done + 4);           // a warp each
-    static_assert(sizeof(Table) * kTables == C::kTableBytes && C::kStages <= 8 && kTables >= 4 &&
+    static_assert(sizeof(Table) * kTables == C::kTableBytes && kTables >= kSBufs &&
                       (32 + 2 * kTables + 4 * kPlaces) * 8 + kMaxThreads / 32 * 4 <= C::kBarBytes,
                   "shared memory layout");
     if (smem_u32(smem) & 1023) {  // (swizzled operands need it; it is where dynamic shared memory begins)
@@ -271,22 +272,30 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_threads = blockDim.x;
     const int n_epilogue = n_threads / 32 - kMoreWarps, quartets = n_epilogue / 4;
-    const bool alone = !a.keys_held && a.n_cols <= 128;          // a quartet takes a tile of S alone
-    const unsigned s_stride = a.n_cols <= 128 ? 128 : 256, s_bufs = kTmemCols / s_stride;  // a power of two
-    const unsigned s_shift = a.n_cols <= 128 ? 2 : 1;            // log2 of s_bufs
+    const int halves = a.n_cols > kSCols ? 2 : 1;                // tiles of S of a column tile (queries held)
+    // bytes of a chunk of the tile of queries and of keys; how many operands there is room to hold,
+    // and stages behind them
+    const int q_rows = a.rows_per * a.heads_per;                 // columns that a copy brings
+    const int q_chunk = a.keys_held ? 16384 : a.n_cols * 128;    // where its chunks lie apart
+    const int held_bytes = C::kChunks * (a.keys_held ? 16384 : q_chunk);
+    const unsigned n_held = 2 * held_bytes <= C::kHeldBytes ? 2 : 1;
+    unsigned char *held = smem, *ring = held + n_held * held_bytes;
+    const unsigned n_stages = min(kMaxStages, (C::kTiles - (int)n_held * held_bytes) / C::kStageBytes);
     const int G = a.n_heads / a.n_kv_heads;
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
-    if (tid == 0) {
-        for (int i = 0; i < C::kStages; ++i) mbar_init(&ring_full[i], 1), mbar_init(&ring_empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&held_full[i], 1), mbar_init(&held_empty[i], 1);
-        // keys held: a tile of S is full when its MMAs are done and its table is there
-        for (int i = 0; i < 4; ++i) mbar_init(&s_full[i], a.keys_held ? 2 : 1), mbar_init(&s_empty[i], alone ? 4 : n_epilogue);
-        for (int i = 0; i < kTables; ++i) mbar_init(&tab_full[i], 1), mbar_init(&tab_empty[i], n_epilogue);
-        for (int i = 0; i < 4 * kPlaces; ++i) mbar_init(&x_full[i], quartets);
-        mbar_init(bar_done, 1);
-        *abort_flag = 0;
+    if (tid < 32) {  // barriers, a few a lane
+        auto init = [&](uint64_t *first, int n, int count) {
+            if (lane < n) mbar_init(first + lane, count);
+        };
+        init(ring_full, 2 * kMaxStages + 4, 1);  // ring and held
+        init(s_full, kSBufs, a.keys_held ? 2 : 1);  // keys held: full when its MMAs are done and its table is there
+        init(s_empty, kSBufs, 4 * halves);
+        init(tab_full, kTables, 1);
+        init(tab_empty, kTables, n_epilogue);
+        init(x_full, 4 * kPlaces, a.keys_held ? 3 : 1);
+        init(bar_done, 1, 1);
+        if (lane == 0) *abort_flag = 0, start[0] = 0, start[1] = a.batch;
         fence_mbarrier_init();
-        start[0] = 0, start[1] = a.batch;
     }
     if (warp == n_epilogue + 1) {
         tmem_alloc(tmem_slot, kTmemCols);
@@ -339,17 +348,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         __syncthreads();
     }
     Walker walk{a, r0, r1, start[0], (int)start[1]};
-    // bytes of a chunk of the tile of queries and of keys; how many operands there is room to hold
-    const int q_rows = a.rows_per * a.heads_per;                 // columns that a copy brings
-    const int q_chunk = a.keys_held ? 16384 : a.n_cols * 128;    // where its chunks lie apart
-    const int held_bytes = C::kChunks * (a.keys_held ? 16384 : q_chunk);
-    const unsigned n_held = 2 * held_bytes <= C::kHeldBytes ? 2 : 1;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag, deadline); };
 
     if (warp == n_epilogue) {
         if (lane == 0) {
             if (a.max_kv_len > 0) tma_prefetch_desc(&a.tm_q), tma_prefetch_desc(&a.tm_k);  // (else there are none)
-            unsigned g = 0, h = 0;  // ring stages and held operands issued
+            unsigned g = 0, h = 0, s = 0, turn = 0;  // stages and held operands issued; place in the ring, times round it
             bool ok = true;
             // chunks [c0, c1) of key tile t, and of the columns of row block rb and head block hb
             auto keys = [&](unsigned char *to, uint64_t *bar, const Run &r, int t, int c0, int c1) {
@@ -369,13 +373,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
                 int rb = (int)(r.x / a.head_blocks), hb = (int)(r.x - (int64_t)rb * a.head_blocks);
                 for (int i = 0; ok && i < r.n; ++i) {
                     for (int p = 0; p < C::kStagesPerTile; ++p, ++g) {
-                        const unsigned s = g % C::kStages;
-                        if (!(ok = wait(&ring_empty[s], ((g / C::kStages) & 1) ^ 1))) break;
-                        if (a.test_skip_load && g == 0) continue;  // test hook: never comes
-                        const int c0 = p * C::kStageChunks;
-                        mbar_arrive_expect_tx(&ring_full[s], C::kStageChunks * (a.keys_held ? q_rows * 128 : 16384));
-                        if (a.keys_held) queries(ring + s * C::kStageBytes, &ring_full[s], r, rb, hb, c0, c0 + C::kStageChunks);
-                        else keys(ring + s * C::kStageBytes, &ring_full[s], r, r.t + i, c0, c0 + C::kStageChunks);
+                        if (turn > 0 && !(ok = wait(&ring_empty[s], (turn & 1) ^ 1))) break;
+                        if (!a.test_skip_load || g > 0) {  // (test hook: the first never comes)
+                            const int c0 = p * C::kStageChunks;
+                            mbar_arrive_expect_tx(&ring_full[s], C::kStageChunks * (a.keys_held ? q_rows * 128 : 16384));
+                            if (a.keys_held) queries(ring + s * C::kStageBytes, &ring_full[s], r, rb, hb, c0, c0 + C::kStageChunks);
+                            else keys(ring + s * C::kStageBytes, &ring_full[s], r, r.t + i, c0, c0 + C::kStageChunks);
+                        }
+                        if (++s == n_stages) s = 0, ++turn;
                     }
                     if (++hb == a.head_blocks) hb = 0, ++rb;
                 }
@@ -383,35 +388,35 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             // every copy lands before the CTA leaves: slot s last held the largest fill s + k * slots
             const uint64_t until = globaltimer_ns() + 100000000ull;
             volatile int no_abort = 0;
-            for (unsigned s = 0; s < C::kStages && s < g; ++s) {
-                const unsigned last = s + (g - 1 - s) / C::kStages * C::kStages;
-                if (!(a.test_skip_load && last == 0)) mbar_wait_bounded(&ring_full[s], (last / C::kStages) & 1, &no_abort, until);
+            for (unsigned x = 0; x < n_stages && x < g; ++x) {
+                const unsigned last = x + (g - 1 - x) / n_stages * n_stages;
+                if (!(a.test_skip_load && last == 0)) mbar_wait_bounded(&ring_full[x], (last / n_stages) & 1, &no_abort, until);
             }
-            for (unsigned s = 0; s < n_held && s < h; ++s) {
-                const unsigned last = s + (h - 1 - s) / n_held * n_held;
-                mbar_wait_bounded(&held_full[s], (last / n_held) & 1, &no_abort, until);
+            for (unsigned x = 0; x < n_held && x < h; ++x) {
+                const unsigned last = x + (h - 1 - x) / n_held * n_held;
+                mbar_wait_bounded(&held_full[x], (last / n_held) & 1, &no_abort, until);
             }
         }
         __syncwarp();
     } else if (warp == n_epilogue + 1) {
         if (lane == 0) {
+            // N of a column tile's first and second tile of S
             const uint32_t idesc = instr_desc(kKeysTile, a.n_cols, false);
             const uint64_t d_ring = sw128_desc(smem_u32(ring)), d_held = sw128_desc(smem_u32(held));
             // a chunk of keys is 16 KB wherever it lies
             const uint64_t q_step = q_chunk >> 4, part = C::kStageChunks * (a.keys_held ? 1024 : q_step);
-            unsigned g = 0, h = 0, step = 0;  // ring stages, held operands, tiles of S
+            unsigned h = 0, step = 0, s = 0, turn = 0;  // held operands, tiles of S; place in the ring, times round it
             bool ok = true;
             for (Run r; ok && walk.next(r); ++h) {
                 const unsigned y = h & (n_held - 1);
                 if (!(ok = wait(&held_full[y], (h >> (n_held - 1)) & 1))) break;
                 const uint64_t kept = d_held + (uint64_t)((y * held_bytes) >> 4);
-                for (int i = 0; ok && i < r.n; ++i, ++step) {
-                    const unsigned buf = step & (s_bufs - 1);
-                    if (step >= s_bufs && !(ok = wait(&s_empty[buf], ((step >> s_shift) & 1) ^ 1))) break;
-                    const uint32_t d = tmem + buf * s_stride;
-                    for (int p = 0; p < C::kStagesPerTile; ++p, ++g) {
-                        const unsigned s = g % C::kStages;
-                        if (!(ok = wait(&ring_full[s], (g / C::kStages) & 1))) break;
+                for (int i = 0; ok && i < r.n; ++i, step += halves) {
+                    const unsigned buf = step % kSBufs;  // (two tiles of S lie side by side and go by the first's barriers)
+                    if (step >= kSBufs && !(ok = wait(&s_empty[buf], ((step / kSBufs) & 1) ^ 1))) break;
+                    const uint32_t d = tmem + buf * kSCols;
+                    for (int p = 0; p < C::kStagesPerTile; ++p) {
+                        if (!(ok = wait(&ring_full[s], turn & 1))) break;
                         tc_fence_after();
                         const uint64_t here = d_ring + (uint64_t)((s * C::kStageBytes) >> 4), there = kept + p * part;
                         const uint64_t dk = a.keys_held ? there : here, dq = a.keys_held ? here : there;
@@ -423,6 +428,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
                                     tc_mma_ss(d, dk + (uint64_t)((c * 16384 + k * 32) >> 4), dq + c * q_step + (uint64_t)(k * 32 >> 4),
                                               idesc, p > 0 || c > 0 || k > 0);
                         tc_commit(&ring_empty[s]);
+                        if (++s == n_stages) s = 0, ++turn;
                     }
                     if (ok) tc_commit(&s_full[buf]);
                 }
@@ -509,8 +515,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             Place p = place_of(r.x + i);
             if (i < r.n) ask(r, p);
             for (; i < r.n; i += 2) {
-                const unsigned k = n + i, u = k & (s_bufs - 1);
-                if (k >= s_bufs && !(ok = wait_warp(&s_empty[u], ((k >> s_shift) & 1) ^ 1))) break;
+                const unsigned k = n + i, u = k % kSBufs;
+                if (k >= kSBufs && !(ok = wait_warp(&s_empty[u], ((k / kSBufs) & 1) ^ 1))) break;
                 fill(tables[u], r, p);
                 if (lane == 0) mbar_arrive(&s_full[u]);
                 if (i + 2 < r.n) {
@@ -525,58 +531,65 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         const int quartet = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
-        // this warp's columns of the tile of S of that number, summed over; false: a wait ran out
-        auto take = [&](unsigned step, const Table &tab, int first, int last, float &total) {
-            const unsigned buf = step & (s_bufs - 1);
-            if (!wait_warp(&s_full[buf], (step >> s_shift) & 1)) return false;
+        // the sum over the tile of S of that number, its columns the table's from `off` on; false: a wait
+        // ran out
+        auto take = [&](unsigned step, const Table &tab, int off, int first, int last, float &total) {
+            const unsigned buf = step % kSBufs, bar = buf & -halves;
+            if (!wait_warp(&s_full[bar], (step / kSBufs) & 1)) return false;
             tc_fence_after();
-            const int count = tab.count, per = alone ? count : (count + 63) / 64 * 16, j = first + row;
-            const int n0 = alone ? 0 : quartet * per, n1 = min(count, n0 + per);
+            const int n1 = min(tab.count - off, kSCols), j = first + row;
             const bool mask = tab.min_hi < last || tab.max_lo >= first;
-            const uint32_t src = lanes + buf * s_stride;
+            const uint32_t src = lanes + buf * kSCols;
             uint64_t part[2] = {0, 0};
-            for (int n = n0; n < n1; n += 32) {
-                uint32_t r0[16], r1[16];
-                const bool two = n + 16 < n1;
-                tmem_ld16(src + n, r0);
-                if (two) tmem_ld16(src + n + 16, r1);
-                tc_wait_ld();
-                if (n + 32 >= n1) {  // the last of them: S may be written again
-                    tc_fence_before();
-                    __syncwarp();
-                    if (!a.keys_held && lane == 0) mbar_arrive(&s_empty[buf]);
-                }
-                if (mask || n + (two ? 32 : 16) > n1) {
-                    add_columns<CAP, true>(part, r0, tab, n, j, a);
-                    if (two) add_columns<CAP, true>(part, r1, tab, n + 16, j, a);
-                } else {
-                    add_columns<CAP, false>(part, r0, tab, n, j, a);
-                    if (two) add_columns<CAP, false>(part, r1, tab, n + 16, j, a);
-                }
-            }
-            if (a.keys_held || n0 >= n1) {  // (the table goes with its tile)
+            auto add = [&](const uint32_t (&r)[16], int n) {
+                if (mask || n + 16 > n1) add_columns<CAP, true>(part, r, tab, off + n, j, a);
+                else add_columns<CAP, false>(part, r, tab, off + n, j, a);
+            };
+            auto let_go = [&] {  // S may be written again (with keys held, the table too)
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[buf]);
+                if (lane == 0) mbar_arrive(&s_empty[bar]);
+            };
+            if constexpr (CAP) {  // (the cap's registers leave no room for more)
+                for (int n = 0; n < n1; n += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(src + n, r);
+                    tc_wait_ld();
+                    if (n + 16 >= n1 && !a.keys_held) let_go();
+                    add(r, n);
+                }
+            } else {  // sixteen columns on their way while sixteen are summed
+                uint32_t r0[16], r1[16];
+                tmem_ld16(src, r0);
+                for (int n = 0;; n += 32) {
+                    tc_wait_ld();
+                    if (n + 16 < n1) tmem_ld16(src + n + 16, r1);
+                    else if (!a.keys_held) let_go();
+                    add(r0, n);
+                    if (n + 16 >= n1) break;
+                    tc_wait_ld();
+                    if (n + 32 < n1) tmem_ld16(src + n + 32, r0);
+                    else if (!a.keys_held) let_go();
+                    add(r1, n + 16);
+                    if (n + 32 >= n1) break;
+                }
             }
+            if (a.keys_held) let_go();
             const float2 p0 = halves_of(part[0]), p1 = halves_of(part[1]);
             total = (p0.x + p0.y) + (p1.x + p1.y);
             return true;
         };
-        // the quartets' sums of item number `item` meet at one of them, which has its turn.  While one
-        // warp is still at an item's sums, its tiles of S let go, the others get through the next four
-        // items at most (one more waits for that warp's share of a tile): their places are not this
-        // one's.
-        auto meet = [&](unsigned item, float &sum, bool turn) {
+        // A quartet's sum of key tile number `item` for the one that has its last tile of S, which adds
+        // them up.  While that one is still at it, its tiles of S let go, the others get through seven
+        // more tiles of S at most (its own next one, done or not, and up to the one after that): the
+        // places that they write to are not this key tile's.
+        auto pass = [&](unsigned item, float sum) {
             const unsigned slot = item % kPlaces;
-            float *place = passed + slot * kMaxQuartets * kKeysTile;
-            place[quartet * kKeysTile + row] = sum;
+            passed[(slot * kMaxQuartets + quartet) * kKeysTile + row] = sum;
             __syncwarp();
             if (lane == 0) mbar_arrive(&x_full[slot * 4 + quarter]);
-            if (!turn) return true;
-            if (!wait_warp(&x_full[slot * 4 + quarter], (item / kPlaces) & 1)) return false;
-            sum = (place[row] + place[kKeysTile + row]) + (place[2 * kKeysTile + row] + place[3 * kKeysTile + row]);
-            return true;
         };
+        auto passed_by = [&](unsigned item, int q) { return passed[(item % kPlaces * kMaxQuartets + q) * kKeysTile + row]; };
         // (this thread alone has the key: no order of additions comes into it)
         auto give = [&](const Run &r, int t, float sum) {
             const int j = t * kKeysTile + row;
@@ -584,33 +597,58 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         };
         unsigned step = 0, runs = 0;  // tiles of S, runs before this one
         bool ok = true;
-        for (Run r; ok && walk.next(r); ++runs, step += r.n) {
+        for (Run r; ok && walk.next(r); ++runs) {
+            const unsigned skip = (unsigned)(quartet - (int)step) & (quartets - 1);  // to this quartet's first tile of S
             if (a.keys_held) {  // one key tile
                 const int first = r.t * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
-                const bool turn = (int)(runs % quartets) == quartet;
+                const unsigned n = (unsigned)r.n;
                 float sum = 0.f, lost = 0.f, part;
-                for (int i = 0; i < r.n; ++i) {
-                    if (!(ok = take(step + i, tables[(step + i) & (s_bufs - 1)], first, last, part))) break;
+                for (unsigned i = skip; i < n; i += quartets) {
+                    if (!(ok = take(step + i, tables[(step + i) % kSBufs], 0, first, last, part))) break;
                     // sum + lost += part (a sum with its rounding error kept)
                     const float more = part + lost, now = sum + more;
                     lost = more - (now - sum);
                     sum = now;
                 }
+                if (!ok) break;
                 sum += lost;
-                if (!ok || !(ok = meet(runs, sum, turn))) break;
-                if (turn) give(r, r.t, sum);
+                const unsigned end = step + n - 1;  // whose quartet adds up
+                if (skip < n && (end & 3) != (unsigned)quartet) pass(runs, sum);
+                if ((end & 3) == (unsigned)quartet) {
+                    const unsigned others = min(n - 1, 3u), slot = runs % kPlaces;
+                    if (others > 0) {
+                        __syncwarp();
+                        if (lane == 0 && others < 3) mbar_arrive_n(&x_full[slot * 4 + quarter], 3 - others);  // for those without
+                        if (!(ok = wait_warp(&x_full[slot * 4 + quarter], (runs / kPlaces) & 1))) break;
+                        for (unsigned k = others; k > 0; --k) sum += passed_by(runs, (int)((end - k) & 3));
+                    } else if (lane == 0) {
+                        mbar_arrive_n(&x_full[slot * 4 + quarter], 3);
+                    }
+                    give(r, r.t, sum);
+                }
+                step += n;
                 continue;
             }
             const Table &tab = tables[runs % kTables];
             if (!(ok = wait_warp(&tab_full[runs % kTables], (runs / kTables) & 1))) break;
-            for (int i = alone ? (int)((unsigned)(quartet - (int)step) & (quartets - 1)) : 0; i < r.n; i += alone ? quartets : 1) {
-                const int first = (r.t + i) * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
-                const bool turn = alone || (int)((step + i) % quartets) == quartet;
+            const int n = r.n * halves;  // tiles of S
+            for (int i = (int)skip; i < n; i += quartets) {
+                const int f = halves == 2 ? i & 1 : 0, t = r.t + (halves == 2 ? i >> 1 : i);
+                const int first = t * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
+                const unsigned item = (step + i) >> 1;  // (two halves: step and the quartet are even with the first)
                 float sum;
-                if (!(ok = take(step + i, tab, first, last, sum))) break;
-                if (!alone && !(ok = meet(step + i, sum, turn))) break;
-                if (turn) give(r, r.t + i, sum);
+                if (!(ok = take(step + i, tab, f * kSCols, first, last, sum))) break;
+                if (halves == 2) {
+                    if (f == 0) {
+                        pass(item, sum);
+                        continue;
+                    }
+                    if (!(ok = wait_warp(&x_full[item % kPlaces * 4 + quarter], (item / kPlaces) & 1))) break;
+                    sum += passed_by(item, quartet - 1);
+                }
+                give(r, t, sum);
             }
+            step += n;
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(&tab_empty[runs % kTables]);
         }
