@@ -1242,6 +1242,7 @@ lat_status lat_kv_evict_rows(lat_dtype dt, void *k_cache, void *v_cache, int64_t
     a.n_keep = n_keep;
     a.batch = batch;
     a.n_kv_heads = n_kv_heads;
+    a.timeout_ns = kDefaultTimeoutNs;
     a.status = status;
     return lat::launch_evict_rows(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
 }

@@ -187,6 +187,7 @@ struct EvictRowsArgs {
     int row_bytes, capacity;
     const int32_t *kept;                      // [batch, n_kv_heads, n_keep]
     int n_keep, batch, n_kv_heads;
+    uint64_t timeout_ns;
     int32_t *status;
 };
 // batch * n_kv_heads * 16 < 2^31

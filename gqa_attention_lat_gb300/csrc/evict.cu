@@ -13,9 +13,10 @@
 //
 // rows: row i of a head becomes its row kept[i] >= i, for ascending i.  A cluster takes K or V of one
 // (sequence, KV head) and moves a stretch of rows at a time: asynchronous copies bring them to shared
-// memory some stretches ahead, and a stretch is written only after the whole cluster has it.  That
-// is all the order that is needed: what a stretch writes lies before every row that a later one
-// reads.  Rows that stay where they are are not touched.
+// memory some stretches ahead, and a stretch is written only when every CTA of the cluster says that
+// its part of it has come (arrivals on barriers in each other's shared memory, which run ahead like
+// the copies).  That is all the order that is needed: what a stretch writes lies before every row
+// that a later one reads.  Rows that stay where they are are not touched.
 // What bounds it: HBM, rows read and written once.
 #include "cache_kernels.h"
 #include "device_common.cuh"
@@ -25,10 +26,13 @@ namespace lat {
 namespace {
 
 // ---------------------------------------------------------------------------------- choose
-constexpr int kChooseThreads = 512, kChooseWarps = kChooseThreads / 32;
-constexpr int kBins = 2048;
-// keys a CTA takes before the cluster grows (64 heads of 65536 keys: 4096 16.0 us, 8192 .. us)
-constexpr int kSliceWanted = 4096;
+constexpr int kChooseThreads = 1024, kChooseWarps = kChooseThreads / 32;
+constexpr int kBins = 2048, kMyBins = kBins / kChooseThreads;
+constexpr int kAtOnce = 4;  // keys of a lane in the places' loops
+// Keys a CTA takes before the cluster grows.  What the CTAs of a cluster say to each other costs more
+// than reading shared memory (a pass over 8 CTAs' bins 3 us, over 2 a third of that): as few as can
+// hold the weights with room for a second CTA's would be.
+constexpr int kSliceWanted = 32768;
 
 // order-preserving: larger weights to larger integers, NaN above all, -0 as 0
 __device__ __forceinline__ uint32_t ordered(float f) {
@@ -38,28 +42,38 @@ __device__ __forceinline__ uint32_t ordered(float f) {
 }
 __device__ __forceinline__ uint32_t load_cluster(const void *p, uint32_t rank) {
     uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)));
     return v;
 }
-// the sum of x over the CTA's threads before this one; `warps` in shared memory
-__device__ __forceinline__ int scan_before(int x, int *warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ uint2 load_cluster2(const void *p, uint32_t rank) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr(p, rank)));
+    return v;
+}
+// the sum of x over the warp's lanes before this one, and over all
+__device__ __forceinline__ int warp_before(int x, int &all) {
+    const int lane = threadIdx.x & 31;
     int incl = x;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += v;
     }
+    all = __shfl_sync(0xffffffffu, incl, 31);
+    return incl - x;
+}
+// the sum of x over the CTA's threads before this one; `warps` in shared memory, read by all
+__device__ __forceinline__ int scan_before(int x, int *warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int all;
+    const int before = warp_before(x, all);
+    if (lane == 0) warps[warp] = all;
     __syncthreads();
-    if (lane == 31) warps[warp] = incl;
-    __syncthreads();
-    int before = incl - x;
-    for (int w = 0; w < warp; ++w) before += warps[w];
-    return before;
+    return before + __reduce_add_sync(0xffffffffu, lane < warp ? warps[lane] : 0);
 }
 
 struct Choose {  // in shared memory, one a CTA
-    uint32_t bins[kBins];
+    alignas(16) uint32_t bins[kBins];
     int warps[kChooseWarps];
     int ties[kChooseWarps], sure[kChooseWarps];  // by warp
     int all_ties, all_sure;
@@ -67,12 +81,13 @@ struct Choose {  // in shared memory, one a CTA
     int above;       // keys in the digits above
 };
 
+template <int P>  // CTAs of a cluster
 __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const EvictChooseArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     Choose &sh = *reinterpret_cast<Choose *>(raw);
     float *held = reinterpret_cast<float *>(raw + sizeof(Choose));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int P = a.cluster, rank = (int)(blockIdx.x % P);
+    const int rank = (int)(blockIdx.x % P);
     const int64_t unit = blockIdx.x / P;
     const int b = (int)(unit / a.n_kv_heads), hk = (int)(unit % a.n_kv_heads);
     const int len = a.kv_lens[b];
@@ -93,6 +108,7 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     // ---- this CTA's slice ------------------------------------------------------------------
     const int slice = (len + P - 1) / P, lo = min(len, rank * slice), n = min(len, lo + slice) - lo;
     const int mid_lo = a.n_first, mid_hi = len - a.n_last;  // keys that are chosen among
+#pragma unroll 8
     for (int i = tid; i < n; i += kChooseThreads) held[i] = __ldcg(w + lo + i);  // (they may be written over)
     auto chosen_among = [&](int i) { return lo + i >= mid_lo && lo + i < mid_hi; };
 
@@ -105,26 +121,26 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
             for (int i = tid; i < kBins; i += kChooseThreads) sh.bins[i] = 0;
             __syncthreads();
+#pragma unroll 4
             for (int i = tid; i < n; i += kChooseThreads) {
                 const uint32_t k = ordered(held[i]);
                 if ((k & mask) == prefix && chosen_among(i)) atomicAdd(&sh.bins[(k >> shift) & ((1u << bits) - 1)], 1u);
             }
             if (P > 1) cluster_sync_all();
             else __syncthreads();
-            // the cluster's counts, largest digits first: thread t has four, and what lies above
-            uint32_t c[4];
-            int mine = 0;
+            // the cluster's counts, largest digits first: thread t has two, and what lies above
+            uint2 part[P];
+            const uint32_t *bins = sh.bins + kBins - kMyBins * (tid + 1);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int bin = kBins - 1 - (4 * tid + q);
-                c[q] = sh.bins[bin];
-                for (int p = 1; p < P; ++p) c[q] += load_cluster(&sh.bins[bin], (uint32_t)((rank + p) % P));
-                mine += (int)c[q];
-            }
-            int above = scan_before(mine, sh.warps);
+            for (int p = 0; p < P; ++p)
+                part[p] = p == 0 ? *reinterpret_cast<const uint2 *>(bins) : load_cluster2(bins, (uint32_t)((rank + p) % P));
+            uint32_t c[kMyBins] = {0, 0};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (above < need && above + (int)c[q] >= need) sh.digit = kBins - 1 - (4 * tid + q), sh.above = above;
+            for (int p = 0; p < P; ++p) c[0] += part[p].y, c[1] += part[p].x;
+            int above = scan_before((int)(c[0] + c[1]), sh.warps);
+#pragma unroll
+            for (int q = 0; q < kMyBins; ++q) {
+                if (above < need && above + (int)c[q] >= need) sh.digit = kBins - 1 - (kMyBins * tid + q), sh.above = above;
                 above += (int)c[q];
             }
             if (P > 1) cluster_sync_all();  // (also: the bins have been read)
@@ -146,45 +162,51 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         const uint32_t k = ordered(held[i]);
         return k > prefix ? 2 : k == prefix ? 1 : 0;
     };
-    const int run = (slice + kChooseWarps * 32 - 1) / (kChooseWarps * 32) * 32;  // keys of a warp
+    constexpr int kStep = 32 * kAtOnce;
+    const int run = (slice + kChooseWarps * kStep - 1) / (kChooseWarps * kStep) * kStep;  // keys of a warp
+    const int run_end = min((warp + 1) * run, n);
     int ties = 0, sure = 0;
-    for (int i0 = warp * run; i0 < (warp + 1) * run; i0 += 32) {
-        const int r = rank_of(i0 + lane);
-        ties += __popc(__ballot_sync(0xffffffffu, r == 1));
-        sure += __popc(__ballot_sync(0xffffffffu, r == 2));
+    for (int i0 = warp * run; i0 < run_end; i0 += kStep) {
+        int r[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) r[q] = rank_of(i0 + 32 * q + lane);
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            ties += __popc(__ballot_sync(0xffffffffu, r[q] == 1));
+            sure += __popc(__ballot_sync(0xffffffffu, r[q] == 2));
+        }
     }
     if (lane == 0) sh.ties[warp] = ties, sh.sure[warp] = sure;
     __syncthreads();
-    if (tid == 0) {
-        int t = 0, s = 0;
-        for (int x = 0; x < kChooseWarps; ++x) {
-            const int ti = sh.ties[x], si = sh.sure[x];
-            sh.ties[x] = t, sh.sure[x] = s;
-            t += ti, s += si;
-        }
-        sh.all_ties = t, sh.all_sure = s;
-    }
-    if (P > 1) cluster_sync_all();
-    else __syncthreads();
-    int ties_before = sh.ties[warp], sure_before = sh.sure[warp];
-    for (int p = 0; p < rank; ++p) {
-        ties_before += (int)load_cluster(&sh.all_ties, (uint32_t)p);
-        sure_before += (int)load_cluster(&sh.all_sure, (uint32_t)p);
+    int all_ties, all_sure;  // of the CTA
+    const int ties_ahead = warp_before(sh.ties[lane], all_ties), sure_ahead = warp_before(sh.sure[lane], all_sure);
+    int ties_before = __shfl_sync(0xffffffffu, ties_ahead, warp), sure_before = __shfl_sync(0xffffffffu, sure_ahead, warp);
+    if constexpr (P > 1) {
+        if (tid == 0) sh.all_ties = all_ties, sh.all_sure = all_sure;
+        cluster_sync_all();
+        const bool earlier = lane < rank;  // (a CTA a lane)
+        ties_before += __reduce_add_sync(0xffffffffu, earlier ? (int)load_cluster(&sh.all_ties, (uint32_t)lane) : 0);
+        sure_before += __reduce_add_sync(0xffffffffu, earlier ? (int)load_cluster(&sh.all_sure, (uint32_t)lane) : 0);
     }
     const uint32_t under = (1u << lane) - 1;
-    for (int i0 = warp * run; i0 < (warp + 1) * run; i0 += 32) {
-        const int i = i0 + lane, r = rank_of(i);
-        const uint32_t tied = __ballot_sync(0xffffffffu, r == 1);
-        const int t = ties_before + __popc(tied & under);  // equal ones before this key
-        const uint32_t stay = __ballot_sync(0xffffffffu, r == 2);
-        if (r == 2 || (r == 1 && t < need)) {
-            // sure ones before, and the equal ones before that stay
-            const int at = sure_before + __popc(stay & under) + min(t, need);
-            kept[at] = lo + i;
-            if (out != nullptr) out[at] = held[i];
+    for (int i0 = warp * run; i0 < run_end; i0 += kStep) {
+        int r[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) r[q] = rank_of(i0 + 32 * q + lane);
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            const int i = i0 + 32 * q + lane;
+            const uint32_t tied = __ballot_sync(0xffffffffu, r[q] == 1), stay = __ballot_sync(0xffffffffu, r[q] == 2);
+            const int t = ties_before + __popc(tied & under);  // equal ones before this key
+            if (r[q] == 2 || (r[q] == 1 && t < need)) {
+                // sure ones before, and the equal ones before that stay
+                const int at = sure_before + __popc(stay & under) + min(t, need);
+                kept[at] = lo + i;
+                if (out != nullptr) out[at] = held[i];
+            }
+            ties_before += __popc(tied);
+            sure_before += __popc(stay);
         }
-        ties_before += __popc(tied);
-        sure_before += __popc(stay);
     }
     if (out != nullptr)
         for (int i = a.n_keep + rank * kChooseThreads + tid; i < len; i += P * kChooseThreads) out[i] = 0.f;
@@ -194,13 +216,20 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
 // ---------------------------------------------------------------------------------- rows
 constexpr int kRowThreads = 256;
 constexpr int kRowStages = 3;
-constexpr int kStretchBytes = 16384;  // of a CTA
+constexpr int kStretchBytes = 32768;  // of a CTA
+constexpr int kPieces = kStretchBytes / 16 / kRowThreads;  // 16-byte pieces of a thread
+constexpr int kRowBars = 2 * kRowStages;
 
 template <int P2>  // log2 of the cluster's CTAs, 0 .. 3
 __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRowsArgs a) {
     constexpr int P = 1 << P2;
     extern __shared__ __align__(128) unsigned char stages[];  // [kRowStages][kStretchBytes]
-    __shared__ int src[kRowStages + 1][kStretchBytes / 128];  // a row of at least 128 bytes each; -1: none
+    __shared__ int src[kRowStages + 1][kStretchBytes / 128];  // rows of at least 128 bytes; -1: none
+    // Stretch s has come to all CTAs.  A CTA that says so of stretch s + kRowBars has seen this one say
+    // it of s + kRowStages, and so be done with s: twice as many barriers as stages, each a phase at
+    // a time.
+    __shared__ __align__(8) uint64_t here[kRowBars];
+    __shared__ int abort_flag;
     const int tid = threadIdx.x, rank = (int)(blockIdx.x & (P - 1));
     const int64_t unit = blockIdx.x >> P2;
     const int64_t bh = unit >> 1;
@@ -209,6 +238,16 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
     unsigned char *base = static_cast<unsigned char *>(unit & 1 ? a.v : a.k) + (int64_t)b * a.cache_seq + (int64_t)hk * a.cache_head;
     const int vecs = a.row_bytes / 16, rows = kStretchBytes / a.row_bytes;  // of a stretch
     const int n_stretches = (a.n_keep + P * rows - 1) / (P * rows);
+    const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
+    // this thread's pieces of a stretch: row and byte within it
+    int row[kPieces], off[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+        const int v = tid + k * kRowThreads;
+        row[k] = v / vecs;
+        off[k] = (v - row[k] * vecs) * 16;
+        if (row[k] >= rows) row[k] = -1;
+    }
     // Where row i of this CTA's stretch s comes from: threads below `rows` read the list one stretch
     // ahead of the copies.
     auto source = [&](int s) {
@@ -226,36 +265,57 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
         unsigned char *to = stages + s % kRowStages * kStretchBytes;
         const int *from = src[s % (kRowStages + 1)];
         if (s < n_stretches)
-            for (int v = tid; v < rows * vecs; v += kRowThreads) {
-                const int r = v / vecs, j = from[r];
-                if (j >= 0) cp_async_16(to + v * 16, base + (int64_t)j * a.cache_rs + (v - r * vecs) * 16, true);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int j = row[k] >= 0 ? from[row[k]] : -1;
+                if (j >= 0) cp_async_16(to + (tid + k * kRowThreads) * 16, base + (int64_t)j * a.cache_rs + off[k], true);
             }
         cp_async_commit();
     };
+    auto tell = [&](int s) {  // (behind a barrier of this CTA's threads)
+        if constexpr (P > 1)
+            if (tid < P && s < n_stretches) mbar_arrive_cluster(cluster_addr(&here[s % kRowBars], (uint32_t)tid));
+    };
+    if (tid == 0) {
+        for (int i = 0; i < kRowBars; ++i) mbar_init(&here[i], P);
+        fence_mbarrier_init();
+        abort_flag = 0;
+    }
 #pragma unroll
     for (int s = 0; s < kRowStages; ++s)
         if (tid < rows) src[s][tid] = source(s);
-    __syncthreads();
+    if constexpr (P > 1) cluster_sync_all();  // everyone's barriers are there
+    else __syncthreads();
 #pragma unroll
     for (int s = 0; s < kRowStages - 1; ++s) fetch(s);
+    cp_async_wait<kRowStages - 2>();
+    __syncthreads();
+    tell(0);
     for (int s = 0; s < n_stretches; ++s) {
         const int next = source(s + kRowStages);
         fetch(s + kRowStages - 1);
-        cp_async_wait<kRowStages - 1>();  // this thread's share of stretch s
+        cp_async_wait<kRowStages - 2>();  // this thread's pieces of stretch s + 1
         if (tid < rows) src[(s + kRowStages) % (kRowStages + 1)][tid] = next;
-        if constexpr (P > 1) cluster_sync_all();  // everyone's
-        else __syncthreads();
-        const unsigned char *here = stages + s % kRowStages * kStretchBytes;
+        if (P > 1 && tid == 0) mbar_wait_bounded_cluster(&here[s % kRowBars], (s / kRowBars) & 1, &abort_flag, deadline);
+        __syncthreads();
+        if (P > 1 && abort_flag) break;  // (one thread's word, seen by all alike)
+        tell(s + 1);
+        const unsigned char *from_stage = stages + s % kRowStages * kStretchBytes;
         const int *from = src[s % (kRowStages + 1)];
         const int64_t i0 = ((int64_t)s * P + rank) * rows;
-        for (int v = tid; v < rows * vecs; v += kRowThreads) {
-            const int r = v / vecs;
-            if (from[r] >= 0)
-                *reinterpret_cast<uint4 *>(base + (i0 + r) * a.cache_rs + (v - r * vecs) * 16) = *reinterpret_cast<const uint4 *>(here + v * 16);
-        }
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k)
+            if (row[k] >= 0 && from[row[k]] >= 0)
+                *reinterpret_cast<uint4 *>(base + (i0 + row[k]) * a.cache_rs + off[k]) =
+                    *reinterpret_cast<const uint4 *>(from_stage + (tid + k * kRowThreads) * 16);
         __syncthreads();  // the stage and the list's entries may be filled again
     }
     cp_async_wait<0>();
+    if constexpr (P > 1) {
+        __syncthreads();
+        if (tid == 0 && abort_flag) report_status(a.status, kErrTimeout);
+        cluster_sync_all();  // nobody's barriers go while another arrives on them
+    }
 }
 
 template <typename Kernel, typename Args>
@@ -283,17 +343,24 @@ cudaError_t launch_evict_choose(EvictChooseArgs a, cudaStream_t s) {
     a.cluster = 1;
     while (a.cluster < kEvictCluster && (int64_t)a.cluster * kSliceWanted < a.max_kv_len) a.cluster *= 2;
     const int slice = (a.max_kv_len + a.cluster - 1) / a.cluster;
+    static_assert(kMyBins == 2 && kChooseWarps == 32, "pairs of bins, a warp a lane");
     static_assert(sizeof(Choose) + 4 * kEvictMaxSlice <= 232448, "shared memory budget");
-    return launch_cluster(evict_choose_kernel, a, (int64_t)a.batch * a.n_kv_heads * a.cluster, kChooseThreads,
-                          (int)sizeof(Choose) + 4 * slice, a.cluster, s);
+    const int64_t grid = (int64_t)a.batch * a.n_kv_heads * a.cluster;
+    const int smem = (int)sizeof(Choose) + 4 * slice;
+    switch (a.cluster) {
+        case 1: return launch_cluster(evict_choose_kernel<1>, a, grid, kChooseThreads, smem, 1, s);
+        case 2: return launch_cluster(evict_choose_kernel<2>, a, grid, kChooseThreads, smem, 2, s);
+        case 4: return launch_cluster(evict_choose_kernel<4>, a, grid, kChooseThreads, smem, 4, s);
+        default: return launch_cluster(evict_choose_kernel<8>, a, grid, kChooseThreads, smem, 8, s);
+    }
 }
 
 cudaError_t launch_evict_rows(const EvictRowsArgs &a, int num_sms, cudaStream_t s) {
     const int64_t units = (int64_t)a.batch * a.n_kv_heads * 2;
     const int rows = kStretchBytes / a.row_bytes;
-    // CTAs for four on every SM, as far as there are stretches for them
+    // CTAs for two on every SM, as many as fit there at once, as far as there are stretches for them
     int p2 = 0;
-    while (p2 < 3 && (units << p2) < 4 * (int64_t)num_sms && ((int64_t)rows << p2) < a.n_keep) ++p2;
+    while (p2 < 3 && (units << (p2 + 1)) <= 2 * (int64_t)num_sms && ((int64_t)rows << p2) < a.n_keep) ++p2;
     const int smem = kRowStages * kStretchBytes;
     switch (p2) {
         case 0: return launch_cluster(evict_rows_kernel<0>, a, units, kRowThreads, smem, 1, s);
