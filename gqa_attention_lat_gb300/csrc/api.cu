@@ -1123,7 +1123,11 @@ lat_status key_weights_impl(lat_dtype dt, const void *q, int64_t q_rs, int n_q, 
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (dt == LAT_F32) {
-        if ((int64_t)batch * n_kv_heads > 65535) return LAT_ERR_UNSUPPORTED;
+        if ((int64_t)batch * n_kv_heads > 65535 || (int64_t)n_q * (n_heads / n_kv_heads) > 0x7fffffffLL)
+            return LAT_ERR_UNSUPPORTED;
+        a.by_heads_per = lat::FastDiv((uint32_t)(n_heads / n_kv_heads));
+        a.q_vec = aligned16(q) && q_rs % 4 == 0;
+        a.k_vec = aligned16(k_cache) && cache_rs % 4 == 0 && cache_head_stride % 4 == 0 && cache_seq_stride % 4 == 0;
         return lat::launch_key_weights_f32(a, s) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
     }
     int sms = 0;

@@ -136,6 +136,7 @@ struct KeyWeightsArgs {
     CUtensorMap tm_q, tm_k;  // bf16: (channel, head, row, sequence), boxes of the plan's columns and of 128 keys
     const void *q, *k;       // fp32
     int64_t q_rs, k_row, k_head, k_seq;  // elements
+    int q_vec, k_vec;        // fp32: rows of 16-byte vectors
     const int32_t *kv_lens;
     int max_kv_len;
     const float *lse;        // [batch * n_q, n_heads]
@@ -144,7 +145,7 @@ struct KeyWeightsArgs {
     int batch, n_q, n_heads, n_kv_heads, head_dim, causal, window;  // window 0: none, else < max_kv_len
     float scale_log2, cap_log2, raw_over_cap;  // as in DecodeArgs
     int keys_held, heads_per, rows_per, head_blocks, n_cols;  // the plan's
-    FastDiv by_heads_per;
+    FastDiv by_heads_per;    // fp32: by the KV head's query heads
     int64_t slots;
     uint64_t timeout_ns;
     int test_skip_load;      // test hook: the first stage never comes

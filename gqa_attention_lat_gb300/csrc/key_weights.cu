@@ -34,8 +34,9 @@
 // What bounds it: HBM (keys once) for few columns; for many the tensor pipe and the exponentials,
 // 128 N D 2 flops against 128 N of them.
 //
-// fp32 (key_weights_f32_kernel): exact fp32 products, 64 keys x 8 or 64 columns a step, a thread 4
-// x 1 or 4 x 8 of them.  Bound by its FMAs.
+// fp32 (key_weights_f32_kernel): fp32 products by FMA, 64 keys x 8, 32 or 64 columns a step, a thread 4
+// x 1, 4 or 8 of them; the next 32 channels come while 32 are used.  Bound by its FMAs, with few
+// columns by HBM.
 #include <math.h>
 
 #include <algorithm>
@@ -665,10 +666,13 @@ constexpr int kF32Keys = 64, kF32Depth = 32, kF32Threads = 128;
 // keys 4 x .. 4 x + 3 and columns y, y + 8, ...
 template <int COLS, bool CAP>
 __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyWeightsArgs a) {
-    constexpr int kPer = COLS / 8;
-    __shared__ float sK[kF32Depth][kF32Keys + 4], sQ[kF32Depth][COLS + 1];
+    constexpr int kPer = COLS / 8, kVecs = kF32Depth / 4;                   // a thread's columns; vectors of a row's 32 channels
+    constexpr int kMyK = kF32Keys * kVecs / kF32Threads;                    // a thread's vectors of keys and of queries
+    constexpr int kMyQ = COLS * kVecs >= kF32Threads ? COLS * kVecs / kF32Threads : 1;
+    __shared__ __align__(16) float sK[kF32Depth][kF32Keys + 4], sQ[kF32Depth][COLS + 4];
     __shared__ float lse2[COLS];
     __shared__ int hi[COLS], lo[COLS];
+    __shared__ int64_t q_at[COLS];                                          // where a column's query begins; -1: no column
     const int tid = threadIdx.x, x = tid / 8, y = tid % 8;
     const int b = blockIdx.y / a.n_kv_heads, hk = blockIdx.y % a.n_kv_heads, G = a.n_heads / a.n_kv_heads, D = a.head_dim;
     const int raw = a.kv_lens[b], first = (int)blockIdx.x * kF32Keys;
@@ -684,41 +688,66 @@ __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyW
     if (a.window > 0) i1 = min(i1, (int64_t)last + a.window - 1 - off);
     if (i0 > i1) return;
     const float *kb = static_cast<const float *>(a.k) + (int64_t)b * a.k_seq + (int64_t)hk * a.k_head;
+    const float *qb = static_cast<const float *>(a.q) + (int64_t)b * a.n_q * a.q_rs + (int64_t)hk * G * D;
+    const float *lb = a.lse + (int64_t)b * a.n_q * a.n_heads + hk * G;
+    // four channels of a row, from d on
+    auto four = [&](const float *p, bool vec) {
+        return vec ? __ldg(reinterpret_cast<const float4 *>(p)) : make_float4(__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3));
+    };
+    float4 kv[kMyK], qv[kMyQ];
+    auto ask = [&](int d0) {
+#pragma unroll
+        for (int e = 0; e < kMyK; ++e) {
+            const int v = tid + e * kF32Threads, d = d0 + v % kVecs * 4, r = v / kVecs;
+            kv[e] = d < D && first + r <= last ? four(kb + (int64_t)(first + r) * a.k_row + d, a.k_vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < kMyQ; ++e) {
+            const int v = tid + e * kF32Threads, d = d0 + v % kVecs * 4, c = v / kVecs;
+            const int64_t at = c < COLS ? q_at[c] : -1;
+            qv[e] = d < D && at >= 0 ? four(qb + at + d, a.q_vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
     float sum[4] = {0.f, 0.f, 0.f, 0.f}, lost[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t c0 = i0 * G; c0 < (i1 + 1) * G; c0 += COLS) {
+    const int64_t c_end = (i1 + 1) * G;
+    for (int64_t c0 = i0 * G; c0 < c_end; c0 += COLS) {
         __syncthreads();  // the table is free
         for (int c = tid; c < COLS; c += kF32Threads) {
+            lse2[c] = INFINITY, hi[c] = -1, lo[c] = -1, q_at[c] = -1;
             const int64_t col = c0 + c;
-            lse2[c] = INFINITY, hi[c] = -1, lo[c] = -1;
-            if (col < (i1 + 1) * G) {
-                const int64_t i = col / G, pos = off + i;
-                const float l = a.lse[((int64_t)b * a.n_q + i) * a.n_heads + hk * G + col % G];
+            if (col < c_end) {  // (columns are fewer than 2^31)
+                const uint32_t i = a.by_heads_per.div((uint32_t)col), g = (uint32_t)col - i * G;
+                const int pos = (int)(off + i);
+                const float l = lb[(int64_t)i * a.n_heads + g];
+                q_at[c] = (int64_t)i * a.q_rs + g * D;
                 if (l != -INFINITY) {
                     lse2[c] = l * 1.4426950408889634f;
-                    hi[c] = a.causal ? (int)pos : 0x7fffffff;
-                    lo[c] = a.window > 0 ? (int)pos - a.window : -1;
+                    hi[c] = a.causal ? pos : 0x7fffffff;
+                    lo[c] = a.window > 0 ? pos - a.window : -1;
                 }
             }
         }
+        __syncthreads();
         float s[4][kPer];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int c = 0; c < kPer; ++c) s[k][c] = 0.f;
+        ask(0);
         for (int d0 = 0; d0 < D; d0 += kF32Depth) {
-            __syncthreads();
-            for (int e = tid; e < kF32Keys * kF32Depth; e += kF32Threads) {
-                const int d = e % kF32Depth, r = e / kF32Depth;
-                sK[d][r] = d0 + d < D && first + r <= last ? kb[(int64_t)(first + r) * a.k_row + d0 + d] : 0.f;
+            if (d0 > 0) __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kMyK; ++e) {
+                const int v = tid + e * kF32Threads, d = v % kVecs * 4, r = v / kVecs;
+                sK[d][r] = kv[e].x, sK[d + 1][r] = kv[e].y, sK[d + 2][r] = kv[e].z, sK[d + 3][r] = kv[e].w;
             }
-            for (int e = tid; e < COLS * kF32Depth; e += kF32Threads) {
-                const int d = e % kF32Depth, c = e / kF32Depth;
-                const int64_t col = c0 + c, i = col / G;
-                sQ[d][c] = d0 + d < D && col < (i1 + 1) * G
-                               ? static_cast<const float *>(a.q)[((int64_t)b * a.n_q + i) * a.q_rs + (int64_t)(hk * G + col % G) * D + d0 + d]
-                               : 0.f;
+#pragma unroll
+            for (int e = 0; e < kMyQ; ++e) {
+                const int v = tid + e * kF32Threads, d = v % kVecs * 4, c = v / kVecs;
+                if (c < COLS) sQ[d][c] = qv[e].x, sQ[d + 1][c] = qv[e].y, sQ[d + 2][c] = qv[e].z, sQ[d + 3][c] = qv[e].w;
             }
             __syncthreads();
+            if (d0 + kF32Depth < D) ask(d0 + kF32Depth);
 #pragma unroll 8
             for (int d = 0; d < kF32Depth; ++d) {
                 const float4 k4 = *reinterpret_cast<const float4 *>(&sK[d][4 * x]);
@@ -825,13 +854,12 @@ cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, cudaStream_t s) {
     // (one block of nothing still sees the lengths)
     const dim3 grid((unsigned)((std::max<int64_t>(a.max_kv_len, 1) + kF32Keys - 1) / kF32Keys), (unsigned)(a.batch * a.n_kv_heads));
     const bool cap = a.cap_log2 > 0.f;
-    if ((int64_t)a.n_q * (a.n_heads / a.n_kv_heads) <= 8) {
-        if (cap) key_weights_f32_kernel<8, true><<<grid, kF32Threads, 0, s>>>(a);
-        else key_weights_f32_kernel<8, false><<<grid, kF32Threads, 0, s>>>(a);
-    } else {
-        if (cap) key_weights_f32_kernel<64, true><<<grid, kF32Threads, 0, s>>>(a);
-        else key_weights_f32_kernel<64, false><<<grid, kF32Threads, 0, s>>>(a);
-    }
+    const int64_t cols = (int64_t)a.n_q * (a.n_heads / a.n_kv_heads);
+    // no more columns at once than there are
+    auto go = [&](auto kernel) { kernel<<<grid, kF32Threads, 0, s>>>(a); };
+    if (cols <= 8) cap ? go(key_weights_f32_kernel<8, true>) : go(key_weights_f32_kernel<8, false>);
+    else if (cols <= 32) cap ? go(key_weights_f32_kernel<32, true>) : go(key_weights_f32_kernel<32, false>);
+    else cap ? go(key_weights_f32_kernel<64, true>) : go(key_weights_f32_kernel<64, false>);
     return cudaGetLastError();
 }
 
