@@ -18,6 +18,8 @@
 //    More columns (a chunk, a prompt): a key tile stays while its tiles of queries stream by, and
 //    items (key tiles) are dealt heaviest first, forwards and backwards in turn.
 //    Either way every key has one owner, so sums are in a fixed order and nothing is atomic.
+//    (Tiles of 256 columns where there are as many: an MMA of 128 x 128 x 16 reads both operands at
+//    what shared memory gives, one of twice the columns three quarters of it.)
 //  * Roles: epilogue warps in quartets (a warp can read the quarter of tensor memory's lanes that
 //    its number says), a warp that issues the copies, one that issues the MMAs, two that prepare
 //    the columns' log-sum-exps and ranges of keys.  S has four buffers of 128 columns in tensor
@@ -51,7 +53,7 @@ namespace lat {
 namespace {
 
 constexpr int kKeysTile = 128;
-constexpr int kMaxCols = 256, kStreamCols = 128;  // columns of a tile: at most, and where they stream
+constexpr int kMaxCols = 256;                     // columns of a tile
 constexpr int kNarrowCols = 64;                   // queries held, up to so many: two quartets are enough
 constexpr int kMaxQuartets = 4;
 constexpr int kMoreWarps = 4;                     // behind them: copies, MMAs, two of tables
@@ -66,8 +68,7 @@ template <int D>
 struct KwCfg {
     static constexpr int kChunks = (D + 63) / 64;           // 64-channel chunks of a row
     static constexpr int kSteps = (D + 15) / 16;            // MMAs of a tile
-    static constexpr int kStageChunks = D == 64 ? 1 : 2;    // chunks of a ring stage, 16 KB each
-    static constexpr int kStagesPerTile = kChunks / kStageChunks;
+    static constexpr int kStageChunks = D == 64 ? 1 : 2;    // chunks of keys in a ring stage, 16 KB each
     static constexpr int kStageBytes = kStageChunks * 16384;
     // The operand that stays has up to 64 KB (head_dim 512: 128 KB): up to 256 (head_dim 256, 512: 128)
     // columns, or 128 keys.  What it leaves of kTiles is the ring's.
@@ -277,11 +278,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     // bytes of a chunk of the tile of queries and of keys; how many operands there is room to hold,
     // and stages behind them
     const int q_rows = a.rows_per * a.heads_per;                 // columns that a copy brings
-    const int q_chunk = a.keys_held ? 16384 : a.n_cols * 128;    // where its chunks lie apart
+    const int q_chunk = a.n_cols * 128;                          // where its chunks lie apart
     const int held_bytes = C::kChunks * (a.keys_held ? 16384 : q_chunk);
     const unsigned n_held = 2 * held_bytes <= C::kHeldBytes ? 2 : 1;
     unsigned char *held = smem, *ring = held + n_held * held_bytes;
-    const unsigned n_stages = min(kMaxStages, (C::kTiles - (int)n_held * held_bytes) / C::kStageBytes);
+    const int stage_bytes = a.keys_held ? q_chunk : C::kStageBytes;  // of queries, one chunk
+    const int stage_chunks = a.keys_held ? 1 : C::kStageChunks, per_tile = C::kChunks / stage_chunks;
+    const unsigned n_stages = min(kMaxStages, (C::kTiles - (int)n_held * held_bytes) / stage_bytes);
     const int G = a.n_heads / a.n_kv_heads;
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
     if (tid < 32) {  // barriers, a few a lane
@@ -373,13 +376,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
                 else queries(held + y * held_bytes, &held_full[y], r, 0, 0, 0, C::kChunks);
                 int rb = (int)(r.x / a.head_blocks), hb = (int)(r.x - (int64_t)rb * a.head_blocks);
                 for (int i = 0; ok && i < r.n; ++i) {
-                    for (int p = 0; p < C::kStagesPerTile; ++p, ++g) {
+                    for (int p = 0; p < per_tile; ++p, ++g) {
                         if (turn > 0 && !(ok = wait(&ring_empty[s], (turn & 1) ^ 1))) break;
                         if (!a.test_skip_load || g > 0) {  // (test hook: the first never comes)
-                            const int c0 = p * C::kStageChunks;
-                            mbar_arrive_expect_tx(&ring_full[s], C::kStageChunks * (a.keys_held ? q_rows * 128 : 16384));
-                            if (a.keys_held) queries(ring + s * C::kStageBytes, &ring_full[s], r, rb, hb, c0, c0 + C::kStageChunks);
-                            else keys(ring + s * C::kStageBytes, &ring_full[s], r, r.t + i, c0, c0 + C::kStageChunks);
+                            mbar_arrive_expect_tx(&ring_full[s], a.keys_held ? q_rows * 128 : C::kStageBytes);
+                            if (a.keys_held) queries(ring + s * stage_bytes, &ring_full[s], r, rb, hb, p, p + 1);
+                            else keys(ring + s * stage_bytes, &ring_full[s], r, r.t + i, p * C::kStageChunks, (p + 1) * C::kStageChunks);
                         }
                         if (++s == n_stages) s = 0, ++turn;
                     }
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             const uint32_t idesc = instr_desc(kKeysTile, a.n_cols, false);
             const uint64_t d_ring = sw128_desc(smem_u32(ring)), d_held = sw128_desc(smem_u32(held));
             // a chunk of keys is 16 KB wherever it lies
-            const uint64_t q_step = q_chunk >> 4, part = C::kStageChunks * (a.keys_held ? 1024 : q_step);
+            const uint64_t q_step = q_chunk >> 4, part = a.keys_held ? 1024 : C::kStageChunks * q_step;
             unsigned h = 0, step = 0, s = 0, turn = 0;  // held operands, tiles of S; place in the ring, times round it
             bool ok = true;
             for (Run r; ok && walk.next(r); ++h) {
@@ -416,18 +418,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
                     const unsigned buf = step % kSBufs;  // (two tiles of S lie side by side and go by the first's barriers)
                     if (step >= kSBufs && !(ok = wait(&s_empty[buf], ((step / kSBufs) & 1) ^ 1))) break;
                     const uint32_t d = tmem + buf * kSCols;
-                    for (int p = 0; p < C::kStagesPerTile; ++p) {
+                    for (int p = 0; p < per_tile; ++p) {
                         if (!(ok = wait(&ring_full[s], turn & 1))) break;
                         tc_fence_after();
-                        const uint64_t here = d_ring + (uint64_t)((s * C::kStageBytes) >> 4), there = kept + p * part;
+                        const uint64_t here = d_ring + (uint64_t)((s * stage_bytes) >> 4), there = kept + p * part;
                         const uint64_t dk = a.keys_held ? there : here, dq = a.keys_held ? here : there;
 #pragma unroll
-                        for (int c = 0; c < C::kStageChunks; ++c)
+                        for (int c = 0; c < C::kStageChunks; ++c) {
+                            if (c >= stage_chunks) break;
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                if (D % 64 == 0 || c * 4 + k < C::kSteps)
+                                if (D % 64 == 0 || (p * stage_chunks + c) * 4 + k < C::kSteps)
                                     tc_mma_ss(d, dk + (uint64_t)((c * 16384 + k * 32) >> 4), dq + c * q_step + (uint64_t)(k * 32 >> 4),
                                               idesc, p > 0 || c > 0 || k > 0);
+                        }
                         tc_commit(&ring_empty[s]);
                         if (++s == n_stages) s = 0, ++turn;
                     }
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             Place p = place_of(r.x + i);
             if (i < r.n) ask(r, p);
             for (; i < r.n; i += 2) {
-                const unsigned k = n + i, u = k % kSBufs;
+                const unsigned k = 2 * (n + i), u = k % kSBufs;  // its first tile of S
                 if (k >= kSBufs && !(ok = wait_warp(&s_empty[u], ((k / kSBufs) & 1) ^ 1))) break;
                 fill(tables[u], r, p);
                 if (lane == 0) mbar_arrive(&s_full[u]);
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             const unsigned buf = step % kSBufs, bar = buf & -halves;
             if (!wait_warp(&s_full[bar], (step / kSBufs) & 1)) return false;
             tc_fence_after();
-            const int n1 = min(tab.count - off, kSCols), j = first + row;
+            const int n1 = max(1, min(tab.count - off, kSCols)), j = first + row;  // (one that is not there is masked)
             const bool mask = tab.min_hi < last || tab.max_lo >= first;
             const uint32_t src = lanes + buf * kSCols;
             uint64_t part[2] = {0, 0};
@@ -556,9 +560,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
                     uint32_t r[16];
                     tmem_ld16(src + n, r);
                     tc_wait_ld();
-                    if (n + 16 >= n1 && !a.keys_held) let_go();
                     add(r, n);
                 }
+                if (!a.keys_held) let_go();
             } else {  // sixteen columns on their way while sixteen are summed
                 uint32_t r0[16], r1[16];
                 tmem_ld16(src, r0);
@@ -602,10 +606,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             const unsigned skip = (unsigned)(quartet - (int)step) & (quartets - 1);  // to this quartet's first tile of S
             if (a.keys_held) {  // one key tile
                 const int first = r.t * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
-                const unsigned n = (unsigned)r.n;
+                const unsigned n = 2 * (unsigned)r.n;  // tiles of S
                 float sum = 0.f, lost = 0.f, part;
                 for (unsigned i = skip; i < n; i += quartets) {
-                    if (!(ok = take(step + i, tables[(step + i) % kSBufs], 0, first, last, part))) break;
+                    if (!(ok = take(step + i, tables[(step + i) % kSBufs & ~1u], (i & 1) * kSCols, first, last, part))) break;
                     // sum + lost += part (a sum with its rounding error kept)
                     const float more = part + lost, now = sum + more;
                     lost = more - (now - sum);
@@ -823,14 +827,14 @@ bool plan_key_weights(int batch, int n_q, int n_heads, int n_kv_heads, int head_
         p->heads_per = G;
         p->rows_per = n_q;
         p->head_blocks = 1;
-    } else if (G <= kStreamCols) {
+    } else if (G <= kMaxCols) {
         p->heads_per = G;
-        p->rows_per = std::min(n_q, kStreamCols / G);
+        p->rows_per = std::min(n_q, kMaxCols / G);
         p->head_blocks = 1;
     } else {
-        p->heads_per = kStreamCols;
+        p->heads_per = kMaxCols;
         p->rows_per = 1;
-        p->head_blocks = (G + kStreamCols - 1) / kStreamCols;
+        p->head_blocks = (G + kMaxCols - 1) / kMaxCols;
     }
     p->n_cols = (p->rows_per * p->heads_per + 15) / 16 * 16;
     const int64_t items = ((int64_t)max_kv_len + kKeysTile - 1) / kKeysTile * batch * n_kv_heads;
