@@ -34,6 +34,26 @@ class Occupancy {
     std::atomic<int> seen_[kDevices] = {};
 };
 
+// A kernel's dynamic shared memory limit, set once per device (setting it costs a call 1 us).
+class SharedLimit {
+  public:
+    template <typename Kernel>
+    cudaError_t operator()(Kernel *k, int smem) {
+        int dev = -1;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::atomic<bool> *done = dev >= 0 && dev < kDevices ? &done_[dev] : nullptr;
+        if (done != nullptr && done->load(std::memory_order_relaxed)) return cudaSuccess;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess && done != nullptr) done->store(true, std::memory_order_relaxed);
+        return e;
+    }
+
+  private:
+    static constexpr int kDevices = 64;
+    std::atomic<bool> done_[kDevices] = {};
+};
+
 // Division of whole numbers below 2^31 by one fixed beforehand: n / d = (n + hi(n m)) >> s
 // (Granlund and Montgomery's round-up multiplier), a handful of instructions where the
 // hardware has no divide.

@@ -553,10 +553,10 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
 template <int D, bool F32>
 cudaError_t launch_q8(const Q8DecodeArgs &a, int grid, cudaStream_t s) {
     using C = Q8Cfg<D, F32>;
-    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
+    // (the plan's question for the occupancy has set the shared memory limit)
     decode_q8_kernel<D, F32><<<grid, C::kThreads, C::kSmem, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess || !a.defer_join) return e;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !a.defer_join) return e;
     const JoinArgs j{a.part_o, a.part_lse, a.piece_count, a.max_splits, a.n_heads, a.out, a.out_rs, a.lse};
     return launch_split_join<D, F32>(j, (int64_t)a.batch * a.n_heads, s);
 }

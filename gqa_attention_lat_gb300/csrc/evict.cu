@@ -318,9 +318,11 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
     }
 }
 
+// `most`: the most shared memory that the kernel is ever given
 template <typename Kernel, typename Args>
-cudaError_t launch_cluster(Kernel *k, const Args &a, int64_t grid, int threads, int smem, int cluster, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch_cluster(Kernel *k, SharedLimit &limit, int most, const Args &a, int64_t grid, int threads, int smem,
+                           int cluster, cudaStream_t s) {
+    cudaError_t e = limit(k, most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -346,12 +348,13 @@ cudaError_t launch_evict_choose(EvictChooseArgs a, cudaStream_t s) {
     static_assert(kMyBins == 2 && kChooseWarps == 32, "pairs of bins, a warp a lane");
     static_assert(sizeof(Choose) + 4 * kEvictMaxSlice <= 232448, "shared memory budget");
     const int64_t grid = (int64_t)a.batch * a.n_kv_heads * a.cluster;
-    const int smem = (int)sizeof(Choose) + 4 * slice;
+    const int most = (int)sizeof(Choose) + 4 * kEvictMaxSlice, smem = (int)sizeof(Choose) + 4 * slice;
+    static SharedLimit limit[4];
     switch (a.cluster) {
-        case 1: return launch_cluster(evict_choose_kernel<1>, a, grid, kChooseThreads, smem, 1, s);
-        case 2: return launch_cluster(evict_choose_kernel<2>, a, grid, kChooseThreads, smem, 2, s);
-        case 4: return launch_cluster(evict_choose_kernel<4>, a, grid, kChooseThreads, smem, 4, s);
-        default: return launch_cluster(evict_choose_kernel<8>, a, grid, kChooseThreads, smem, 8, s);
+        case 1: return launch_cluster(evict_choose_kernel<1>, limit[0], most, a, grid, kChooseThreads, smem, 1, s);
+        case 2: return launch_cluster(evict_choose_kernel<2>, limit[1], most, a, grid, kChooseThreads, smem, 2, s);
+        case 4: return launch_cluster(evict_choose_kernel<4>, limit[2], most, a, grid, kChooseThreads, smem, 4, s);
+        default: return launch_cluster(evict_choose_kernel<8>, limit[3], most, a, grid, kChooseThreads, smem, 8, s);
     }
 }
 
@@ -362,11 +365,12 @@ cudaError_t launch_evict_rows(const EvictRowsArgs &a, int num_sms, cudaStream_t 
     int p2 = 0;
     while (p2 < 3 && (units << (p2 + 1)) <= 2 * (int64_t)num_sms && ((int64_t)rows << p2) < a.n_keep) ++p2;
     const int smem = kRowStages * kStretchBytes;
+    static SharedLimit limit[4];
     switch (p2) {
-        case 0: return launch_cluster(evict_rows_kernel<0>, a, units, kRowThreads, smem, 1, s);
-        case 1: return launch_cluster(evict_rows_kernel<1>, a, units << 1, kRowThreads, smem, 2, s);
-        case 2: return launch_cluster(evict_rows_kernel<2>, a, units << 2, kRowThreads, smem, 4, s);
-        default: return launch_cluster(evict_rows_kernel<3>, a, units << 3, kRowThreads, smem, 8, s);
+        case 0: return launch_cluster(evict_rows_kernel<0>, limit[0], smem, a, units, kRowThreads, smem, 1, s);
+        case 1: return launch_cluster(evict_rows_kernel<1>, limit[1], smem, a, units << 1, kRowThreads, smem, 2, s);
+        case 2: return launch_cluster(evict_rows_kernel<2>, limit[2], smem, a, units << 2, kRowThreads, smem, 4, s);
+        default: return launch_cluster(evict_rows_kernel<3>, limit[3], smem, a, units << 3, kRowThreads, smem, 8, s);
     }
 }
 

@@ -280,6 +280,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_threads = blockDim.x;
+    // what takes a round trip first: the first of this thread's lengths, the tensor maps (there are none
+    // for caches that hold nothing)
+    const int per_thread = a.batch <= n_threads ? 1 : (a.batch + n_threads - 1) / n_threads;
+    const int b_lo = min(a.batch, tid * per_thread), b_hi = min(a.batch, b_lo + per_thread);
+    const int len_lo = b_lo < b_hi ? a.kv_lens[b_lo] : 0;
+    if (tid == 0 && a.max_kv_len > 0) tma_prefetch_desc(&a.tm_q), tma_prefetch_desc(&a.tm_k);
     const int n_epilogue = n_threads / 32 - kMoreWarps, quartets = n_epilogue / 4;
     const int halves = a.n_cols > kSCols ? 2 : 1;                // tiles of S of a column tile (queries held)
     // bytes of a chunk of the tile of queries and of keys; how many operands there is room to hold,
@@ -314,13 +320,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     }
     // ---- this CTA's share: per-thread sums over a slice of the sequences, then a scan ----------
     // (item counts stay below 2^31)
-    const int per_thread = (a.batch + n_threads - 1) / n_threads;
-    const int b_lo = min(a.batch, tid * per_thread), b_hi = min(a.batch, b_lo + per_thread);
     int mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
-        const int n = a.kv_lens[b];
-        if (blockIdx.x == 0 && (n < 0 || n > a.max_kv_len)) report_status(a.status, kErrBounds);
-        const int2 seen = tiles_seen(a, length_of(a, b));
+        const int n = b == b_lo ? len_lo : a.kv_lens[b];
+        const bool bad = n < 0 || n > a.max_kv_len;
+        if (blockIdx.x == 0 && bad) report_status(a.status, kErrBounds);
+        const int2 seen = tiles_seen(a, bad ? 0 : n);
         mine += (seen.y - seen.x) * a.n_kv_heads;
     }
     int incl = mine;
@@ -363,7 +368,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
 
     if (warp == n_epilogue) {
         if (lane == 0) {
-            if (a.max_kv_len > 0) tma_prefetch_desc(&a.tm_q), tma_prefetch_desc(&a.tm_k);  // (else there are none)
             unsigned g = 0, h = 0, s = 0, turn = 0;  // stages and held operands issued; place in the ring, times round it
             bool ok = true;
             // chunks [c0, c1) of key tile t, and of the columns of row block rb and head block hb
@@ -590,7 +594,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         // (this thread alone has the key: no order of additions comes into it)
         auto give = [&](const Run &r, int t, float sum) {
             const int j = t * kKeysTile + row;
-            if (j < r.len) atomicAdd(a.weights + (int64_t)r.b * a.w_seq + (int64_t)r.hk * a.w_head + j, sum);
+            if (j < r.len && sum != 0.f) atomicAdd(a.weights + (int64_t)r.b * a.w_seq + (int64_t)r.hk * a.w_head + j, sum);
         };
         unsigned step = 0, runs = 0;  // tiles of S, runs before this one
         bool ok = true;
@@ -788,7 +792,8 @@ int held_cols() { return KwCfg<D>::kHeldCols; }
 template <int D, bool CAP>
 cudaError_t launch_tc(const KeyWeightsArgs &a, int grid, cudaStream_t s) {
     using C = KwCfg<D>;
-    const cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<D, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static SharedLimit limit;
+    const cudaError_t e = limit(key_weights_kernel<D, CAP>, C::kSmem);
     if (e != cudaSuccess) return e;
     const int threads = 128 * (!a.keys_held && a.n_cols <= kNarrowCols ? 2 : kMaxQuartets) + 32 * kMoreWarps;
     key_weights_kernel<D, CAP><<<grid, threads, C::kSmem, s>>>(a);

@@ -503,7 +503,8 @@ lat_status lat_attn_decode_q8(lat_dtype dt, const void *q, int64_t q_rs, const v
  *   q   element (b,i,h,d) at q[(b*n_q + i)*q_rs + h*head_dim + d]
  *   lse fp32 at lse[(b*n_q + i)*n_heads + h]
  *   weights fp32 at weights[b*weights_seq_stride + hk*weights_head_stride + j], strides at least
- *     max_kv_len; entries of keys that no row sees keep their value
+ *     max_kv_len; entries of keys that no row sees keep their value.  What is below the least
+ *     normal number (1.2e-38) may count as 0, in a weight or in a sum
  * k_cache, its strides, kv_lens and max_kv_len as in lat_attn_decode (the cache holds max_kv_len rows
  * per sequence; those at or past kv_lens[b] may hold anything).  A length outside [0, max_kv_len]
  * sets *status = LAT_ERR_BOUNDS and leaves that sequence's weights as they were.  Products and sums are
