@@ -24,6 +24,9 @@
 //    fp16's least is 2^-31 of the largest.
 //  * A query is brought to [2^8, 2^9) by a power of two of its own and taken as one fp16 number
 //    (a bf16 channel above 2^-22 of the largest is exact) or, LAT_F32, two (22 bits and signs).
+//  * LAT_F32: the scores' sums of 64 channels and the outputs' of 16 keys are chains of their own,
+//    joined by rounded adds.  (8 x 131072 tokens, 32 heads over 8: 308 us, as without; head_dim 512
+//    189 -> 210 us; the output's error 2.3e-6 -> 5e-7 of it over long caches.)
 //  * Waits are bounded; on expiry the CTA records LAT_ERR_TIMEOUT, drains its copies, quits.
 // What bounds it: HBM.  A 16-key tile of a warp is about 190 instructions at head_dim 128 for its
 // 4 KB.  mma.sync rather than tcgen05: one query token fills 8 of N, and tcgen05 would need P in
@@ -32,6 +35,7 @@
 
 #include "cache_kernels.h"
 #include "device_common.cuh"
+#include "f32x2.cuh"
 #include "q8_block.cuh"
 #include "score_cap.cuh"
 #include "split_join.cuh"
@@ -49,7 +53,7 @@ struct Q8Cfg {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTerms = F32 ? 2 : 1;               // fp16 terms of a weight and of q
     static constexpr int kRow = 2 * D;
-    static constexpr int kSub = D == 64 ? 4 : D == 512 ? 1 : 2;  // 16-key MMA tiles a warp takes at once
+    static constexpr int kSub = D <= 80 ? 4 : D == 512 ? 1 : 2;  // 16-key MMA tiles a warp takes at once
     static constexpr int kKeys = 16 * kSub;
     static constexpr int kTileKeys = kKeys * kWarps;
     static constexpr int kStages = 2;
@@ -88,6 +92,24 @@ __device__ __forceinline__ void split_pair(uint32_t (&o)[TERMS], float x, float 
     }
 }
 __device__ __forceinline__ uint32_t f16_codes(uint32_t w, int half) { return e4m3x2_to_f16x2((uint16_t)(w >> (16 * half))); }
+
+// d += the product of a with every term.
+template <int TERMS>
+__device__ __forceinline__ void mma_terms(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b0)[TERMS],
+                                          const uint32_t (&b1)[TERMS]) {
+#pragma unroll
+    for (int t = TERMS - 1; t >= 0; --t) mma_f16_16816(d, a, b0[t], b1[t]);
+}
+// d += x, rounded.  The tensor pipe cuts a sum off where its last bit ends, always toward zero: along
+// a chain of n products that is up to n 2^-23 of it, all to one side.  So LAT_F32's chains are short
+// sums of their own, joined by these.
+__device__ __forceinline__ void add_rounded(float (&d)[4], const float (&x)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const float2 s = halves_of(add2(pair_of(d[e], d[e + 1]), pair_of(x[e], x[e + 1])));
+        d[e] = s.x, d[e + 1] = s.y;
+    }
+}
 
 template <int D, bool F32>
 __global__ void __launch_bounds__(Q8Cfg<D, F32>::kThreads, Q8Cfg<D, F32>::kMinBlocks)
@@ -199,7 +221,7 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
 
         // ---- the unit's queries: lane (r, c) holds of head r the channels that its codes of
         // K will meet, four a step; hs brings the scores of heads 2 c and 2 c + 1 to the log2 domain
-        uint32_t qf[C::kQReg ? C::kSteps : 1][kTerms][2];
+        uint32_t qf[C::kQReg ? C::kSteps : 1][2][kTerms];
         float hs[2], pre[2];
         {
             const unsigned char *raw = sQ + (pi & 1) * C::kRawBytes + r * C::kRawRow;
@@ -245,7 +267,7 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
                 split_pair<kTerms>(y, v[2] * by, v[3] * by);
 #pragma unroll
                 for (int t = 0; t < kTerms; ++t) {
-                    if constexpr (C::kQReg) qf[s][t][0] = x[t], qf[s][t][1] = y[t];
+                    if constexpr (C::kQReg) qf[s][0][t] = x[t], qf[s][1][t] = y[t];
                     else frag[(s * 32 + lane) * kTerms + t] = make_uint2(x[t], y[t]);
                 }
             }
@@ -283,22 +305,21 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
             float sc[C::kSub][4], v_exp[C::kSub];
 #pragma unroll
             for (int u = 0; u < C::kSub; ++u) sc[u][0] = sc[u][1] = sc[u][2] = sc[u][3] = 0.f;
-            auto query = [&](int step, uint32_t (&q)[kTerms][2]) {
+            auto query = [&](int step, uint32_t (&q)[2][kTerms]) {
                 if constexpr (C::kQReg) {
 #pragma unroll
-                    for (int t = 0; t < kTerms; ++t) q[t][0] = qf[step][t][0], q[t][1] = qf[step][t][1];
+                    for (int t = 0; t < kTerms; ++t) q[0][t] = qf[step][0][t], q[1][t] = qf[step][1][t];
                 } else {
                     const uint2 *frag = reinterpret_cast<const uint2 *>(sQ + 2 * C::kRawBytes) + (step * 32 + lane) * kTerms;
 #pragma unroll
-                    for (int t = 0; t < kTerms; ++t) q[t][0] = frag[t].x, q[t][1] = frag[t].y;
+                    for (int t = 0; t < kTerms; ++t) q[0][t] = frag[t].x, q[1][t] = frag[t].y;
                 }
             };
             auto score_step = [&](float (&d)[4], uint32_t x, uint32_t y, int step) {
                 const uint32_t k[4] = {f16_codes(x, 0), f16_codes(y, 0), f16_codes(x, 1), f16_codes(y, 1)};
-                uint32_t q[kTerms][2];
+                uint32_t q[2][kTerms];
                 query(step, q);
-#pragma unroll
-                for (int t = kTerms - 1; t >= 0; --t) mma_f16_16816(d, k, q[t][0], q[t][1]);
+                mma_terms<kTerms>(d, k, q[0], q[1]);
             };
 #pragma unroll
             for (int u = 0; u < C::kSub; ++u) {
@@ -307,10 +328,12 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
                 for (int h = 0; h < C::kMain; ++h) {
                     const int off = q8_place<D>(16 * (c + 4 * h), r);
                     const uint4 wx = *reinterpret_cast<const uint4 *>(x + off), wy = *reinterpret_cast<const uint4 *>(y + off);
-                    score_step(sc[u], wx.x, wy.x, 4 * h);
-                    score_step(sc[u], wx.y, wy.y, 4 * h + 1);
-                    score_step(sc[u], wx.z, wy.z, 4 * h + 2);
-                    score_step(sc[u], wx.w, wy.w, 4 * h + 3);
+                    float x64[4] = {0.f, 0.f, 0.f, 0.f}, (&d)[4] = F32 ? x64 : sc[u];  // (of these 64 channels)
+                    score_step(d, wx.x, wy.x, 4 * h);
+                    score_step(d, wx.y, wy.y, 4 * h + 1);
+                    score_step(d, wx.z, wy.z, 4 * h + 2);
+                    score_step(d, wx.w, wy.w, 4 * h + 3);
+                    if constexpr (F32) add_rounded(sc[u], x64);
                 }
                 if constexpr (C::kTail) {
                     const int off = 64 + 4 * c;
@@ -399,6 +422,15 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
             }
             // ---- O^T += V^T P^T: lane (r, c) takes channels of its own for rows 2 c, 2 c + 1, 2 c + 8
             // and 2 c + 9 of a tile; bytes 2 i and 2 i + 1 are rows r and r + 8 of MMA tile i --------
+            auto add_product = [&](float (&d)[4], const uint32_t (&v)[4], int u) {
+                if constexpr (F32) {
+                    float x[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_terms<kTerms>(x, v, w0[u], w1[u]);
+                    add_rounded(d, x);
+                } else {
+                    mma_terms<kTerms>(d, v, w0[u], w1[u]);
+                }
+            };
 #pragma unroll
             for (int u = 0; u < C::kSub; ++u) {
                 const unsigned char *row[4];
@@ -414,11 +446,8 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
                     const uint32_t x1 = __byte_perm(w[0], w[1], 0x7362), y1 = __byte_perm(w[2], w[3], 0x7362);
                     const uint32_t a0[4] = {f16_codes(x0, 0), f16_codes(x0, 1), f16_codes(y0, 0), f16_codes(y0, 1)};
                     const uint32_t a1[4] = {f16_codes(x1, 0), f16_codes(x1, 1), f16_codes(y1, 0), f16_codes(y1, 1)};
-#pragma unroll
-                    for (int k = kTerms - 1; k >= 0; --k) {
-                        mma_f16_16816(acc[i], a0, w0[u][k], w1[u][k]);
-                        mma_f16_16816(acc[i + 1], a1, w0[u][k], w1[u][k]);
-                    }
+                    add_product(acc[i], a0, u);
+                    add_product(acc[i + 1], a1, u);
                 };
                 if constexpr (D >= 128) {
 #pragma unroll
@@ -446,8 +475,7 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
                         for (int k = 0; k < 4; ++k) w[k] = *reinterpret_cast<const uint16_t *>(row[k] + D + 64 + 2 * r);
                         const uint32_t x = __byte_perm(w[0], w[1], 0x5140), y = __byte_perm(w[2], w[3], 0x5140);
                         const uint32_t a0[4] = {f16_codes(x, 0), f16_codes(x, 1), f16_codes(y, 0), f16_codes(y, 1)};
-#pragma unroll
-                        for (int k = kTerms - 1; k >= 0; --k) mma_f16_16816(acc[C::kSteps - 1], a0, w0[u][k], w1[u][k]);
+                        add_product(acc[C::kSteps - 1], a0, u);
                     }
                 }
             }

@@ -516,6 +516,36 @@ def test_two_streams_with_a_workspace_each():
         check_decode(got[i][0][0], got[i][0][1], qs[i], kh, vh, lens, "bf16", Hq, D, 0, 0.0, "stream %d" % i)
 
 
+@pytest.mark.parametrize("D", HEAD_DIMS)
+def test_32_bit_sums_lean_to_no_side(D):
+    """Long shares of values around 0, in LAT_F32: the root mean square of the output's error.
+
+    A weight's error: four roundings of a score below 16 in magnitude (its sum, its scale, its
+    distance from the reference, what the exponential takes), each at most 2^-21, root mean square
+    2^-21 / sqrt(3), 3.8e-7 of the weight in all; the exponential's own 2^-22 and the two fp16 terms'
+    2^-23, 2.7e-7 together at their most.  Errors of the weights that have no common sign move a sum of
+    values around 0 by as much of itself: 4.7e-7 (the squares add up).  Each rounded add of the sum moves it by 2^-24 /
+    sqrt(3) at most, 128 of them by 3.9e-7.  6.1e-7 in all, and 1e-6 leaves room for the output's
+    being smaller than its share of the weights says.  (Sums cut off toward zero lose 128 * 2^-24 =
+    7.6e-6.)"""
+    B, Hkv, G, n = (76, 2, 1, 8192) if D < 512 else (38, 2, 1, 4096)
+    c = Cache(B, n, Hkv, D, 64)
+    for b in range(B):
+        kb, vb = (W.normal((1, n, Hkv, D), dtype="f32", device="cuda", seed=900 + b, role=r) for r in ("k", "v"))
+        c.append(kb, vb, [0], n, dt="f32", b0=b)
+    k, v = c.expand([0] * B, n)
+    q = W.normal((B, Hkv * G * D), dtype="f32", device="cuda", seed=77, role="q")
+    out = decode(c, q, i32([n] * B), "f32", Hkv * G)[0]
+    got, q = out.reshape(B, Hkv, D).double(), q.reshape(B, Hkv, D).double()
+    wrong = size = 0.0
+    for b in range(B):
+        s = torch.einsum("hd,nhd->hn", q[b], k[b].double()) / math.sqrt(D)
+        want = torch.einsum("hn,nhd->hd", torch.softmax(s, -1), v[b].double())
+        assert s.abs().max().item() * math.log2(math.e) < 16
+        wrong, size = wrong + (got[b] - want).square().sum().item(), size + want.square().sum().item()
+    assert math.sqrt(wrong / size) <= 1e-6
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_nothing_cached_anywhere(dt):
     """max_kv_len 0, and caches of every length 0: zeros and -inf, no read of the cache."""
