@@ -1199,6 +1199,8 @@ lat_status lat_kv_evict_choose(const float *weights, int64_t weights_head_stride
         return LAT_ERR_INVALID_ARG;
     if (max_kv_len > lat::kEvictMaxKeys || (int64_t)batch * n_kv_heads > 0x7fffffffLL / lat::kEvictCluster)
         return LAT_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
     lat::EvictChooseArgs a{};
     a.weights = weights;
     a.w_seq = weights_seq_stride;
@@ -1216,7 +1218,7 @@ lat_status lat_kv_evict_choose(const float *weights, int64_t weights_head_stride
     a.batch = batch;
     a.n_kv_heads = n_kv_heads;
     a.status = status;
-    return lat::launch_evict_choose(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+    return lat::launch_evict_choose(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
 }
 
 lat_status lat_kv_evict_rows(lat_dtype dt, void *k_cache, void *v_cache, int64_t cache_rs, int64_t cache_head_stride,

@@ -200,7 +200,7 @@ struct EvictChooseArgs {
     int32_t *status;
 };
 // batch * n_kv_heads * kEvictCluster < 2^31
-cudaError_t launch_evict_choose(EvictChooseArgs a, cudaStream_t s);
+cudaError_t launch_evict_choose(EvictChooseArgs a, int num_sms, cudaStream_t s);
 
 struct EvictRowsArgs {
     void *k, *v;

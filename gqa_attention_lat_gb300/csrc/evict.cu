@@ -2,14 +2,18 @@
 // and their rows moved up in place.
 //
 // choose: a cluster of up to eight CTAs takes one (sequence, KV head).  Each CTA reads its slice of
-// the weights once, into shared memory; what follows runs there.  The n-th largest weight is found
-// digit by digit (11, 11 and 10 bits of an order-preserving integer), counting a digit's keys into
-// 2048 bins that the cluster adds up through distributed shared memory.  Then a key stays if it is
-// among the first or the last, is above that weight, or equals it and few equal ones come before it;
+// the weights once, into shared memory (as order-preserving integers); what follows runs there.  The
+// n-th largest weight is found digit by digit (11, 11 and 10 bits), counting a digit's keys into
+// 2048 bins whose 16-bit counts the cluster's CTAs read from each other; it is done early where all
+// keys with the prefix stay, which two digits mostly bring about.  Then a key stays if it is among
+// the first or the last, is above that weight, or equals it and few equal ones come before it;
 // ballots and a scan over warps and CTAs give its place, so lists are ascending, ties go to the
 // lowest key, and nothing depends on an order of execution.  Since the weights wait in shared memory,
 // they may be written over the ones they came from.
-// What bounds it: barriers and round trips within the cluster, then HBM (4 bytes a key).
+// What bounds it: the loops over a slice (a third of them shared atomics) and barriers and round
+// trips within the cluster, then HBM (4 bytes a key).  32 heads of 65536 keys, a quarter kept: 22 us;
+// clusters of 2 35, of 8 (more CTAs than SMs) 44.  Masks kept between the loops over the places
+// and bins of their own for odd lanes brought nothing.
 //
 // rows: row i of a head becomes its row kept[i] >= i, for ascending i.  A cluster takes K or V of one
 // (sequence, KV head) and moves a stretch of rows at a time: asynchronous copies bring them to shared
@@ -28,11 +32,11 @@ namespace {
 // ---------------------------------------------------------------------------------- choose
 constexpr int kChooseThreads = 1024, kChooseWarps = kChooseThreads / 32;
 constexpr int kBins = 2048, kMyBins = kBins / kChooseThreads;
-constexpr int kAtOnce = 4;  // keys of a lane in the places' loops
-// Keys a CTA takes before the cluster grows.  What the CTAs of a cluster say to each other costs more
-// than reading shared memory (a pass over 8 CTAs' bins 3 us, over 2 a third of that): as few as can
-// hold the weights with room for a second CTA's would be.
-constexpr int kSliceWanted = 32768;
+constexpr int kAtOnce = 4;  // keys of a lane at once, for the places
+constexpr int kLoads = 8;   // of a thread, under way at once
+// Keys of a CTA below which a larger cluster costs more talk than it saves (8 heads of 4097 keys,
+// rows moved: 17.3 us, in clusters of two 18.7).
+constexpr int kSliceLeast = 8192;
 
 // order-preserving: larger weights to larger integers, NaN above all, -0 as 0
 __device__ __forceinline__ uint32_t ordered(float f) {
@@ -40,16 +44,14 @@ __device__ __forceinline__ uint32_t ordered(float f) {
     const uint32_t b = __float_as_uint(f + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float weight_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 __device__ __forceinline__ uint32_t load_cluster(const void *p, uint32_t rank) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)));
     return v;
 }
-__device__ __forceinline__ uint2 load_cluster2(const void *p, uint32_t rank) {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr(p, rank)));
-    return v;
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // the sum of x over the warp's lanes before this one, and over all
 __device__ __forceinline__ int warp_before(int x, int &all) {
     const int lane = threadIdx.x & 31;
@@ -74,18 +76,19 @@ __device__ __forceinline__ int scan_before(int x, int *warps) {
 
 struct Choose {  // in shared memory, one a CTA
     alignas(16) uint32_t bins[kBins];
+    uint32_t told[2][kBins / 2];                 // this CTA's counts for the others, two bins a word
     int warps[kChooseWarps];
     int ties[kChooseWarps], sure[kChooseWarps];  // by warp
     int all_ties, all_sure;
     uint32_t digit;
-    int above;       // keys in the digits above
+    int above, in;   // keys in the digits above, and in that one
 };
 
 template <int P>  // CTAs of a cluster
 __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const EvictChooseArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     Choose &sh = *reinterpret_cast<Choose *>(raw);
-    float *held = reinterpret_cast<float *>(raw + sizeof(Choose));
+    uint32_t *held = reinterpret_cast<uint32_t *>(raw + sizeof(Choose));  // the slice's weights, as ordered()
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = (int)(blockIdx.x % P);
     const int64_t unit = blockIdx.x / P;
@@ -105,77 +108,104 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
             for (int i = rank * kChooseThreads + tid; i < len; i += P * kChooseThreads) out[i] = w[i];
         return;
     }
-    // ---- this CTA's slice ------------------------------------------------------------------
+    // ---- this CTA's slice, and the counts of the first digit ---------------------------------
     const int slice = (len + P - 1) / P, lo = min(len, rank * slice), n = min(len, lo + slice) - lo;
     const int mid_lo = a.n_first, mid_hi = len - a.n_last;  // keys that are chosen among
-#pragma unroll 8
-    for (int i = tid; i < n; i += kChooseThreads) held[i] = __ldcg(w + lo + i);  // (they may be written over)
     auto chosen_among = [&](int i) { return lo + i >= mid_lo && lo + i < mid_hi; };
+    uint2 *my_bins = reinterpret_cast<uint2 *>(sh.bins) + (kChooseThreads - 1 - tid);  // thread 0: the largest digits
+    *my_bins = make_uint2(0, 0);
+    __syncthreads();
+    for (int i0 = tid; i0 < n; i0 += kLoads * kChooseThreads) {
+        float v[kLoads];
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int i = i0 + q * kChooseThreads;
+            v[q] = i < n ? __ldcg(w + lo + i) : 0.f;  // (they may be written over)
+        }
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int i = i0 + q * kChooseThreads;
+            if (i >= n) continue;
+            const uint32_t k = ordered(v[q]);
+            held[i] = k;
+            if (chosen_among(i)) atomicAdd(&sh.bins[k >> 21], 1u);
+        }
+    }
 
     // ---- the weight that the last chosen key has, digit by digit ---------------------------------
     int need = a.n_keep - a.n_first - a.n_last;  // keys still to be chosen among those with the prefix
     uint32_t prefix = 0, mask = 0;
-    if (need > 0) {
 #pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-            for (int i = tid; i < kBins; i += kChooseThreads) sh.bins[i] = 0;
-            __syncthreads();
+    for (int pass = 0; pass < 3 && need > 0; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+        if (pass > 0) {
 #pragma unroll 4
             for (int i = tid; i < n; i += kChooseThreads) {
-                const uint32_t k = ordered(held[i]);
+                const uint32_t k = held[i];
                 if ((k & mask) == prefix && chosen_among(i)) atomicAdd(&sh.bins[(k >> shift) & ((1u << bits) - 1)], 1u);
             }
-            if (P > 1) cluster_sync_all();
-            else __syncthreads();
-            // the cluster's counts, largest digits first: thread t has two, and what lies above
-            uint2 part[P];
-            const uint32_t *bins = sh.bins + kBins - kMyBins * (tid + 1);
-#pragma unroll
-            for (int p = 0; p < P; ++p)
-                part[p] = p == 0 ? *reinterpret_cast<const uint2 *>(bins) : load_cluster2(bins, (uint32_t)((rank + p) % P));
-            uint32_t c[kMyBins] = {0, 0};
-#pragma unroll
-            for (int p = 0; p < P; ++p) c[0] += part[p].y, c[1] += part[p].x;
-            int above = scan_before((int)(c[0] + c[1]), sh.warps);
-#pragma unroll
-            for (int q = 0; q < kMyBins; ++q) {
-                if (above < need && above + (int)c[q] >= need) sh.digit = kBins - 1 - (kMyBins * tid + q), sh.above = above;
-                above += (int)c[q];
-            }
-            if (P > 1) cluster_sync_all();  // (also: the bins have been read)
-            else __syncthreads();
-            prefix |= sh.digit << shift;
-            mask |= ((1u << bits) - 1) << shift;
-            need -= sh.above;
-            __syncthreads();
         }
-    } else {
-        mask = 0xffffffffu, prefix = 0xffffffffu;  // (NaN would tie; `need` 0 keeps none)
+        __syncthreads();
+        // the cluster's counts, largest digits first: thread t has two, and what lies above
+        const uint2 mine = *my_bins;
+        *my_bins = make_uint2(0, 0);
+        uint32_t c[kMyBins] = {mine.y, mine.x};
+        if constexpr (P > 1) {
+            // (a slice's counts fit 16 bits; the words of the last pass but one have been read by all)
+            sh.told[pass & 1][tid] = mine.y | mine.x << 16;
+            cluster_sync_all();
+            uint32_t part[P];
+#pragma unroll
+            for (int p = 1; p < P; ++p) part[p] = load_cluster(&sh.told[pass & 1][tid], (uint32_t)((rank + p) % P));
+#pragma unroll
+            for (int p = 1; p < P; ++p) c[0] += part[p] & 0xffffu, c[1] += part[p] >> 16;
+        }
+        int above = scan_before((int)(c[0] + c[1]), sh.warps);
+#pragma unroll
+        for (int q = 0; q < kMyBins; ++q) {
+            if (above < need && above + (int)c[q] >= need)
+                sh.digit = kBins - 1 - (kMyBins * tid + q), sh.above = above, sh.in = (int)c[q];
+            above += (int)c[q];
+        }
+        __syncthreads();
+        prefix |= sh.digit << shift;
+        mask |= ((1u << bits) - 1) << shift;
+        need -= sh.above;
+        if (need == sh.in) break;  // all keys with this prefix stay: no further digit tells them apart
     }
     // ---- places: a warp takes a run of the slice, in order ------------------------------------------
-    // (a key of rank: 2 stays, 1 is one of the equal ones, 0 goes)
-    auto rank_of = [&](int i) {
-        if (i >= n) return 0;
-        if (!chosen_among(i)) return 2;
-        if (a.n_keep == a.n_first + a.n_last) return 0;
-        const uint32_t k = ordered(held[i]);
-        return k > prefix ? 2 : k == prefix ? 1 : 0;
-    };
+    // a key's rank: 2 stays, 1 is one of the equal ones, 0 goes
     constexpr int kStep = 32 * kAtOnce;
+    const bool none = a.n_keep == a.n_first + a.n_last;
+    auto ranks = [&](int i0, uint32_t (&k)[kAtOnce], int (&r)[kAtOnce]) {
+        if (i0 + kStep <= n && lo + i0 >= mid_lo && lo + i0 + kStep <= mid_hi && !none) {
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) k[q] = held[i0 + 32 * q + lane];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) r[q] = (k[q] & mask) > prefix ? 2 : (k[q] & mask) == prefix ? 1 : 0;
+            return;
+        }
+#pragma unroll 1
+        for (int q = 0; q < kAtOnce; ++q) {
+            const int i = i0 + 32 * q + lane;
+            const uint32_t x = i < n ? held[i] : 0, m = x & mask;
+            const int at = i >= n ? 0 : !chosen_among(i) ? 2 : none ? 0 : m > prefix ? 2 : m == prefix ? 1 : 0;
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+                if (u == q) k[u] = x, r[u] = at;
+        }
+    };
     const int run = (slice + kChooseWarps * kStep - 1) / (kChooseWarps * kStep) * kStep;  // keys of a warp
     const int run_end = min((warp + 1) * run, n);
     int ties = 0, sure = 0;
     for (int i0 = warp * run; i0 < run_end; i0 += kStep) {
+        uint32_t k[kAtOnce];
         int r[kAtOnce];
+        ranks(i0, k, r);
 #pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) r[q] = rank_of(i0 + 32 * q + lane);
-#pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) {
-            ties += __popc(__ballot_sync(0xffffffffu, r[q] == 1));
-            sure += __popc(__ballot_sync(0xffffffffu, r[q] == 2));
-        }
+        for (int q = 0; q < kAtOnce; ++q) ties += r[q] == 1, sure += r[q] == 2;
     }
+    ties = __reduce_add_sync(0xffffffffu, ties), sure = __reduce_add_sync(0xffffffffu, sure);
     if (lane == 0) sh.ties[warp] = ties, sh.sure[warp] = sure;
     __syncthreads();
     int all_ties, all_sure;  // of the CTA
@@ -187,30 +217,35 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         const bool earlier = lane < rank;  // (a CTA a lane)
         ties_before += __reduce_add_sync(0xffffffffu, earlier ? (int)load_cluster(&sh.all_ties, (uint32_t)lane) : 0);
         sure_before += __reduce_add_sync(0xffffffffu, earlier ? (int)load_cluster(&sh.all_sure, (uint32_t)lane) : 0);
+        cluster_arrive();  // (the others' shared memory has been read)
     }
     const uint32_t under = (1u << lane) - 1;
     for (int i0 = warp * run; i0 < run_end; i0 += kStep) {
+        uint32_t k[kAtOnce];
         int r[kAtOnce];
-#pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) r[q] = rank_of(i0 + 32 * q + lane);
+        ranks(i0, k, r);
 #pragma unroll
         for (int q = 0; q < kAtOnce; ++q) {
-            const int i = i0 + 32 * q + lane;
             const uint32_t tied = __ballot_sync(0xffffffffu, r[q] == 1), stay = __ballot_sync(0xffffffffu, r[q] == 2);
-            const int t = ties_before + __popc(tied & under);  // equal ones before this key
-            if (r[q] == 2 || (r[q] == 1 && t < need)) {
-                // sure ones before, and the equal ones before that stay
-                const int at = sure_before + __popc(stay & under) + min(t, need);
-                kept[at] = lo + i;
-                if (out != nullptr) out[at] = held[i];
+            // sure ones before, and the equal ones before that stay
+            int at = sure_before + __popc(stay & under) + min(ties_before, need);
+            bool stays = r[q] == 2;
+            if (tied != 0) {
+                const int t = ties_before + __popc(tied & under);
+                at += min(t, need) - min(ties_before, need);
+                stays |= r[q] == 1 && t < need;
+                ties_before += __popc(tied);
             }
-            ties_before += __popc(tied);
+            if (stays) {
+                kept[at] = lo + i0 + 32 * q + lane;
+                if (out != nullptr) out[at] = weight_of(k[q]);
+            }
             sure_before += __popc(stay);
         }
     }
     if (out != nullptr)
         for (int i = a.n_keep + rank * kChooseThreads + tid; i < len; i += P * kChooseThreads) out[i] = 0.f;
-    if (P > 1) cluster_sync_all();  // nobody's shared memory goes while another reads it
+    if (P > 1) cluster_wait();  // nobody's shared memory goes while another reads it
 }
 
 // ---------------------------------------------------------------------------------- rows
@@ -341,9 +376,14 @@ cudaError_t launch_cluster(Kernel *k, SharedLimit &limit, int most, const Args &
 
 }  // namespace
 
-cudaError_t launch_evict_choose(EvictChooseArgs a, cudaStream_t s) {
+cudaError_t launch_evict_choose(EvictChooseArgs a, int num_sms, cudaStream_t s) {
     a.cluster = 1;
-    while (a.cluster < kEvictCluster && (int64_t)a.cluster * kSliceWanted < a.max_kv_len) a.cluster *= 2;
+    // more CTAs a head while its slices do not fit, or while there are SMs for them (256 heads of 32768
+    // keys, rows moved: 98 us, in clusters of two 102)
+    const int64_t units = (int64_t)a.batch * a.n_kv_heads;
+    while (a.cluster < kEvictCluster && ((int64_t)a.cluster * kEvictMaxSlice < a.max_kv_len ||
+                                         (units * a.cluster * 2 <= num_sms && a.cluster * kSliceLeast < a.max_kv_len)))
+        a.cluster *= 2;
     const int slice = (a.max_kv_len + a.cluster - 1) / a.cluster;
     static_assert(kMyBins == 2 && kChooseWarps == 32, "pairs of bins, a warp a lane");
     static_assert(sizeof(Choose) + 4 * kEvictMaxSlice <= 232448, "shared memory budget");
