@@ -63,7 +63,7 @@ constexpr int kTables = 4;
 constexpr int kPlaces = 8;                        // key tiles whose sums can be under way at once
 constexpr int kSBufs = 4, kSCols = 128;           // tiles of S in tensor memory
 constexpr uint32_t kTmemCols = kSBufs * kSCols;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 8, kMaxHeld = 8;
 
 template <int D>
 struct KwCfg {
@@ -75,6 +75,7 @@ struct KwCfg {
     // columns, or 128 keys.  What it leaves of kTiles is the ring's.
     static constexpr int kHeldBytes = D == 512 ? 131072 : 65536;
     static constexpr int kHeldCols = kHeldBytes / (kChunks * 128) < kMaxCols ? kHeldBytes / (kChunks * 128) : kMaxCols;
+    static constexpr int kManyHeldBytes = 32768;
     static constexpr int kTiles = 196608;
     static constexpr int kTableBytes = kTables * (3 * kMaxCols + 4) * 4;
     static constexpr int kPassed = kPlaces * kMaxQuartets * kKeysTile * 4;          // [key tile % kPlaces][quartet][key] sums
@@ -115,13 +116,15 @@ struct Walker {
     int64_t pos, end;  // next tile, and behind the last; or the round
     int64_t base;      // queries held: where sequence b's tiles begin
     int b;
+    int of, len;       // queries held: the sequence whose length is at hand, and that
+    int2 seen;
 
     __device__ bool next(Run &r) { return a.keys_held ? next_dealt(r) : next_shared(r); }
     __device__ bool next_shared(Run &r) {
         if (pos >= end) return false;
         for (;; ++b) {
-            r.len = length_of(a, b);
-            const int2 seen = tiles_seen(a, r.len);
+            if (b != of) of = b, len = length_of(a, b), seen = tiles_seen(a, len);
+            r.len = len;
             const int n = seen.y - seen.x;
             const int64_t all = (int64_t)n * a.n_kv_heads;
             if (pos >= base + all) {
@@ -236,9 +239,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     float *passed = reinterpret_cast<float *>(tables + kTables);  // [key tile % kPlaces][quartet][key]
     uint64_t *bars = reinterpret_cast<uint64_t *>(passed + kPlaces * kMaxQuartets * kKeysTile);
     uint64_t *ring_full = bars, *ring_empty = bars + 8;          // [n_stages]
-    uint64_t *held_full = bars + 16, *held_empty = bars + 18;    // [2]
-    uint64_t *s_full = bars + 20, *s_empty = bars + 24;          // [4]
-    uint64_t *tab_full = bars + 28, *tab_empty = tab_full + kTables;
+    uint64_t *held_full = bars + 16, *held_empty = bars + 24;    // [n_held]
+    uint64_t *s_full = bars + 32, *s_empty = bars + 36;          // [4]
+    uint64_t *tab_full = bars + 40, *tab_empty = tab_full + kTables;
     uint64_t *x_full = tab_empty + kTables;                      // [key tile % kPlaces][quarter of the lanes]
     uint64_t *bar_done = x_full + 4 * kPlaces;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bar_done + 1);
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     int64_t *start = reinterpret_cast<int64_t *>(bar_done + 2);  // share: base, b
     int *scan = reinterpret_cast<int *>(bar_done + 4);           // a warp each
     static_assert(sizeof(Table) * kTables == C::kTableBytes && kTables >= kSBufs &&
-                      (32 + 2 * kTables + 4 * kPlaces) * 8 + kMaxThreads / 32 * 4 <= C::kBarBytes,
+                      (44 + 2 * kTables + 4 * kPlaces) * 8 + kMaxThreads / 32 * 4 <= C::kBarBytes,
                   "shared memory layout");
     if (smem_u32(smem) & 1023) {  // (swizzled operands need it; it is where dynamic shared memory begins)
         if (threadIdx.x == 0) report_status(a.status, kErrCuda);
@@ -266,7 +269,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     const int q_rows = a.rows_per * a.heads_per;                 // columns that a copy brings
     const int q_chunk = a.n_cols * 128;                          // where its chunks lie apart
     const int held_bytes = C::kChunks * (a.keys_held ? 16384 : q_chunk);
-    const unsigned n_held = 2 * held_bytes <= C::kHeldBytes ? 2 : 1;
+    // (two where there is room, more while they are small: short sequences are over before the next
+    // one's queries have come.  32 sequences of 1 to 4096 keys, one row: two 36.2 us, eight 32.2)
+    int held_log2 = 2 * held_bytes <= C::kHeldBytes ? 1 : 0;
+    while (!a.keys_held && (2 << held_log2) <= kMaxHeld && (2 << held_log2) * held_bytes <= C::kManyHeldBytes) ++held_log2;
+    const unsigned n_held = 1u << held_log2;
     unsigned char *held = smem, *ring = held + n_held * held_bytes;
     const int stage_bytes = a.keys_held ? q_chunk : C::kStageBytes;  // of queries, one chunk
     const int stage_chunks = a.keys_held ? 1 : C::kStageChunks, per_tile = C::kChunks / stage_chunks;
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         auto init = [&](uint64_t *first, int n, int count) {
             if (lane < n) mbar_init(first + lane, count);
         };
-        init(ring_full, 2 * kMaxStages + 4, 1);  // ring and held
+        init(ring_full, 2 * kMaxStages + 2 * kMaxHeld, 1);  // ring and held
         init(s_full, kSBufs, a.keys_held ? 2 : 1);  // keys held: full when its MMAs are done and its table is there
         init(s_empty, kSBufs, 4 * halves);
         init(tab_full, kTables, 1);
@@ -312,12 +319,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    int total = 0, before = incl - mine;
-    for (int w = 0; w < n_threads / 32; ++w) {
-        const int v = scan[w];
-        if (w < warp) before += v;
-        total += v;
-    }
+    const int of_warp = lane < n_threads / 32 ? scan[lane] : 0;
+    const int total = __reduce_add_sync(0xffffffffu, of_warp);
+    const int before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
     int64_t r0 = 0, r1 = a.slots;
     if (!a.keys_held) {
         const int each = total / (int)gridDim.x, more = total % (int)gridDim.x, c = blockIdx.x;
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         }
         __syncthreads();
     }
-    Walker walk{a, r0, r1, start[0], (int)start[1]};
+    Walker walk{a, r0, r1, start[0], (int)start[1], -1};
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag, deadline); };
 
     if (warp == n_epilogue) {
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             };
             for (Run r; ok && walk.next(r); ++h) {
                 const unsigned y = h & (n_held - 1);
-                if (!(ok = wait(&held_empty[y], ((h >> (n_held - 1)) & 1) ^ 1))) break;
+                if (!(ok = wait(&held_empty[y], ((h >> held_log2) & 1) ^ 1))) break;
                 mbar_arrive_expect_tx(&held_full[y], C::kChunks * (a.keys_held ? 16384 : q_rows * 128));
                 if (a.keys_held) keys(held + y * held_bytes, &held_full[y], r, r.t, 0, C::kChunks);
                 else queries(held + y * held_bytes, &held_full[y], r, 0, 0, 0, C::kChunks);
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             bool ok = true;
             for (Run r; ok && walk.next(r); ++h) {
                 const unsigned y = h & (n_held - 1);
-                if (!(ok = wait(&held_full[y], (h >> (n_held - 1)) & 1))) break;
+                if (!(ok = wait(&held_full[y], (h >> held_log2) & 1))) break;
                 const uint64_t kept = d_held + (uint64_t)((y * held_bytes) >> 4);
                 for (int i = 0; ok && i < r.n; ++i, step += halves) {
                     const unsigned buf = step % kSBufs;  // (two tiles of S lie side by side and go by the first's barriers)
@@ -487,19 +491,25 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
         unsigned n = 0;  // tables before this run's
         bool ok = true;
-        for (Run r; ok && walk.next(r);) {
-            if (!a.keys_held) {
-                if ((n & 1) == (unsigned)odd) {
-                    const unsigned u = n % kTables;
-                    const Place p = place_of(0);
-                    ask(r, p);
-                    if (!(ok = wait_warp(&tab_empty[u], ((n / kTables) & 1) ^ 1))) break;
-                    fill(tables[u], r, p);
-                    if (lane == 0) mbar_arrive(&tab_full[u]);
-                }
-                ++n;
-                continue;
+        if (!a.keys_held) {
+            // this warp's runs, the next one's log-sum-exps on their way while one is filled
+            const Place p = place_of(0);
+            Run r;
+            bool more = walk.next(r) && (odd == 0 || walk.next(r));
+            n = odd;
+            while (more) {
+                ask(r, p);
+                Run next = r;
+                more = walk.next(next) && walk.next(next);
+                const unsigned u = n % kTables;
+                if (!(ok = wait_warp(&tab_empty[u], ((n / kTables) & 1) ^ 1))) break;
+                fill(tables[u], r, p);
+                if (lane == 0) mbar_arrive(&tab_full[u]);
+                r = next;
+                n += 2;
             }
+        }
+        for (Run r; a.keys_held && ok && walk.next(r);) {
             int i = (n & 1) == (unsigned)odd ? 0 : 1;  // this warp's first of the run
             Place p = place_of(r.x + i);
             if (i < r.n) ask(r, p);
