@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
         if (tid >= rows || s >= n_stretches || i >= a.n_keep) return -1;
         const int j = __ldg(kept + i), before = i > 0 ? __ldg(kept + i - 1) : -1;
         if (j == -1) return -1;
-        if (j < 0 || j >= a.capacity || j <= before || (i > 0 && before < 0)) {
+        if (j < i || j >= a.capacity || j <= before || (i > 0 && before < 0)) {  // (ascending lists never have j < i)
             report_status(a.status, kErrBounds);
             return -1;
         }

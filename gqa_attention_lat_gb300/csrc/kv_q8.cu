@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) append_q8_kernel(const Q8StoreArgs a
         return;
     }
     const int n = (pos >> a.block_shift) + (int)m, first = n << a.block_shift;  // the block and its first row
-    const int lo = max(pos, first), hi = min(pos + a.n, first + (1 << a.block_shift));
+    const int lo = max(pos, first), hi = first + min(pos + a.n - first, 1 << a.block_shift);
     if (lo >= hi) return;
     const T *src = static_cast<const T *>(which ? a.v : a.k) + ((int64_t)b * a.n + (lo - pos)) * a.rs + (int64_t)hk * D;
     unsigned char *rec = a.cache + (int64_t)b * a.cache_seq + (int64_t)n * a.cache_block + (int64_t)hk * a.cache_head;

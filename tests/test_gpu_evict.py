@@ -206,6 +206,21 @@ def test_a_list_that_is_none_is_reported(bad):
         assert torch.equal(x[0, 8:], y[0, 8:])
 
 
+@pytest.mark.parametrize("D", [64, 256])
+def test_lists_that_begin_again_stay_below_the_capacity(D):
+    """Lists longer than the cache that count up several times: a stretch of rows of its own ends at each."""
+    B, H, cap = 1, 2, 700
+    k, v = caches(B, 1500, H, D, "bf16", 2)
+    was = [k.clone(), v.clone()]
+    kept = torch.arange(1300, dtype=torch.int32).remainder(cap)
+    kept = torch.stack([kept, torch.arange(1300, dtype=torch.int32) // 2])[None].cuda()
+    st = move(k, v, kept, "bf16", D, capacity=cap)
+    torch.cuda.synchronize()
+    assert int(st.item()) == binding.LAT_ERR_BOUNDS
+    for x, y in zip((k, v), was):
+        assert torch.equal(x[:, cap:], y[:, cap:])
+
+
 def test_a_long_cache_past_32_bit_offsets():
     """Rows that come from beyond 2^32 bytes behind the cache's begin."""
     cap, D, n = 4_300_000, 512, 3000
