@@ -169,6 +169,22 @@ def test_every_length_around_a_tile(D, n_q):
     check(w, was, added, worst, lens, "D%d q%d" % (D, n_q))
 
 
+@pytest.mark.parametrize("D,n_q,window", [(64, 1, 0), (80, 2, 50), (128, 1, 0), (128, 5, 140), (256, 1, 0), (256, 20, 0),
+                                          (512, 1, 0), (512, 9, 0)])
+def test_many_short_sequences(D, n_q, window):
+    """A CTA's share is a dozen or more (sequence, head)s of one or two tiles, empty ones between."""
+    B, Hq, Hkv, cap = 900, 4, 2, 200
+    lens = [(b * 89) % 201 if b % 7 else 0 for b in range(B)]
+    q, k = inputs(B, Hq, Hkv, D, cap, n_q, "bf16", 17 + D)
+    added, lse, worst = definition(q.reshape(B, n_q, Hq, D), k, lens, n_q, 1, window, D ** -0.5, 0.0)
+    w = start(B, Hkv, cap, 7)
+    was = w.clone()
+    st = run(q, k, lens, "bf16", Hq, Hkv, D, n_q, torch.from_numpy(lse).cuda(), w, window=window)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check(w, was, added, worst, lens, "D%d q%d" % (D, n_q))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("n_q", [1, 300])
 def test_rows_without_a_log_sum_exp_give_nothing(dt, n_q):
