@@ -1122,15 +1122,16 @@ lat_status key_weights_impl(lat_dtype dt, const void *q, int64_t q_rs, int n_q, 
     a.test_skip_load = skip_load;
     a.status = status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int sms = 0;
     if (dt == LAT_F32) {
         if ((int64_t)batch * n_kv_heads > 65535 || (int64_t)n_q * (n_heads / n_kv_heads) > 0x7fffffffLL)
             return LAT_ERR_UNSUPPORTED;
         a.by_heads_per = lat::FastDiv((uint32_t)(n_heads / n_kv_heads));
         a.q_vec = aligned16(q) && q_rs % 4 == 0;
         a.k_vec = aligned16(k_cache) && cache_rs % 4 == 0 && cache_head_stride % 4 == 0 && cache_seq_stride % 4 == 0;
-        return lat::launch_key_weights_f32(a, s) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+        if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
+        return lat::launch_key_weights_f32(a, sms, s) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
     }
-    int sms = 0;
     if (!current_sm_count(&sms)) return LAT_ERR_CUDA;
     lat::KeyWeightsPlan plan;
     if (!lat::plan_key_weights(batch, n_q, n_heads, n_kv_heads, head_dim, max_kv_len, sms, &plan))

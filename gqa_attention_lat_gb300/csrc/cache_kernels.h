@@ -181,7 +181,7 @@ bool plan_key_weights(int batch, int n_q, int n_heads, int n_kv_heads, int head_
                       KeyWeightsPlan *p);
 cudaError_t launch_key_weights(const KeyWeightsArgs &a, int grid, cudaStream_t s);
 // batch * n_kv_heads <= 65535
-cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, cudaStream_t s);
+cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- eviction
 constexpr int kEvictCluster = 8, kEvictMaxSlice = 53248;  // CTAs of a head, keys of one in shared memory

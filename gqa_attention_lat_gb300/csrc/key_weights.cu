@@ -36,9 +36,12 @@
 // What bounds it: HBM (keys once) for few columns; for many the tensor pipe and the exponentials,
 // 128 N D 2 flops against 128 N of them.
 //
-// fp32 (key_weights_f32_kernel): fp32 products by FMA, 64 keys x 8, 32 or 64 columns a step, a thread 4
-// x 1, 4 or 8 of them; the next 32 channels come while 32 are used.  Bound by its FMAs, with few
-// columns by HBM.
+// fp32 (key_weights_f32_kernel): fp32 products by FMA, 64 keys x 32 or 64 columns a step, a thread 4
+// x 4 or 8 of them; the next 32 channels come while 32 are used.  Bound by its FMAs.  Up to eight
+// columns (a decode step) go to key_weights_few_kernel, whose keys do not pass through shared
+// memory (2 x 40000 keys, 24 heads over 8, head_dim 128: 75.7 -> 47.6 us, 3.5 TB/s; 32 caches of up
+// to 4096, 12 heads over 4, head_dim 64: 35.8 -> 26.5).  It is bound by what a key costs beside its
+// products: 31 exchanges for 32 sums, each two selections, a shuffle and an addition.
 #include <math.h>
 
 #include <algorithm>
@@ -651,7 +654,7 @@ template <int COLS, bool CAP>
 __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyWeightsArgs a) {
     constexpr int kPer = COLS / 8, kVecs = kF32Depth / 4;                   // a thread's columns; vectors of a row's 32 channels
     constexpr int kMyK = kF32Keys * kVecs / kF32Threads;                    // a thread's vectors of keys and of queries
-    constexpr int kMyQ = COLS * kVecs >= kF32Threads ? COLS * kVecs / kF32Threads : 1;
+    constexpr int kMyQ = COLS * kVecs / kF32Threads;
     __shared__ __align__(16) float sK[kF32Depth][kF32Keys + 4], sQ[kF32Depth][COLS + 4];
     __shared__ float lse2[COLS];
     __shared__ int hi[COLS], lo[COLS];
@@ -687,7 +690,7 @@ __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyW
 #pragma unroll
         for (int e = 0; e < kMyQ; ++e) {
             const int v = tid + e * kF32Threads, d = d0 + v % kVecs * 4, c = v / kVecs;
-            const int64_t at = c < COLS ? q_at[c] : -1;
+            const int64_t at = q_at[c];
             qv[e] = d < D && at >= 0 ? four(qb + at + d, a.q_vec) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyW
 #pragma unroll
             for (int e = 0; e < kMyQ; ++e) {
                 const int v = tid + e * kF32Threads, d = v % kVecs * 4, c = v / kVecs;
-                if (c < COLS) sQ[d][c] = qv[e].x, sQ[d + 1][c] = qv[e].y, sQ[d + 2][c] = qv[e].z, sQ[d + 3][c] = qv[e].w;
+                sQ[d][c] = qv[e].x, sQ[d + 1][c] = qv[e].y, sQ[d + 2][c] = qv[e].z, sQ[d + 3][c] = qv[e].w;
             }
             __syncthreads();
             if (d0 + kF32Depth < D) ask(d0 + kF32Depth);
@@ -766,6 +769,133 @@ __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyW
         for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         const int j = first + 4 * x + k;
         if (y == 0 && j <= last) a.weights[(int64_t)b * a.w_seq + (int64_t)hk * a.w_head + j] += v;
+    }
+}
+
+// Few columns (a decode step): keys go from memory to registers, a warp 32 / COLS of them at once, a
+// lane W channels of each 32 W; queries wait in shared memory.  A lane's 32 sums (key, column) become
+// one through five exchanges that halve them, lane l keeping key l / COLS and column l % COLS.
+constexpr int kFewSpan = 64;  // a CTA takes a multiple of these keys
+
+template <int W>
+struct Channels {
+    float v[W];
+    __device__ __forceinline__ void load(const float *p, bool vec) {
+        if constexpr (W == 4) {
+            if (vec) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+                return;
+            }
+        } else {
+            if (vec) {
+                const float2 x = __ldg(reinterpret_cast<const float2 *>(p));
+                v[0] = x.x, v[1] = x.y;
+                return;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = __ldg(p + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = 0.f;
+    }
+};
+
+template <int COLS, int W, bool CAP>
+__global__ void __launch_bounds__(kF32Threads, 4) key_weights_few_kernel(const KeyWeightsArgs a, int span) {
+    constexpr int kKeys = 32 / COLS, kWarps = kF32Threads / 32;
+    extern __shared__ __align__(16) float sQ[];  // [COLS][chunks * 32 W], zeros where there is nothing
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.y / a.n_kv_heads, hk = blockIdx.y % a.n_kv_heads, G = a.n_heads / a.n_kv_heads, D = a.head_dim;
+    const int raw = a.kv_lens[b], cols = a.n_q * G;
+    if (raw < 0 || raw > a.max_kv_len) {
+        if (blockIdx.x == 0 && hk == 0 && tid == 0) report_status(a.status, kErrBounds);
+        return;
+    }
+    const int64_t off = (int64_t)raw - a.n_q, from = (int64_t)blockIdx.x * span;
+    const int end = (int)min(from + span, (int64_t)raw);
+    // the first key that some row sees
+    const int first = (int)max(from, a.window > 0 ? off - a.window + 1 : (int64_t)0);
+    if (first >= end) return;
+    const int n = end - first;
+    const int chunks = (D + 32 * W - 1) / (32 * W), pitch = chunks * 32 * W;
+    const float *kb = static_cast<const float *>(a.k) + (int64_t)b * a.k_seq + (int64_t)hk * a.k_head;
+    const float *qb = static_cast<const float *>(a.q) + (int64_t)b * a.n_q * a.q_rs + (int64_t)hk * G * D;
+
+    // group g of this CTA's keys: first + g kKeys ...; this warp's are warp, warp + kWarps, ...
+    Channels<W> held[kKeys];
+    auto ask = [&](int g, int chunk) {
+        const int d = (chunk * 32 + lane) * W;
+#pragma unroll
+        for (int k = 0; k < kKeys; ++k) {
+            if (g * kKeys + k < n && d < D) held[k].load(kb + (int64_t)(first + g * kKeys + k) * a.k_row + d, a.k_vec);
+            else held[k].zero();
+        }
+    };
+    ask(warp, 0);
+    for (int i = tid; i < COLS * pitch; i += kF32Threads) {
+        const int c = i / pitch, d = i - c * pitch, row = c / G;
+        sQ[i] = c < cols && d < D ? __ldg(qb + (int64_t)row * a.q_rs + (int64_t)(c - row * G) * D + d) : 0.f;
+    }
+    // this lane's column
+    const int col = lane % COLS, my_row = col / G;
+    float lse2 = INFINITY;
+    int hi = -1, lo = -1;
+    if (col < cols) {
+        const float l = a.lse[((int64_t)b * a.n_q + my_row) * a.n_heads + hk * G + col - my_row * G];
+        const int64_t pos = off + my_row;
+        if (l != -INFINITY && pos >= 0) {
+            lse2 = l * 1.4426950408889634f;
+            hi = a.causal ? (int)pos : 0x7fffffff;
+            lo = a.window > 0 ? (int)(pos - a.window) : -1;
+        }
+    }
+    __syncthreads();
+    float *w = a.weights + (int64_t)b * a.w_seq + (int64_t)hk * a.w_head;
+    for (int g = warp; g * kKeys < n; g += kWarps) {
+        float s[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = 0.f;
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            Channels<W> k[kKeys];
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) k[i] = held[i];
+            if (chunk + 1 < chunks) ask(g, chunk + 1);
+            else ask(g + kWarps, 0);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                Channels<W> q;
+                const float *at = sQ + c * pitch + (chunk * 32 + lane) * W;
+                if constexpr (W == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(at);
+                    q.v[0] = x.x, q.v[1] = x.y, q.v[2] = x.z, q.v[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(at);
+                    q.v[0] = x.x, q.v[1] = x.y;
+                }
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i)
+#pragma unroll
+                    for (int e = 0; e < W; ++e) s[i * COLS + c] = fmaf(k[i].v[e], q.v[e], s[i * COLS + c]);
+            }
+        }
+#pragma unroll
+        for (int half = 16; half > 0; half >>= 1) {
+            const bool upper = lane & half;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const float keep = upper ? s[i + half] : s[i], give = upper ? s[i] : s[i + half];
+                s[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+            }
+        }
+        const int i = g * kKeys + lane / COLS, j = first + i;
+        const float x = CAP ? a.cap_log2 * tanhf(s[0] * a.raw_over_cap) - lse2 : fmaf(s[0], a.scale_log2, -lse2);
+        float p = i < n && j <= hi && j > lo ? fast_exp2(x) : 0.f;
+#pragma unroll
+        for (int o = 1; o < COLS; o <<= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+        if (col == 0 && p != 0.f) atomicAdd(w + j, p);  // (this lane alone has the key; p is 0 where there is none)
     }
 }
 
@@ -834,15 +964,28 @@ cudaError_t launch_key_weights(const KeyWeightsArgs &a, int grid, cudaStream_t s
     }
 }
 
-cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, cudaStream_t s) {
+cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, int num_sms, cudaStream_t s) {
     // (one block of nothing still sees the lengths)
     const dim3 grid((unsigned)((std::max<int64_t>(a.max_kv_len, 1) + kF32Keys - 1) / kF32Keys), (unsigned)(a.batch * a.n_kv_heads));
     const bool cap = a.cap_log2 > 0.f;
     const int64_t cols = (int64_t)a.n_q * (a.n_heads / a.n_kv_heads);
     // no more columns at once than there are
     auto go = [&](auto kernel) { kernel<<<grid, kF32Threads, 0, s>>>(a); };
-    if (cols <= 8) cap ? go(key_weights_f32_kernel<8, true>) : go(key_weights_f32_kernel<8, false>);
-    else if (cols <= 32) cap ? go(key_weights_f32_kernel<32, true>) : go(key_weights_f32_kernel<32, false>);
+    if (cols <= 8) {
+        // longer stretches a CTA while there are eight CTAs an SM all the same (32 caches of 4096, head_dim
+        // 128: 34 us; down to two CTAs an SM 42, sixteen 42)
+        int span = kFewSpan;
+        while (span < 1024 && ((int64_t)a.max_kv_len + 2 * span - 1) / (2 * span) * grid.y >= 8 * (int64_t)num_sms) span *= 2;
+        const int width = a.head_dim == 64 ? 2 : 4, pitch = (a.head_dim + 32 * width - 1) / (32 * width) * 32 * width;
+        auto few = [&](auto kernel, int columns) {
+            kernel<<<dim3((unsigned)((std::max<int64_t>(a.max_kv_len, 1) + span - 1) / span), grid.y), kF32Threads,
+                     columns * pitch * sizeof(float), s>>>(a, span);
+        };
+        if (cols <= 4 && width == 2) cap ? few(key_weights_few_kernel<4, 2, true>, 4) : few(key_weights_few_kernel<4, 2, false>, 4);
+        else if (cols <= 4) cap ? few(key_weights_few_kernel<4, 4, true>, 4) : few(key_weights_few_kernel<4, 4, false>, 4);
+        else if (width == 2) cap ? few(key_weights_few_kernel<8, 2, true>, 8) : few(key_weights_few_kernel<8, 2, false>, 8);
+        else cap ? few(key_weights_few_kernel<8, 4, true>, 8) : few(key_weights_few_kernel<8, 4, false>, 8);
+    } else if (cols <= 32) cap ? go(key_weights_f32_kernel<32, true>) : go(key_weights_f32_kernel<32, false>);
     else cap ? go(key_weights_f32_kernel<64, true>) : go(key_weights_f32_kernel<64, false>);
     return cudaGetLastError();
 }
