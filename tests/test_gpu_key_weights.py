@@ -185,6 +185,28 @@ def test_many_short_sequences(D, n_q, window):
     check(w, was, added, worst, lens, "D%d q%d" % (D, n_q))
 
 
+@pytest.mark.parametrize("D", [64, 80, 128, 256, 512])
+@pytest.mark.parametrize("Hq,Hkv,n_q", [(2, 2, 1), (6, 2, 1), (6, 1, 1), (4, 2, 3), (6, 2, 9)])
+@pytest.mark.parametrize("odd", [False, True])
+def test_32_bit_rows_at_any_stride_and_address(D, Hq, Hkv, n_q, odd):
+    """One column to 27, whole stretches of keys and what is left of one, a window that begins in either."""
+    B, cap, lens, window = 3, 1100, [1100, 517, 2], 900
+    q0, k0 = inputs(B, Hq, Hkv, D, cap, n_q, "f32", 5 + D, pad=0)
+    pad = 3 if odd else 4
+    q = torch.full((B * n_q, Hq * D + 2 * pad), float("nan"), device="cuda")[:, pad:pad + Hq * D]
+    k = torch.full((B, cap, Hkv, D + 2 * pad), float("nan"), device="cuda")[..., pad:pad + D]
+    q.copy_(q0), k.copy_(k0)
+    added, lse, worst = definition(q.reshape(B, n_q, Hq, D), k, lens, n_q, 1, window, D ** -0.5, 30.0)
+    for b, n in enumerate(lens):
+        k[b, n:] = float("nan")
+    w = start(B, Hkv, cap, 8, pad=5)
+    was = w.clone()
+    st = run(q, k, lens, "f32", Hq, Hkv, D, n_q, torch.from_numpy(lse).cuda(), w, window=window, cap=30.0)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check(w, was, added, worst, lens, "D%d q%d" % (D, n_q))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("n_q", [1, 300])
 def test_rows_without_a_log_sum_exp_give_nothing(dt, n_q):
