@@ -1,13 +1,16 @@
 // kv_q8.cu — rows into and out of an 8-bit KV cache (the record: q8_block.cuh).
 //
-// append: a team (a warp where the new rows of a block are few, else a CTA) takes K or V of one
+// append: a team (a warp, four or sixteen, by what a block's new rows need) takes K or V of one
 // (sequence, touched block, KV head).  It reads the block's new rows once into registers, reduces
 // their largest magnitude, raises the stored scale's exponent where a block begun earlier needs it
 // (then brings the codes before the new rows to the new scale), and writes the codes.  Rows that
 // do not fit the registers are read again.
-// expand: a thread takes one 16-byte part of a row, four rows apart at once, so that a warp reads
-// and writes whole lines.
-// What bounds them: HBM on whole chunks; the launch on single tokens.
+// expand: a thread takes one 16-byte part of a row, so that a warp reads and writes whole lines (four
+// rows a thread 28.6 us, two 26.9, one 26.5 for 512 rows in and 2048 back, eight sequences).
+// What bounds them: HBM on whole chunks (head_dim 128, blocks of 64: 64 % of the copy rate, of which
+// the way back is two thirds); the launch on single tokens.
+#include <algorithm>
+
 #include "cache_kernels.h"
 #include "device_common.cuh"
 #include "q8_block.cuh"
@@ -73,9 +76,9 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float by) {
 }
 
 template <typename T, int D, int TEAM>
-__global__ void __launch_bounds__(kThreads) append_q8_kernel(const Q8StoreArgs a) {
-    constexpr int kOcts = D / 8, kTeams = kThreads / TEAM, kRow = 2 * D;
-    __shared__ float most[kThreads / 32];
+__global__ void __launch_bounds__(TEAM > kThreads ? TEAM : kThreads) append_q8_kernel(const Q8StoreArgs a) {
+    constexpr int kOcts = D / 8, kTeams = TEAM > kThreads ? 1 : kThreads / TEAM, kRow = 2 * D;
+    __shared__ float most[(TEAM > kThreads ? TEAM : kThreads) / 32];
     const int t = threadIdx.x % TEAM;
     const int64_t unit = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM;
     if (TEAM == 32 && unit >= a.units) return;  // (a warp by itself; a CTA has one unit)
@@ -197,55 +200,48 @@ __device__ __forceinline__ void put16(T *dst, const uint32_t (&w)[4], float s, b
     }
 }
 
-constexpr int kExpandThreads = 256, kExpandAhead = 4;
+constexpr int kExpandThreads = 256;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kExpandThreads) expand_q8_kernel(const Q8StoreArgs a) {
-    constexpr int kParts = D / 8, kRows = kExpandThreads / kParts, kRow = 2 * D;  // rows at once
-    const int p = threadIdx.x % kParts, r = threadIdx.x / kParts;
-    if (r >= kRows) return;
-    const int which = p >= kParts / 2;
-    uint4 w[kExpandAhead];
-    float s[kExpandAhead];
-    int64_t to[kExpandAhead];
-#pragma unroll
-    for (int i = 0; i < kExpandAhead; ++i) {
-        const int64_t x = ((int64_t)blockIdx.x * kExpandAhead + i) * kRows + r;  // a row of one head
-        to[i] = -1;
-        if (x >= a.units) continue;
-        const uint32_t bt = a.by_heads.div((uint32_t)x), hk = (uint32_t)x - bt * a.n_kv_heads;
-        const uint32_t b = a.by_n.div(bt), t = bt - b * a.n;
-        const int pos = a.pos[b];
-        if (pos < 0 || pos > a.capacity - a.n) {
-            if (p == 0 && t == 0 && hk == 0) report_status(a.status, kErrBounds);
-            continue;
-        }
-        const int j = pos + (int)t, n = j >> a.block_shift, row = j & ((1 << a.block_shift) - 1);
-        const unsigned char *rec = a.cache + (int64_t)b * a.cache_seq + (int64_t)n * a.cache_block + (int64_t)hk * a.cache_head;
-        w[i] = __ldg(reinterpret_cast<const uint4 *>(rec + (int64_t)row * kRow + q8_place<D>(16 * p, row)));
-        s[i] = __ldg(reinterpret_cast<const float *>(rec + ((int64_t)kRow << a.block_shift)) + which);
-        to[i] = (int64_t)bt * a.rs + (int64_t)hk * D + 16 * (p - which * (kParts / 2));
+    constexpr int kParts = D / 8, kRows = kExpandThreads / kParts, kRow = 2 * D;  // rows of a CTA
+    const int p = threadIdx.x % kParts, r = threadIdx.x / kParts, which = p >= kParts / 2;
+    const int64_t x = (int64_t)blockIdx.x * kRows + r;  // a row of one head
+    if (r >= kRows || x >= a.units) return;
+    const uint32_t bt = a.by_heads.div((uint32_t)x), hk = (uint32_t)x - bt * a.n_kv_heads;
+    const uint32_t b = a.by_n.div(bt), t = bt - b * a.n;
+    const int pos = a.pos[b];
+    if (pos < 0 || pos > a.capacity - a.n) {
+        if (p == 0 && t == 0 && hk == 0) report_status(a.status, kErrBounds);
+        return;
     }
-    T *out = static_cast<T *>(which ? a.v_out : a.k_out);
-#pragma unroll
-    for (int i = 0; i < kExpandAhead; ++i)
-        if (to[i] >= 0) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            put16(out + to[i], x, s[i], a.vec != 0);
-        }
+    const int j = pos + (int)t, n = j >> a.block_shift, row = j & ((1 << a.block_shift) - 1);
+    const unsigned char *rec = a.cache + (int64_t)b * a.cache_seq + (int64_t)n * a.cache_block + (int64_t)hk * a.cache_head;
+    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(rec + (int64_t)row * kRow + q8_place<D>(16 * p, row)));
+    const float s = __ldg(reinterpret_cast<const float *>(rec + ((int64_t)kRow << a.block_shift)) + which);
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    put16(static_cast<T *>(which ? a.v_out : a.k_out) + (int64_t)bt * a.rs + (int64_t)hk * D + 16 * (p - which * (kParts / 2)),
+          words, s, a.vec != 0);
 }
 
 template <typename T, int D>
 cudaError_t launch(const Q8StoreArgs &a, bool expand, cudaStream_t s) {
     if (expand) {
-        constexpr int per = kExpandThreads / (D / 8) * kExpandAhead;
+        constexpr int per = kExpandThreads / (D / 8);
         expand_q8_kernel<T, D><<<(unsigned)((a.units + per - 1) / per), kExpandThreads, 0, s>>>(a);
-    } else if ((int64_t)a.n * (D / 8) <= 64) {
-        // new rows of up to two octets a lane: a warp each
-        append_q8_kernel<T, D, 32><<<(unsigned)((a.units + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s>>>(a);
-    } else {
-        append_q8_kernel<T, D, kThreads><<<(unsigned)a.units, kThreads, 0, s>>>(a);
+        return cudaGetLastError();
     }
+    // A block's new rows fit a warp's registers, or those of a CTA, or are less than twice that and are
+    // read again (cheaper than a CTA of 512: fp32, head_dim 128, blocks of 64 47.9 us, so 49.8), or take
+    // 512 (head_dim 512: 28.2, read again 35.3).  A CTA on what a warp can hold: blocks of 16
+    // 33.4 us, by warps 26.9.  (512 rows in, 2048 back, eight sequences of eight heads)
+    const int64_t octs = (int64_t)std::min(a.n, 1 << a.block_shift) * (D / 8);
+    if (octs <= 32 * kHeld<T>)
+        append_q8_kernel<T, D, 32><<<(unsigned)((a.units + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s>>>(a);
+    else if (octs <= 2 * kThreads * kHeld<T>)
+        append_q8_kernel<T, D, kThreads><<<(unsigned)a.units, kThreads, 0, s>>>(a);
+    else
+        append_q8_kernel<T, D, 512><<<(unsigned)a.units, 512, 0, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T>
