@@ -221,12 +221,12 @@ decode_q4_kernel(const __grid_constant__ Q4DecodeArgs a) {
     const int G = a.n_heads / a.n_kv_heads, HB = (G + kHeads - 1) / kHeads;
     constexpr int TK = C::kTileKeys;
 
-    if (tid == 0) {
+    auto prepare = [&] {
         for (int i = 0; i < C::kWarps * C::kStages; ++i) mbar_init(&full[i], 1);
         fence_mbarrier_init();
         if (a.max_kv_len > 0) tma_prefetch_desc(&a.tm);  // (else there is none)
-    }
-    if (!stream_begin<TK, 1, C::kWarps, T>(a, HB, D, st)) return;
+    };
+    if (!stream_begin<TK, 1, C::kWarps, T>(a, HB, D, st, prepare)) return;
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
 
     // ---- this warp's copies -------------------------------------------------------------

@@ -131,11 +131,11 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.n_heads / a.n_kv_heads, HB = (G + kHeads - 1) / kHeads;
-    if (tid == 0) {
+    auto prepare = [&] {
         for (int i = 0; i < C::kWarps * C::kStages; ++i) mbar_init(&full[i], 1);
         fence_mbarrier_init();
-    }
-    if (!stream_begin<TK, C::kKeys, C::kWarps, T>(a, HB, D, st)) return;
+    };
+    if (!stream_begin<TK, C::kKeys, C::kWarps, T>(a, HB, D, st, prepare)) return;
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
 
     // ---- this warp's copies -------------------------------------------------------------

@@ -118,10 +118,10 @@ __device__ bool next_piece(const SplitDecodeArgs &a, Walk &w, int HB, Piece &p) 
 
 // The stream's length in tiles of TK keys and this CTA's share: per-thread sums over a slice of
 // the sequences, then a scan.  Sequences with nothing to stream get their zeros from CTA 0.  False
-// for a CTA without a share; else the first piece stands in st.pieces[0] (two barriers have
-// passed, the first of them behind what the threads wrote before the call).
-template <int TK, int Align, int kWarps, typename T>
-__device__ __forceinline__ bool stream_begin(const SplitDecodeArgs &a, int HB, int D, StreamState &st) {
+// for a CTA without a share; else the first piece stands in st.pieces[0].  Thread 0 calls `prepare`
+// while lengths are under way, a barrier before anyone goes on.
+template <int TK, int Align, int kWarps, typename T, typename Prepare>
+__device__ __forceinline__ bool stream_begin(const SplitDecodeArgs &a, int HB, int D, StreamState &st, Prepare prepare) {
     constexpr int kThreads = 32 * kWarps;
     static_assert(kWarps <= 4, "st.scan");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, HU = a.n_kv_heads * HB;
@@ -154,6 +154,7 @@ __device__ __forceinline__ bool stream_begin(const SplitDecodeArgs &a, int HB, i
         st.walk.pos = 0;
         st.walk.end = 0;
         st.walk.b = a.batch;
+        prepare();
         st.abort_flag = 0;
         st.joins[0].nseg = st.joins[1].nseg = st.joins[0].last = st.joins[1].last = 0;
     }
