@@ -121,6 +121,8 @@ _SIGNATURES = {
                                               _U64, _P, _P]),
     "lat_test_key_weights_timeout": (_I32, [_P, _I64, _I32, _P, _I64, _I64, _I64, _P, _I32, _P, _P,
                                             _I64, _I64, _I32, _I32, _I32, _I32, _U64, _P, _P]),
+    "lat_test_evict_rows_timeout": (_I32, [_I32, _P, _P, _I64, _I64, _I64, _I32, _P, _I32, _I32,
+                                           _I32, _I32, _U64, _P, _P]),
     "lat_test_capped_scores": (_I32, [_P, _I64, _F32, _F32, _P, _P]),
 }
 
@@ -552,6 +554,15 @@ def lat_test_key_weights_timeout(q, q_rs, n_q, k_cache, cache_rs, cache_head_str
         q, q_rs, n_q, k_cache, cache_rs, cache_head_stride, cache_seq_stride, kv_lens, max_kv_len,
         lse, weights, weights_head_stride, weights_seq_stride, batch, n_heads, n_kv_heads,
         head_dim, timeout_ns, status, _stream(stream)), "lat_test_key_weights_timeout")
+
+
+def lat_test_evict_rows_timeout(dt, k_cache, v_cache, cache_rs, cache_head_stride,
+                                cache_seq_stride, capacity, kept, n_keep, batch, n_kv_heads,
+                                head_dim, timeout_ns, status, stream=None):
+    _check(_calls().lat_test_evict_rows_timeout(
+        dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, kept,
+        n_keep, batch, n_kv_heads, head_dim, timeout_ns, status, _stream(stream)),
+        "lat_test_evict_rows_timeout")
 
 
 def lat_test_capped_scores(raw, n, scale, softcap, out, stream=None):

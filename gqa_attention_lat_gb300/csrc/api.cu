@@ -1222,16 +1222,22 @@ lat_status lat_kv_evict_choose(const float *weights, int64_t weights_head_stride
     return lat::launch_evict_choose(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
 }
 
-lat_status lat_kv_evict_rows(lat_dtype dt, void *k_cache, void *v_cache, int64_t cache_rs, int64_t cache_head_stride,
-                             int64_t cache_seq_stride, int capacity, const int32_t *kept, int n_keep, int batch,
-                             int n_kv_heads, int head_dim, int32_t *status, void *stream) {
+}  // extern "C"
+
+namespace {
+
+lat_status evict_rows_impl(lat_dtype dt, void *k_cache, void *v_cache, int64_t cache_rs, int64_t cache_head_stride,
+                           int64_t cache_seq_stride, int capacity, const int32_t *kept, int n_keep, int batch,
+                           int n_kv_heads, int head_dim, int32_t *status, void *stream, uint64_t timeout_ns,
+                           int skip_tell) {
     if (dt != LAT_F32 && dt != LAT_BF16) return LAT_ERR_INVALID_ARG;
     if (batch < 0 || capacity < 0 || n_keep < 1 || n_kv_heads <= 0) return LAT_ERR_INVALID_ARG;
     if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
     if (batch == 0) return LAT_OK;
     const int es = dt == LAT_BF16 ? 2 : 4;
     constexpr int64_t kMost = INT64_MAX / 4;  // elements whose bytes are still counted
-    if (cache_rs > kMost || cache_head_stride > kMost || cache_seq_stride > kMost || !k_cache || !v_cache || !kept || !aligned16(k_cache) || !aligned16(v_cache) ||
+    if (cache_rs > kMost || cache_head_stride > kMost || cache_seq_stride > kMost || !k_cache || !v_cache || !kept ||
+        !aligned16(k_cache) || !aligned16(v_cache) ||
         !q4_strides_ok(cache_rs * es, cache_head_stride * es, cache_seq_stride * es))
         return LAT_ERR_INVALID_ARG;
     if ((int64_t)batch * n_kv_heads > 0x7fffffffLL / 16) return LAT_ERR_UNSUPPORTED;
@@ -1249,9 +1255,29 @@ lat_status lat_kv_evict_rows(lat_dtype dt, void *k_cache, void *v_cache, int64_t
     a.n_keep = n_keep;
     a.batch = batch;
     a.n_kv_heads = n_kv_heads;
-    a.timeout_ns = kDefaultTimeoutNs;
+    a.timeout_ns = timeout_ns;
+    a.test_skip_tell = skip_tell;
     a.status = status;
     return lat::launch_evict_rows(a, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? LAT_OK : LAT_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+lat_status lat_kv_evict_rows(lat_dtype dt, void *k_cache, void *v_cache, int64_t cache_rs, int64_t cache_head_stride,
+                             int64_t cache_seq_stride, int capacity, const int32_t *kept, int n_keep, int batch,
+                             int n_kv_heads, int head_dim, int32_t *status, void *stream) {
+    return evict_rows_impl(dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, kept, n_keep,
+                           batch, n_kv_heads, head_dim, status, stream, kDefaultTimeoutNs, 0);
+}
+
+lat_status lat_test_evict_rows_timeout(lat_dtype dt, void *k_cache, void *v_cache, int64_t cache_rs,
+                                       int64_t cache_head_stride, int64_t cache_seq_stride, int capacity,
+                                       const int32_t *kept, int n_keep, int batch, int n_kv_heads, int head_dim,
+                                       uint64_t timeout_ns, int32_t *status, void *stream) {
+    return evict_rows_impl(dt, k_cache, v_cache, cache_rs, cache_head_stride, cache_seq_stride, capacity, kept, n_keep,
+                           batch, n_kv_heads, head_dim, status, stream, timeout_ns, 1);
 }
 
 }  // extern "C"

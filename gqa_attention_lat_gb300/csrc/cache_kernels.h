@@ -209,6 +209,7 @@ struct EvictRowsArgs {
     const int32_t *kept;                      // [batch, n_kv_heads, n_keep]
     int n_keep, batch, n_kv_heads;
     uint64_t timeout_ns;
+    int test_skip_tell;                       // test hook: the first CTA of a cluster does not say that its first rows are there
     int32_t *status;
 };
 // batch * n_kv_heads * 16 < 2^31

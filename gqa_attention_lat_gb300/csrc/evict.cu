@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
     };
     auto tell = [&](int s) {  // (behind a barrier of this CTA's threads)
         if constexpr (P > 1)
-            if (tid < P && s < n_stretches) mbar_arrive_cluster(cluster_addr(&here[s % kRowBars], (uint32_t)tid));
+            if (tid < P && s < n_stretches && !(a.test_skip_tell && rank + s == 0)) mbar_arrive_cluster(cluster_addr(&here[s % kRowBars], (uint32_t)tid));
     };
     if (tid == 0) {
         for (int i = 0; i < kRowBars; ++i) mbar_init(&here[i], P);

@@ -24,6 +24,13 @@
  * K/V stage of every CTA is never filled): window 0, scale 1/8, no cap, no lse.  Arguments,
  * layout and workspace rules are theirs.
  *
+ * lat_test_decode_q8_timeout does to lat_attn_decode_q8 what the 4-bit one does (dt its type; every
+ * warp's first copy never comes; window 0, scale 1/8, no cap, no lse), lat_test_key_weights_timeout
+ * to the LAT_BF16 form of lat_attn_key_weights (a CTA's first copy that streams never comes; causal,
+ * no window, scale 1/8, no cap), and lat_test_evict_rows_timeout to lat_kv_evict_rows: where
+ * several CTAs share a head's rows, the first never says that its first rows are there, so all
+ * waits for them run out and nothing is moved.  Arguments and rules are theirs.
+ *
  * lat_test_capped_scores evaluates the score cap of the bf16 kernels (the Gemma 2 softcap
  * of the larql "BLAS-Fused Attention" step 2, folded into the log2 domain) on n raw dot
  * products: out[i] = softcap * log2(e) * tanh(raw[i] * scale / softcap), formed exactly as
@@ -84,6 +91,12 @@ lat_status lat_test_key_weights_timeout(const void *q, int64_t q_rs, int n_q,
                                         int64_t weights_seq_stride, int batch, int n_heads,
                                         int n_kv_heads, int head_dim, uint64_t timeout_ns,
                                         int32_t *status, void *stream);
+lat_status lat_test_evict_rows_timeout(lat_dtype dt, void *k_cache, void *v_cache,
+                                       int64_t cache_rs, int64_t cache_head_stride,
+                                       int64_t cache_seq_stride, int capacity,
+                                       const int32_t *kept, int n_keep, int batch,
+                                       int n_kv_heads, int head_dim, uint64_t timeout_ns,
+                                       int32_t *status, void *stream);
 lat_status lat_test_capped_scores(const float *raw, int64_t n, float scale, float softcap,
                                   float *out, void *stream);
 

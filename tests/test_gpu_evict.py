@@ -381,3 +381,27 @@ def test_choice_and_rows_in_a_graph_and_on_two_streams():
     assert int(st.item()) == 0
     for x, y, z in got + [(a, b, (kept, None, new))]:
         assert torch.equal(x, rk) and torch.equal(y, rv) and torch.equal(z[0], ref[0]) and torch.equal(z[2], ref[2])
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f32", 512)])
+def test_the_waits_of_the_rows_run_out(dt, D):
+    """A hook keeps one CTA of each cluster silent: LAT_ERR_TIMEOUT, and the next call is right."""
+    B, H, cap, n = 2, 2, 3000, 2000
+    k, v = caches(B, cap, H, D, dt, 3)
+    kept = torch.arange(0, 2 * n, 2, dtype=torch.int32)[:n].clamp(max=cap - 1)
+    kept = torch.unique(kept)
+    kept = torch.cat([kept, torch.full((n - len(kept),), -1, dtype=torch.int32)]).expand(B, H, n).contiguous().cuda()
+    was = [k.clone(), v.clone()]
+    st = status_tensor()
+    binding.lat_test_evict_rows_timeout(DT[dt], k, v, k.stride(1), k.stride(2), k.stride(0), cap, kept, n, B, H, D,
+                                        20_000_000, st)
+    torch.cuda.synchronize()  # the kernel ends by itself: no fault, no hang
+    assert int(st.item()) == binding.LAT_ERR_TIMEOUT
+    assert torch.equal(k, was[0]) and torch.equal(v, was[1])
+    st = move(k, v, kept, dt, D)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    m = int((kept[0, 0] >= 0).sum())
+    at = kept[0, 0, :m].long()
+    for x, y in zip((k, v), was):
+        assert torch.equal(x[:, :m], y[:, at]) and torch.equal(x[:, m:], y[:, m:])
