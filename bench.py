@@ -876,7 +876,7 @@ def kernel_info(wl, step, peaks):
         flops, alg_bytes, _ = prefill_work(wl)
         return (flops, alg_bytes, flops / 1e12, "TFLOP/s", "prefill_tc_kernel<%d>" % wl.D,
                 prefill_bound(wl, peaks), "prefill_tc_%s.md" % wl.name,
-                ["prefill_tc.cu", "device_common.cuh", "kernels.h"])
+                ["prefill_tc.cu", "tc_desc.cuh", "device_common.cuh", "kernels.h"])
     if wl.kind == "producer":
         alg_bytes = producer_bytes(wl)
         return (0.0, alg_bytes, alg_bytes / 1e9, "GB/s", "qkv_producer_fast<%d>" % wl.D, "hbm",
