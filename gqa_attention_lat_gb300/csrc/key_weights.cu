@@ -23,9 +23,9 @@
 //  * Roles: epilogue warps in quartets (a warp can read the quarter of tensor memory's lanes that
 //    its number says), a warp that issues the copies, one that issues the MMAs, two that prepare
 //    the columns' log-sum-exps and ranges of keys.  S has four buffers of 128 columns in tensor
-//    memory; every quartet takes every fourth tile of S (two quartets where a tile is small, every
-//    other) whole, so that its waits are few.  Where a key tile has several tiles of S, the quartets'
-//    sums meet in shared memory at its end.  Where a range cuts a tile, pairs are masked one by one.
+//    memory; the quartets take tiles of S in turn, each whole, so that its waits are few.  Where a
+//    key tile has several tiles of S, the quartets' sums meet in shared memory at its end.  Where a range
+//    cuts a tile, pairs are masked one by one.
 //  * What a role does for every tile is kept short (a wait that need not wait costs a thread 100
 //    to 200 cycles): walks go by runs of tiles, tables come with the tile of S they belong to, and
 //    a key's sum goes to memory as a reduction that nothing waits for.
@@ -58,12 +58,11 @@ namespace {
 
 constexpr int kKeysTile = 128;
 constexpr int kMaxCols = 256;                     // columns of a tile
-constexpr int kNarrowCols = 64;                   // queries held, up to so many: two quartets are enough
-constexpr int kMaxQuartets = 4;
+constexpr int kQuartets = 2, kEpilogue = 4 * kQuartets;  // of epilogue warps; those
 constexpr int kMoreWarps = 4;                     // behind them: copies, MMAs, two of tables
-constexpr int kMaxThreads = 128 * kMaxQuartets + 32 * kMoreWarps;
+constexpr int kThreads = 32 * (kEpilogue + kMoreWarps);
 constexpr int kTables = 4;
-constexpr int kPlaces = 8;                        // key tiles whose sums can be under way at once
+constexpr int kPlaces = 4;                        // key tiles whose sums can be under way at once
 constexpr int kSBufs = 4, kSCols = 128;           // tiles of S in tensor memory
 constexpr uint32_t kTmemCols = kSBufs * kSCols;
 constexpr int kMaxStages = 8, kMaxHeld = 8;
@@ -81,7 +80,7 @@ struct KwCfg {
     static constexpr int kManyHeldBytes = 32768;
     static constexpr int kTiles = 196608;
     static constexpr int kTableBytes = kTables * (3 * kMaxCols + 4) * 4;
-    static constexpr int kPassed = kPlaces * kMaxQuartets * kKeysTile * 4;          // [key tile % kPlaces][quartet][key] sums
+    static constexpr int kPassed = kPlaces * kKeysTile * 4;  // [key tile % kPlaces][key] sums
     static constexpr int kBarBytes = 1024;
     static constexpr int kSmem = kTiles + kTableBytes + kPassed + kBarBytes;
     static_assert(kSmem <= 232448, "shared memory budget");
@@ -235,12 +234,12 @@ __device__ __forceinline__ void add_columns(uint64_t (&sum)[2], const uint32_t (
 }
 
 template <int D, bool CAP>
-__global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_constant__ KeyWeightsArgs a) {
     using C = KwCfg<D>;
     extern __shared__ __align__(1024) unsigned char smem[];      // (an aligned-up pointer would load as generic)
     Table *tables = reinterpret_cast<Table *>(smem + C::kTiles);  // [kTables]
-    float *passed = reinterpret_cast<float *>(tables + kTables);  // [key tile % kPlaces][quartet][key]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(passed + kPlaces * kMaxQuartets * kKeysTile);
+    float *passed = reinterpret_cast<float *>(tables + kTables);  // [key tile % kPlaces][key]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(passed + kPlaces * kKeysTile);
     uint64_t *ring_full = bars, *ring_empty = bars + 8;          // [n_stages]
     uint64_t *held_full = bars + 16, *held_empty = bars + 24;    // [n_held]
     uint64_t *s_full = bars + 32, *s_empty = bars + 36;          // [4]
@@ -252,20 +251,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     int64_t *start = reinterpret_cast<int64_t *>(bar_done + 2);  // share: base, b
     int *scan = reinterpret_cast<int *>(bar_done + 4);           // a warp each
     static_assert(sizeof(Table) * kTables == C::kTableBytes && kTables >= kSBufs &&
-                      (44 + 2 * kTables + 4 * kPlaces) * 8 + kMaxThreads / 32 * 4 <= C::kBarBytes,
+                      (44 + 2 * kTables + 4 * kPlaces) * 8 + kThreads / 32 * 4 <= C::kBarBytes,
                   "shared memory layout");
     if (smem_u32(smem) & 1023) {  // (swizzled operands need it; it is where dynamic shared memory begins)
         if (threadIdx.x == 0) report_status(a.status, kErrCuda);
         return;
     }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n_threads = blockDim.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // what takes a round trip first: the first of this thread's lengths, the tensor maps (there are none
     // for caches that hold nothing)
-    const int per_thread = a.batch <= n_threads ? 1 : (a.batch + n_threads - 1) / n_threads;
+    const int per_thread = (a.batch + kThreads - 1) / kThreads;
     const int b_lo = min(a.batch, tid * per_thread), b_hi = min(a.batch, b_lo + per_thread);
     const int len_lo = b_lo < b_hi ? a.kv_lens[b_lo] : 0;
     if (tid == 0 && a.max_kv_len > 0) tma_prefetch_desc(&a.tm_q), tma_prefetch_desc(&a.tm_k);
-    const int n_epilogue = n_threads / 32 - kMoreWarps, quartets = n_epilogue / 4;
     const int halves = a.n_cols > kSCols ? 2 : 1;                // tiles of S of a column tile (queries held)
     // bytes of a chunk of the tile of queries and of keys; how many operands there is room to hold,
     // and stages behind them
@@ -291,13 +289,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         init(s_full, kSBufs, a.keys_held ? 2 : 1);  // keys held: full when its MMAs are done and its table is there
         init(s_empty, kSBufs, 4 * halves);
         init(tab_full, kTables, 1);
-        init(tab_empty, kTables, n_epilogue);
-        init(x_full, 4 * kPlaces, a.keys_held ? 3 : 1);
+        init(tab_empty, kTables, kEpilogue);
+        init(x_full, 4 * kPlaces, 1);
         init(bar_done, 1, 1);
         if (lane == 0) *abort_flag = 0, start[0] = 0, start[1] = a.batch;
         fence_mbarrier_init();
     }
-    if (warp == n_epilogue + 1) {
+    if (warp == kEpilogue + 1) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
@@ -322,7 +320,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int of_warp = lane < n_threads / 32 ? scan[lane] : 0;
+    const int of_warp = lane < kThreads / 32 ? scan[lane] : 0;
     const int total = __reduce_add_sync(0xffffffffu, of_warp);
     const int before = incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
     int64_t r0 = 0, r1 = a.slots;
@@ -346,7 +344,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     Walker walk{a, r0, r1, start[0], (int)start[1], -1};
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag, deadline); };
 
-    if (warp == n_epilogue) {
+    if (warp == kEpilogue) {
         if (lane == 0) {
             unsigned g = 0, h = 0, s = 0, turn = 0;  // stages and held operands issued; place in the ring, times round it
             bool ok = true;
@@ -392,7 +390,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             }
         }
         __syncwarp();
-    } else if (warp == n_epilogue + 1) {
+    } else if (warp == kEpilogue + 1) {
         if (lane == 0) {
             // N of a column tile's first and second tile of S
             const uint32_t idesc = instr_desc(kKeysTile, a.n_cols, false);
@@ -436,12 +434,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             mbar_wait_bounded(bar_done, 0, &no_abort, globaltimer_ns() + 100000000ull);
         }
         __syncwarp();
-    } else if (warp >= n_epilogue + 2) {
+    } else if (warp >= kEpilogue + 2) {
         // ---- tables.  Queries held: one a run, the warps in turn.  Keys held: one a tile of columns,
         // the warps in turn, in the place of its tile of S; the next one's log-sum-exps are on their way
         // while one is filled.  Lane i has columns i, i + 32, ...: rows and heads that do not change.
         constexpr int kMine = kMaxCols / 32;
-        const int odd = warp - n_epilogue - 2;
+        const int odd = warp - kEpilogue - 2;
         int col_row[kMine], col_at[kMine];
 #pragma unroll
         for (int e = 0; e < kMine; ++e) {
@@ -543,40 +541,66 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
             const bool mask = tab.min_hi < last || tab.max_lo >= first;
             const uint32_t src = lanes + buf * kSCols;
             uint64_t part[2] = {0, 0};
-            auto add = [&](const uint32_t (&r)[16], int n) {
-                if (mask || n + 16 > n1) add_columns<CAP, true>(part, r, tab, off + n, j, a);
-                else add_columns<CAP, false>(part, r, tab, off + n, j, a);
-            };
             auto let_go = [&] {  // S may be written again (with keys held, the table too)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_empty[bar]);
             };
-            // (asking for the next sixteen columns ahead takes registers that the sums use better: 64 rows
-            // over four caches 55.7 us, so 49.8)
-            for (int n = 0; n < n1; n += 16) {
-                uint32_t r[16];
-                tmem_ld16(src + n, r);
-                tc_wait_ld();
-                if (!CAP && n + 16 >= n1 && !a.keys_held) let_go();
-                add(r, n);
+            // 64 columns at a time where none is masked, so that loads, FMAs and exponentials of many overlap
+            // (sixteen at a time by twice the warps with half the registers: 64 rows over four caches 49.3 us,
+            // so 44.2; a prompt at head_dim 128 159, so 123)
+            if (n1 == kSCols && !mask) {
+                uint32_t r[4][16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld16(src + 64 * h + 16 * q, r[q]);
+                    tc_wait_ld();
+                    if (h == 1 && !a.keys_held) let_go();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) add_columns<CAP, false>(part, r[q], tab, off + 64 * h + 16 * q, j, a);
+                }
+            } else {
+                int n = 0;
+                if (!mask && n1 >= 64) {
+                    uint32_t r[4][16];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld16(src + 16 * q, r[q]);
+                    tc_wait_ld();
+                    if (n1 == 64 && !a.keys_held) let_go();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) add_columns<CAP, false>(part, r[q], tab, off + 16 * q, j, a);
+                    n = 64;
+                }
+                for (; n < n1; n += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(src + n, r);
+                    tc_wait_ld();
+                    if (n + 16 >= n1 && !a.keys_held) let_go();
+                    if (mask || n + 16 > n1) add_columns<CAP, true>(part, r, tab, off + n, j, a);
+                    else add_columns<CAP, false>(part, r, tab, off + n, j, a);
+                }
             }
-            if (CAP || a.keys_held) let_go();
+            if (a.keys_held) let_go();
             const float2 p0 = halves_of(part[0]), p1 = halves_of(part[1]);
             total = (p0.x + p0.y) + (p1.x + p1.y);
             return true;
         };
-        // A quartet's sum of key tile number `item` for the one that has its last tile of S, which adds
-        // them up.  While that one is still at it, its tiles of S let go, the others get through seven
-        // more tiles of S at most (its own next one, done or not, and up to the one after that): the
-        // places that they write to are not this key tile's.
+        // The first quartet's sum of key tile number `item`, for the second to add its own.  While that one
+        // is still at it, its tiles of S let go, the first gets through two more key tiles at most: the
+        // places that it writes to are not this one's.
         auto pass = [&](unsigned item, float sum) {
             const unsigned slot = item % kPlaces;
-            passed[(slot * kMaxQuartets + quartet) * kKeysTile + row] = sum;
+            passed[slot * kKeysTile + row] = sum;
             __syncwarp();
             if (lane == 0) mbar_arrive(&x_full[slot * 4 + quarter]);
         };
-        auto passed_by = [&](unsigned item, int q) { return passed[(item % kPlaces * kMaxQuartets + q) * kKeysTile + row]; };
+        auto passed_by = [&](unsigned item, float &sum) {
+            const unsigned slot = item % kPlaces;
+            if (!wait_warp(&x_full[slot * 4 + quarter], (item / kPlaces) & 1)) return false;
+            sum += passed[slot * kKeysTile + row];
+            return true;
+        };
         // (this thread alone has the key: no order of additions comes into it)
         auto give = [&](const Run &r, int t, float sum) {
             const int j = t * kKeysTile + row;
@@ -585,13 +609,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
         unsigned step = 0, runs = 0;  // tiles of S, runs before this one
         bool ok = true;
         for (Run r; ok && walk.next(r); ++runs) {
-            const unsigned skip = (unsigned)(quartet - (int)step) & (quartets - 1);  // to this quartet's first tile of S
-            if (a.keys_held) {  // one key tile
+            if (a.keys_held) {  // one key tile; the quartets' tiles of S are the columns' halves
                 const int first = r.t * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
-                const unsigned n = 2 * (unsigned)r.n;  // tiles of S
                 float sum = 0.f, lost = 0.f, part;
-                for (unsigned i = skip; i < n; i += quartets) {
-                    if (!(ok = take(step + i, tables[(step + i) % kSBufs & ~1u], (i & 1) * kSCols, first, last, part))) break;
+                for (int i = 0; i < r.n; ++i, step += 2) {
+                    if (!(ok = take(step + quartet, tables[step % kSBufs], quartet * kSCols, first, last, part))) break;
                     // sum + lost += part (a sum with its rounding error kept)
                     const float more = part + lost, now = sum + more;
                     lost = more - (now - sum);
@@ -599,41 +621,23 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
                 }
                 if (!ok) break;
                 sum += lost;
-                const unsigned end = step + n - 1;  // whose quartet adds up
-                if (skip < n && (end & 3) != (unsigned)quartet) pass(runs, sum);
-                if ((end & 3) == (unsigned)quartet) {
-                    const unsigned others = min(n - 1, 3u), slot = runs % kPlaces;
-                    if (others > 0) {
-                        __syncwarp();
-                        if (lane == 0 && others < 3) mbar_arrive_n(&x_full[slot * 4 + quarter], 3 - others);  // for those without
-                        if (!(ok = wait_warp(&x_full[slot * 4 + quarter], (runs / kPlaces) & 1))) break;
-                        for (unsigned k = others; k > 0; --k) sum += passed_by(runs, (int)((end - k) & 3));
-                    } else if (lane == 0) {
-                        mbar_arrive_n(&x_full[slot * 4 + quarter], 3);
-                    }
-                    give(r, r.t, sum);
-                }
-                step += n;
+                if (quartet == 0) pass(runs, sum);
+                else if (!(ok = passed_by(runs, sum))) break;
+                else give(r, r.t, sum);
                 continue;
             }
             const Table &tab = tables[runs % kTables];
             if (!(ok = wait_warp(&tab_full[runs % kTables], (runs / kTables) & 1))) break;
             const int n = r.n * halves;  // tiles of S
-            for (int i = (int)skip; i < n; i += quartets) {
-                const int f = halves == 2 ? i & 1 : 0, t = r.t + (halves == 2 ? i >> 1 : i);
+            for (int i = (int)((quartet + step) & 1); i < n; i += 2) {
+                const int f = halves == 2 ? quartet : 0, t = r.t + (halves == 2 ? i >> 1 : i);
                 const int first = t * kKeysTile, last = min(first + kKeysTile, r.len) - 1;
-                const unsigned item = (step + i) >> 1;  // (two halves: step and the quartet are even with the first)
+                const unsigned item = (step + i) >> 1;  // (two halves: step is even)
                 float sum;
                 if (!(ok = take(step + i, tab, f * kSCols, first, last, sum))) break;
-                if (halves == 2) {
-                    if (f == 0) {
-                        pass(item, sum);
-                        continue;
-                    }
-                    if (!(ok = wait_warp(&x_full[item % kPlaces * 4 + quarter], (item / kPlaces) & 1))) break;
-                    sum += passed_by(item, quartet - 1);
-                }
-                give(r, t, sum);
+                if (halves == 2 && f == 0) pass(item, sum);
+                else if (halves == 2 && !(ok = passed_by(item, sum))) break;
+                else give(r, t, sum);
             }
             step += n;
             __syncwarp();
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) key_weights_kernel(const __gri
     }
     __syncthreads();
     if (tid == 0 && *abort_flag) report_status(a.status, kErrTimeout);
-    if (warp == n_epilogue + 1) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kEpilogue + 1) tmem_dealloc(tmem, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------------- fp32
@@ -908,8 +912,7 @@ cudaError_t launch_tc(const KeyWeightsArgs &a, int grid, cudaStream_t s) {
     static SharedLimit limit;
     const cudaError_t e = limit(key_weights_kernel<D, CAP>, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int threads = 128 * (!a.keys_held && a.n_cols <= kNarrowCols ? 2 : kMaxQuartets) + 32 * kMoreWarps;
-    key_weights_kernel<D, CAP><<<grid, threads, C::kSmem, s>>>(a);
+    key_weights_kernel<D, CAP><<<grid, kThreads, C::kSmem, s>>>(a);
     return cudaGetLastError();
 }
 template <int D>
