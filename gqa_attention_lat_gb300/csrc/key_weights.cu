@@ -37,7 +37,9 @@
 // 128 N D 2 flops against 128 N of them.
 //
 // fp32 (key_weights_f32_kernel): fp32 products by FMA, 64 keys x 32 or 64 columns a step, a thread 4
-// x 4 or 8 of them; the next 32 channels come while 32 are used.  Bound by its FMAs.  Up to eight
+// x 4 or 8 of them; the next 32 channels come while 32 are used.  Bound by its FMAs, or by their
+// chain where keys are few: then a cluster shares the columns (one sequence of 200 keys and rows, 12
+// heads over one: 231 -> 30 us in eight CTAs).  Up to eight
 // columns (a decode step) go to key_weights_few_kernel, whose keys do not pass through shared
 // memory (2 x 40000 keys, 24 heads over 8, head_dim 128: 75.7 -> 47.6 us, 3.5 TB/s; 32 caches of up
 // to 4096, 12 heads over 4, head_dim 64: 35.8 -> 26.5).  It is bound by what a key costs beside its
@@ -652,10 +654,18 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
 // ---------------------------------------------------------------------------------- fp32
 constexpr int kF32Keys = 64, kF32Depth = 32, kF32Threads = 128;
 
-// One CTA: 64 keys of one (sequence, KV head) over its columns, COLS at once.  Thread (x, y) takes
+__device__ __forceinline__ float load_shared_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A cluster of 2^log2 CTAs (SHARED, else one): 64 keys of one (sequence, KV head) over its columns, COLS at once, a CTA
+// its share of them; the first adds the others' sums to its own, in order.  Thread (x, y) takes
 // keys 4 x .. 4 x + 3 and columns y, y + 8, ...
-template <int COLS, bool CAP>
-__global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyWeightsArgs a) {
+template <int COLS, bool CAP, bool SHARED>
+__global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyWeightsArgs a, int log2) {
+    const int parts_log2 = SHARED ? log2 : 0, parts = 1 << parts_log2;
     constexpr int kPer = COLS / 8, kVecs = kF32Depth / 4;                   // a thread's columns; vectors of a row's 32 channels
     constexpr int kMyK = kF32Keys * kVecs / kF32Threads;                    // a thread's vectors of keys and of queries
     constexpr int kMyQ = COLS * kVecs / kF32Threads;
@@ -665,8 +675,9 @@ __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyW
     __shared__ int64_t q_at[COLS];                                          // where a column's query begins; -1: no column
     const int tid = threadIdx.x, x = tid / 8, y = tid % 8;
     const int b = blockIdx.y / a.n_kv_heads, hk = blockIdx.y % a.n_kv_heads, G = a.n_heads / a.n_kv_heads, D = a.head_dim;
-    const int raw = a.kv_lens[b], first = (int)blockIdx.x * kF32Keys;
-    if (raw < 0 || raw > a.max_kv_len) {
+    const int rank = (int)blockIdx.x & (parts - 1);
+    const int raw = a.kv_lens[b], first = (int)(blockIdx.x >> parts_log2) * kF32Keys;
+    if (raw < 0 || raw > a.max_kv_len) {  // (the whole cluster alike, here and below)
         if (blockIdx.x == 0 && hk == 0 && tid == 0) report_status(a.status, kErrBounds);
         return;
     }
@@ -699,8 +710,13 @@ __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyW
         }
     };
     float sum[4] = {0.f, 0.f, 0.f, 0.f}, lost[4] = {0.f, 0.f, 0.f, 0.f};
-    const int64_t c_end = (i1 + 1) * G;
-    for (int64_t c0 = i0 * G; c0 < c_end; c0 += COLS) {
+    int64_t c_begin = i0 * G, c_end = (i1 + 1) * G;
+    if (SHARED) {  // this CTA's columns, whole steps of them but the last
+        const int64_t steps = (c_end - c_begin + COLS - 1) / COLS;
+        if (rank + 1 < parts) c_end = c_begin + (steps * (rank + 1) >> parts_log2) * COLS;
+        c_begin += (steps * rank >> parts_log2) * COLS;
+    }
+    for (int64_t c0 = c_begin; c0 < c_end; c0 += COLS) {
         __syncthreads();  // the table is free
         for (int c = tid; c < COLS; c += kF32Threads) {
             lse2[c] = INFINITY, hi[c] = -1, lo[c] = -1, q_at[c] = -1;
@@ -766,13 +782,30 @@ __global__ void __launch_bounds__(kF32Threads) key_weights_f32_kernel(const KeyW
             sum[k] = now;
         }
     }
+    float v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        float v = sum[k] + lost[k];
+        v[k] = sum[k] + lost[k];
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int j = first + 4 * x + k;
-        if (y == 0 && j <= last) a.weights[(int64_t)b * a.w_seq + (int64_t)hk * a.w_head + j] += v;
+        for (int o = 1; o < 8; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+    __shared__ __align__(16) float mine[kF32Keys];
+    if constexpr (SHARED) {
+        if (rank > 0 && y == 0) *reinterpret_cast<float4 *>(mine + 4 * x) = make_float4(v[0], v[1], v[2], v[3]);
+        cluster_sync_all();
+        if (rank == 0 && y == 0)
+            for (int p = 1; p < parts; ++p)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] += load_shared_cluster(cluster_addr(mine + 4 * x + k, (uint32_t)p));
+        cluster_sync_all();  // nobody's shared memory goes while it is read
+    }
+    if (rank == 0 && y == 0) {
+        float *w = a.weights + (int64_t)b * a.w_seq + (int64_t)hk * a.w_head + first + 4 * x, was[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) was[k] = first + 4 * x + k <= last ? w[k] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (first + 4 * x + k <= last) w[k] = was[k] + v[k];
     }
 }
 
@@ -969,11 +1002,30 @@ cudaError_t launch_key_weights(const KeyWeightsArgs &a, int grid, cudaStream_t s
 
 cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, int num_sms, cudaStream_t s) {
     // (one block of nothing still sees the lengths)
-    const dim3 grid((unsigned)((std::max<int64_t>(a.max_kv_len, 1) + kF32Keys - 1) / kF32Keys), (unsigned)(a.batch * a.n_kv_heads));
+    dim3 grid((unsigned)((std::max<int64_t>(a.max_kv_len, 1) + kF32Keys - 1) / kF32Keys), (unsigned)(a.batch * a.n_kv_heads));
     const bool cap = a.cap_log2 > 0.f;
     const int64_t cols = (int64_t)a.n_q * (a.n_heads / a.n_kv_heads);
-    // no more columns at once than there are
-    auto go = [&](auto kernel) { kernel<<<grid, kF32Threads, 0, s>>>(a); };
+    // no more columns at once than there are; CTAs share them while the SMs have room for four each
+    auto go = [&](auto kernel, auto shared, int columns) {
+        int log2 = 0;
+        while (log2 < 3 && ((int64_t)grid.x * grid.y << (log2 + 1)) <= 4 * (int64_t)num_sms && ((int64_t)columns << log2) < cols) ++log2;
+        if (log2 == 0) {
+            kernel<<<grid, kF32Threads, 0, s>>>(a, 0);
+            return cudaGetLastError();
+        }
+        grid.x <<= log2;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1u << log2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kF32Threads);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, shared, a, log2);
+    };
     if (cols <= 8) {
         // longer stretches a CTA while there are eight CTAs an SM all the same (32 caches of 4096, head_dim
         // 128: 34 us; down to two CTAs an SM 42, sixteen 42)
@@ -988,9 +1040,12 @@ cudaError_t launch_key_weights_f32(const KeyWeightsArgs &a, int num_sms, cudaStr
         else if (cols <= 4) cap ? few(key_weights_few_kernel<4, 4, true>, 4) : few(key_weights_few_kernel<4, 4, false>, 4);
         else if (width == 2) cap ? few(key_weights_few_kernel<8, 2, true>, 8) : few(key_weights_few_kernel<8, 2, false>, 8);
         else cap ? few(key_weights_few_kernel<8, 4, true>, 8) : few(key_weights_few_kernel<8, 4, false>, 8);
-    } else if (cols <= 32) cap ? go(key_weights_f32_kernel<32, true>) : go(key_weights_f32_kernel<32, false>);
-    else cap ? go(key_weights_f32_kernel<64, true>) : go(key_weights_f32_kernel<64, false>);
-    return cudaGetLastError();
+        return cudaGetLastError();
+    }
+    const cudaError_t e = cols <= 32 ? cap ? go(key_weights_f32_kernel<32, true, false>, key_weights_f32_kernel<32, true, true>, 32) : go(key_weights_f32_kernel<32, false, false>, key_weights_f32_kernel<32, false, true>, 32)
+                          : cap      ? go(key_weights_f32_kernel<64, true, false>, key_weights_f32_kernel<64, true, true>, 64)
+                                     : go(key_weights_f32_kernel<64, false, false>, key_weights_f32_kernel<64, false, true>, 64);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace lat

@@ -207,6 +207,26 @@ def test_32_bit_rows_at_any_stride_and_address(D, Hq, Hkv, n_q, odd):
     check(w, was, added, worst, lens, "D%d q%d" % (D, n_q))
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,D,cap,n_q,window", [(1, 12, 1, 64, 200, 200, 0), (1, 12, 1, 80, 200, 3, 0),
+                                                       (3, 10, 2, 128, 150, 90, 0), (1, 3, 3, 256, 513, 333, 40),
+                                                       (2, 9, 1, 512, 70, 70, 0), (2, 6, 2, 64, 1000, 11, 0)])
+def test_32_bit_columns_shared_by_ctas(B, Hq, Hkv, D, cap, n_q, window):
+    """Few keys and many columns: 2, 4 or 8 CTAs share a key's, some of them without any."""
+    lens = [cap, 1, cap // 2][:B]
+    q, k = inputs(B, Hq, Hkv, D, cap, n_q, "f32", 3 + D)
+    added, lse, worst = definition(q.reshape(B, n_q, Hq, D), k, lens, n_q, 1, window, D ** -0.5, 0.0)
+    for b, n in enumerate(lens):
+        k[b, n:] = float("nan")
+    w = start(B, Hkv, cap, 9, pad=1)
+    was, again = w.clone(), w.clone()
+    lse = torch.from_numpy(lse).cuda()
+    st = run(q, k, lens, "f32", Hq, Hkv, D, n_q, lse, w, window=window)
+    run(q, k, lens, "f32", Hq, Hkv, D, n_q, lse, again, window=window, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.equal(w, again)
+    check(w, was, added, worst, lens, "D%d q%d" % (D, n_q))
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("n_q", [1, 300])
 def test_rows_without_a_log_sum_exp_give_nothing(dt, n_q):
