@@ -19,9 +19,12 @@
 //    factor.  V's is a power of two and goes into the exponent of the weights:
 //    w_j = 2^(x_j + e_n - r), r a running reference of x + e of its own, so that blocks of very
 //    different size keep their weights in fp16's range; the sum of the softmax has its own
-//    weights 2^(x_j - m), in fp32.  A weight is one fp16 term, 2^-12 of it (LAT_F32: two); the
-//    references lie within 2^8 of the maxima and weights are taken 2^7 higher, so what falls under
-//    fp16's least is 2^-31 of the largest.
+//    weights 2^(x_j - m), in fp32.  A weight is two fp16 terms, 2^-23 of it; the references lie
+//    within 2^8 of the maxima and weights are taken 2^7 higher, so what falls under fp16's least is
+//    2^-32 of the largest.  (One term, 2^-12 of a weight, moves one bf16 output in ten to the next
+//    number: 8e-4 of the output, beside the 1.6e-3 of its rounding.  The second costs no time over long
+//    caches, 8 x 131072 keys 305.4 us so 302.2, and 1 to 2 % on short ones: 32 ragged sequences of up
+//    to 4096 keys 31.5 us, so 31.8.)
 //  * A query is brought to [2^8, 2^9) by a power of two of its own and taken as one fp16 number
 //    (a bf16 channel above 2^-22 of the largest is exact) or, LAT_F32, two (22 bits and signs).
 //  * LAT_F32: the scores' sums of 64 channels and the outputs' of 16 keys are chains of their own,
@@ -51,7 +54,8 @@ template <int D, bool F32>
 struct Q8Cfg {
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kTerms = F32 ? 2 : 1;               // fp16 terms of a weight and of q
+    static constexpr int kTerms = F32 ? 2 : 1;               // fp16 terms of q
+    static constexpr int kWTerms = 2;                        // of a weight
     static constexpr int kRow = 2 * D;
     static constexpr int kSub = D <= 80 ? 4 : D == 512 ? 1 : 2;  // 16-key MMA tiles a warp takes at once
     static constexpr int kKeys = 16 * kSub;
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(Q8Cfg<D, F32>::kThreads, Q8Cfg<D, F32>::kMinBl
 decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
     using C = Q8Cfg<D, F32>;
     using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-    constexpr int kTerms = C::kTerms, TK = C::kTileKeys;
+    constexpr int kTerms = C::kTerms, kWTerms = C::kWTerms, TK = C::kTileKeys;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *ring = smem;                                              // [warp][stage]
     unsigned char *sQ = ring + C::kWarps * C::kStages * C::kStageBytes;      // raw queries, then fragments
@@ -398,7 +402,7 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
                     acc[i][3] *= corr[1];
                 }
             }
-            uint32_t w0[C::kSub][kTerms], w1[C::kSub][kTerms];
+            uint32_t w0[C::kSub][kWTerms], w1[C::kSub][kWTerms];
             {
                 float m_use[2], v_use[2];
 #pragma unroll
@@ -414,10 +418,10 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
                         w[e] = fast_exp2(sc[u][e] - (v_use[e & 1] - v_exp[u]));
                         l_run[e & 1] += fast_exp2(sc[u][e] - m_use[e & 1]);
                     }
-                    split_pair<kTerms>(w0[u], w[0], w[1]);
-                    split_pair<kTerms>(w1[u], w[2], w[3]);
+                    split_pair<kWTerms>(w0[u], w[0], w[1]);
+                    split_pair<kWTerms>(w1[u], w[2], w[3]);
 #pragma unroll
-                    for (int k = 0; k < kTerms; ++k) w0[u][k] = movmatrix_trans(w0[u][k]), w1[u][k] = movmatrix_trans(w1[u][k]);
+                    for (int k = 0; k < kWTerms; ++k) w0[u][k] = movmatrix_trans(w0[u][k]), w1[u][k] = movmatrix_trans(w1[u][k]);
                 }
             }
             // ---- O^T += V^T P^T: lane (r, c) takes channels of its own for rows 2 c, 2 c + 1, 2 c + 8
@@ -425,10 +429,10 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
             auto add_product = [&](float (&d)[4], const uint32_t (&v)[4], int u) {
                 if constexpr (F32) {
                     float x[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_terms<kTerms>(x, v, w0[u], w1[u]);
+                    mma_terms<kWTerms>(x, v, w0[u], w1[u]);
                     add_rounded(d, x);
                 } else {
-                    mma_terms<kTerms>(d, v, w0[u], w1[u]);
+                    mma_terms<kWTerms>(d, v, w0[u], w1[u]);
                 }
             };
 #pragma unroll

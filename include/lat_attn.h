@@ -467,10 +467,9 @@ lat_status lat_kv_expand_q8(lat_dtype dt, const void *cache, int64_t cache_block
  * Size limits (LAT_ERR_UNSUPPORTED): batch <= 65535, n_heads * head_dim < 2^31, batch * n_heads *
  * ceil(head_dim / 128) < 2^31, and batch * n_kv_heads * ceil(n_heads / n_kv_heads / 8) work units of
  * up to ceil(max_kv_len / 64) + 2 tiles < 2^31 in all.
- * Sums, maxima and the joins are fp32.  A softmax weight that meets the values is held to 11 bits
- * for LAT_BF16 (2^-12 of it; the output's own rounding to bf16 is the error that shows) and to 22
- * for LAT_F32, and below 2^-21 of the largest weight (times its block's scale) to 2^-32 of that;
- * the log-sum-exp has none of this.  A query's channels are exact from 2^-22 of its largest on
+ * Sums, maxima and the joins are fp32.  A softmax weight that meets the values is held to 22 bits
+ * (2^-23 of it), but no closer than 2^-32 of the largest weight (times its block's scale); the
+ * log-sum-exp has none of this.  A query's channels are exact from 2^-22 of its largest on
  * (LAT_F32: within 2^-23 of themselves, or 2^-33 of the largest).
  * A query that holds a NaN or an infinity gives NaN, as does a visible key that holds a NaN.
  */
