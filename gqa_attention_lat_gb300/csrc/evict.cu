@@ -103,7 +103,9 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     }
     if (hk == 0 && rank == 0 && tid == 0) a.new_lens[b] = min(len, a.n_keep);
     if (len <= a.n_keep) {  // everything stays
-        for (int i = rank * kChooseThreads + tid; i < a.n_keep; i += P * kChooseThreads) kept[i] = i < len ? i : -1;
+        // (counted without a sign: a list may be nearly 2^31 entries long)
+        for (uint32_t i = rank * kChooseThreads + tid; i < (uint32_t)a.n_keep; i += P * kChooseThreads)
+            kept[i] = i < (uint32_t)len ? (int)i : -1;
         if (out != nullptr && out != w)
             for (int i = rank * kChooseThreads + tid; i < len; i += P * kChooseThreads) out[i] = w[i];
         return;
