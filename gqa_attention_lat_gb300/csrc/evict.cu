@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
     const int32_t *kept = a.kept + bh * a.n_keep;
     unsigned char *base = static_cast<unsigned char *>(unit & 1 ? a.v : a.k) + (int64_t)b * a.cache_seq + (int64_t)hk * a.cache_head;
     const int vecs = a.row_bytes / 16, rows = kStretchBytes / a.row_bytes;  // of a stretch
-    const int n_stretches = (a.n_keep + P * rows - 1) / (P * rows);
+    // (no entry from the capacity on can be a row: ascending, it would be past it)
+    const int n_rows = min(a.n_keep, a.capacity), n_stretches = (int)(((int64_t)n_rows + P * rows - 1) / (P * rows));
     const uint64_t deadline = globaltimer_ns() + a.timeout_ns;
     // this thread's pieces of a stretch: row and byte within it
     int row[kPieces], off[kPieces];
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
     // ahead of the copies.
     auto source = [&](int s) {
         const int64_t i = ((int64_t)s * P + rank) * rows + tid;
-        if (tid >= rows || s >= n_stretches || i >= a.n_keep) return -1;
+        if (tid >= rows || s >= n_stretches || i >= n_rows) return -1;
         const int j = __ldg(kept + i), before = i > 0 ? __ldg(kept + i - 1) : -1;
         if (j == -1) return -1;
         if (j < i || j >= a.capacity || j <= before || (i > 0 && before < 0)) {  // (ascending lists never have j < i)
@@ -313,6 +314,12 @@ __global__ void __launch_bounds__(kRowThreads) evict_rows_kernel(const EvictRows
         if constexpr (P > 1)
             if (tid < P && s < n_stretches && !(a.test_skip_tell && rank + s == 0)) mbar_arrive_cluster(cluster_addr(&here[s % kRowBars], (uint32_t)tid));
     };
+    if (!(unit & 1) && a.n_keep > n_rows) {  // what is not read below has to be -1
+        bool none = true;
+        for (uint32_t i = (uint32_t)n_rows + rank * kRowThreads + tid; i < (uint32_t)a.n_keep; i += P * kRowThreads)
+            none &= __ldg(kept + i) == -1;
+        if (!none) report_status(a.status, kErrBounds);
+    }
     if (tid == 0) {
         for (int i = 0; i < kRowBars; ++i) mbar_init(&here[i], P);
         fence_mbarrier_init();

@@ -550,9 +550,9 @@ lat_status lat_kv_evict_choose(const float *weights, int64_t weights_head_stride
  * -1 (lists as lat_kv_evict_choose writes them).  Rows behind keep their values, as do all other
  * bytes.  Keys keep the rotation of the position they were appended at; positions of keys in
  * the cache are no longer those of their tokens, so a window counts kept keys from then on.
- * An entry that is not above the one before it, or not below `capacity`, sets *status =
- * LAT_ERR_BOUNDS, is not moved, and leaves that head's rows unspecified.  After LAT_ERR_TIMEOUT all
- * listed heads' rows are unspecified.
+ * An entry that is not above the one before it, comes right behind a -1, or is not below `capacity`
+ * sets *status = LAT_ERR_BOUNDS, is not moved, and leaves that head's rows unspecified.  After
+ * LAT_ERR_TIMEOUT all listed heads' rows are unspecified.
  * The caches must be 16-byte aligned, must not overlap each other, and their strides positive
  * multiples of 16 bytes, n_keep >= 1, else LAT_ERR_INVALID_ARG; 16 * batch * n_kv_heads < 2^31, else
  * LAT_ERR_UNSUPPORTED.
