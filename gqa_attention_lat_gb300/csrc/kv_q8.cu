@@ -93,9 +93,10 @@ __global__ void __launch_bounds__(TEAM > kThreads ? TEAM : kThreads) append_q8_k
         if (t == 0 && m == 0 && hk == 0) report_status(a.status, kErrBounds);
         return;
     }
-    const int n = (pos >> a.block_shift) + (int)m, first = n << a.block_shift;  // the block and its first row
+    const int n = (pos >> a.block_shift) + (int)m;  // the block
+    if (n > (pos + a.n - 1) >> a.block_shift) return;  // (not reached: there may be none, nor an int for its rows)
+    const int first = n << a.block_shift;  // its first row
     const int lo = max(pos, first), hi = first + min(pos + a.n - first, 1 << a.block_shift);
-    if (lo >= hi) return;
     const T *src = static_cast<const T *>(which ? a.v : a.k) + ((int64_t)b * a.n + (lo - pos)) * a.rs + (int64_t)hk * D;
     unsigned char *rec = a.cache + (int64_t)b * a.cache_seq + (int64_t)n * a.cache_block + (int64_t)hk * a.cache_head;
     float *scale = reinterpret_cast<float *>(rec + ((int64_t)kRow << a.block_shift)) + which;
