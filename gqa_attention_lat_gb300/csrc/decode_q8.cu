@@ -348,7 +348,8 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
                 // ---- the log2 domain, the cap, the mask ------------------------------------------
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float f = fminf(hs[e] * scales.x, 3e38f);  // (an infinity must not meet a score of 0)
+                    // (an infinity, of either sign, must not meet a score of 0)
+                    const float f = fmaxf(fminf(hs[e] * scales.x, 3e38f), -3e38f);
                     sc[u][e] = sc[u][e] * pre[e] * f;
                     sc[u][e + 2] = sc[u][e + 2] * pre[e] * f;
                 }

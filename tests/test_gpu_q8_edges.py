@@ -6,7 +6,7 @@ import workloads as W
 from gpu_helpers import DT, ensure_library, status_tensor
 from gqa_attention_lat_gb300 import binding
 from oracle import q8
-from test_gpu_q8 import assert_same, f64, i32, rows
+from test_gpu_q8 import Cache, assert_same, check_decode, decode, f64, held, i32, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,25 @@ def test_the_last_rows_that_an_int_can_say(dt, block, D):
     used[:, :n * 2 * D] = used[:, block * 2 * D:block * 2 * D + 8] = True
     assert (t[:at] == 255).all() and (t[at + Hkv * rb:] == 255).all()
     assert (t[at:at + Hkv * rb].view(Hkv, rb)[~used] == 255).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [-0.1, 0.1])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_a_key_of_zeros_among_huge_ones(dt, scale, softcap):
+    """A block whose scale times the query's leaves fp32: its key of zeros has the score 0 all the
+    same, and all the weight where the others' scores lie far below."""
+    B, Hq, Hkv, D, cap, block, at = 2, 4, 1, 128, 70, 32, 40
+    k = rows(B, cap, Hkv, D, "f32", 1, "k").abs() + 0.5
+    k = k * (2.0 ** 123 if scale < 0 else -2.0 ** 123)
+    k[:, at] = 0.0
+    v = rows(B, cap, Hkv, D, "f32", 1, "v")
+    q = (W.normal((B, Hq * D), dtype="f32", device="cuda", seed=2, role="q").abs() + 0.5) * 2.0 ** 40
+    k, v, q = (x.to(W.torch_dtype(dt)) for x in (k, v, q))
+    c = Cache(B, cap, Hkv, D, block)
+    c.append(k, v, [0] * B, cap, dt=dt)
+    lens = [cap, at + 1]
+    out, lse, st = decode(c, q, i32(lens), dt, Hq, softcap=softcap, scale=scale)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check_decode(out, lse, q, held(k, block), held(v, block), lens, dt, Hq, D, 0, softcap, "zeros", scale=scale)
