@@ -183,8 +183,19 @@ __device__ __forceinline__ void add_columns(uint64_t (&sum)[2], const uint32_t (
     for (int k = 0; k < 8; ++k) x[k] = pair_of(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
     // A capped score is cap * y * f(y^2), y the score over the cap, f(z) = tanh(sqrt z) / sqrt z.  Most
     // lie well below the cap, where f is a polynomial through Chebyshev's nodes of [0, 0.0225] (to z^2,
-    // within 4e-8) or [0, 0.09] (to z^3, 2e-8).
+    // within 4e-8) or [0, 0.09] (to z^3, 2e-8).  Which form serves is decided by the pairs
+    // that count: what else lies in the tile must not show in a key's bits.
     uint64_t f[8];
+    uint32_t seen = 0;  // which columns see the key
+    if constexpr (CAP && MASK) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int4 hi = *reinterpret_cast<const int4 *>(tab.hi + n + 4 * q);
+            const int4 lo = *reinterpret_cast<const int4 *>(tab.lo + n + 4 * q);
+            seen |= (j <= hi.x && j > lo.x ? 1u << 4 * q : 0u) | (j <= hi.y && j > lo.y ? 2u << 4 * q : 0u) |
+                    (j <= hi.z && j > lo.z ? 4u << 4 * q : 0u) | (j <= hi.w && j > lo.w ? 8u << 4 * q : 0u);
+        }
+    }
     if constexpr (CAP) {
         float most = 0.f;
         uint64_t z[8];
@@ -193,7 +204,8 @@ __device__ __forceinline__ void add_columns(uint64_t (&sum)[2], const uint32_t (
             x[k] = mul2(x[k], twice(a.raw_over_cap));
             z[k] = mul2(x[k], x[k]);
             const float2 y = halves_of(z[k]);
-            most = fmaxf(most, fmaxf(y.x, y.y));
+            if constexpr (MASK) most = fmaxf(most, fmaxf(seen & 1u << 2 * k ? y.x : 0.f, seen & 2u << 2 * k ? y.y : 0.f));
+            else most = fmaxf(most, fmaxf(y.x, y.y));
         }
         const float c = a.cap_log2;
         if (!__any_sync(0xffffffffu, !(most < 0.0225f))) {
@@ -224,7 +236,10 @@ __device__ __forceinline__ void add_columns(uint64_t (&sum)[2], const uint32_t (
             const uint64_t y = fma2(x[2 * q + k], CAP ? f[2 * q + k] : twice(a.scale_log2), ls[k]);
             float2 p = halves_of(y);
             p.x = fast_exp2(p.x), p.y = fast_exp2(p.y);
-            if constexpr (MASK) {
+            if constexpr (CAP && MASK) {
+                p.x = seen & 1u << (4 * q + 2 * k) ? p.x : 0.f;
+                p.y = seen & 2u << (4 * q + 2 * k) ? p.y : 0.f;
+            } else if constexpr (MASK) {
                 const int2 hi = *reinterpret_cast<const int2 *>(tab.hi + n + 4 * q + 2 * k);
                 const int2 lo = *reinterpret_cast<const int2 *>(tab.lo + n + 4 * q + 2 * k);
                 p.x = j <= hi.x && j > lo.x ? p.x : 0.f;
@@ -477,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                 int hi = -1, lo = -1;
                 if (i < p.count) {
                     if (pos >= 0 && l[e] != -INFINITY) {  // (else the row sees nothing)
-                        hi = a.causal ? pos : 0x7fffffff;
+                        hi = a.causal ? pos : CAP ? r.len - 1 : 0x7fffffff;
                         lo = a.window > 0 ? pos - a.window : -1;
                     }
                     min_hi = min(min_hi, hi);
@@ -540,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             if (!wait_warp(&s_full[bar], (step / kSBufs) & 1)) return false;
             tc_fence_after();
             const int n1 = max(1, min(tab.count - off, kSCols)), j = first + row;  // (one that is not there is masked)
-            const bool mask = tab.min_hi < last || tab.max_lo >= first;
+            // (capped, keys that are not there must be known, so that they do not vote)
+            const bool mask = tab.min_hi < last || tab.max_lo >= first || (CAP && last - first < kKeysTile - 1);
             const uint32_t src = lanes + buf * kSCols;
             uint64_t part[2] = {0, 0};
             auto let_go = [&] {  // S may be written again (with keys held, the table too)
