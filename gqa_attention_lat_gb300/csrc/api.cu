@@ -1091,8 +1091,9 @@ lat_status key_weights_impl(lat_dtype dt, const void *q, int64_t q_rs, int n_q, 
     if (dt == LAT_BF16 && (!aligned16(q) || !aligned16(k_cache) || q_rs % 8 || cache_rs % 8 || cache_head_stride % 8 ||
                            cache_seq_stride % 8))
         return LAT_ERR_INVALID_ARG;
-    if (batch > 65535 || !query_row_ok(n_heads, head_dim) || (int64_t)batch * n_q > 0x7fffffffLL ||
-        ((int64_t)max_kv_len + 127) / 128 * n_kv_heads > 0x7fffffffLL / batch)
+    // (the kernels count to the end of a key's tile, and a key behind it, in int)
+    if (max_kv_len > 0x7fffff80 || batch > 65535 || !query_row_ok(n_heads, head_dim) ||
+        (int64_t)batch * n_q > 0x7fffffffLL || ((int64_t)max_kv_len + 127) / 128 * n_kv_heads > 0x7fffffffLL / batch)
         return LAT_ERR_UNSUPPORTED;
     lat::KeyWeightsArgs a{};
     a.q = q;

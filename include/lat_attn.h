@@ -511,8 +511,8 @@ lat_status lat_attn_decode_q8(lat_dtype dt, const void *q, int64_t q_rs, const v
  * For LAT_BF16, q and k_cache must be 16-byte aligned and q_rs and the cache strides multiples of
  * 8; softcap and scale finite, softcap >= 0, else LAT_ERR_INVALID_ARG (a cap above 1e36 counts
  * as 1e36).  batch <= 65535 (LAT_F32: batch * n_kv_heads), batch * n_q < 2^31, n_heads *
- * head_dim < 2^31 and batch * n_kv_heads * ceil(max_kv_len / 128) < 2^31, else
- * LAT_ERR_UNSUPPORTED.  After LAT_ERR_TIMEOUT the weights are unspecified.
+ * head_dim < 2^31, max_kv_len <= 2^31 - 128 and batch * n_kv_heads * ceil(max_kv_len / 128) < 2^31,
+ * else LAT_ERR_UNSUPPORTED.  After LAT_ERR_TIMEOUT the weights are unspecified.
  */
 lat_status lat_attn_key_weights(lat_dtype dt, const void *q, int64_t q_rs, int n_q,
                                 const void *k_cache, int64_t cache_rs,

@@ -2,8 +2,9 @@
 import pytest
 import torch
 
+import workloads as W
 from gpu_helpers import ensure_library
-from test_gpu_key_weights import inputs, run
+from test_gpu_key_weights import check, definition, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +66,25 @@ def test_capped_weights_hang_on_nothing_else(D, Hq, n_q):
             assert int(st.item()) == 0
             got.append(w)
     assert all(torch.equal(w, got[0]) for w in got)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("Hq,n_q", [(2, 1), (6, 9), (2, 300)])
+def test_the_last_keys_that_are_taken(dt, causal, Hq, n_q):
+    """A sequence of 2^31 - 128 keys, of which the last are seen.  (Rows begin 16 bytes apart, so each shares all
+    but 16 bytes with the next: 34 GB.)"""
+    L, D, window, n = 2 ** 31 - 128, 64, 500, 2000
+    step = 8 if dt == "bf16" else 4
+    q, _ = inputs(1, Hq, 1, D, 1, n_q, dt, 8)
+    buf = torch.empty(L * step + D, dtype=q.dtype, device="cuda")
+    buf[-n * step - D:] = W.normal((n * step + D,), dtype=dt, device="cuda", seed=4, role="k")
+    k = buf.as_strided((1, n, 1, D), (buf.numel() // 8 * 8, step, step, 1), (L - n) * step)
+    added, lse, worst = definition(q.reshape(1, n_q, Hq, D), k, [n], n_q, causal, window, D ** -0.5, 0.0)
+    w = torch.zeros(1, 1, L, device="cuda")
+    whole = buf.as_strided((1, L, 1, D), k.stride())
+    st = run(q, whole, [L], dt, Hq, 1, D, n_q, torch.from_numpy(lse).cuda(), w, causal, window)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    check(w[:, :, L - n:], torch.zeros(1, 1, n), added, worst, [n], "last keys")
+    assert all(int(x.count_nonzero()) == 0 for x in w[0, 0, :L - n].split(1 << 28))
