@@ -1236,9 +1236,9 @@ lat_status evict_rows_impl(lat_dtype dt, void *k_cache, void *v_cache, int64_t c
     if (!supported_head_dim(head_dim)) return LAT_ERR_UNSUPPORTED;
     if (batch == 0) return LAT_OK;
     const int es = dt == LAT_BF16 ? 2 : 4;
-    constexpr int64_t kMost = INT64_MAX / 4;  // elements whose bytes are still counted
-    if (cache_rs > kMost || cache_head_stride > kMost || cache_seq_stride > kMost || !k_cache || !v_cache || !kept ||
-        !aligned16(k_cache) || !aligned16(v_cache) ||
+    auto countable = [](int64_t stride) { return stride > 0 && stride <= INT64_MAX / 4; };  // in bytes, too
+    if (!countable(cache_rs) || !countable(cache_head_stride) || !countable(cache_seq_stride) || !k_cache || !v_cache ||
+        !kept || !aligned16(k_cache) || !aligned16(v_cache) ||
         !q4_strides_ok(cache_rs * es, cache_head_stride * es, cache_seq_stride * es))
         return LAT_ERR_INVALID_ARG;
     if ((int64_t)batch * n_kv_heads > 0x7fffffffLL / 16) return LAT_ERR_UNSUPPORTED;
