@@ -22,18 +22,21 @@
 //    weights 2^(x_j - m), in fp32.  A weight is two fp16 terms, 2^-23 of it; the references lie
 //    within 2^8 of the maxima and weights are taken 2^7 higher, so what falls under fp16's least is
 //    2^-32 of the largest.  (One term, 2^-12 of a weight, moves one bf16 output in ten to the next
-//    number: 8e-4 of the output, beside the 1.6e-3 of its rounding.  The second costs no time over long
-//    caches, 8 x 131072 keys 305.4 us so 302.2, and 1 to 2 % on short ones: 32 ragged sequences of up
-//    to 4096 keys 31.5 us, so 31.8.)
+//    number: 8e-4 of the output, beside the 1.6e-3 of its rounding.  The second costs 0.5 % over long
+//    caches, 8 x 131072 keys 300.8 -> 302.4 us, and 1 to 2 % on short ones: 32 ragged sequences of up
+//    to 4096 keys 31.5 -> 31.8.)
 //  * A query is brought to [2^8, 2^9) by a power of two of its own and taken as one fp16 number
 //    (a bf16 channel above 2^-22 of the largest is exact) or, LAT_F32, two (22 bits and signs).
 //  * LAT_F32: the scores' sums of 64 channels and the outputs' of 16 keys are chains of their own,
 //    joined by rounded adds.  (8 x 131072 tokens, 32 heads over 8: 308 us, as without; head_dim 512
-//    189 -> 210 us; the output's error 2.3e-6 -> 5e-7 of it over long caches.)
+//    189 -> 210 us; the output's error 2.3e-6 -> 5e-7 of it over long caches.)  So are bf16's outputs up
+//    to head_dim 128, where it is hidden behind HBM: 8 x 131072 keys 307.5 us, so 306.9, head_dim 64
+//    160.6 -> 162.4, and the share of bf16 outputs that are the next number to the exact one's falls from 1 in
+//    100 to next to none.  At head_dim 256 and 512 it would show, 312 -> 337 and 161 -> 181 us.
 //  * Waits are bounded; on expiry the CTA records LAT_ERR_TIMEOUT, drains its copies, quits.
-// What bounds it: HBM.  A 16-key tile of a warp is about 190 instructions at head_dim 128 for its
+// What bounds it: HBM.  A 16-key tile of a warp is about 300 instructions at head_dim 128 for its
 // 4 KB.  mma.sync rather than tcgen05: one query token fills 8 of N, and tcgen05 would need P in
-// e4m3 terms, written to shared memory, for a kernel whose tensor pipe is a tenth busy.
+// e4m3 terms, written to shared memory, for a kernel whose tensor pipe is a third busy.
 #include <algorithm>
 
 #include "cache_kernels.h"
@@ -56,6 +59,7 @@ struct Q8Cfg {
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kTerms = F32 ? 2 : 1;               // fp16 terms of q
     static constexpr int kWTerms = 2;                        // of a weight
+    static constexpr bool kRounded = F32 || D <= 128;        // outputs' sums joined by rounded adds
     static constexpr int kRow = 2 * D;
     static constexpr int kSub = D <= 80 ? 4 : D == 512 ? 1 : 2;  // 16-key MMA tiles a warp takes at once
     static constexpr int kKeys = 16 * kSub;
@@ -105,8 +109,8 @@ __device__ __forceinline__ void mma_terms(float (&d)[4], const uint32_t (&a)[4],
     for (int t = TERMS - 1; t >= 0; --t) mma_f16_16816(d, a, b0[t], b1[t]);
 }
 // d += x, rounded.  The tensor pipe cuts a sum off where its last bit ends, always toward zero: along
-// a chain of n products that is up to n 2^-23 of it, all to one side.  So LAT_F32's chains are short
-// sums of their own, joined by these.
+// a chain of n products that is up to n 2^-23 of it, all to one side.  So long chains are short sums
+// of their own, joined by these.
 __device__ __forceinline__ void add_rounded(float (&d)[4], const float (&x)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; e += 2) {
@@ -428,7 +432,7 @@ decode_q8_kernel(const __grid_constant__ Q8DecodeArgs a) {
             // ---- O^T += V^T P^T: lane (r, c) takes channels of its own for rows 2 c, 2 c + 1, 2 c + 8
             // and 2 c + 9 of a tile; bytes 2 i and 2 i + 1 are rows r and r + 8 of MMA tile i --------
             auto add_product = [&](float (&d)[4], const uint32_t (&v)[4], int u) {
-                if constexpr (F32) {
+                if constexpr (C::kRounded) {
                     float x[4] = {0.f, 0.f, 0.f, 0.f};
                     mma_terms<kWTerms>(x, v, w0[u], w1[u]);
                     add_rounded(d, x);

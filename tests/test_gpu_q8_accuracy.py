@@ -89,3 +89,38 @@ def test_one_unit_over_every_cta(G):
     c, kh, vh = filled(B, cap, Hkv, D, [8999], "bf16", 17)
     check(c, queries(B, G, D, 5), [8999], G, kh, vh, 0, "one unit, G%d" % G)
     check(c, queries(B, G, D, 6), [8999], G, kh, vh, 3, "three keys, G%d" % G)
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+def test_sums_over_long_shares_lean_to_no_side(D):
+    """Outputs around 0 over 32768 keys a CTA, against the exact ones rounded to bf16.
+
+    Scores are small (queries of a tenth), so that a score's D / 16 cuts of 2^-22 of at most 1.6 (the
+    exponents of 2) are below 3e-6, 2.1e-6 of a weight; its other roundings, the exponential and the
+    weight's two terms 2^-22 each at most, 5e-7 together.  These have no sign in common with the values, so
+    they move a sum of values around 0 by as much of its own size; and 512 rounded adds by sqrt(512) *
+    2^-24 / sqrt(3), 7.8e-7.  2.3e-6 of the outputs' root mean square in all (squares added): six times that,
+    1.5e-5, is what no output passes.  Sums cut off toward zero 1024 times by 2^-24 of what they have come to,
+    two thirds of it in the mean, are 4e-5 off.  (A number is not between two that are rounded to
+    bf16 only if it has gone over a border between them.)"""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B, Hkv, n = sms, 2, 32768  # a unit a CTA
+    c = Cache(B, n, Hkv, D, 64, head_major=True)
+    q = (torch.randn(B, Hkv * D, generator=torch.Generator().manual_seed(3)) * 0.1).cuda().bfloat16()
+    want = torch.empty(B, Hkv, D, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        g = torch.Generator(device="cuda").manual_seed(500 + b)
+        k, v = (torch.randn(1, n, Hkv, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+        c.append(k, v, [0], n, b0=b)
+        one = Cache(1, n, Hkv, D, 64)
+        one.append(k, v, [0], n)
+        k, v = (x[0].double() for x in one.expand([0], n))
+        s = torch.einsum("hd,nhd->hn", q[b].view(Hkv, D).double(), k) / math.sqrt(D)
+        assert s.abs().max().item() * math.log2(math.e) < 1.6
+        want[b] = torch.einsum("hn,nhd->hd", torch.softmax(s, -1), v)
+    out, _, st = decode(c, q, i32([n] * B), "bf16", Hkv)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    got, E = out.view(B, Hkv, D).double(), 1.5e-5 * want.square().mean().sqrt()
+    over = (got < (want - E).bfloat16().double()) | (got > (want + E).bfloat16().double())
+    assert int(over.sum()) == 0, "%d of %d" % (over.sum(), over.numel())
