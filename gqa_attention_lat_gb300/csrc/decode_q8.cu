@@ -34,9 +34,9 @@
 //    160.6 -> 162.4, and the share of bf16 outputs that are the next number to the exact one's falls from 1 in
 //    100 to next to none.  At head_dim 256 and 512 it would show, 312 -> 337 and 161 -> 181 us.
 //  * Waits are bounded; on expiry the CTA records LAT_ERR_TIMEOUT, drains its copies, quits.
-// What bounds it: HBM.  A 16-key tile of a warp is about 300 instructions at head_dim 128 for its
+// What bounds it: HBM.  A 16-key tile of a warp is about 290 instructions at head_dim 128 for its
 // 4 KB.  mma.sync rather than tcgen05: one query token fills 8 of N, and tcgen05 would need P in
-// e4m3 terms, written to shared memory, for a kernel whose tensor pipe is a third busy.
+// e4m3 terms, written to shared memory, for a kernel whose tensor pipe is busy 29 % of the time.
 #include <algorithm>
 
 #include "cache_kernels.h"

@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         __syncwarp();
     } else if (warp == kEpilogue + 1) {
         if (lane == 0) {
-            // N of a column tile's first and second tile of S
+            // N is the whole tile of columns: its two tiles of S lie side by side
             const uint32_t idesc = instr_desc(kKeysTile, a.n_cols, false);
             const uint64_t d_ring = sw128_desc(smem_u32(ring)), d_held = sw128_desc(smem_u32(held));
             // a chunk of keys is 16 KB wherever it lies

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(TEAM > kThreads ? TEAM : kThreads) append_q8_k
     if (t == 0 && (!begun || e > was)) *scale = two_to(e);
 }
 
-// two values as a pair in T's memory
+// the sixteen values of a part, s times its codes, into T's memory
 template <typename T>
 __device__ __forceinline__ void put16(T *dst, const uint32_t (&w)[4], float s, bool vec) {
     float v[16];
