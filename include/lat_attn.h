@@ -533,10 +533,10 @@ lat_status lat_attn_key_weights(lat_dtype dt, const void *q, int64_t q_rs, int n
  *     way): entry i takes the weight of key kept[i], entries from there to kv_lens[b] become 0
  *   new_lens: int32 [batch], min(kv_lens[b], n_keep); it must not overlap kv_lens
  * A length outside [0, max_kv_len] sets *status = LAT_ERR_BOUNDS and leaves that sequence's outputs
- * unwritten (lat_kv_evict_rows would move its rows by the list that an earlier call left there: look at
- * the status first, or fill `kept` with -1 before).  n_keep >= 1, n_first and n_last >= 0, n_first + n_last <= n_keep, strides at least
- * max_kv_len, else LAT_ERR_INVALID_ARG; max_kv_len <= 425984 and 8 * batch * n_kv_heads < 2^31,
- * else LAT_ERR_UNSUPPORTED.
+ * unwritten (lat_kv_evict_rows would move its rows by the list that an earlier call left there: look
+ * at the status first, or fill `kept` with -1 before).  n_keep >= 1, n_first and n_last >= 0,
+ * n_first + n_last <= n_keep, strides at least max_kv_len, else LAT_ERR_INVALID_ARG; max_kv_len <=
+ * 425984 and 8 * batch * n_kv_heads < 2^31, else LAT_ERR_UNSUPPORTED.
  */
 lat_status lat_kv_evict_choose(const float *weights, int64_t weights_head_stride,
                                int64_t weights_seq_stride, const int32_t *kv_lens,
